@@ -29,6 +29,50 @@ struct GemmLaunch {
     cudaStream_t stream;
 };
 
+// Encode a tiled tensor map with the 128-byte swizzle: `rank` dimensions of
+// `dims` elements (innermost first), strides in bytes of dimensions 1.., boxes
+// of `box` elements.  Out-of-range elements of a load read as zero.
+ts_status encode_map(CUtensorMap *m, const void *ptr, CUtensorMapDataType dt, int rank, const int64_t *dims,
+                     const int64_t *strides, const int *box);
+
+// Launch a kernel as a programmatic dependent of the previous kernel in its
+// stream (it calls grid_dep_wait before its first global memory access).
+template <class... KArgs, class... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                             Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Multiplier and shift of FastDiv for divisor d (1 <= d < 2^31; an empty grid's
+// divisor 0 is taken as 1, it divides nothing).
+inline FastDiv fast_div_for(int64_t d) {
+    if (d < 1) d = 1;
+    int l = 0;
+    while ((int64_t{1} << l) < d) ++l;
+    FastDiv f;
+    f.s = 31 + l;
+    f.m = ((uint64_t{1} << f.s) + static_cast<uint64_t>(d) - 1) / static_cast<uint64_t>(d);
+    f.pad = 0;
+    return f;
+}
+
+inline bool ranges_overlap(const void *a, int64_t abytes, const void *b, int64_t bbytes) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return a0 < b0 + static_cast<uintptr_t>(bbytes) && b0 < a0 + static_cast<uintptr_t>(abytes);
+}
+
 struct GemmVariant {
     int bn, cg, out, epi_warps, merge, log, stages, smem_bytes;
     ts_gemm_protocol protocol;  // barrier layout and arrival counts of this variant

@@ -59,6 +59,31 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn(ts_status *err) {
     return fn;
 }
 
+}  // namespace
+
+ts_status encode_map(CUtensorMap *m, const void *ptr, CUtensorMapDataType dt, int rank, const int64_t *dims,
+                     const int64_t *strides, const int *box) {
+    ts_status err = TS_OK;
+    auto fn = encode_fn(&err);
+    if (!fn) return err;
+    cuuint64_t d[3], st[2];
+    cuuint32_t b[3], e[3] = {1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = static_cast<cuuint64_t>(dims[i]);
+        b[i] = static_cast<cuuint32_t>(box[i]);
+        if (i > 0) st[i - 1] = static_cast<cuuint64_t>(strides[i - 1]);
+    }
+    CUresult r = fn(m, dt, static_cast<cuuint32_t>(rank), const_cast<void *>(ptr), d, st, b, e,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(TS_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled failed (%d) for rows of %lld elements, pitch %lld B",
+                    static_cast<int>(r), static_cast<long long>(dims[0]), static_cast<long long>(strides[0]));
+    return TS_OK;
+}
+
+namespace {
+
 // 2-D row-major tensor [rows][cols] with row pitch `ld` elements, copied in
 // boxes of box_rows x box_cols with the 128-byte swizzle.  Out-of-range
 // elements of a load read as zero; a store is clipped to the tensor.
@@ -102,19 +127,6 @@ ts_status make_map_d(CUtensorMap *m, const void *ptr, CUtensorMapDataType dt, in
     return TS_OK;
 }
 
-// Multiplier and shift of FastDiv for divisor d (1 <= d < 2^31; an empty grid's
-// divisor 0 is taken as 1, it divides nothing).
-FastDiv fast_div_for(int64_t d) {
-    if (d < 1) d = 1;
-    int l = 0;
-    while ((int64_t{1} << l) < d) ++l;
-    FastDiv f;
-    f.s = 31 + l;
-    f.m = ((uint64_t{1} << f.s) + static_cast<uint64_t>(d) - 1) / static_cast<uint64_t>(d);
-    f.pad = 0;
-    return f;
-}
-
 template <class T>
 __global__ void zero_fill_kernel(T *D, int64_t M, int64_t N, int64_t ldd) {
     const int64_t total = M * N;
@@ -123,11 +135,6 @@ __global__ void zero_fill_kernel(T *D, int64_t M, int64_t N, int64_t ldd) {
         const int64_t r = i / N, c = i - r * N;
         D[r * ldd + c] = T(0);
     }
-}
-
-bool ranges_overlap(const void *a, int64_t abytes, const void *b, int64_t bbytes) {
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + static_cast<uintptr_t>(bbytes) && b0 < a0 + static_cast<uintptr_t>(abytes);
 }
 
 struct Plan {
@@ -166,8 +173,6 @@ constexpr int64_t kTinyK = 128;
 // 8 us), far longer than a request takes.  Shorter loops keep two requests in
 // flight: with one k-block per tile the producer runs several tiles ahead.
 constexpr int64_t kLazyClcKBlocks = 32;
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The raster's group size and division constants for a planned launch.
 void set_raster(GemmParams &p, const Plan &pl, const ts_gemm_opts *o) {

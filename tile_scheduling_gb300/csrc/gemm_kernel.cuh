@@ -67,6 +67,7 @@
 
 #include "gemm_params.h"
 #include "ptx.cuh"
+#include "waits.cuh"
 
 namespace ts {
 
@@ -163,68 +164,6 @@ struct GemmCfg {
 __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t smem_addr) {
     return uint64_t((smem_addr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) |
            (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
-
-__device__ __forceinline__ void report_timeout(const GemmParams &p, int where) {
-    const unsigned long long info = (static_cast<unsigned long long>(where) << 32) | blockIdx.x;
-    if (atomicCAS(&p.status[0], 0ull, 1ull) == 0ull) atomicExch(&p.status[1], info);
-    atomicAdd(&p.status[2], 1ull);
-}
-
-// Bounded phase wait.  honor_abort: give up as soon as another role aborted
-// (role loops); drains pass false and rely on their own limit alone.
-static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int *abort_flag,
-                                       bool honor_abort, const GemmParams &p, int where) {
-    const uint64_t t0 = globaltimer();
-    for (uint32_t n = 1;; ++n) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((n & 15u) == 0) {
-            if (honor_abort && *abort_flag) return false;
-            if (globaltimer() - t0 > limit_ns) {
-                report_timeout(p, where);
-                *abort_flag = 1;
-                return false;
-            }
-        }
-    }
-}
-
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                           const GemmParams &p, int where) {
-    if (mbar_try_wait(bar, parity)) return true;
-    return wait_slow(bar, parity, p.timeout_ns, abort_flag, true, p, where);
-}
-
-// Bounded wait for roles whose waits last about a tile and whose wake-up is not
-// on the critical path (epilogue warps waiting for an accumulator, the CLC
-// scheduler waiting for a free slot): it sleeps between polls, leaving the
-// issue slots and shared-memory port of its SM sub-partition to the producer
-// and the MMA issuer.  Measured: 0.5-1 % faster at 8192^3 than polling.
-static __device__ __noinline__ bool wait_long_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                                   const GemmParams &p, int where) {
-    const uint64_t t0 = globaltimer();
-    for (;;) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (globaltimer() - t0 > p.timeout_ns) {
-            report_timeout(p, where);
-            *abort_flag = 1;
-            return false;
-        }
-        __nanosleep(500);
-    }
-}
-
-__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                          const GemmParams &p, int where) {
-    if (mbar_try_wait(bar, parity)) return true;
-    return wait_long_slow(bar, parity, abort_flag, p, where);
-}
-
-__device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                           const GemmParams &p) {
-    if (mbar_try_wait(bar, parity)) return true;
-    return wait_slow(bar, parity, p.drain_ns, abort_flag, false, p, WAIT_DRAIN);
 }
 
 // Protocol log: the barrier operations of each role's thread, in program

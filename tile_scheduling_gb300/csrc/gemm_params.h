@@ -22,8 +22,11 @@ enum : int32_t {
 
 // Device status word (library-owned, one per device):
 //   [0] first error code (0 = none, 1 = wait timeout, 2 = row bounds of the
-//       jagged copy outside [0, n])
-//   [1] code 1: (where << 32) | blockIdx.x;  code 2: the row index
+//       jagged copy outside [0, n], 3 = pieces of a chunked copy past its tiles,
+//       4 = row offsets of a grouped 8-bit product not ordered in [0, M],
+//       5 = a quantisation's gather index past the input, 6 = a combine's
+//       position past y, 7 = an expert index past the last expert)
+//   [1] code 1: (where << 32) | blockIdx.x;  otherwise the row, group or slot index
 //   [2] number of errors since the last check
 constexpr int kStatusWords = 4;
 
@@ -133,8 +136,9 @@ TS_HOST_DEVICE int32_t fast_div(int32_t n, const FastDiv &d) {
 // FastDiv: the epilogue warps decode every tile on their own critical path,
 // where the GPU's multi-instruction integer divide cost ~270 cycles per tile.
 // The host evaluates the same function to report the mapping
-// (ts_gemm_tile_coords).
-TS_HOST_DEVICE void raster(int32_t tile, const GemmParams &p, int32_t &mb, int32_t &nb) {
+// (ts_gemm_tile_coords).  P is a kernel's parameter block with the raster's fields.
+template <class P>
+TS_HOST_DEVICE void raster(int32_t tile, const P &p, int32_t &mb, int32_t &nb) {
     const int32_t G = p.raster_group;
     const int32_t g = fast_div(tile, p.div_group_tiles);
     const int32_t first_m = g * G;
