@@ -489,6 +489,197 @@ ts_status ts_copy_i16_rows(const int16_t *src, int16_t *dst, int64_t n, const in
 ts_status ts_copy_rows_launch_info(int64_t n, int64_t rows, int32_t sched, const ts_rows_opts *opts,
                                    ts_launch_info *info);
 
+/* ------------------------------------------------------------------------
+ * Mixture-of-experts operators: routing, 8-bit quantisation, block-scaled 8-bit
+ * products (plain and per expert), and the combine.  Every call is asynchronous
+ * on `stream`, allocates nothing and launches programmatic dependents, as the
+ * calls above.  An index that is out of range is found on the device, its work
+ * is left out, and the next ts_sync_and_check returns TS_ERR_INVALID_ARG naming
+ * the first one.
+ * ---------------------------------------------------------------------- */
+typedef enum { TS_FP8_E4M3 = 0, TS_FP8_E5M2 = 1 } ts_fp8_type;
+typedef enum {
+    TS_SCALE_BLOCK = 0, /* one scale for each 128 x 128 block of B */
+    TS_SCALE_ROW = 1    /* one scale for each row of B and 128 elements of K */
+} ts_scale;
+typedef enum { TS_SCORE_SOFTMAX = 0, TS_SCORE_SIGMOID = 1 } ts_score;
+
+/* Optional knobs for ts_gemm_fp8 and ts_gemm_fp8_grouped; zero means "default" for every field. */
+typedef struct {
+    int32_t a_type, b_type;  /* ts_fp8_type of A and of B (they may differ) */
+    int32_t b_scale;         /* ts_scale; TS_SCALE_ROW: plain product, trans_b = 0 only */
+    int32_t trans_b;         /* 0: B is [N][K]; 1: B is [K][N] (the product with the transposed matrix, read in
+                                place: the input gradient of a layer whose weights are B) */
+    int32_t tile;            /* ts_tile; results do not depend on it */
+    int32_t max_workers;     /* cap on persistent workers (CTAs or 2-CTA clusters) */
+    int64_t lda, ldb, ldd;   /* row strides in elements; 0 = dense rows */
+    int64_t b_group;         /* grouped: elements between the groups of B; 0 = dense */
+    int64_t sa_row, sa_blk;  /* strides of SA along M and along the K blocks; 0 = 1 and M (K-block major,
+                                the layout that reads fastest) */
+    int64_t sb_row, sb_blk;  /* strides of SB along its rows and columns; 0 = dense rows */
+    int64_t sb_group;        /* grouped: elements between the groups of SB; 0 = dense */
+    double timeout_s;        /* per-wait limit for every mbarrier wait in the kernel; 0 = 2 s */
+} ts_fp8_opts;
+
+/*
+ * ts_gemm_fp8 -- block-scaled product of 8-bit floating point matrices:
+ *
+ *   D[m][n] = sum over K blocks b of  SA[m][b] * SB(n, b) * sum_{128 b <= k < 128 (b + 1)} A[m][k] * B[n][k]
+ *
+ *   A      device, [M][K] row-major, e4m3 or e5m2
+ *   SA     device, fp32 scale of row m and K block b at SA[m * sa_row + b * sa_blk]
+ *   B      device, [N][K] row-major (trans_b = 0) or [K][N] (trans_b = 1)
+ *   SB     device, fp32: [ceil(rows of B / 128)][ceil(columns of B / 128)], or with
+ *          TS_SCALE_ROW [N][ceil(K / 128)]
+ *   D      device, [M][N] row-major, bf16 (rounded to nearest even from fp32) or fp32
+ *   M, N, K  sizes, each in [0, 2^31 - 1]; K need not be a multiple of 128
+ *
+ * Each K block's sum is accumulated by the tensor cores in fp32, scaled, and added
+ * in fp32.  A scale is fp32 of any value; an infinity or NaN in an operand or a
+ * scale shows in the rows and columns that use it.
+ * M == 0 or N == 0: no-op.  K == 0: D is filled with zeros.  A, B and their rows
+ * must start on 16-byte boundaries (lda and ldb multiples of 16), or the call
+ * returns TS_ERR_UNSUPPORTED; D may have any row pitch.  D must not overlap A or B.
+ */
+ts_status ts_gemm_fp8(const void *A, const float *SA, const void *B, const float *SB, void *D, int64_t M, int64_t N,
+                      int64_t K, int32_t out_dtype, const ts_fp8_opts *opts, void *stream);
+
+/*
+ * ts_gemm_fp8_grouped -- the experts' products: rows offsets[g] .. offsets[g + 1] of A
+ * times group g of B,
+ *
+ *   D[m][n] = as ts_gemm_fp8 with B and SB of group g,   offsets[g] <= m < offsets[g + 1]
+ *
+ *   A, SA, D  as for ts_gemm_fp8, M rows in all; rows of D outside every group are
+ *             not written
+ *   B, SB     device, `groups` matrices (and their block scales) one after another
+ *   offsets   DEVICE int64 array of groups + 1 non-decreasing row offsets in [0, M],
+ *             8-byte aligned, read by the kernel: the host need not know them.  A
+ *             group whose offsets are not ordered in [0, M] is not computed and is
+ *             reported by ts_sync_and_check.  An empty group costs nothing.
+ *   groups    0 .. 1024
+ */
+ts_status ts_gemm_fp8_grouped(const void *A, const float *SA, const void *B, const float *SB, void *D,
+                              const int64_t *offsets, int64_t groups, int64_t M, int64_t N, int64_t K,
+                              int32_t out_dtype, const ts_fp8_opts *opts, void *stream);
+
+/* Optional knobs for ts_quant_fp8; zero means "default" for every field. */
+typedef struct {
+    const int32_t *rows;   /* device gather index or NULL: output row r is input row rows[r] / rows_div; a
+                              negative entry gives zeros with scale 0 */
+    int64_t out_rows;      /* with rows: output rows */
+    int32_t rows_div;      /* 0 = 1 */
+    int32_t transpose;     /* 1: q is [N][M], blocks of 128 along M */
+    int64_t ldx, ldq;      /* row strides in elements; 0 = dense rows */
+    int64_t s_row, s_blk;  /* strides of scales along q's rows and along a row's blocks; 0 = 1 and q's
+                              rows (K-block major) */
+} ts_quant_opts;
+
+/*
+ * ts_quant_fp8 -- quantise a matrix to 8-bit floating point, one fp32 scale for each
+ * row of q and 128 of its columns:
+ *
+ *   a = max(max |x| over the block, 2^-100),  scale = a / top,  q = rne(x * (top / a))
+ *
+ * with top = 448 (e4m3) or 57344 (e5m2), so that q * scale restores x.
+ *
+ *   x       device, [M][N] row-major, bf16 (x_type = TS_OUT_BF16) or fp32 (TS_OUT_F32)
+ *   q       device, one byte per element: [M][N], [out_rows][N] with opts->rows, or
+ *           [N][M] with opts->transpose
+ *   scales  device, fp32, [rows of q][ceil(columns of q / 128)] at the strides of opts
+ * Any alignment and pitch is taken; rows of x on 16-byte and of q on 8-byte
+ * boundaries move in vectors.  A NaN stays a NaN in q; a block that holds an
+ * infinity has an infinite scale and a NaN there, so a product with it is NaN.
+ * q must not overlap x.
+ */
+ts_status ts_quant_fp8(const void *x, void *q, float *scales, int64_t M, int64_t N, int32_t x_type, int32_t q_type,
+                       const ts_quant_opts *opts, void *stream);
+
+/* Optional knobs for the router; zero means "default" for every field. */
+typedef struct {
+    const float *bias;     /* device fp32 [E] or NULL: added to the scores for the choice only */
+    int32_t score;         /* ts_score */
+    int32_t groups;        /* equal groups of consecutive experts, at most 32; 0 = 1 */
+    int32_t keep_groups;   /* groups that stay; 0 = all */
+    int32_t group_best;    /* a group's score is the sum of its 1 or 2 best experts; 0 = 1 */
+    int32_t no_renorm;     /* 1: weights are the scores themselves; 0: divided by their sum */
+    float scale;           /* factor of the weights; 0 = 1 */
+    int32_t reserved;
+    int64_t ldx, ldg;      /* row strides of logits and grad_logits in elements; 0 = E */
+} ts_route_opts;
+
+/*
+ * ts_moe_route -- choose top_k experts for each token.
+ *
+ *   s = softmax(logits) or sigmoid(logits),  c = s + bias
+ *   the keep_groups best groups by their best experts' c; the top_k best experts by c
+ *   in them, best first;  weights = scale * s / (sum of the chosen s)
+ *
+ * Equal values go to the lower index.  An expert whose logit is -inf (or whose c is
+ * -inf or NaN) cannot be chosen; where fewer than top_k are left the last slots hold
+ * expert -1 and weight 0 (a fully masked token holds nothing else).  A row with a NaN
+ * logit chooses among its other experts and all its weights are NaN.  The softmax's
+ * denominator is summed by halving the zero-padded expert axis (to a power of two of
+ * at least 32), so the choice is the same on every run and for every batch.
+ *
+ *   logits   device, [T][E] row-major, bf16 (dtype = TS_OUT_BF16) or fp32 (TS_OUT_F32)
+ *   experts  device int32 [T][top_k];  weights  device fp32 [T][top_k]
+ *   E        1 .. 1024;  top_k  1 .. 32
+ */
+ts_status ts_moe_route(const void *logits, int32_t *experts, float *weights, int64_t T, int32_t E, int32_t top_k,
+                       int32_t dtype, const ts_route_opts *opts, void *stream);
+
+/*
+ * ts_moe_route_grad -- gradient of ts_moe_route's weights by the logits, for the
+ * experts it chose (the choice itself has none; opts->bias and the groups are not
+ * used).  grad_logits is [T][E] in the logits' type, written whole; slots with
+ * expert -1 give nothing.
+ */
+ts_status ts_moe_route_grad(const void *logits, const int32_t *experts, const float *grad_weights, void *grad_logits,
+                            int64_t T, int32_t E, int32_t top_k, int32_t dtype, const ts_route_opts *opts,
+                            void *stream);
+
+/*
+ * ts_moe_plan -- sort the routed slots by expert, stably: the layout in which
+ * ts_gemm_fp8_grouped takes the tokens.
+ *
+ *   experts   device int32 [slots] (ts_moe_route's, flattened; negative = dropped)
+ *   offsets   device int64 [E + 1]: rows offsets[e] .. offsets[e + 1] belong to expert e
+ *   order     device int32 [slots]: the slot of each row, -1 past offsets[E]
+ *   position  device int32 [slots]: the row of each slot, -1 if dropped
+ *   workspace device scratch of ts_moe_plan_workspace(slots, E) bytes (may be NULL when
+ *             that is 0), 4-byte aligned, no initialisation; launches that may overlap
+ *             on the GPU need separate workspaces
+ */
+ts_status ts_moe_plan(const int32_t *experts, int64_t *offsets, int32_t *order, int32_t *position, int64_t slots,
+                      int32_t E, void *workspace, int64_t workspace_bytes, void *stream);
+int64_t ts_moe_plan_workspace(int64_t slots, int32_t E);
+
+/*
+ * ts_moe_combine -- each token's weighted sum of its experts' rows:
+ *
+ *   out[t][n] = sum_j weights[t][j] * y[position[t][j]][n]
+ *
+ * over the slots with position >= 0, in order, in fp32; weights NULL takes 1 (the
+ * gradient of a gather by tokens).  y [R][N] and out [T][N] are row-major with row
+ * strides ldy and ldo (0 = N), both bf16 or both fp32 (dtype).  out must not overlap y.
+ */
+ts_status ts_moe_combine(const void *y, const int32_t *position, const float *weights, void *out, int64_t T,
+                         int32_t top_k, int64_t N, int64_t R, int32_t dtype, int64_t ldy, int64_t ldo, void *stream);
+
+/*
+ * ts_moe_combine_grad -- the gradient of ts_moe_combine:
+ *
+ *   grad_y[position[t][j]][n] = weights[t][j] * grad_out[t][n]
+ *   grad_weights[t][j] = sum_n grad_out[t][n] * y[position[t][j]][n]   (fp32; 0 for a dropped slot)
+ *
+ * Rows of grad_y that no slot takes are not written; two slots must not take the
+ * same row.  grad_weights may be NULL.  grad_y must not overlap grad_out or y.
+ */
+ts_status ts_moe_combine_grad(const void *grad_out, const void *y, const int32_t *position, const float *weights,
+                              void *grad_y, float *grad_weights, int64_t T, int32_t top_k, int64_t N, int64_t R,
+                              int32_t dtype, int64_t ldy, int64_t ldo, int64_t ldg, void *stream);
+
 /*
  * ts_spin -- occupy `ctas` SMs for `duration_ns` nanoseconds (measured with
  * %globaltimer), to make part of the GPU unavailable to a following kernel.

@@ -70,6 +70,27 @@ class RowsOpts(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_int64), ("pack", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class Fp8Opts(ctypes.Structure):
+    _fields_ = [("a_type", ctypes.c_int32), ("b_type", ctypes.c_int32), ("b_scale", ctypes.c_int32),
+                ("trans_b", ctypes.c_int32), ("tile", ctypes.c_int32), ("max_workers", ctypes.c_int32),
+                ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64), ("ldd", ctypes.c_int64), ("b_group", ctypes.c_int64),
+                ("sa_row", ctypes.c_int64), ("sa_blk", ctypes.c_int64), ("sb_row", ctypes.c_int64),
+                ("sb_blk", ctypes.c_int64), ("sb_group", ctypes.c_int64), ("timeout_s", ctypes.c_double)]
+
+
+class QuantOpts(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_void_p), ("out_rows", ctypes.c_int64), ("rows_div", ctypes.c_int32),
+                ("transpose", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ldq", ctypes.c_int64),
+                ("s_row", ctypes.c_int64), ("s_blk", ctypes.c_int64)]
+
+
+class RouteOpts(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("score", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("keep_groups", ctypes.c_int32), ("group_best", ctypes.c_int32), ("no_renorm", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32), ("ldx", ctypes.c_int64),
+                ("ldg", ctypes.c_int64)]
+
+
 class GemmProtocol(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "cluster", "stages", "tx_bytes", "full_arrivals", "empty_arrivals", "accumulators", "tmem_full_arrivals",
@@ -112,7 +133,19 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ts_status_string.restype = ctypes.c_char_p
     lib.ts_last_error_detail.argtypes = []
     lib.ts_last_error_detail.restype = ctypes.c_char_p
-    for name in ("ts_gemm_bf16", "ts_gemm_bf16_ex", "ts_gemm_launch_info", "ts_gemm_bf16_checked_noalloc",
+    F8, QO, RO = ctypes.POINTER(Fp8Opts), ctypes.POINTER(QuantOpts), ctypes.POINTER(RouteOpts)
+    lib.ts_gemm_fp8.argtypes = [P, P, P, P, P, I64, I64, I64, I32, F8, P]
+    lib.ts_gemm_fp8_grouped.argtypes = [P, P, P, P, P, P, I64, I64, I64, I64, I32, F8, P]
+    lib.ts_quant_fp8.argtypes = [P, P, P, I64, I64, I32, I32, QO, P]
+    lib.ts_moe_route.argtypes = [P, P, P, I64, I32, I32, I32, RO, P]
+    lib.ts_moe_route_grad.argtypes = [P, P, P, P, I64, I32, I32, I32, RO, P]
+    lib.ts_moe_plan.argtypes = [P, P, P, P, I64, I32, P, I64, P]
+    lib.ts_moe_plan_workspace.argtypes = [I64, I32]
+    lib.ts_moe_plan_workspace.restype = I64
+    lib.ts_moe_combine.argtypes = [P, P, P, P, I64, I32, I64, I64, I32, I64, I64, P]
+    lib.ts_moe_combine_grad.argtypes = [P, P, P, P, P, P, I64, I32, I64, I64, I32, I64, I64, I64, P]
+    for name in ("ts_gemm_fp8", "ts_gemm_fp8_grouped", "ts_quant_fp8", "ts_moe_route", "ts_moe_route_grad",
+                 "ts_moe_plan", "ts_moe_combine", "ts_moe_combine_grad", "ts_gemm_bf16", "ts_gemm_bf16_ex", "ts_gemm_launch_info", "ts_gemm_bf16_checked_noalloc",
                  "ts_gemm_tile_coords", "ts_gemm_protocol_info", "ts_gemm_bf16_grouped", "ts_gemm_grouped_launch_info",
                  "ts_gemm_grouped_order", "ts_copy_i16", "ts_copy_i16_rows", "ts_copy_rows_launch_info", "ts_spin",
                  "ts_spin_wait_started", "ts_sync_and_check"):
@@ -514,6 +547,253 @@ def ts_copy_i16_rows_ptr(src: int, dst: int, n: int, offsets: int, rows: int, sc
     o = _rows_opts(**opts)
     return _lib.ts_copy_i16_rows(ctypes.c_void_p(src), ctypes.c_void_p(dst), int(n), ctypes.c_void_p(offsets),
                                  int(rows), _sched(sched), ctypes.byref(o), _stream_handle(stream))
+
+
+TS_FP8_E4M3, TS_FP8_E5M2 = 0, 1
+TS_SCALE_BLOCK, TS_SCALE_ROW = 0, 1
+TS_SCORE_SOFTMAX, TS_SCORE_SIGMOID = 0, 1
+_FP8 = {torch.float8_e4m3fn: TS_FP8_E4M3, torch.float8_e5m2: TS_FP8_E5M2}
+_SCORE = {"softmax": TS_SCORE_SOFTMAX, "sigmoid": TS_SCORE_SIGMOID}
+
+
+def _tensor(t, name: str, dtypes, dims: int) -> None:
+    """Check a CUDA tensor's type (one of ``dtypes``) and number of dimensions."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise TypeError(f"{name} must be a tensor of {', '.join(str(d) for d in dtypes)}")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be on a CUDA device")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must be {dims}-D")
+
+
+def _rows_of(t, name: str) -> int:
+    """Row stride of a matrix whose last dimension is dense (0, for the default, with a single row)."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.stride(-2) if t.shape[-2] > 1 else 0
+
+
+def _dense(t, name: str, dtype, shape) -> int:
+    _tensor(t, name, (dtype,), len(shape))
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _fp8_opts(A, SA, B, SB, D, trans_b, tile, max_workers, timeout_s):
+    """Checks and options that the plain and the grouped 8-bit product share; returns (opts, M, N, K)."""
+    _tensor(A, "A", _FP8, 2)
+    _tensor(B, "B", _FP8, 3 if B.dim() == 3 else 2)
+    _tensor(D, "D", _OUT, 2)
+    _tensor(SA, "SA", (torch.float32,), 2)
+    _tensor(SB, "SB", (torch.float32,), B.dim())
+    M, K = A.shape
+    R, C = B.shape[-2:]
+    N = C if trans_b else R
+    if (R if trans_b else C) != K or tuple(D.shape) != (M, N):
+        raise ValueError(f"shape mismatch: A {tuple(A.shape)}, B {tuple(B.shape)}, D {tuple(D.shape)}")
+    kb = -(-K // 128)
+    if tuple(SA.shape) != (M, kb):
+        raise ValueError(f"SA must be [{M}, {kb}], not {tuple(SA.shape)}")
+    o = Fp8Opts()
+    if tuple(SB.shape[-2:]) == (-(-R // 128), -(-C // 128)):
+        pass
+    elif not trans_b and tuple(SB.shape) == (N, kb):
+        o.b_scale = TS_SCALE_ROW
+    else:
+        raise ValueError(f"SB {tuple(SB.shape)} holds neither a scale for each 128 x 128 block of B {tuple(B.shape)} "
+                         "nor one for each row and 128 columns")
+    o.a_type, o.b_type = _FP8[A.dtype], _FP8[B.dtype]
+    o.trans_b = int(bool(trans_b))
+    o.tile = _TILE[tile] if isinstance(tile, str) else int(tile)
+    o.max_workers = int(max_workers)
+    o.lda, o.ldb, o.ldd = _rows_of(A, "A"), _rows_of(B, "B"), _rows_of(D, "D")
+    o.sa_row, o.sa_blk = SA.stride()
+    o.sb_row, o.sb_blk = SB.stride()[-2:]
+    o.timeout_s = float(timeout_s)
+    return o, M, N, K
+
+
+def ts_gemm_fp8(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch.Tensor, D: torch.Tensor, trans_b=False,
+                tile="auto", max_workers=0, timeout_s=0.0, stream=None) -> None:
+    """D = (A * SA) @ (B * SB).T for 8-bit floating point A [M, K] and B [N, K]; D [M, N] is bf16 or fp32.
+
+    SA [M, ceil(K / 128)] holds a scale for each row and 128 columns of A; SB one for each 128 x 128
+    block of B ([ceil(N / 128), ceil(K / 128)]) or for each row and 128 columns ([N, ceil(K / 128)]).
+    Where both shapes are the same (N = 1) the two mean the same.  Scales may have any strides; SA reads
+    fastest with its rows contiguous (the transpose of a [ceil(K / 128), M] tensor).  ``trans_b``: B is
+    [K, N] with block scales [ceil(K / 128), ceil(N / 128)].  Rows may be strided; rows of A and B start
+    on 16-byte boundaries.  Asynchronous on ``stream`` (default: torch's current stream)."""
+    if B.dim() != 2:
+        raise ValueError("B must be 2-D")
+    o, M, N, K = _fp8_opts(A, SA, B, SB, D, trans_b, tile, max_workers, timeout_s)
+    _check(_lib.ts_gemm_fp8(A.data_ptr(), SA.data_ptr(), B.data_ptr(), SB.data_ptr(), D.data_ptr(), M, N, K,
+                            _OUT[D.dtype], o, _stream_handle(stream)))
+
+
+def ts_gemm_fp8_grouped(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch.Tensor, D: torch.Tensor,
+                        offsets: torch.Tensor, trans_b=False, tile="auto", max_workers=0, timeout_s=0.0,
+                        stream=None) -> None:
+    """D[o_g:o_g+1] = (A * SA)[o_g:o_g+1] @ (B[g] * SB[g]).T for every group g, o = offsets (int64, on the device).
+
+    B [groups, N, K] (``trans_b``: [groups, K, N]) with block scales SB of the same leading dimension;
+    everything else as ts_gemm_fp8.  Rows outside every group are not written."""
+    if B.dim() != 3:
+        raise ValueError("B must be [groups, N, K] or, with trans_b, [groups, K, N]")
+    G = B.shape[0]
+    o, M, N, K = _fp8_opts(A, SA, B, SB, D, trans_b, tile, max_workers, timeout_s)
+    if SB.shape[0] != G:
+        raise ValueError(f"SB must hold the scales of {G} groups")
+    o.b_group, o.sb_group = (B.stride(0), SB.stride(0)) if G > 1 else (0, 0)
+    _check(_lib.ts_gemm_fp8_grouped(A.data_ptr(), SA.data_ptr(), B.data_ptr(), SB.data_ptr(), D.data_ptr(),
+                                    _dense(offsets, "offsets", torch.int64, (G + 1,)), G, M, N, K, _OUT[D.dtype], o,
+                                    _stream_handle(stream)))
+
+
+def ts_quant_fp8(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, rows=None, rows_div=1, transpose=False,
+                 stream=None) -> None:
+    """Quantise x [M, N] (bf16 or fp32) to 8-bit floating point q with one fp32 scale for each row and 128 columns of q.
+
+    q is [M, N]; with ``rows`` (int32, on the device) [len(rows), N], row r taken from x's row
+    rows[r] // rows_div (zeros for a negative entry); with ``transpose`` [N, M].  scales is
+    [rows of q, ceil(columns of q / 128)] of any strides; with its rows contiguous it is what
+    ts_gemm_fp8 reads fastest."""
+    _tensor(x, "x", _OUT, 2)
+    _tensor(q, "q", _FP8, 2)
+    _tensor(scales, "scales", (torch.float32,), 2)
+    M, N = x.shape
+    o = QuantOpts()
+    if rows is not None:
+        if transpose:
+            raise ValueError("rows and transpose cannot be combined")
+        if rows.dim() != 1:
+            raise ValueError("rows must be 1-D")
+        o.rows = _dense(rows, "rows", torch.int32, rows.shape)
+        o.out_rows = rows.shape[0]
+        o.rows_div = int(rows_div)
+        if o.rows_div < 1:
+            raise ValueError("rows_div must be at least 1")
+    want = (N, M) if transpose else (o.out_rows if rows is not None else M, N)
+    if tuple(q.shape) != want or tuple(scales.shape) != (want[0], -(-want[1] // 128)):
+        raise ValueError(f"q must be {want} and scales {(want[0], -(-want[1] // 128))}, not {tuple(q.shape)} and "
+                         f"{tuple(scales.shape)}")
+    if rows is not None and want[0] == 0:
+        return
+    o.transpose = int(bool(transpose))
+    o.ldx, o.ldq = _rows_of(x, "x"), _rows_of(q, "q")
+    o.s_row, o.s_blk = scales.stride()
+    _check(_lib.ts_quant_fp8(x.data_ptr(), q.data_ptr(), scales.data_ptr(), M, N, _OUT[x.dtype], _FP8[q.dtype], o,
+                             _stream_handle(stream)))
+
+
+def _route_opts(logits, score, renorm, scale, bias=None, groups=1, keep_groups=0, group_best=1):
+    _tensor(logits, "logits", _OUT, 2)
+    o = RouteOpts()
+    o.score = _SCORE[score] if isinstance(score, str) else int(score)
+    o.groups, o.keep_groups, o.group_best = int(groups), int(keep_groups), int(group_best)
+    o.no_renorm = int(not renorm)
+    o.scale = float(scale)
+    if bias is not None:
+        o.bias = _dense(bias, "bias", torch.float32, (logits.shape[1],))
+    o.ldx = _rows_of(logits, "logits")
+    return o
+
+
+def ts_moe_route(logits: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, bias=None, score="softmax",
+                 groups=1, keep_groups=0, group_best=1, renorm=True, scale=1.0, stream=None) -> None:
+    """Choose experts [T, k] (int32, best first) and their weights [T, k] (fp32) from logits [T, E] (bf16 or fp32).
+
+    ``score``: "softmax" or "sigmoid"; ``bias`` [E] is added to the scores for the choice only; of
+    ``groups`` equal groups of experts the ``keep_groups`` best (0: all) stay, by the sum of their
+    ``group_best`` (1 or 2) best experts.  Equal values go to the lower index; an expert with logit -inf is
+    never chosen, and slots without one hold -1 and weight 0.  ``renorm`` divides the weights by their sum."""
+    o = _route_opts(logits, score, renorm, scale, bias, groups, keep_groups, group_best)
+    T, E = logits.shape
+    _tensor(experts, "experts", (torch.int32,), 2)
+    k = experts.shape[1]
+    _check(_lib.ts_moe_route(logits.data_ptr(), _dense(experts, "experts", torch.int32, (T, k)),
+                             _dense(weights, "weights", torch.float32, (T, k)), T, E, k, _OUT[logits.dtype], o,
+                             _stream_handle(stream)))
+
+
+def ts_moe_route_grad(logits: torch.Tensor, experts: torch.Tensor, grad_weights: torch.Tensor,
+                      grad_logits: torch.Tensor, score="softmax", renorm=True, scale=1.0, stream=None) -> None:
+    """grad_logits [T, E] (the logits' type) from grad_weights [T, k], for the experts that ts_moe_route chose."""
+    o = _route_opts(logits, score, renorm, scale)
+    T, E = logits.shape
+    _tensor(experts, "experts", (torch.int32,), 2)
+    k = experts.shape[1]
+    _tensor(grad_logits, "grad_logits", (logits.dtype,), 2)
+    if tuple(grad_logits.shape) != (T, E):
+        raise ValueError(f"grad_logits must be {(T, E)}")
+    o.ldg = _rows_of(grad_logits, "grad_logits")
+    _check(_lib.ts_moe_route_grad(logits.data_ptr(), _dense(experts, "experts", torch.int32, (T, k)),
+                                  _dense(grad_weights, "grad_weights", torch.float32, (T, k)), grad_logits.data_ptr(),
+                                  T, E, k, _OUT[logits.dtype], o, _stream_handle(stream)))
+
+
+def ts_moe_plan_workspace(slots: int, experts: int) -> int:
+    """Bytes of workspace that ts_moe_plan needs for that many slots and experts."""
+    return int(_lib.ts_moe_plan_workspace(int(slots), int(experts)))
+
+
+def ts_moe_plan(experts: torch.Tensor, offsets: torch.Tensor, order: torch.Tensor, position: torch.Tensor,
+                workspace=None, stream=None) -> None:
+    """Sort the slots of experts (int32, negative = dropped) by expert, stably.
+
+    offsets [E + 1] (int64): the rows of each expert; order [slots] (int32): the slot of each row, -1 past
+    the last; position (int32, experts' shape): the row of each slot, -1 if dropped.  The workspace that
+    many slots need is allocated here unless one is passed."""
+    n = experts.numel()
+    E = offsets.numel() - 1
+    _tensor(experts, "experts", (torch.int32,), experts.dim())
+    need = _lib.ts_moe_plan_workspace(n, E)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=experts.device)
+    if workspace is not None and (not workspace.is_cuda or not workspace.is_contiguous()):
+        raise TypeError("workspace must be a contiguous CUDA tensor")
+    ptr, size = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else (0, 0)
+    _check(_lib.ts_moe_plan(_dense(experts, "experts", torch.int32, experts.shape),
+                            _dense(offsets, "offsets", torch.int64, (E + 1,)),
+                            _dense(order, "order", torch.int32, (n,)),
+                            _dense(position, "position", torch.int32, experts.shape), n, E, ptr, size,
+                            _stream_handle(stream)))
+
+
+def ts_moe_combine(y: torch.Tensor, position: torch.Tensor, out: torch.Tensor, weights=None, stream=None) -> None:
+    """out[t] = sum_j weights[t, j] * y[position[t, j]] over the slots with position >= 0 (weights None: 1).
+
+    y [R, N] and out [T, N] are both bf16 or both fp32; position [T, k] int32; weights [T, k] fp32."""
+    _tensor(y, "y", _OUT, 2)
+    _tensor(out, "out", (y.dtype,), 2)
+    _tensor(position, "position", (torch.int32,), 2)
+    T, k = position.shape
+    R, N = y.shape
+    if tuple(out.shape) != (T, N):
+        raise ValueError(f"out must be {(T, N)}")
+    w = _dense(weights, "weights", torch.float32, (T, k)) if weights is not None else 0
+    _check(_lib.ts_moe_combine(y.data_ptr(), _dense(position, "position", torch.int32, (T, k)), w, out.data_ptr(), T,
+                               k, N, R, _OUT[y.dtype], _rows_of(y, "y"), _rows_of(out, "out"), _stream_handle(stream)))
+
+
+def ts_moe_combine_grad(grad_out: torch.Tensor, y: torch.Tensor, position: torch.Tensor, weights, grad_y: torch.Tensor,
+                        grad_weights=None, stream=None) -> None:
+    """The gradient of ts_moe_combine: grad_y[position[t, j]] = weights[t, j] * grad_out[t] and
+    grad_weights[t, j] = <grad_out[t], y[position[t, j]]>; rows of grad_y that no slot takes are not written."""
+    _tensor(y, "y", _OUT, 2)
+    _tensor(grad_out, "grad_out", (y.dtype,), 2)
+    _tensor(grad_y, "grad_y", (y.dtype,), 2)
+    _tensor(position, "position", (torch.int32,), 2)
+    T, k = position.shape
+    R, N = y.shape
+    if tuple(grad_out.shape) != (T, N) or tuple(grad_y.shape) != (R, N):
+        raise ValueError(f"grad_out must be {(T, N)} and grad_y {(R, N)}")
+    w = _dense(weights, "weights", torch.float32, (T, k)) if weights is not None else 0
+    gw = _dense(grad_weights, "grad_weights", torch.float32, (T, k)) if grad_weights is not None else 0
+    _check(_lib.ts_moe_combine_grad(grad_out.data_ptr(), y.data_ptr(),
+                                    _dense(position, "position", torch.int32, (T, k)), w, grad_y.data_ptr(), gw, T, k,
+                                    N, R, _OUT[y.dtype], _rows_of(y, "y"), _rows_of(grad_out, "grad_out"),
+                                    _rows_of(grad_y, "grad_y"), _stream_handle(stream)))
 
 
 def ts_spin(ctas: int, duration_ns: int, started: torch.Tensor, stream=None) -> None:

@@ -1,0 +1,300 @@
+// The way back from the experts: each token's weighted sum of its experts' rows,
+// and its gradient.
+//
+//   out[t] = sum_j w[t][j] * y[position[t][j]]            (slots with position < 0 are dropped)
+//   grad_y[position[t][j]] = w[t][j] * grad_out[t],   grad_w[t][j] = <grad_out[t], y[position[t][j]]>
+//
+// Both are bound by memory: each row of y moves once.  Sums run in fp32, a
+// token's slots in order, so results do not depend on timing.
+#include <algorithm>
+
+#include "common.h"
+#include "ptx.cuh"
+
+namespace ts {
+namespace {
+
+constexpr int64_t kMaxDim = 0x7fffffffLL;
+constexpr int kThreads = 256;
+constexpr int kSlots = 8;  // slots whose rows are in flight together
+
+struct CombineParams {
+    const void *y, *grad_out;
+    void *out, *grad_y;
+    float *grad_w;
+    const float *w;  // nullptr: every weight is 1
+    const int32_t *position;
+    int64_t T, N, R;
+    int64_t ldy, ldo, ldg;  // rows of y, of out (or grad_out), of grad_y
+    int32_t k;
+    int32_t vec;
+    unsigned long long *status;
+};
+
+template <class T>
+constexpr int kVec = 16 / sizeof(T);
+
+template <class T>
+__device__ __forceinline__ void load_vec(const T *x, bool vec, int64_t n, float (&v)[kVec<T>]) {
+    if (vec && n >= kVec<T>) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x));
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                v[i] = __uint_as_float(w[i]);
+            } else {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i) {
+            v[i] = 0.f;
+            if (i < n) {
+                if constexpr (sizeof(T) == 4)
+                    v[i] = x[i];
+                else
+                    v[i] = __uint_as_float(uint32_t(x[i]) << 16);
+            }
+        }
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void store_vec(T *x, bool vec, int64_t n, const float (&v)[kVec<T>]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4)
+            w[i] = __float_as_uint(v[i]);
+        else
+            w[i] = pack_bf16x2(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]));
+    }
+    if (vec && n >= kVec<T>) {
+        __stcs(reinterpret_cast<uint4 *>(x), make_uint4(w[0], w[1], w[2], w[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i) {
+            if (i < n) {
+                if constexpr (sizeof(T) == 4)
+                    x[i] = __uint_as_float(w[i]);
+                else
+                    x[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+            }
+        }
+    }
+}
+
+// The row of y that slot (t, j) takes, or -1.
+__device__ __forceinline__ int32_t slot_row(const CombineParams &p, int64_t t, int32_t j) {
+    if (j >= p.k) return -1;
+    const int32_t at = p.position[t * p.k + j];
+    if (at >= p.R) {
+        if (threadIdx.x == 0) {
+            if (atomicCAS(&p.status[0], 0ull, 6ull) == 0ull)
+                atomicExch(&p.status[1], static_cast<unsigned long long>(t * p.k + j));
+            atomicAdd(&p.status[2], 1ull);
+        }
+        return -1;
+    }
+    return at;
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant__ CombineParams p) {
+    grid_dep_wait();
+    grid_dep_launch();
+    constexpr int V = kVec<T>;
+    const int64_t t = blockIdx.x;
+    const int64_t c = (static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x) * V;
+    float sum[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum[i] = 0.f;
+    for (int32_t j0 = 0; j0 < p.k; j0 += kSlots) {
+        float v[kSlots][V], w[kSlots];
+        bool has[kSlots];
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+            const int32_t at = slot_row(p, t, j0 + j);
+            has[j] = at >= 0;
+            w[j] = at >= 0 && p.w ? p.w[t * p.k + j0 + j] : 1.f;
+            load_vec(static_cast<const T *>(p.y) + (at >= 0 ? at : 0) * p.ldy + c, p.vec, at >= 0 ? p.N - c : 0, v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j)
+            if (has[j]) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum[i] = fmaf(w[j], v[j][i], sum[i]);
+            }
+    }
+    if (c < p.N) store_vec(static_cast<T *>(p.out) + t * p.ldo + c, p.vec, p.N - c, sum);
+}
+
+// One CTA per token: grad_out's row is read for each group of kSlots slots (from
+// L2 after the first), the slots' dot products are reduced in fixed order.
+template <class T>
+__global__ void __launch_bounds__(kThreads) combine_grad_kernel(const __grid_constant__ CombineParams p) {
+    __shared__ float part[kSlots][kThreads / 32];
+    grid_dep_wait();
+    grid_dep_launch();
+    constexpr int V = kVec<T>;
+    const int64_t t = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int32_t j0 = 0; j0 < p.k; j0 += kSlots) {
+        int32_t at[kSlots];
+        float w[kSlots], dot[kSlots];
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+            at[j] = slot_row(p, t, j0 + j);
+            w[j] = at[j] >= 0 && p.w ? p.w[t * p.k + j0 + j] : 1.f;
+            dot[j] = 0.f;
+        }
+        for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < p.N; c += kThreads * V) {
+            float g[V];
+            load_vec(static_cast<const T *>(p.grad_out) + t * p.ldo + c, p.vec, p.N - c, g);
+            float y[kSlots][V];
+#pragma unroll
+            for (int j = 0; j < kSlots; ++j)
+                if (at[j] >= 0) load_vec(static_cast<const T *>(p.y) + at[j] * p.ldy + c, p.vec, p.N - c, y[j]);
+#pragma unroll
+            for (int j = 0; j < kSlots; ++j) {
+                if (at[j] < 0) continue;
+                float o[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    dot[j] = fmaf(g[i], y[j][i], dot[j]);
+                    o[i] = w[j] * g[i];
+                }
+                store_vec(static_cast<T *>(p.grad_y) + at[j] * p.ldg + c, p.vec, p.N - c, o);
+            }
+        }
+        if (p.grad_w) {
+#pragma unroll
+            for (int j = 0; j < kSlots; ++j) {
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
+                if (lane == 0) part[j][warp] = dot[j];
+            }
+            __syncthreads();
+            if (threadIdx.x < kSlots && j0 + static_cast<int>(threadIdx.x) < p.k) {
+                float s = 0.f;
+#pragma unroll
+                for (int i = 0; i < kThreads / 32; ++i) s += part[threadIdx.x][i];
+                p.grad_w[t * p.k + j0 + threadIdx.x] = s;  // 0 for a dropped slot
+            }
+            __syncthreads();
+        }
+    }
+}
+
+bool row16(const void *x, int64_t ld, int esize) {
+    return reinterpret_cast<uintptr_t>(x) % 16 == 0 && (ld * esize) % 16 == 0;
+}
+
+ts_status combine_check(int64_t T, int32_t k, int64_t N, int64_t R, int32_t dtype, int64_t ldy, int64_t ldo,
+                        int64_t ldg) {
+    if (T < 0 || N < 0 || R < 0 || T > kMaxDim || N > kMaxDim || R > kMaxDim)
+        return fail(TS_ERR_INVALID_ARG, "sizes must be in [0, 2^31-1] (T=%lld N=%lld R=%lld)",
+                    static_cast<long long>(T), static_cast<long long>(N), static_cast<long long>(R));
+    if (k < 0 || k > 1024) return fail(TS_ERR_INVALID_ARG, "top_k = %d (0 to 1024)", k);
+    if (dtype != TS_OUT_BF16 && dtype != TS_OUT_F32) return fail(TS_ERR_INVALID_ARG, "dtype %d", dtype);
+    if (ldy < N || ldo < N || ldg < N)
+        return fail(TS_ERR_INVALID_ARG, "leading dimensions must cover a row (%lld, %lld, %lld)",
+                    static_cast<long long>(ldy), static_cast<long long>(ldo), static_cast<long long>(ldg));
+    return TS_OK;
+}
+
+}  // namespace
+}  // namespace ts
+
+extern "C" {
+
+ts_status ts_moe_combine(const void *y, const int32_t *position, const float *weights, void *out, int64_t T,
+                         int32_t top_k, int64_t N, int64_t R, int32_t dtype, int64_t ldy, int64_t ldo, void *stream) {
+    using namespace ts;
+    ldy = ldy ? ldy : N;
+    ldo = ldo ? ldo : N;
+    ts_status s = combine_check(T, top_k, N, R, dtype, ldy, ldo, N);
+    if (s != TS_OK) return s;
+    if (T == 0 || N == 0) return TS_OK;
+    const int esize = dtype == TS_OUT_F32 ? 4 : 2;
+    if (!out || (top_k > 0 && !position) || (R > 0 && !y))
+        return fail(TS_ERR_INVALID_ARG, "y, position or out is NULL");
+    if (reinterpret_cast<uintptr_t>(out) % esize || reinterpret_cast<uintptr_t>(y) % esize ||
+        reinterpret_cast<uintptr_t>(position) % 4 || reinterpret_cast<uintptr_t>(weights) % 4)
+        return fail(TS_ERR_INVALID_ARG, "a pointer is not aligned to its element size");
+    if (R > 0 && ranges_overlap(out, ((T - 1) * ldo + N) * esize, y, ((R - 1) * ldy + N) * esize))
+        return fail(TS_ERR_INVALID_ARG, "out overlaps y");
+    CombineParams p = {};
+    p.status = device_status_word(&s);
+    if (!p.status) return s;
+    p.y = y;
+    p.out = out;
+    p.w = weights;
+    p.position = position;
+    p.T = T;
+    p.N = N;
+    p.R = R;
+    p.ldy = ldy;
+    p.ldo = ldo;
+    p.k = top_k;
+    p.vec = row16(y, ldy, esize) && row16(out, ldo, esize);
+    const int64_t per_cta = kThreads * (16 / esize);
+    if (cdiv(N, per_cta) > 65535) return fail(TS_ERR_UNSUPPORTED, "rows of %lld values", static_cast<long long>(N));
+    const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(cdiv(N, per_cta)));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = dtype == TS_OUT_F32 ? launch_pdl(combine_kernel<float>, grid, dim3(kThreads), 0, st, p)
+                                        : launch_pdl(combine_kernel<uint16_t>, grid, dim3(kThreads), 0, st, p);
+    return e == cudaSuccess ? TS_OK : cuda_fail(e, "combine launch");
+}
+
+ts_status ts_moe_combine_grad(const void *grad_out, const void *y, const int32_t *position, const float *weights,
+                              void *grad_y, float *grad_weights, int64_t T, int32_t top_k, int64_t N, int64_t R,
+                              int32_t dtype, int64_t ldy, int64_t ldo, int64_t ldg, void *stream) {
+    using namespace ts;
+    ldy = ldy ? ldy : N;
+    ldo = ldo ? ldo : N;
+    ldg = ldg ? ldg : N;
+    ts_status s = combine_check(T, top_k, N, R, dtype, ldy, ldo, ldg);
+    if (s != TS_OK) return s;
+    if (T == 0 || top_k == 0) return TS_OK;
+    const int esize = dtype == TS_OUT_F32 ? 4 : 2;
+    if (!position || (N > 0 && !grad_out) || (R > 0 && N > 0 && (!y || !grad_y)))
+        return fail(TS_ERR_INVALID_ARG, "grad_out, y, position or grad_y is NULL");
+    if (reinterpret_cast<uintptr_t>(grad_out) % esize || reinterpret_cast<uintptr_t>(y) % esize ||
+        reinterpret_cast<uintptr_t>(grad_y) % esize || reinterpret_cast<uintptr_t>(position) % 4 ||
+        reinterpret_cast<uintptr_t>(weights) % 4 || reinterpret_cast<uintptr_t>(grad_weights) % 4)
+        return fail(TS_ERR_INVALID_ARG, "a pointer is not aligned to its element size");
+    if (R > 0 && N > 0) {
+        const int64_t gbytes = ((R - 1) * ldg + N) * esize;
+        if (ranges_overlap(grad_y, gbytes, grad_out, ((T - 1) * ldo + N) * esize) ||
+            ranges_overlap(grad_y, gbytes, y, ((R - 1) * ldy + N) * esize))
+            return fail(TS_ERR_INVALID_ARG, "grad_y overlaps grad_out or y");
+    }
+    CombineParams p = {};
+    p.status = device_status_word(&s);
+    if (!p.status) return s;
+    p.y = y;
+    p.grad_out = grad_out;
+    p.grad_y = grad_y;
+    p.grad_w = grad_weights;
+    p.w = weights;
+    p.position = position;
+    p.T = T;
+    p.N = N;
+    p.R = R;
+    p.ldy = ldy;
+    p.ldo = ldo;
+    p.ldg = ldg;
+    p.k = top_k;
+    p.vec = row16(y, ldy, esize) && row16(grad_out, ldo, esize) && row16(grad_y, ldg, esize);
+    const dim3 grid(static_cast<unsigned>(T));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = dtype == TS_OUT_F32 ? launch_pdl(combine_grad_kernel<float>, grid, dim3(kThreads), 0, st, p)
+                                        : launch_pdl(combine_grad_kernel<uint16_t>, grid, dim3(kThreads), 0, st, p);
+    return e == cudaSuccess ? TS_OK : cuda_fail(e, "combine gradient launch");
+}
+
+}  // extern "C"

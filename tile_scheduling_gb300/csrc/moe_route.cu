@@ -1,0 +1,643 @@
+// Routing of tokens to experts, its gradient, and the plan that sorts the routed
+// slots by expert.
+//
+//   s = sigmoid(x) or softmax(x),  c = s + bias  (-inf where x is -inf or NaN)
+//   groups: score = the sum of a group's 1 or 2 largest c; the keep best groups stay
+//   experts = the top_k largest c of those groups;  w_j = scale * s_j (/ sum_j s_j)
+//
+// Equal values go to the lower index.  The choice is reproducible to the bit from
+// the definition: sigmoid is 1 / (1 + exp(-x)) with each operation rounded to fp32,
+// and softmax divides exp(x - max) by a sum that folds the upper half of the
+// (zero-padded, power of two, at least 32) expert axis onto the lower one until
+// one value is left.
+//
+// One warp takes one token.  Expert e sits in lane e % 32, slot e / 32, so the
+// halving sum is first a tree over a lane's slots, then a butterfly over lanes,
+// and a round of the choice is one scan of a lane's slots and two warp
+// reductions on order-preserving integer keys.
+#include <algorithm>
+#include <type_traits>
+
+#include "common.h"
+#include "ptx.cuh"
+
+namespace ts {
+namespace {
+
+constexpr int64_t kMaxDim = 0x7fffffffLL;
+constexpr int kRouteWarps = 4;
+constexpr int kMaxRouteExperts = 1024;
+constexpr int kMaxTopK = 32;  // lane j of the warp holds choice j
+constexpr uint32_t kAll = 0xffffffffu;
+
+struct RouteParams {
+    const void *logits;
+    int64_t ldx;
+    const float *bias;
+    int32_t *experts;
+    float *weights;
+    const float *grad_w;
+    void *grad_x;
+    int64_t ldg;
+    int64_t T;
+    int32_t E, k;
+    int32_t softmax, renorm;
+    int32_t groups, keep, best, group_size;
+    float scale;
+    unsigned long long *status;
+};
+
+template <class T>
+__device__ __forceinline__ float load_logit(const T *x) {
+    if constexpr (sizeof(T) == 4)
+        return *x;
+    else
+        return __uint_as_float(uint32_t(*x) << 16);
+}
+
+// Unsigned keys in the order of the floats (no NaN; -0 as +0), above 0 for every
+// number: 0 stands for "not to be chosen".
+__device__ __forceinline__ uint32_t key_of(float v) {
+    const uint32_t b = __float_as_uint(v + 0.f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+// Scores of one token: x[i] becomes s of expert i * 32 + lane; masked[i] tells the
+// experts that cannot be chosen.  Returns whether any logit of the row is NaN.
+template <int NS>
+__device__ __forceinline__ bool scores(float (&x)[NS], bool (&masked)[NS], bool softmax) {
+    bool nan = false;
+    float top = -3.402823466e38f;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        nan |= isnan(x[i]);
+        masked[i] = !(x[i] > -INFINITY);
+        if (masked[i]) x[i] = -INFINITY;
+        x[i] = fminf(x[i], 3.402823466e38f);  // +inf as the largest number
+        top = fmaxf(top, x[i]);
+    }
+    if (softmax) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+        float sum[NS];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            x[i] = expf(x[i] - top);
+            sum[i] = x[i];
+        }
+#pragma unroll
+        for (int n = NS / 2; n > 0; n >>= 1) {
+#pragma unroll
+            for (int i = 0; i < n; ++i) sum[i] += sum[i + n];
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum[0] += __shfl_xor_sync(kAll, sum[0], d);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) x[i] = sum[0] > 0.f ? x[i] / sum[0] : 0.f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) x[i] = 1.f / (1.f + expf(-x[i]));
+    }
+    return __any_sync(kAll, nan);
+}
+
+template <class T, int NS>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_constant__ RouteParams p) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+    if (t >= p.T) return;
+    const T *const row = static_cast<const T *>(p.logits) + t * p.ldx;
+    float s[NS];
+    bool masked[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const int e = i * 32 + lane;
+        s[i] = e < p.E ? load_logit(row + e) : -INFINITY;
+    }
+    const bool nan = scores<NS>(s, masked, p.softmax);
+    uint32_t key[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const int e = i * 32 + lane;
+        float c = s[i];
+        if (p.bias && e < p.E) c += __ldg(p.bias + e);
+        key[i] = masked[i] || !(c > -INFINITY) ? 0u : key_of(c);
+    }
+    if (p.groups > 1) {
+        // lane g holds the key of group g's score
+        uint32_t gkey = 0;
+        for (int g = 0; g < p.groups; ++g) {
+            const int lo = g * p.group_size, hi = lo + p.group_size;
+            uint32_t k1 = 0, k2 = 0;  // this lane's two largest of the group
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const int e = i * 32 + lane;
+                const uint32_t k = e >= lo && e < hi ? key[i] : 0u;
+                k2 = max(k2, min(k1, k));
+                k1 = max(k1, k);
+            }
+            const uint32_t m1 = __reduce_max_sync(kAll, k1);
+            uint32_t score = m1;
+            if (p.best == 2 && m1) {
+                const int owner = __ffs(__ballot_sync(kAll, k1 == m1)) - 1;
+                const uint32_t m2 = __reduce_max_sync(kAll, lane == owner ? k2 : k1);
+                if (m2) score = key_of(value_of(m1) + value_of(m2));
+            }
+            if (lane == g) gkey = score;
+        }
+        uint32_t kept = 0;  // bit g: group g stays
+        for (int r = 0; r < p.keep; ++r) {
+            const uint32_t m = __reduce_max_sync(kAll, gkey);
+            if (!m) break;
+            const int g = __ffs(__ballot_sync(kAll, gkey == m)) - 1;
+            kept |= 1u << g;
+            if (lane == g) gkey = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int e = i * 32 + lane;
+            if (e < p.E && !((kept >> (e / p.group_size)) & 1u)) key[i] = 0;
+        }
+    }
+    int32_t mine = -1;  // lane j: choice j
+    float w = 0.f;
+    for (int j = 0; j < p.k; ++j) {
+        uint32_t best = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+            }
+        const uint32_t m = __reduce_max_sync(kAll, best);
+        if (!m) break;
+        const int e = static_cast<int>(__reduce_min_sync(kAll, best == m ? static_cast<uint32_t>(at * 32 + lane) : kAll));
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            if (i * 32 + lane == e) {
+                key[i] = 0;
+                v = s[i];
+            }
+        v = __shfl_sync(kAll, v, e & 31);
+        if (lane == j) {
+            mine = e;
+            w = v;
+        }
+    }
+    if (p.renorm) {
+        float sum = w;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+        w = sum > 0.f ? w / sum : 0.f;
+    }
+    if (lane < p.k) {
+        p.experts[t * p.k + lane] = mine;
+        p.weights[t * p.k + lane] = nan ? __int_as_float(0x7fffffff) : w * p.scale;
+    }
+}
+
+// The gradient recomputes the scores.  With g_j = scale * grad_w_j:
+//   d s_j = (g_j - sum_i g_i s_i / S) / S with S = sum_j s_j (renorm), else g_j
+//   sigmoid: dx = ds * s * (1 - s);   softmax: dx_e = s_e * (ds_e - sum_i ds_i s_i)
+// 1 - s is sigmoid(-x), which keeps its digits where s is close to 1.
+template <class T, int NS>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const __grid_constant__ RouteParams p) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+    if (t >= p.T) return;
+    const T *const row = static_cast<const T *>(p.logits) + t * p.ldx;
+    float s[NS], x[NS];
+    bool masked[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const int e = i * 32 + lane;
+        s[i] = e < p.E ? load_logit(row + e) : -INFINITY;
+        x[i] = s[i];
+    }
+    const bool nan = scores<NS>(s, masked, p.softmax);
+    int32_t mine = -1;
+    float g = 0.f;
+    if (lane < p.k) {
+        mine = p.experts[t * p.k + lane];
+        if (mine >= p.E) {
+            if (atomicCAS(&p.status[0], 0ull, 7ull) == 0ull)
+                atomicExch(&p.status[1], static_cast<unsigned long long>(t * p.k + lane));
+            atomicAdd(&p.status[2], 1ull);
+            mine = -1;
+        }
+        if (mine >= 0) g = p.grad_w[t * p.k + lane] * p.scale;
+    }
+    float sj = 0.f;  // lane j: the score of choice j
+    for (int j = 0; j < p.k; ++j) {
+        const int e = __shfl_sync(kAll, mine, j);
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            if (i * 32 + lane == e) v = s[i];
+        v = __shfl_sync(kAll, v, e & 31);
+        if (lane == j) sj = v;
+    }
+    if (mine < 0) sj = 0.f;
+    float ds = g;
+    if (p.renorm) {
+        float sum = sj, dot = g * sj;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            sum += __shfl_xor_sync(kAll, sum, d);
+            dot += __shfl_xor_sync(kAll, dot, d);
+        }
+        ds = mine >= 0 && sum > 0.f ? (g - dot / sum) / sum : 0.f;
+    }
+    float mean = 0.f;
+    if (p.softmax) {
+        mean = ds * sj;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) mean += __shfl_xor_sync(kAll, mean, d);
+    }
+    float dx[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) dx[i] = 0.f;
+    for (int j = 0; j < p.k; ++j) {
+        const int e = __shfl_sync(kAll, mine, j);
+        const float v = __shfl_sync(kAll, ds, j);
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            if (i * 32 + lane == e) dx[i] += v;
+    }
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const int e = i * 32 + lane;
+        if (p.softmax)
+            dx[i] = s[i] * (dx[i] - mean);
+        else
+            dx[i] = masked[i] ? 0.f : dx[i] * s[i] * (1.f / (1.f + expf(fminf(x[i], 3.402823466e38f))));
+        if (nan) dx[i] = __int_as_float(0x7fffffff);
+        if (e < p.E) {
+            if constexpr (sizeof(T) == 4)
+                static_cast<float *>(p.grad_x)[t * p.ldg + e] = dx[i];
+            else
+                static_cast<uint16_t *>(p.grad_x)[t * p.ldg + e] =
+                    static_cast<uint16_t>(pack_bf16x2(__float_as_uint(dx[i]), 0u));
+        }
+    }
+}
+
+template <bool GRAD, class T>
+cudaError_t route_launch(const RouteParams &p, cudaStream_t st) {
+    const dim3 grid(static_cast<unsigned>(cdiv(p.T, kRouteWarps))), block(32 * kRouteWarps);
+    auto go = [&](auto ns) {
+        constexpr int NS = decltype(ns)::value;
+        if constexpr (GRAD)
+            return launch_pdl(route_grad_kernel<T, NS>, grid, block, 0, st, p);
+        else
+            return launch_pdl(route_kernel<T, NS>, grid, block, 0, st, p);
+    };
+    if (p.E <= 32) return go(std::integral_constant<int, 1>{});
+    if (p.E <= 64) return go(std::integral_constant<int, 2>{});
+    if (p.E <= 128) return go(std::integral_constant<int, 4>{});
+    if (p.E <= 256) return go(std::integral_constant<int, 8>{});
+    if (p.E <= 512) return go(std::integral_constant<int, 16>{});
+    return go(std::integral_constant<int, 32>{});
+}
+
+ts_status route_check(RouteParams &p, const void *logits, int64_t T, int32_t E, int32_t k, int32_t dtype,
+                      const ts_route_opts *opts) {
+    const ts_route_opts z = {};
+    const ts_route_opts *o = opts ? opts : &z;
+    if (T < 0 || T > kMaxDim) return fail(TS_ERR_INVALID_ARG, "tokens = %lld", static_cast<long long>(T));
+    if (E < 1 || k < 1 || k > E) return fail(TS_ERR_INVALID_ARG, "experts = %d, top_k = %d", E, k);
+    if (E > kMaxRouteExperts || k > kMaxTopK)
+        return fail(TS_ERR_UNSUPPORTED, "experts = %d (at most %d), top_k = %d (at most %d)", E, kMaxRouteExperts, k,
+                    kMaxTopK);
+    if (dtype != TS_OUT_BF16 && dtype != TS_OUT_F32) return fail(TS_ERR_INVALID_ARG, "dtype %d", dtype);
+    if (o->score != TS_SCORE_SOFTMAX && o->score != TS_SCORE_SIGMOID)
+        return fail(TS_ERR_INVALID_ARG, "score %d", o->score);
+    if (o->no_renorm != 0 && o->no_renorm != 1)
+        return fail(TS_ERR_INVALID_ARG, "no_renorm = %d (0 or 1)", o->no_renorm);
+    const int32_t groups = o->groups ? o->groups : 1, keep = o->keep_groups ? o->keep_groups : groups;
+    const int32_t best = o->group_best ? o->group_best : 1;
+    if (groups < 1 || E % groups) return fail(TS_ERR_INVALID_ARG, "%d experts do not form %d equal groups", E, groups);
+    if (groups > 32) return fail(TS_ERR_UNSUPPORTED, "groups = %d (at most 32)", groups);
+    if (keep < 1 || keep > groups || static_cast<int64_t>(keep) * (E / groups) < k)
+        return fail(TS_ERR_INVALID_ARG, "keep_groups = %d leaves fewer than top_k = %d experts", keep, k);
+    if (best != 1 && best != 2) return fail(TS_ERR_INVALID_ARG, "group_best = %d (1 or 2)", best);
+    p.ldx = o->ldx ? o->ldx : E;
+    p.ldg = o->ldg ? o->ldg : E;
+    if (p.ldx < E || p.ldg < E) return fail(TS_ERR_INVALID_ARG, "leading dimensions must cover a row");
+    if (T > 0 && (!logits || reinterpret_cast<uintptr_t>(logits) % (dtype == TS_OUT_F32 ? 4 : 2)))
+        return fail(TS_ERR_INVALID_ARG, "logits is NULL or not aligned to its element size");
+    p.logits = logits;
+    p.T = T;
+    p.E = E;
+    p.k = k;
+    p.softmax = o->score == TS_SCORE_SOFTMAX;
+    p.renorm = !o->no_renorm;
+    p.groups = groups;
+    p.keep = keep;
+    p.best = best;
+    p.group_size = E / groups;
+    p.scale = o->scale != 0.f ? o->scale : 1.f;
+    p.bias = o->bias;
+    ts_status s = TS_OK;
+    p.status = T > 0 ? device_status_word(&s) : nullptr;
+    return s;
+}
+
+// ------------------------------------------------------------------- plan
+// A stable counting sort of the slots by expert.  A CTA takes tiles of
+// kPlanSlots consecutive slots, a warp kWarpSlots of them in order; equal
+// experts of a warp's 32 slots rank by lane.
+constexpr int kPlanWarps = 16;
+constexpr int kWarpSlots = 128;
+constexpr int kPlanSlots = kPlanWarps * kWarpSlots;
+constexpr int kOneCtaSlots = 4 * kPlanSlots;  // up to here one CTA does it all
+
+struct PlanParams {
+    const int32_t *experts;
+    int64_t *offsets;
+    int32_t *order, *position;
+    int32_t *counts;  // [tiles][E] workspace: counts, then first rows
+    int64_t n;
+    int32_t E, tiles;
+    unsigned long long *status;
+};
+
+// Expert of slot i, or -1 (dropped, past the end, or out of range: reported).
+__device__ __forceinline__ int32_t plan_expert(const PlanParams &p, int64_t i, bool report) {
+    const int32_t e = i < p.n ? p.experts[i] : -1;
+    if (e < p.E) return e;
+    if (report) {
+        if (atomicCAS(&p.status[0], 0ull, 7ull) == 0ull) atomicExch(&p.status[1], static_cast<unsigned long long>(i));
+        atomicAdd(&p.status[2], 1ull);
+    }
+    return -1;
+}
+
+// Per-warp counts of one tile's slots in hist[warp][E].
+__device__ __forceinline__ void plan_count(const PlanParams &p, int64_t first, int32_t *hist, bool report) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int32_t i = threadIdx.x; i < kPlanWarps * p.E; i += blockDim.x) hist[i] = 0;
+    __syncthreads();
+    int32_t *const h = hist + warp * p.E;
+    int32_t e[kWarpSlots / 32];
+#pragma unroll
+    for (int r = 0; r < kWarpSlots / 32; ++r)
+        e[r] = plan_expert(p, first + warp * kWarpSlots + r * 32 + lane, report);
+#pragma unroll
+    for (int r = 0; r < kWarpSlots / 32; ++r) {
+        const uint32_t same = __match_any_sync(kAll, e[r]);
+        if (e[r] >= 0 && lane == __ffs(same) - 1) h[e[r]] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+}
+
+// Rows of one tile's slots: hist[warp][e] holds the first row of the warp's slots of e.
+__device__ __forceinline__ void plan_place(const PlanParams &p, int64_t first, int32_t *hist) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int32_t *const h = hist + warp * p.E;
+    int32_t e[kWarpSlots / 32];
+#pragma unroll
+    for (int r = 0; r < kWarpSlots / 32; ++r)
+        e[r] = plan_expert(p, first + warp * kWarpSlots + r * 32 + lane, false);
+#pragma unroll
+    for (int r = 0; r < kWarpSlots / 32; ++r) {
+        const int64_t i = first + warp * kWarpSlots + r * 32 + lane;
+        const uint32_t same = __match_any_sync(kAll, e[r]);
+        int32_t row = -1;
+        if (e[r] >= 0) row = h[e[r]] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (e[r] >= 0 && lane == __ffs(same) - 1) h[e[r]] += __popc(same);
+        __syncwarp();
+        if (i < p.n) {
+            p.position[i] = row;
+            if (row >= 0) p.order[row] = static_cast<int32_t>(i);
+        }
+    }
+    __syncthreads();
+}
+
+// Exclusive sum over the experts of tot[e] into offsets and tot itself (one warp's work).
+__device__ __forceinline__ void plan_offsets(const PlanParams &p, int32_t *tot) {
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int32_t run = 0;
+        for (int32_t e0 = 0; e0 < p.E; e0 += 32) {
+            const int32_t e = e0 + lane;
+            const int32_t own = e < p.E ? tot[e] : 0;
+            int32_t v = own;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int32_t o = __shfl_up_sync(kAll, v, d);
+                if (lane >= d) v += o;
+            }
+            if (e < p.E) {
+                tot[e] = run + v - own;
+                p.offsets[e] = run + v - own;
+            }
+            run += __shfl_sync(kAll, v, 31);
+        }
+        if (lane == 0) {
+            p.offsets[p.E] = run;
+            tot[p.E] = run;
+        }
+    }
+    __syncthreads();
+}
+
+// Few slots: one CTA counts, sums and places.
+__global__ void __launch_bounds__(32 * kPlanWarps) plan_one_kernel(const __grid_constant__ PlanParams p) {
+    extern __shared__ int32_t smem[];
+    int32_t *const hist = smem, *const next = smem + kPlanWarps * p.E;  // next[e]: next free row
+    grid_dep_wait();
+    grid_dep_launch();
+    for (int32_t e = threadIdx.x; e <= p.E; e += blockDim.x) next[e] = 0;
+    for (int32_t t = 0; t < p.tiles; ++t) {
+        plan_count(p, static_cast<int64_t>(t) * kPlanSlots, hist, true);
+        for (int32_t e = threadIdx.x; e < p.E; e += blockDim.x) {
+            int32_t c = next[e];
+            for (int w = 0; w < kPlanWarps; ++w) c += hist[w * p.E + e];
+            next[e] = c;
+        }
+        __syncthreads();
+    }
+    plan_offsets(p, next);
+    const int32_t valid = next[p.E];
+    for (int32_t t = 0; t < p.tiles; ++t) {
+        plan_count(p, static_cast<int64_t>(t) * kPlanSlots, hist, false);
+        for (int32_t e = threadIdx.x; e < p.E; e += blockDim.x) {
+            int32_t c = next[e];
+            for (int w = 0; w < kPlanWarps; ++w) {
+                const int32_t n = hist[w * p.E + e];
+                hist[w * p.E + e] = c;
+                c += n;
+            }
+            next[e] = c;
+        }
+        __syncthreads();
+        plan_place(p, static_cast<int64_t>(t) * kPlanSlots, hist);
+    }
+    for (int64_t r = valid + threadIdx.x; r < p.n; r += blockDim.x) p.order[r] = -1;
+}
+
+__global__ void __launch_bounds__(32 * kPlanWarps) plan_count_kernel(const __grid_constant__ PlanParams p) {
+    extern __shared__ int32_t smem[];
+    grid_dep_wait();
+    grid_dep_launch();
+    plan_count(p, static_cast<int64_t>(blockIdx.x) * kPlanSlots, smem, true);
+    for (int32_t e = threadIdx.x; e < p.E; e += blockDim.x) {
+        int32_t c = 0;
+        for (int w = 0; w < kPlanWarps; ++w) c += smem[w * p.E + e];
+        p.counts[static_cast<int64_t>(blockIdx.x) * p.E + e] = c;
+    }
+}
+
+// One CTA: each expert's running sum over the tiles, then over the experts.
+__global__ void __launch_bounds__(1024) plan_scan_kernel(const __grid_constant__ PlanParams p) {
+    __shared__ int32_t tot[kMaxRouteExperts + 1];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int32_t e = threadIdx.x;
+    if (e < p.E) {
+        int32_t c = 0;
+#pragma unroll 8
+        for (int32_t t = 0; t < p.tiles; ++t) c += p.counts[static_cast<int64_t>(t) * p.E + e];
+        tot[e] = c;
+    }
+    __syncthreads();
+    plan_offsets(p, tot);
+    if (e < p.E) {
+        int32_t c = tot[e];
+#pragma unroll 8
+        for (int32_t t = 0; t < p.tiles; ++t) {
+            const int32_t n = p.counts[static_cast<int64_t>(t) * p.E + e];
+            p.counts[static_cast<int64_t>(t) * p.E + e] = c;
+            c += n;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(32 * kPlanWarps) plan_place_kernel(const __grid_constant__ PlanParams p) {
+    extern __shared__ int32_t smem[];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kPlanSlots;
+    plan_count(p, first, smem, false);
+    for (int32_t e = threadIdx.x; e < p.E; e += blockDim.x) {
+        int32_t c = p.counts[static_cast<int64_t>(blockIdx.x) * p.E + e];
+        for (int w = 0; w < kPlanWarps; ++w) {
+            const int32_t n = smem[w * p.E + e];
+            smem[w * p.E + e] = c;
+            c += n;
+        }
+    }
+    __syncthreads();
+    plan_place(p, first, smem);
+    const int64_t valid = p.offsets[p.E];
+    for (int64_t r = first + threadIdx.x; r < first + kPlanSlots && r < p.n; r += blockDim.x)
+        if (r >= valid) p.order[r] = -1;
+}
+
+}  // namespace
+}  // namespace ts
+
+extern "C" {
+
+ts_status ts_moe_route(const void *logits, int32_t *experts, float *weights, int64_t T, int32_t E, int32_t top_k,
+                       int32_t dtype, const ts_route_opts *opts, void *stream) {
+    using namespace ts;
+    RouteParams p = {};
+    ts_status s = route_check(p, logits, T, E, top_k, dtype, opts);
+    if (s != TS_OK || T == 0) return s;
+    if (!experts || !weights || reinterpret_cast<uintptr_t>(experts) % 4 || reinterpret_cast<uintptr_t>(weights) % 4 ||
+        reinterpret_cast<uintptr_t>(p.bias) % 4)
+        return fail(TS_ERR_INVALID_ARG, "experts, weights or bias is NULL or not aligned to 4 bytes");
+    p.experts = experts;
+    p.weights = weights;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = dtype == TS_OUT_F32 ? route_launch<false, float>(p, st) : route_launch<false, uint16_t>(p, st);
+    return e == cudaSuccess ? TS_OK : cuda_fail(e, "routing launch");
+}
+
+ts_status ts_moe_route_grad(const void *logits, const int32_t *experts, const float *grad_weights, void *grad_logits,
+                            int64_t T, int32_t E, int32_t top_k, int32_t dtype, const ts_route_opts *opts,
+                            void *stream) {
+    using namespace ts;
+    RouteParams p = {};
+    ts_status s = route_check(p, logits, T, E, top_k, dtype, opts);
+    if (s != TS_OK || T == 0) return s;
+    if (!experts || !grad_weights || !grad_logits || reinterpret_cast<uintptr_t>(experts) % 4 ||
+        reinterpret_cast<uintptr_t>(grad_weights) % 4 ||
+        reinterpret_cast<uintptr_t>(grad_logits) % (dtype == TS_OUT_F32 ? 4 : 2))
+        return fail(TS_ERR_INVALID_ARG, "experts, grad_weights or grad_logits is NULL or misaligned");
+    p.experts = const_cast<int32_t *>(experts);
+    p.grad_w = grad_weights;
+    p.grad_x = grad_logits;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = dtype == TS_OUT_F32 ? route_launch<true, float>(p, st) : route_launch<true, uint16_t>(p, st);
+    return e == cudaSuccess ? TS_OK : cuda_fail(e, "routing gradient launch");
+}
+
+int64_t ts_moe_plan_workspace(int64_t slots, int32_t E) {
+    using namespace ts;
+    if (slots <= kOneCtaSlots || E < 1) return 0;
+    return cdiv(slots, kPlanSlots) * E * static_cast<int64_t>(sizeof(int32_t));
+}
+
+ts_status ts_moe_plan(const int32_t *experts, int64_t *offsets, int32_t *order, int32_t *position, int64_t slots,
+                      int32_t E, void *workspace, int64_t workspace_bytes, void *stream) {
+    using namespace ts;
+    if (slots < 0 || slots > kMaxDim) return fail(TS_ERR_INVALID_ARG, "slots = %lld", static_cast<long long>(slots));
+    if (E < 1) return fail(TS_ERR_INVALID_ARG, "experts = %d", E);
+    if (E > kMaxRouteExperts) return fail(TS_ERR_UNSUPPORTED, "experts = %d (at most %d)", E, kMaxRouteExperts);
+    if (!offsets || (slots > 0 && (!experts || !order || !position)))
+        return fail(TS_ERR_INVALID_ARG, "experts, offsets, order or position is NULL");
+    if (reinterpret_cast<uintptr_t>(offsets) % 8 || reinterpret_cast<uintptr_t>(experts) % 4 ||
+        reinterpret_cast<uintptr_t>(order) % 4 || reinterpret_cast<uintptr_t>(position) % 4)
+        return fail(TS_ERR_INVALID_ARG, "a pointer is not aligned to its element size");
+    const int64_t need = ts_moe_plan_workspace(slots, E);
+    if (need > 0 && (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 4))
+        return fail(TS_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", static_cast<long long>(workspace_bytes),
+                    static_cast<long long>(need));
+    PlanParams p = {};
+    ts_status s;
+    p.status = device_status_word(&s);
+    if (!p.status) return s;
+    p.experts = experts;
+    p.offsets = offsets;
+    p.order = order;
+    p.position = position;
+    p.counts = static_cast<int32_t *>(workspace);
+    p.n = slots;
+    p.E = E;
+    p.tiles = static_cast<int32_t>(cdiv(slots, kPlanSlots));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const dim3 block(32 * kPlanWarps);
+    const size_t hist = static_cast<size_t>(kPlanWarps) * E * 4;
+    // up to 1024 experts take 68 KB: above the default limit
+    cudaError_t e = cudaSuccess;
+    for (auto *k : {plan_one_kernel, plan_count_kernel, plan_place_kernel})
+        if (e == cudaSuccess && hist + 4 * (E + 1) > 48 * 1024)
+            e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kPlanWarps * kMaxRouteExperts * 4 + 4 * (kMaxRouteExperts + 1));
+    if (e == cudaSuccess && need == 0) {
+        e = launch_pdl(plan_one_kernel, dim3(1), block, hist + 4 * (E + 1), st, p);
+    } else if (e == cudaSuccess) {
+        const dim3 grid(static_cast<unsigned>(p.tiles));
+        e = launch_pdl(plan_count_kernel, grid, block, hist, st, p);
+        if (e == cudaSuccess) e = launch_pdl(plan_scan_kernel, dim3(1), dim3(1024), 0, st, p);
+        if (e == cudaSuccess) e = launch_pdl(plan_place_kernel, grid, block, hist, st, p);
+    }
+    return e == cudaSuccess ? TS_OK : cuda_fail(e, "plan launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,275 @@
+// Quantisation to 8-bit floating point with one scale for each row and 128
+// columns (or, transposed, each column and 128 rows) of a bf16 or fp32 matrix:
+//
+//   a = max |x| over the block (at least 2^-100),  s = a / top,  q = rne(x * (top / a))
+//
+// with top = 448 (e4m3) or 57344 (e5m2).  The row form may gather: output row r
+// is input row rows[r] / rows_div, which lays tokens out by expert and quantises
+// them in one pass.  A not-a-number stays one in q; an infinity gives s = inf and
+// q = NaN at that place, so that both come out of a product as NaN.
+#include <algorithm>
+
+#include "common.h"
+#include "ptx.cuh"
+
+namespace ts {
+namespace {
+
+constexpr int64_t kMaxDim = 0x7fffffffLL;
+constexpr int kBlk = 128;
+constexpr int kQThreads = 256;
+
+struct QuantParams {
+    const void *x;
+    int64_t ldx;
+    int64_t M, N;          // input rows and columns
+    uint8_t *q;
+    int64_t ldq;
+    float *s;
+    int64_t s_row, s_blk;  // strides of s along q's rows and along the blocks of a row
+    const int32_t *rows;   // gather index or nullptr
+    int64_t R;             // output rows
+    int32_t rows_div;
+    int32_t vec;           // 16-byte loads and 8-byte stores are aligned
+    unsigned long long *status;
+};
+
+__device__ __forceinline__ float top_of(bool e5m2) { return e5m2 ? 57344.f : 448.f; }
+
+// Four fp32 values to four 8-bit ones, rounded to nearest even; past the largest
+// value they saturate, a NaN stays one.
+template <bool E5M2>
+__device__ __forceinline__ uint32_t pack_f8x4(float a, float b, float c, float d) {
+    uint16_t lo, hi;
+    if constexpr (E5M2) {
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    } else {
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    }
+    return uint32_t(lo) | (uint32_t(hi) << 16);
+}
+
+// Eight values at x[i .. i + 8) as fp32; n: how many of them exist (the rest read as 0).
+template <class T>
+__device__ __forceinline__ void load8(const T *x, bool vec, int64_t n, float (&v)[8]) {
+    if (vec && n >= 8) {
+        if constexpr (sizeof(T) == 4) {
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(x));
+            const float4 b = __ldg(reinterpret_cast<const float4 *>(x) + 1);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x));
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = 0.f;
+            if (i < n) {
+                if constexpr (sizeof(T) == 4)
+                    v[i] = x[i];
+                else
+                    v[i] = __uint_as_float(uint32_t(x[i]) << 16);
+            }
+        }
+    }
+}
+
+// Row form.  Sixteen lanes take one block of one row, eight values each; a CTA
+// takes 16 rows and 8 blocks, so a warp reads whole 256-byte (bf16) runs.
+template <class T, bool E5M2>
+__global__ void __launch_bounds__(kQThreads) quant_rows_kernel(const __grid_constant__ QuantParams p) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int part = threadIdx.x & 15;
+    const int64_t r = static_cast<int64_t>(blockIdx.y) * 16 + (threadIdx.x >> 4);
+    const int64_t kb0 = static_cast<int64_t>(blockIdx.x) * 8;
+    const int64_t blocks = (p.N + kBlk - 1) / kBlk;
+    int64_t src = r;
+    bool there = r < p.R;
+    if (there && p.rows) {
+        const int32_t at = p.rows[r];
+        src = at / p.rows_div;
+        if (at < 0) {
+            there = false;  // an empty slot: q and s are zero
+            src = -1;
+        } else if (src >= p.M) {
+            if (part == 0 && blockIdx.x == 0) {
+                if (atomicCAS(&p.status[0], 0ull, 5ull) == 0ull) atomicExch(&p.status[1], static_cast<unsigned long long>(r));
+                atomicAdd(&p.status[2], 1ull);
+            }
+            there = false;
+        }
+    }
+    const T *const x = static_cast<const T *>(p.x) + (there ? src : 0) * p.ldx;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t kb = kb0 + i;
+        const int64_t c = kb * kBlk + part * 8;
+        float v[8];
+        load8(x + c, p.vec, there ? p.N - c : 0, v);
+        float a = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(v[j]));
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+        a = fmaxf(a, 0x1p-100f);
+        const float f = top_of(E5M2) / a;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= f;
+        const uint32_t lo = pack_f8x4<E5M2>(v[0], v[1], v[2], v[3]);
+        const uint32_t hi = pack_f8x4<E5M2>(v[4], v[5], v[6], v[7]);
+        if (r < p.R && kb < blocks) {
+            uint8_t *const dst = p.q + r * p.ldq + c;
+            if (p.vec && c + 8 <= p.N) {
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(lo, hi);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c + j < p.N) dst[j] = static_cast<uint8_t>((j < 4 ? lo : hi) >> (8 * (j & 3)));
+            }
+            if (part == 0) p.s[r * p.s_row + kb * p.s_blk] = there ? a / top_of(E5M2) : 0.f;
+        }
+    }
+}
+
+// Transposed form: q[n][m] from x[m][n], blocks of 128 along m.  A CTA takes one
+// block of 128 rows by 64 columns; each thread holds four consecutive rows of
+// eight columns, so its four values of a column make one 32-bit word of q.
+template <class T, bool E5M2>
+__global__ void __launch_bounds__(kQThreads) quant_trans_kernel(const __grid_constant__ QuantParams p) {
+    constexpr int PITCH = kBlk / 4 + 1;  // words of a column's 128 values, padded
+    __shared__ float amax[8][64];
+    __shared__ uint32_t tile[64 * PITCH];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3;  // column octet, row quad
+    const int64_t mb = blockIdx.x;
+    const int64_t n0 = static_cast<int64_t>(blockIdx.y) * 64;
+    const int64_t m0 = mb * kBlk + rg * 4;
+    const int64_t n = n0 + cg * 8;
+    float v[4][8], a[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        load8(static_cast<const T *>(p.x) + (m0 + i < p.M ? m0 + i : 0) * p.ldx + n, p.vec, m0 + i < p.M ? p.N - n : 0,
+              v[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        a[j] = fmaxf(fmaxf(fabsf(v[0][j]), fabsf(v[1][j])), fmaxf(fabsf(v[2][j]), fabsf(v[3][j])));
+        a[j] = fmaxf(a[j], __shfl_xor_sync(0xffffffffu, a[j], 8));
+        a[j] = fmaxf(a[j], __shfl_xor_sync(0xffffffffu, a[j], 16));
+    }
+    if (lane < 8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax[warp][lane * 8 + j] = a[j];
+    }
+    __syncthreads();
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float t = 0x1p-100f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) t = fmaxf(t, amax[w][cg * 8 + j]);
+        f[j] = top_of(E5M2) / t;
+        if (rg == 0 && n + j < p.N) p.s[(n + j) * p.s_row + mb * p.s_blk] = t / top_of(E5M2);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        tile[(cg * 8 + j) * PITCH + rg] =
+            pack_f8x4<E5M2>(v[0][j] * f[j], v[1][j] * f[j], v[2][j] * f[j], v[3][j] * f[j]);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int col = warp + 8 * i;  // each warp stores a column's 128 bytes
+        if (n0 + col >= p.N) break;
+        const uint32_t w = tile[col * PITCH + lane];
+        uint8_t *const dst = p.q + (n0 + col) * p.ldq + mb * kBlk + lane * 4;
+        const int64_t left = p.M - (mb * kBlk + lane * 4);
+        if (p.ldq % 4 == 0 && reinterpret_cast<uintptr_t>(p.q) % 4 == 0 && left >= 4) {
+            *reinterpret_cast<uint32_t *>(dst) = w;
+        } else {
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                if (b < left) dst[b] = static_cast<uint8_t>(w >> (8 * b));
+        }
+    }
+}
+
+template <class T>
+cudaError_t quant_launch(const QuantParams &p, bool e5m2, bool transpose, cudaStream_t st) {
+    if (transpose) {
+        const dim3 grid(static_cast<unsigned>(cdiv(p.M, kBlk)), static_cast<unsigned>(cdiv(p.N, 64)));
+        return e5m2 ? launch_pdl(quant_trans_kernel<T, true>, grid, dim3(kQThreads), 0, st, p)
+                    : launch_pdl(quant_trans_kernel<T, false>, grid, dim3(kQThreads), 0, st, p);
+    }
+    const dim3 grid(static_cast<unsigned>(cdiv(p.N, 8 * kBlk)), static_cast<unsigned>(cdiv(p.R, 16)));
+    return e5m2 ? launch_pdl(quant_rows_kernel<T, true>, grid, dim3(kQThreads), 0, st, p)
+                : launch_pdl(quant_rows_kernel<T, false>, grid, dim3(kQThreads), 0, st, p);
+}
+
+}  // namespace
+}  // namespace ts
+
+extern "C" ts_status ts_quant_fp8(const void *x, void *q, float *scales, int64_t M, int64_t N, int32_t x_type,
+                                  int32_t q_type, const ts_quant_opts *opts, void *stream) {
+    using namespace ts;
+    const ts_quant_opts z = {};
+    const ts_quant_opts *o = opts ? opts : &z;
+    if (M < 0 || N < 0 || M > kMaxDim || N > kMaxDim || o->out_rows < 0 || o->out_rows > kMaxDim)
+        return fail(TS_ERR_INVALID_ARG, "sizes must be in [0, 2^31-1] (M=%lld N=%lld out_rows=%lld)",
+                    static_cast<long long>(M), static_cast<long long>(N), static_cast<long long>(o->out_rows));
+    if (x_type != TS_OUT_BF16 && x_type != TS_OUT_F32) return fail(TS_ERR_INVALID_ARG, "x_type %d", x_type);
+    if (q_type != TS_FP8_E4M3 && q_type != TS_FP8_E5M2) return fail(TS_ERR_INVALID_ARG, "q_type %d", q_type);
+    if (o->transpose != 0 && o->transpose != 1)
+        return fail(TS_ERR_INVALID_ARG, "transpose = %d (0 or 1)", o->transpose);
+    if (o->transpose && o->rows) return fail(TS_ERR_UNSUPPORTED, "the transposed form does not gather rows");
+    if (o->rows_div < 0) return fail(TS_ERR_INVALID_ARG, "rows_div = %d", o->rows_div);
+    const int64_t R = o->rows ? o->out_rows : M;
+    const int64_t q_rows = o->transpose ? N : R, q_cols = o->transpose ? M : N;
+    QuantParams p = {};
+    p.ldx = o->ldx ? o->ldx : N;
+    p.ldq = o->ldq ? o->ldq : q_cols;
+    if (p.ldx < N || p.ldq < q_cols)
+        return fail(TS_ERR_INVALID_ARG, "leading dimensions must cover a row (ldx=%lld ldq=%lld)",
+                    static_cast<long long>(p.ldx), static_cast<long long>(p.ldq));
+    if (q_rows == 0 || q_cols == 0) return TS_OK;
+    const int esize = x_type == TS_OUT_F32 ? 4 : 2;
+    if ((!x && M > 0) || !q || !scales) return fail(TS_ERR_INVALID_ARG, "x, q or scales is NULL");
+    if (reinterpret_cast<uintptr_t>(x) % esize || reinterpret_cast<uintptr_t>(scales) % 4 ||
+        reinterpret_cast<uintptr_t>(o->rows) % 4)
+        return fail(TS_ERR_INVALID_ARG, "x, scales or rows is not aligned to its element size");
+    const int64_t xbytes = M > 0 ? ((M - 1) * p.ldx + N) * esize : 0;
+    if (ranges_overlap(x, xbytes, q, (q_rows - 1) * p.ldq + q_cols))
+        return fail(TS_ERR_INVALID_ARG, "q overlaps x");
+    // grid limits: 65535 CTAs along y, 16 rows (64 columns, transposed) each
+    if (cdiv(o->transpose ? N : R, o->transpose ? 64 : 16) > 65535)
+        return fail(TS_ERR_UNSUPPORTED, "too many rows (columns, transposed) for one launch");
+    ts_status s;
+    p.status = device_status_word(&s);
+    if (!p.status) return s;
+    p.x = x;
+    p.M = M;
+    p.N = N;
+    p.q = static_cast<uint8_t *>(q);
+    p.s = scales;
+    p.s_row = o->s_row ? o->s_row : 1;
+    p.s_blk = o->s_blk ? o->s_blk : q_rows;
+    p.rows = o->rows;
+    p.R = R;
+    p.rows_div = o->rows_div ? o->rows_div : 1;
+    const bool x_ok = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (p.ldx * esize) % 16 == 0;
+    p.vec = x_ok && (o->transpose || (reinterpret_cast<uintptr_t>(q) % 8 == 0 && p.ldq % 8 == 0));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool e5m2 = q_type == TS_FP8_E5M2;
+    cudaError_t e = x_type == TS_OUT_F32 ? quant_launch<float>(p, e5m2, o->transpose, st)
+                                         : quant_launch<uint16_t>(p, e5m2, o->transpose, st);
+    return e == cudaSuccess ? TS_OK : cuda_fail(e, "quantisation launch");
+}

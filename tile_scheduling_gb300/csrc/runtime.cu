@@ -138,6 +138,19 @@ ts_status ts_sync_and_check(void *stream) {
                         "row %llu of the chunked copy has pieces past the launch's work tiles (overlapping rows "
                         "need a larger tiles); %llu rows not fully copied",
                         h[1], h[2]);
+    if (h[0] == 4)
+        return ts::fail(TS_ERR_INVALID_ARG,
+                        "group %llu of a grouped 8-bit product has row offsets outside [0, M] or decreasing; %llu groups "
+                        "not computed",
+                        h[1], h[2]);
+    if (h[0] == 5)
+        return ts::fail(TS_ERR_INVALID_ARG, "output row %llu of a quantisation gathers a row past the input; %llu reported",
+                        h[1], h[2]);
+    if (h[0] == 6)
+        return ts::fail(TS_ERR_INVALID_ARG, "slot %llu of a combine has a position past y's rows; %llu reported", h[1],
+                        h[2]);
+    if (h[0] == 7)
+        return ts::fail(TS_ERR_INVALID_ARG, "slot %llu names an expert past the last one; %llu reported", h[1], h[2]);
     const int where = static_cast<int>(h[1] >> 32);
     const unsigned block = static_cast<unsigned>(h[1] & 0xffffffffu);
     return ts::fail(TS_ERR_TIMEOUT, "barrier wait timed out (%s) in block %u; %llu errors recorded",
