@@ -29,11 +29,12 @@ struct GemmLaunch {
     cudaStream_t stream;
 };
 
-// Encode a tiled tensor map with the 128-byte swizzle: `rank` dimensions of
+// Encode a tiled tensor map: `rank` dimensions of
 // `dims` elements (innermost first), strides in bytes of dimensions 1.., boxes
 // of `box` elements.  Out-of-range elements of a load read as zero.
 ts_status encode_map(CUtensorMap *m, const void *ptr, CUtensorMapDataType dt, int rank, const int64_t *dims,
-                     const int64_t *strides, const int *box);
+                     const int64_t *strides, const int *box,
+                     CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
 // Launch a kernel as a programmatic dependent of the previous kernel in its
 // stream (it calls grid_dep_wait before its first global memory access).

@@ -9,7 +9,8 @@
 
 namespace ts {
 
-extern const Fp8Variant fp8_128_1_block, fp8_128_1_row, fp8_128_1_grouped;
+extern const Fp8Variant fp8_128_1_block, fp8_128_1_row, fp8_128_1_grouped, fp8_256_1_block, fp8_256_1_row,
+    fp8_256_1_grouped, fp8_256_2_block, fp8_256_2_row, fp8_256_2_grouped;
 
 namespace {
 
@@ -34,7 +35,9 @@ __global__ void fp8_zero_kernel(T *D, int64_t N, int64_t ldd, const __grid_const
 }
 
 const Fp8Variant *find_fp8(int bn, int cg, bool rows, bool grouped) {
-    static const Fp8Variant *const all[] = {&fp8_128_1_block, &fp8_128_1_row, &fp8_128_1_grouped};
+    static const Fp8Variant *const all[] = {&fp8_128_1_block, &fp8_128_1_row, &fp8_128_1_grouped,
+                                            &fp8_256_1_block, &fp8_256_1_row, &fp8_256_1_grouped,
+                                            &fp8_256_2_block, &fp8_256_2_row, &fp8_256_2_grouped};
     for (const Fp8Variant *v : all)
         if (v->bn == bn && v->cg == cg && v->rows == rows && v->grouped == grouped) return v;
     return nullptr;
@@ -123,7 +126,18 @@ ts_status fp8_product(const void *A, const float *SA, const void *B, const float
 
     const int sms = device_sms(current_device());
     if (sms <= 0) return fail(TS_ERR_CUDA, "cannot query the SM count");
-    int bn = 128, cg = 1;
+    int tile = o->tile;
+    if (tile == TS_TILE_AUTO) {
+        // the largest tile that still gives every SM work
+        const int64_t g = grouped ? groups : 1, rows_each = cdiv(M, g);
+        if (cdiv(rows_each, 256) * cdiv(N, 256) * g * 2 >= sms)
+            tile = TS_TILE_256x256_2CTA;
+        else if (cdiv(rows_each, 128) * cdiv(N, 256) * g >= sms)
+            tile = TS_TILE_128x256;
+        else
+            tile = TS_TILE_128x128;
+    }
+    const int bn = tile == TS_TILE_128x128 ? 128 : 256, cg = tile == TS_TILE_256x256_2CTA ? 2 : 1;
     const Fp8Variant *v = find_fp8(bn, cg, rows, grouped);
     if (!v) return fail(TS_ERR_UNSUPPORTED, "no compiled variant");
 
@@ -150,9 +164,9 @@ ts_status fp8_product(const void *A, const float *SA, const void *B, const float
     p.tma_store = p.vec_store;
     if (p.tma_store) {
         const int64_t dims[3] = {N, M, 1}, strides[2] = {ldd * esize, M * ldd * esize};
-        const int box[3] = {128 / esize, 32, 1};
+        const int box[3] = {64 / esize, 32, 1};  // a warp's staging buffer
         if ((s = encode_map(&L.d, D, out == TS_OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                            3, dims, strides, box)) != TS_OK)
+                            3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B)) != TS_OK)
             return s;
     }
     unsigned long long *status = device_status_word(&s);

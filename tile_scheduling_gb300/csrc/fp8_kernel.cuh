@@ -6,17 +6,20 @@
 // 128 elements of K, and for each 128 x 128 block (or each row) of B.
 //
 // The scales change every 128 elements of K, so the tensor core cannot carry one
-// accumulator through the K loop.  Each K block is a chain of four MMAs (K = 32
-// each) into one of two TMEM accumulators; promotion warps read it back, scale
-// it, and add it to fp32 registers that hold the tile's running sum, while the
-// MMAs of the next K block fill the other accumulator.
+// accumulator through the K loop.  Each K block of 128 columns of the tile is a
+// chain of four MMAs (K = 32 each) into one of four TMEM slots; promotion warps
+// read it back, scale it, and add it to fp32 registers that hold the tile's
+// running sum, while the MMAs fill the other slots.  From the commit of a slot to
+// its hand-back some 1000 cycles pass, most of them latencies, and its MMAs take
+// 256: with two 256-column accumulators that round trip bounded the kernel
+// (8192^3: 560 us on 128x256 tiles, 603 us on pairs); four slots hide it.
 //
 // Warp roles (384 threads, one CTA per SM):
 //   warp 0       TMA producer of the operand ring
 //   warp 1       TMEM allocator and MMA issuer
-//   warp 3       barrier initialisation
-//   warps 4..11  promotion and epilogue: warp 4 + j holds rows 32 * (j % 4) and the
-//                column half j / 4 of the tile, one row per lane
+//   warp 2       scales: copies them to shared memory, a chunk of four K blocks at a time
+//   warps 4..11  promotion and epilogue: warp 4 + j holds rows 32 * (j % 4) of the
+//                tile, one row per lane; j / 4 picks the columns (see Fp8Cfg)
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -31,7 +34,7 @@
 
 namespace ts {
 
-template <int BN_, int CG_, bool ROWS_, bool GROUPED_>
+template <int BN_, int CG_, bool ROWS_, bool GROUPED_, int SC_>
 struct Fp8Cfg {
     static constexpr int BN = BN_, CG = CG_;
     static constexpr bool ROWS = ROWS_, GROUPED = GROUPED_;
@@ -45,18 +48,43 @@ struct Fp8Cfg {
     static constexpr int B_BYTES = B_ROWS * BK;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int TX_BYTES = STAGE_BYTES * CG;
+    // TMEM slots of SC columns; a K block fills H of them.  H = 1: all eight promotion
+    // warps read every slot, warp j the half j / 4 of its columns.  H = 2: the warps with
+    // j / 4 = h read slot h of the K block whole; on a CTA pair its MMA takes 64 rows of B
+    // from each CTA's tile, so its two 64-column segments lie 128 columns apart.
+    static constexpr int SC = SC_;
+    static constexpr int SLOTS = 512 / SC;
+    static constexpr int H = BN / SC;
     static constexpr int COLS = BN / 2;  // columns of one promotion warp
-    static constexpr int TMEM_COLS = 2 * BN;
-    static constexpr int EPI_BUF = 32 * 128;  // store staging of one warp: 32 rows x 128 bytes
-    static constexpr int EPI_BYTES = EPI_WARPS * EPI_BUF;
-    static constexpr int SCALE_BYTES = ROWS ? EPI_WARPS * 2 * COLS * 4 : 0;  // a warp's column scales, two K blocks
+    static constexpr int TEMPTY_ARRIVALS = 8 / H * CG;
+    static constexpr int TMEM_COLS = 512;
+    // First column, within the tile, of a promotion warp's 64-column segment seg.
+    static __device__ __forceinline__ int32_t seg_col(int h, int seg) {
+        if constexpr (H == 2 && CG == 2) return 64 * h + 128 * seg;
+        return COLS * h + 64 * seg;
+    }
+    // A 256-column tile's running sums take 128 registers of a promotion thread, with the
+    // loads in flight more than an even split of the register file gives it: the role
+    // warps hand theirs over.  128 * ROLE_REGS + 256 * EPI_REGS = 384 * LAUNCH_REGS.
+    static constexpr bool SHIFT_REGS = BN == 256;
+    static constexpr int LAUNCH_REGS = 168, ROLE_REGS = 56, EPI_REGS = 224;
+    static_assert(128 * ROLE_REGS + 256 * EPI_REGS == 384 * LAUNCH_REGS, "register split");
+    // Store staging of one warp: three buffers of 32 rows x 64 bytes.
+    static constexpr int EPI_ROW = 64, EPI_BUF = 32 * EPI_ROW, EPI_BUFS = 3;
+    static constexpr int EPI_BYTES = EPI_WARPS * EPI_BUFS * EPI_BUF;
+    // Scales travel in chunks of four K blocks, two chunks deep: per K block those of the
+    // tile's rows, then those of its one or two 128-column blocks (ROWS: its columns).
+    static constexpr int CHUNK = 4, CHUNKS = 2;
+    static constexpr int KB_SCALES = 128 + (ROWS ? BN : 4);
+    static constexpr int CHUNK_BYTES = CHUNK * KB_SCALES * 4;
+    static constexpr int SCALE_BYTES = CHUNKS * CHUNK_BYTES;
     static constexpr int PREFIX_BYTES = GROUPED ? (kMaxExperts + 8) * 4 : 0;
     static constexpr int BAR_BYTES = 256;
     static constexpr int FIXED_BYTES = 1024 + EPI_BYTES + SCALE_BYTES + PREFIX_BYTES + BAR_BYTES;
     static constexpr int STAGES = (kSmemLimit - FIXED_BYTES) / STAGE_BYTES;
     static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * STAGE_BYTES;
     static_assert(STAGES >= 2, "ring too shallow");
-    static_assert((2 * STAGES + 5) * 8 + 16 <= BAR_BYTES, "barrier region");
+    static_assert((2 * STAGES + 2 * SLOTS + 2 * CHUNKS + 1) * 8 + 16 <= BAR_BYTES, "barrier region");
 };
 
 // Shared-memory descriptor of a B tile whose rows run along N (B is [K][N]): rows of
@@ -106,11 +134,11 @@ __device__ __forceinline__ Fp8Unit fp8_unit(int32_t u, const Fp8Params &p, const
     return w;
 }
 
-template <int BN, int CG, bool ROWS, bool GROUPED>
+template <int BN, int CG, bool ROWS, bool GROUPED, int SC>
 __global__ void __launch_bounds__(384, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmD, const __grid_constant__ Fp8Params p) {
-    using C = Fp8Cfg<BN, CG, ROWS, GROUPED>;
+    using C = Fp8Cfg<BN, CG, ROWS, GROUPED, SC>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -125,13 +153,16 @@ __global__ void __launch_bounds__(384, 1)
     auto full = [&](uint32_t s) { return s_bar + 8u * s; };
     auto empty = [&](uint32_t s) { return s_bar + 8u * (C::STAGES + s); };
     auto tfull = [&](uint32_t a) { return s_bar + 8u * (2 * C::STAGES + a); };
-    auto tempty = [&](uint32_t a) { return s_bar + 8u * (2 * C::STAGES + 2 + a); };
-    const uint32_t mma_done = s_bar + 8u * (2 * C::STAGES + 4);
-    const uint32_t tail = s_bar + 8u * (2 * C::STAGES + 5);
+    auto tempty = [&](uint32_t a) { return s_bar + 8u * (2 * C::STAGES + C::SLOTS + a); };
+    auto sfull = [&](uint32_t c) { return s_bar + 8u * (2 * C::STAGES + 2 * C::SLOTS + c); };
+    auto sempty = [&](uint32_t c) { return s_bar + 8u * (2 * C::STAGES + 2 * C::SLOTS + C::CHUNKS + c); };
+    const uint32_t mma_done = s_bar + 8u * (2 * C::STAGES + 2 * C::SLOTS + 2 * C::CHUNKS);
+    const uint32_t tail = s_bar + 8u * (2 * C::STAGES + 2 * C::SLOTS + 2 * C::CHUNKS + 1);
     volatile uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(gbase + (tail - base));
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(gbase + (tail - base) + 4);
 
-    const int warp = threadIdx.x >> 5;
+    // uniform across the warp, and known to be: the role loops then run on uniform registers
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
 
@@ -145,9 +176,13 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
         }
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < C::SLOTS; ++a) {
             mbar_init(tfull(a), 1);
-            mbar_init(tempty(a), C::EPI_WARPS * CG);
+            mbar_init(tempty(a), C::TEMPTY_ARRIVALS);
+        }
+        for (int c = 0; c < C::CHUNKS; ++c) {
+            mbar_init(sfull(c), 32);  // every lane of the scale warp, when its copies have landed
+            mbar_init(sempty(c), C::EPI_WARPS);
         }
         mbar_init(mma_done, 1);
         *abort_flag = 0;
@@ -195,9 +230,12 @@ __global__ void __launch_bounds__(384, 1)
     const int32_t first = static_cast<int32_t>(blockIdx.x) / CG;
     const int32_t step = static_cast<int32_t>(gridDim.x) / CG;
 
+    if (warp < kRoleWarps) {
+    if constexpr (C::SHIFT_REGS) regs_dec<C::ROLE_REGS>();
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
-        if (lane == 0) {
+        {
+            const bool leader = elect_one();
             uint32_t stage = 0, phase = 0, issued = 0;
             bool alive = true;
             for (int32_t u = first; u < num_units && alive; u += step) {
@@ -209,7 +247,7 @@ __global__ void __launch_bounds__(384, 1)
                         alive = false;
                         break;
                     }
-                    if (rank == 0) mbar_arrive_expect_tx(full(stage), C::TX_BYTES);
+                    if (rank == 0 && leader) mbar_arrive_expect_tx(full(stage), C::TX_BYTES);
                     const uint32_t da = s_a + stage * C::A_BYTES;
                     const uint32_t db = s_b + stage * C::B_BYTES;
                     const uint32_t fb = CG == 2 ? mapa(full(stage), 0) : full(stage);
@@ -220,16 +258,19 @@ __global__ void __launch_bounds__(384, 1)
                         else
                             tma_load_3d_pair(dst, &tmB, fb, x, y, w.group);
                     };
-                    if constexpr (CG == 1)
-                        tma_load_2d(da, &tmA, fb, k, a_row);
-                    else
-                        tma_load_2d_pair(da, &tmA, fb, k, a_row);
-                    if (p.trans_b) {
+                    if (leader) {
+                        if constexpr (CG == 1)
+                            tma_load_2d(da, &tmA, fb, k, a_row);
+                        else
+                            tma_load_2d_pair(da, &tmA, fb, k, a_row);
+                        if (p.trans_b) {
 #pragma unroll
-                        for (int c = 0; c < C::B_ROWS / 128; ++c) load_b(db + c * 16384, b_row + 128 * c, k);
-                    } else {
-                        load_b(db, k, b_row);
+                            for (int c = 0; c < C::B_ROWS / 128; ++c) load_b(db + c * 16384, b_row + 128 * c, k);
+                        } else {
+                            load_b(db, k, b_row);
+                        }
                     }
+                    __syncwarp();
                     ++issued;
                     if (++stage == C::STAGES) {
                         stage = 0;
@@ -256,212 +297,281 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------- MMA issuer
-        if (lane == 0 && rank == 0) {
-            const uint32_t idesc = p.idesc | (uint32_t(BN >> 3) << 17) | (uint32_t(C::TILE_M >> 4) << 24);
-            // start-address step (in 16-byte units) of one K = 32 MMA: 32 bytes along a
-            // K-major row, or 32 rows of 128 bytes
-            const uint32_t b_step = p.trans_b ? (32 * 128) >> 4 : 32 >> 4;
-            uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+        // The whole warp runs the loop, one elected lane issues: with the loop inside one
+        // lane's branch every descriptor went through per-thread registers, and a K block
+        // took some 630 cycles to issue (8192^3, no promotion: 362 us against 286).
+        if (rank == 0) {
+            const bool leader = elect_one();
+            const uint32_t idesc = p.idesc | (uint32_t(SC >> 3) << 17) | (uint32_t(C::TILE_M >> 4) << 24);
+            // steps of B's start address in 16-byte units: one K = 32 MMA (32 bytes along a
+            // K-major row, or 32 rows of 128 bytes) and one slot (its rows, or, along a row of
+            // n, half of it or the next box)
+            const uint32_t k_step = p.trans_b ? (32 * 128) >> 4 : 32 >> 4;
+            const uint32_t h_step = p.trans_b ? (CG == 2 ? 64 : 16384) >> 4 : (C::B_BYTES / C::H) >> 4;
+            uint32_t stage = 0, phase = 0, slot = 0, slot_phase = 0;
             bool alive = true;
             for (int32_t u = first; u < num_units && alive; u += step) {
-                for (int32_t kb = 0; kb < p.num_kb; ++kb) {
-                    if (!wait_phase(tempty(acc), acc_phase ^ 1u, abort_flag, p, WAIT_MMA_TMEM_EMPTY) ||
-                        !wait_phase(full(stage), phase, abort_flag, p, WAIT_MMA_FULL)) {
+                for (int32_t kb = 0; kb < p.num_kb && alive; ++kb) {
+                    if (!wait_phase(full(stage), phase, abort_flag, p, WAIT_MMA_FULL)) {
                         alive = false;
                         break;
                     }
-                    tc_fence_after();
                     const uint64_t da = sw128_kmajor_desc(s_a + stage * C::A_BYTES);
                     const uint32_t b_at = s_b + stage * C::B_BYTES;
                     const uint64_t db = p.trans_b ? sw128_nmajor_desc(b_at) : sw128_kmajor_desc(b_at);
+#pragma unroll 1
+                    for (int h = 0; h < C::H; ++h) {
+                        if (!wait_phase(tempty(slot), slot_phase ^ 1u, abort_flag, p, WAIT_MMA_TMEM_EMPTY)) {
+                            alive = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (leader) {
 #pragma unroll
-                    for (int kk = 0; kk < C::BK / C::UMMA_K; ++kk)
-                        mma_f8<CG>(tmem_base + acc * BN, da + 2u * kk, db + b_step * kk, idesc, kk != 0);
-                    if constexpr (CG == 1) {
-                        mma_commit(empty(stage));
-                        mma_commit(tfull(acc));
-                    } else {
-                        mma_commit_pair(empty(stage), 0x3);
-                        mma_commit_pair(tfull(acc), 0x3);
+                            for (int kk = 0; kk < C::BK / C::UMMA_K; ++kk)
+                                mma_f8<CG>(tmem_base + slot * SC, da + 2u * kk, db + h_step * h + k_step * kk, idesc,
+                                           kk != 0);
+                            if constexpr (CG == 1)
+                                mma_commit(tfull(slot));
+                            else
+                                mma_commit_pair(tfull(slot), 0x3);
+                        }
+                        __syncwarp();
+                        if (++slot == C::SLOTS) {
+                            slot = 0;
+                            slot_phase ^= 1u;
+                        }
                     }
+                    if (!alive) break;
+                    if (leader) {
+                        if constexpr (CG == 1)
+                            mma_commit(empty(stage));
+                        else
+                            mma_commit_pair(empty(stage), 0x3);
+                    }
+                    __syncwarp();
                     if (++stage == C::STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
-                    if (++acc == 2) {
-                        acc = 0;
-                        acc_phase ^= 1u;
-                    }
                 }
             }
             // every MMA has completed before TMEM is freed
-            if constexpr (CG == 1)
-                mma_commit(mma_done);
-            else
-                mma_commit_pair(mma_done, 0x1);
+            if (leader) {
+                if constexpr (CG == 1)
+                    mma_commit(mma_done);
+                else
+                    mma_commit_pair(mma_done, 0x1);
+            }
+            __syncwarp();
             wait_drain(mma_done, 0, abort_flag, p);
         }
         __syncwarp();
-    } else if (warp >= kRoleWarps) {
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ scales
+        // Asynchronous copies, completing on the chunk's barrier: nothing here waits for
+        // global memory, and the promotion warps' K loop holds no global load (in it, a
+        // load's latency of some 1000 cycles showed through a distance of two K blocks).
+        // The loop is kept small: a warp that shares its scheduler with two promotion warps
+        // slows them by what it pushes out of the instruction cache.
+        uint32_t chunk = 0;
+        bool alive = true;
+        for (int32_t u = first; u < num_units && alive; u += step) {
+            const Fp8Unit w = fp8_unit<C>(u, p, prefix);
+            const int32_t row = w.row0 + static_cast<int32_t>(rank) * C::BM + lane;
+            const float *pa = p.sa + static_cast<int64_t>(row) * p.sa_row;
+            // this lane's first column (ROWS) or block of columns
+            const int32_t n = w.col0 + (ROWS ? 1 : kScaleBlock) * lane;
+            const bool has_b = ROWS || lane < BN / 128;
+            const float *pb = p.sb + w.group * p.sb_group + static_cast<int64_t>(ROWS ? n : n / kScaleBlock) * p.sb_n;
+            for (int32_t kb = 0; kb < p.num_kb; ++kb) {
+                const uint32_t buf = chunk % C::CHUNKS;
+                if (kb % C::CHUNK == 0) {
+                    const bool ok = wait_inline(sempty(buf), ((chunk / C::CHUNKS) & 1u) ^ 1u, abort_flag, p, WAIT_SCALES);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        alive = false;
+                        break;
+                    }
+                }
+                const uint32_t at = s_scale + buf * C::CHUNK_BYTES + (kb % C::CHUNK) * (C::KB_SCALES * 4) + lane * 4;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    copy_async_f32(at + 128 * i, row + 32 * i < w.row_end ? pa + 32 * i * p.sa_row : p.sa, row + 32 * i < w.row_end);
+                pa += p.sa_blk;
+                if constexpr (ROWS) {
+#pragma unroll
+                    for (int i = 0; i < BN / 32; ++i)
+                        copy_async_f32(at + 512 + 128 * i, n + 32 * i < p.N ? pb + 32 * i * p.sb_n : p.sb, n + 32 * i < p.N);
+                } else if (has_b) {
+                    copy_async_f32(at + 512, n < p.N ? pb : p.sb, n < p.N);
+                }
+                pb += p.sb_k;
+                if (kb % C::CHUNK == C::CHUNK - 1 || kb + 1 == p.num_kb) {
+                    copy_async_arrive(sfull(buf));
+                    ++chunk;
+                }
+            }
+        }
+        copy_async_wait();
+        __syncwarp();
+    }
+    } else {
         // ------------------------------------------- promotion and epilogue
+        if constexpr (C::SHIFT_REGS) regs_inc<C::EPI_REGS>();
         const int j = warp - kRoleWarps;
         const int q = j & 3, h = j >> 2;
-        const uint32_t stg = s_epi + static_cast<uint32_t>(j) * C::EPI_BUF;
-        const uint32_t wsc = s_scale + static_cast<uint32_t>(j) * (2 * C::COLS * 4);
+        const uint32_t stg = s_epi + static_cast<uint32_t>(j) * (C::EPI_BUFS * C::EPI_BUF);
+        uint32_t buf = 0;
         const uint64_t store_policy = policy_evict_first();
-        uint32_t acc_i = 0, acc_phase = 0;
+        // slots of this warp: count s of its K blocks since the start gives slot and phase
+        uint32_t count = C::H == 2 ? h : 0, chunk = 0;
         bool alive = true;
         for (int32_t u = first; u < num_units && alive; u += step) {
             const Fp8Unit w = fp8_unit<C>(u, p, prefix);
             const int32_t row0 = w.row0 + static_cast<int32_t>(rank) * C::BM + 32 * q;
             const int32_t row = row0 + lane;
-            const int32_t col0 = w.col0 + h * C::COLS;
+            const int32_t col0 = w.col0 + C::seg_col(h, 0);
             const bool work = row0 < w.row_end && col0 < p.N;  // otherwise only the barriers are served
             const bool mine = work && row < w.row_end;
-            const float *const sa = p.sa + static_cast<int64_t>(row) * p.sa_row;
-            const float *const sb = p.sb + w.group * p.sb_group + (ROWS ? 0 : (col0 / kScaleBlock) * p.sb_n);
-            // Scales are read two K blocks ahead: their latency (an L2 hit) is about that long.
-            auto load_a = [&](int32_t kb) { return mine && kb < p.num_kb ? __ldg(sa + kb * p.sa_blk) : 0.f; };
-            auto load_b = [&](int32_t kb) {
-                return !ROWS && mine && kb < p.num_kb ? __ldg(sb + kb * p.sb_k) : 1.f;
-            };
-            float col_scale[C::COLS / 32];
-            auto load_cols = [&](int32_t kb) {
-                if constexpr (ROWS) {
-#pragma unroll
-                    for (int i = 0; i < C::COLS / 32; ++i) {
-                        const int32_t n = col0 + lane + 32 * i;
-                        col_scale[i] = n < p.N && kb < p.num_kb ? __ldg(sb + n * p.sb_n + kb * p.sb_k) : 0.f;
-                    }
-                }
-            };
-            float a0 = load_a(0), b0 = load_b(0), a1 = load_a(1), b1 = load_b(1);
-            load_cols(0);
+            // on a pair a slot's two segments lie in two scale blocks, else in one
+            constexpr int NB = !ROWS && C::H == 2 && CG == 2 ? 2 : 1;
             uint64_t sum[C::COLS / 2];
 #pragma unroll
             for (int i = 0; i < C::COLS / 2; ++i) sum[i] = 0ull;
             for (int32_t kb = 0; kb < p.num_kb; ++kb) {
-                const float sc = a0 * b0;
-                a0 = a1;
-                b0 = b1;
-                a1 = load_a(kb + 2);
-                b1 = load_b(kb + 2);
-                const uint32_t sbuf = wsc + (kb & 1) * (C::COLS * 4);
-                if constexpr (ROWS) {
-                    if (work) {
-#pragma unroll
-                        for (int i = 0; i < C::COLS / 32; ++i)
-                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sbuf + (lane + 32 * i) * 4), "f"(col_scale[i])
-                                         : "memory");
-                        __syncwarp();
-                        load_cols(kb + 1);
+                if (kb % C::CHUNK == 0) {
+                    const bool ok = wait_inline(sfull(chunk % C::CHUNKS), (chunk / C::CHUNKS) & 1u, abort_flag, p, WAIT_SCALES);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        alive = false;
+                        break;
                     }
                 }
-                const bool ok = wait_phase(tfull(acc_i), acc_phase, abort_flag, p, WAIT_EPI_TMEM_FULL);
+                const uint32_t sc_at = s_scale + (chunk % C::CHUNKS) * C::CHUNK_BYTES + (kb % C::CHUNK) * (C::KB_SCALES * 4);
+                const float row_scale = ld_shared_f32(sc_at + (32 * q + lane) * 4);
+                uint64_t s2[2];
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const int blk = NB == 2 ? i : (BN == 256 ? h : 0);
+                    const float f = ROWS ? row_scale : row_scale * ld_shared_f32(sc_at + 512 + 4 * blk);
+                    s2[i] = pair_f32(f, f);
+                }
+                // the chunk is read: back to the scale warp
+                auto chunk_done = [&] {
+                    if (kb % C::CHUNK == C::CHUNK - 1 || kb + 1 == p.num_kb) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(sempty(chunk % C::CHUNKS));
+                        ++chunk;
+                    }
+                };
+                if (!ROWS || !work) chunk_done();
+                const uint32_t slot = count % C::SLOTS;
+                const bool ok = wait_inline(tfull(slot), (count / C::SLOTS) & 1u, abort_flag, p, WAIT_EPI_TMEM_FULL);
+                count += C::H;
                 if (!__all_sync(0xffffffffu, ok)) {
                     alive = false;
                     break;
                 }
                 tc_fence_after();
-                const uint64_t s2 = pair_f32(sc, sc);
-                if (work) {
-                    const uint32_t taddr =
-                        tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc_i * BN + h * C::COLS;
-                    uint32_t v[2][32];
-                    tmem_ld_32x32b_x32(taddr, v[0]);
-                    tmem_ld_wait(v[0]);
-#pragma unroll
-                    for (int c = 0; c < C::COLS / 32; ++c) {
-                        if (c + 1 < C::COLS / 32) tmem_ld_32x32b_x32(taddr + 32 * (c + 1), v[(c + 1) & 1]);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const uint64_t x = pair_u32(v[c & 1][2 * i], v[c & 1][2 * i + 1]);
-                            if constexpr (ROWS) {
-                                uint64_t cs;
-                                asm volatile("ld.shared.b64 %0, [%1];" : "=l"(cs) : "r"(sbuf + (32 * c + 2 * i) * 4));
-                                fma2(sum[16 * c + i], mul2(x, s2), cs);
-                            } else {
-                                fma2(sum[16 * c + i], x, s2);
-                            }
-                        }
-                        if (c + 1 < C::COLS / 32) tmem_ld_wait(v[(c + 1) & 1]);
+                // the slot is read: back to the MMA issuer
+                auto release = [&] {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (CG == 1)
+                            mbar_arrive(tempty(slot));
+                        else
+                            mbar_arrive_cluster(mapa(tempty(slot), 0));
                     }
+                };
+                if (!work) {
+                    release();
+                    continue;
                 }
-                // this warp's part of the accumulator is read: back to the MMA issuer
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (CG == 1)
-                        mbar_arrive(tempty(acc_i));
-                    else
-                        mbar_arrive_cluster(mapa(tempty(acc_i), 0));
-                }
-                if (++acc_i == 2) {
-                    acc_i = 0;
-                    acc_phase ^= 1u;
-                }
-            }
-            if (!alive || !work) continue;
-            // Store the tile part: 128-byte wide subtiles through swizzled staging and a
-            // TMA store where the subtile lies inside D (and, grouped, inside the
-            // group), else each lane its own row.
-            auto emit = [&](auto out_tag, int s, const uint64_t *part) {
-                constexpr int OUT = decltype(out_tag)::value;
-                constexpr int SUB = OUT == OUT_F32 ? 32 : 64;
-                uint32_t o[32];
-                if constexpr (OUT == OUT_F32) {
+                const uint32_t taddr =
+                    tmem_base + (static_cast<uint32_t>(32 * q) << 16) + slot * SC + (C::H == 1 ? C::COLS * h : 0);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) unpair(part[i], o[2 * i], o[2 * i + 1]);
-                } else {
+                for (int c = 0; c < C::COLS / 64; ++c) {
+                    uint32_t v[64];
+                    tmem_ld(taddr + 64 * c, v);
+                    tmem_ld_wait();
+                    // handed back once its last columns are in registers
+                    if (c + 1 == C::COLS / 64) release();
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        uint32_t lo, hi;
-                        unpair(part[i], lo, hi);
+                        const uint64_t x = pair_u32(v[2 * i], v[2 * i + 1]);
+                        if constexpr (ROWS)
+                            fma2(sum[32 * c + i], mul2(x, s2[0]),
+                                 ld_shared_u64(sc_at + 512 + (C::seg_col(h, c) + 2 * i) * 4));
+                        else
+                            fma2(sum[32 * c + i], x, s2[NB == 2 ? c : 0]);
+                    }
+                }
+                if (ROWS) chunk_done();
+            }
+            if (!alive || !work) continue;
+            // Store the tile part: 64-byte wide subtiles through swizzled staging and a TMA
+            // store where the subtile lies inside D (and, grouped, inside the group), else
+            // each lane its own row.
+            auto emit = [&](auto out_tag, int s, const uint64_t *part) {
+                constexpr int OUT = decltype(out_tag)::value;
+                constexpr int SUB = C::EPI_ROW / (OUT == OUT_F32 ? 4 : 2);  // columns
+                constexpr int W = C::EPI_ROW / 4;                           // words of a row
+                const int32_t col = w.col0 + C::seg_col(h, s * SUB / 64) + s * SUB % 64;
+                if (col >= p.N) return;
+                uint32_t o[W];
+#pragma unroll
+                for (int i = 0; i < SUB / 2; ++i) {
+                    uint32_t lo, hi;
+                    unpair(part[i], lo, hi);
+                    if constexpr (OUT == OUT_F32) {
+                        o[2 * i] = lo;
+                        o[2 * i + 1] = hi;
+                    } else {
                         o[i] = pack_bf16x2(lo, hi);
                     }
                 }
-                const int32_t col = col0 + s * SUB;
-                if (col >= p.N) return;
                 const bool whole = col + SUB <= p.N;
                 if (p.tma_store && whole && (!GROUPED || row0 + 32 <= w.row_end)) {
-                    if (lane == 0) bulk_wait_read<0>();
+                    if (lane == 0) bulk_wait_read<C::EPI_BUFS - 1>();  // the store that used this buffer has read it
                     __syncwarp();
-                    const uint32_t at = stg + static_cast<uint32_t>(lane) * 128u;
+                    const uint32_t at = stg + buf * C::EPI_BUF + static_cast<uint32_t>(lane) * C::EPI_ROW;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        st_shared_v4(at + ((static_cast<uint32_t>(i) ^ (lane & 7u)) << 4), o[4 * i], o[4 * i + 1],
+                    for (int i = 0; i < W / 4; ++i)
+                        st_shared_v4(at + ((static_cast<uint32_t>(i) ^ ((lane >> 1) & 3u)) << 4), o[4 * i], o[4 * i + 1],
                                      o[4 * i + 2], o[4 * i + 3]);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_3d(&tmD, stg, col, row0, 0, store_policy);
+                        tma_store_3d(&tmD, stg + buf * C::EPI_BUF, col, row0, 0, store_policy);
                         bulk_commit();
                     }
+                    buf = buf + 1 == C::EPI_BUFS ? 0 : buf + 1;
                 } else if (mine) {
                     const int64_t at = static_cast<int64_t>(row) * p.ldd + col;
                     if (p.vec_store && whole) {
                         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<char *>(p.D) + at * (OUT == OUT_F32 ? 4 : 2));
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        for (int i = 0; i < W / 4; ++i)
+                            dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     } else if constexpr (OUT == OUT_F32) {
                         float *dst = static_cast<float *>(p.D) + at;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
+                        for (int i = 0; i < SUB; ++i)
                             if (col + i < p.N) dst[i] = __uint_as_float(o[i]);
                     } else {
                         uint16_t *dst = static_cast<uint16_t *>(p.D) + at;
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
+                        for (int i = 0; i < SUB; ++i)
                             if (col + i < p.N) dst[i] = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
                     }
                 }
             };
             if (p.out == OUT_F32) {
 #pragma unroll
-                for (int s = 0; s < C::COLS / 32; ++s) emit(std::integral_constant<int, OUT_F32>{}, s, sum + 16 * s);
+                for (int s = 0; s < C::COLS / 16; ++s) emit(std::integral_constant<int, OUT_F32>{}, s, sum + 8 * s);
             } else {
 #pragma unroll
-                for (int s = 0; s < C::COLS / 64; ++s) emit(std::integral_constant<int, OUT_BF16>{}, s, sum + 32 * s);
+                for (int s = 0; s < C::COLS / 32; ++s) emit(std::integral_constant<int, OUT_BF16>{}, s, sum + 16 * s);
             }
         }
         if (lane == 0) bulk_wait<0>();

@@ -8,16 +8,23 @@
 namespace ts {
 namespace {
 
-template <int BN, int CG, bool ROWS, bool GROUPED>
+template <int BN, int CG, bool ROWS, bool GROUPED, int SC>
 cudaError_t fp8_launch(const Fp8Launch &L) {
-    using C = Fp8Cfg<BN, CG, ROWS, GROUPED>;
-    auto *kernel = fp8_gemm_kernel<BN, CG, ROWS, GROUPED>;
+    using C = Fp8Cfg<BN, CG, ROWS, GROUPED, SC>;
+    auto *kernel = fp8_gemm_kernel<BN, CG, ROWS, GROUPED, SC>;
     static std::atomic<uint64_t> done{0};  // cudaFuncSetAttribute once per device
     const int dev = current_device();
     const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
     if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
         if (e != cudaSuccess) return e;
+        if (C::SHIFT_REGS) {
+            // the promotion warps wait for registers that the block must have been launched with
+            cudaFuncAttributes a;
+            e = cudaFuncGetAttributes(&a, kernel);
+            if (e != cudaSuccess) return e;
+            if (a.numRegs != C::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
+        }
         if (bit) done.fetch_or(bit, std::memory_order_acq_rel);
     }
     cudaLaunchConfig_t cfg = {};
@@ -43,8 +50,8 @@ cudaError_t fp8_launch(const Fp8Launch &L) {
 }  // namespace
 }  // namespace ts
 
-#define TS_FP8_VARIANT(NAME, BN, CG, ROWS, GROUPED)                                              \
+#define TS_FP8_VARIANT(NAME, BN, CG, ROWS, GROUPED, SC)                                          \
     namespace ts {                                                                               \
     extern const Fp8Variant NAME;                                                                \
-    const Fp8Variant NAME = {BN, CG, ROWS, GROUPED, &fp8_launch<BN, CG, ROWS, GROUPED>};         \
+    const Fp8Variant NAME = {BN, CG, ROWS, GROUPED, &fp8_launch<BN, CG, ROWS, GROUPED, SC>};         \
     }

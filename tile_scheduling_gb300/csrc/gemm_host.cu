@@ -62,7 +62,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn(ts_status *err) {
 }  // namespace
 
 ts_status encode_map(CUtensorMap *m, const void *ptr, CUtensorMapDataType dt, int rank, const int64_t *dims,
-                     const int64_t *strides, const int *box) {
+                     const int64_t *strides, const int *box, CUtensorMapSwizzle swizzle) {
     ts_status err = TS_OK;
     auto fn = encode_fn(&err);
     if (!fn) return err;
@@ -74,7 +74,7 @@ ts_status encode_map(CUtensorMap *m, const void *ptr, CUtensorMapDataType dt, in
         if (i > 0) st[i - 1] = static_cast<cuuint64_t>(strides[i - 1]);
     }
     CUresult r = fn(m, dt, static_cast<cuuint32_t>(rank), const_cast<void *>(ptr), d, st, b, e,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(TS_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled failed (%d) for rows of %lld elements, pitch %lld B",

@@ -18,6 +18,7 @@ enum : int32_t {
     WAIT_DRAIN = 7,
     WAIT_ROWS_CLC = 8,
     WAIT_SCHED_PRODUCER = 9,
+    WAIT_SCALES = 10,
 };
 
 // Device status word (library-owned, one per device):

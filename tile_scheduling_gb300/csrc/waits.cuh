@@ -42,6 +42,26 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
     return wait_slow(bar, parity, p.timeout_ns, abort_flag, true, p, where);
 }
 
+// The same without a function call, for code whose registers are too many to be
+// kept across one.
+template <class P>
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int *abort_flag, const P &p,
+                                            int where) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    for (uint32_t n = 1;; ++n) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((n & 15u) == 0) {
+            if (*abort_flag) return false;
+            if (globaltimer() - t0 > p.timeout_ns) {
+                report_timeout(p, where);
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+}
+
 // Bounded wait for roles whose waits last about a tile and whose wake-up is not
 // on the critical path (epilogue warps waiting for an accumulator, the CLC
 // scheduler waiting for a free slot): it sleeps between polls, leaving the
