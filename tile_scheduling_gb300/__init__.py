@@ -556,8 +556,8 @@ _FP8 = {torch.float8_e4m3fn: TS_FP8_E4M3, torch.float8_e5m2: TS_FP8_E5M2}
 _SCORE = {"softmax": TS_SCORE_SOFTMAX, "sigmoid": TS_SCORE_SIGMOID}
 
 
-def _tensor(t, name: str, dtypes, dims: int) -> None:
-    """Check a CUDA tensor's type (one of ``dtypes``) and number of dimensions."""
+def _require(t, name: str, dtypes, dims: int) -> None:
+    """Raise unless t is a CUDA tensor of one of ``dtypes`` with ``dims`` dimensions."""
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
         raise TypeError(f"{name} must be a tensor of {', '.join(str(d) for d in dtypes)}")
     if not t.is_cuda:
@@ -566,52 +566,82 @@ def _tensor(t, name: str, dtypes, dims: int) -> None:
         raise ValueError(f"{name} must be {dims}-D")
 
 
-def _rows_of(t, name: str) -> int:
-    """Row stride of a matrix whose last dimension is dense (0, for the default, with a single row)."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+_F32 = {torch.float32: 0}
+_I32 = {torch.int32: 0}
+_I64 = {torch.int64: 0}
+
+
+def _matrix_of(t, name: str, dtypes, dims: int = 2):
+    """(dtype code, shape, row stride) of a CUDA tensor with dense last dimension; the stride is 0, for
+    the default, with a single row."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or not t.is_cuda or t.dim() != dims:
+        _require(t, name, dtypes, dims)
+    shape, stride = t.shape, t.stride()
+    if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must have unit column stride")
-    return t.stride(-2) if t.shape[-2] > 1 else 0
+    return dtypes[t.dtype], shape, stride[-2] if shape[-2] > 1 else 0
 
 
-def _dense(t, name: str, dtype, shape) -> int:
-    _tensor(t, name, (dtype,), len(shape))
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+def _dense(t, name: str, dtypes, shape) -> int:
+    """Address of a contiguous CUDA tensor of the given type and shape."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or not t.is_cuda or t.dim() != len(shape):
+        _require(t, name, dtypes, len(shape))
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}")
     return t.data_ptr()
 
 
-def _fp8_opts(A, SA, B, SB, D, trans_b, tile, max_workers, timeout_s):
-    """Checks and options that the plain and the grouped 8-bit product share; returns (opts, M, N, K)."""
-    _tensor(A, "A", _FP8, 2)
-    _tensor(B, "B", _FP8, 3 if B.dim() == 3 else 2)
-    _tensor(D, "D", _OUT, 2)
-    _tensor(SA, "SA", (torch.float32,), 2)
-    _tensor(SB, "SB", (torch.float32,), B.dim())
-    M, K = A.shape
-    R, C = B.shape[-2:]
-    N = C if trans_b else R
-    if (R if trans_b else C) != K or tuple(D.shape) != (M, N):
+def _scales(t, name: str, dims: int):
+    """(shape, strides) of an fp32 scale tensor of any strides."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda or t.dim() != dims:
+        _require(t, name, _F32, dims)
+    return t.shape, t.stride()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _stream_of(stream) -> int:
+    """The cudaStream_t of ``stream``, or of torch's current stream; the small operators below are called
+    often enough that building a torch.cuda.Stream object for it each time would show."""
+    if stream is None:
+        if _raw_stream is not None and _raw_device is not None:
+            return _raw_stream(_raw_device())
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _fp8_opts(A, SA, B, SB, D, dims, trans_b, tile, max_workers, timeout_s):
+    """Checks and options that the plain and the grouped 8-bit product share; returns (opts, M, N, K, out)."""
+    a_type, (M, K), lda = _matrix_of(A, "A", _FP8)
+    b_type, b_shape, ldb = _matrix_of(B, "B", _FP8, dims)
+    out, d_shape, ldd = _matrix_of(D, "D", _OUT)
+    sa_shape, sa_stride = _scales(SA, "SA", 2)
+    sb_shape, sb_stride = _scales(SB, "SB", dims)
+    R, C = b_shape[-2], b_shape[-1]
+    N, depth = (C, R) if trans_b else (R, C)
+    if depth != K or d_shape[0] != M or d_shape[1] != N:
         raise ValueError(f"shape mismatch: A {tuple(A.shape)}, B {tuple(B.shape)}, D {tuple(D.shape)}")
     kb = -(-K // 128)
-    if tuple(SA.shape) != (M, kb):
+    if sa_shape[0] != M or sa_shape[1] != kb:
         raise ValueError(f"SA must be [{M}, {kb}], not {tuple(SA.shape)}")
-    o = Fp8Opts()
-    if tuple(SB.shape[-2:]) == (-(-R // 128), -(-C // 128)):
-        pass
-    elif not trans_b and tuple(SB.shape) == (N, kb):
-        o.b_scale = TS_SCALE_ROW
-    else:
-        raise ValueError(f"SB {tuple(SB.shape)} holds neither a scale for each 128 x 128 block of B {tuple(B.shape)} "
-                         "nor one for each row and 128 columns")
-    o.a_type, o.b_type = _FP8[A.dtype], _FP8[B.dtype]
-    o.trans_b = int(bool(trans_b))
-    o.tile = _TILE[tile] if isinstance(tile, str) else int(tile)
-    o.max_workers = int(max_workers)
-    o.lda, o.ldb, o.ldd = _rows_of(A, "A"), _rows_of(B, "B"), _rows_of(D, "D")
-    o.sa_row, o.sa_blk = SA.stride()
-    o.sb_row, o.sb_blk = SB.stride()[-2:]
-    o.timeout_s = float(timeout_s)
-    return o, M, N, K
+    b_scale = TS_SCALE_BLOCK
+    if sb_shape[-2] != -(-R // 128) or sb_shape[-1] != -(-C // 128):
+        if trans_b or dims != 2 or sb_shape[0] != N or sb_shape[1] != kb:
+            raise ValueError(f"SB {tuple(SB.shape)} holds neither a scale for each 128 x 128 block of B "
+                             f"{tuple(B.shape)} nor one for each row and 128 columns")
+        b_scale = TS_SCALE_ROW
+    b_group = sb_group = 0
+    if dims == 3:
+        if sb_shape[0] != b_shape[0]:
+            raise ValueError(f"SB must hold the scales of {b_shape[0]} groups")
+        if b_shape[0] > 1:
+            b_group, sb_group = B.stride(0), sb_stride[0]
+    o = Fp8Opts(a_type, b_type, b_scale, 1 if trans_b else 0, _TILE[tile] if isinstance(tile, str) else int(tile),
+                max_workers, lda, ldb, ldd, b_group, sa_stride[0], sa_stride[1], sb_stride[-2], sb_stride[-1],
+                sb_group, timeout_s)
+    return o, M, N, K, out
 
 
 def ts_gemm_fp8(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch.Tensor, D: torch.Tensor, trans_b=False,
@@ -624,11 +654,11 @@ def ts_gemm_fp8(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch.Te
     fastest with its rows contiguous (the transpose of a [ceil(K / 128), M] tensor).  ``trans_b``: B is
     [K, N] with block scales [ceil(K / 128), ceil(N / 128)].  Rows may be strided; rows of A and B start
     on 16-byte boundaries.  Asynchronous on ``stream`` (default: torch's current stream)."""
-    if B.dim() != 2:
-        raise ValueError("B must be 2-D")
-    o, M, N, K = _fp8_opts(A, SA, B, SB, D, trans_b, tile, max_workers, timeout_s)
-    _check(_lib.ts_gemm_fp8(A.data_ptr(), SA.data_ptr(), B.data_ptr(), SB.data_ptr(), D.data_ptr(), M, N, K,
-                            _OUT[D.dtype], o, _stream_handle(stream)))
+    o, M, N, K, out = _fp8_opts(A, SA, B, SB, D, 2, trans_b, tile, max_workers, timeout_s)
+    st = _lib.ts_gemm_fp8(A.data_ptr(), SA.data_ptr(), B.data_ptr(), SB.data_ptr(), D.data_ptr(), M, N, K, out, o,
+                          _stream_of(stream))
+    if st:
+        _check(st)
 
 
 def ts_gemm_fp8_grouped(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch.Tensor, D: torch.Tensor,
@@ -638,16 +668,12 @@ def ts_gemm_fp8_grouped(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: 
 
     B [groups, N, K] (``trans_b``: [groups, K, N]) with block scales SB of the same leading dimension;
     everything else as ts_gemm_fp8.  Rows outside every group are not written."""
-    if B.dim() != 3:
-        raise ValueError("B must be [groups, N, K] or, with trans_b, [groups, K, N]")
+    o, M, N, K, out = _fp8_opts(A, SA, B, SB, D, 3, trans_b, tile, max_workers, timeout_s)
     G = B.shape[0]
-    o, M, N, K = _fp8_opts(A, SA, B, SB, D, trans_b, tile, max_workers, timeout_s)
-    if SB.shape[0] != G:
-        raise ValueError(f"SB must hold the scales of {G} groups")
-    o.b_group, o.sb_group = (B.stride(0), SB.stride(0)) if G > 1 else (0, 0)
-    _check(_lib.ts_gemm_fp8_grouped(A.data_ptr(), SA.data_ptr(), B.data_ptr(), SB.data_ptr(), D.data_ptr(),
-                                    _dense(offsets, "offsets", torch.int64, (G + 1,)), G, M, N, K, _OUT[D.dtype], o,
-                                    _stream_handle(stream)))
+    st = _lib.ts_gemm_fp8_grouped(A.data_ptr(), SA.data_ptr(), B.data_ptr(), SB.data_ptr(), D.data_ptr(),
+                                  _dense(offsets, "offsets", _I64, (G + 1,)), G, M, N, K, out, o, _stream_of(stream))
+    if st:
+        _check(st)
 
 
 def ts_quant_fp8(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, rows=None, rows_div=1, transpose=False,
@@ -658,45 +684,33 @@ def ts_quant_fp8(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, rows=No
     rows[r] // rows_div (zeros for a negative entry); with ``transpose`` [N, M].  scales is
     [rows of q, ceil(columns of q / 128)] of any strides; with its rows contiguous it is what
     ts_gemm_fp8 reads fastest."""
-    _tensor(x, "x", _OUT, 2)
-    _tensor(q, "q", _FP8, 2)
-    _tensor(scales, "scales", (torch.float32,), 2)
-    M, N = x.shape
-    o = QuantOpts()
+    x_type, (M, N), ldx = _matrix_of(x, "x", _OUT)
+    q_type, q_shape, ldq = _matrix_of(q, "q", _FP8)
+    s_shape, s_stride = _scales(scales, "scales", 2)
+    index, out_rows, want_r, want_c = 0, 0, M, N
     if rows is not None:
         if transpose:
             raise ValueError("rows and transpose cannot be combined")
-        if rows.dim() != 1:
-            raise ValueError("rows must be 1-D")
-        o.rows = _dense(rows, "rows", torch.int32, rows.shape)
-        o.out_rows = rows.shape[0]
-        o.rows_div = int(rows_div)
-        if o.rows_div < 1:
+        if rows_div < 1:
             raise ValueError("rows_div must be at least 1")
-    want = (N, M) if transpose else (o.out_rows if rows is not None else M, N)
-    if tuple(q.shape) != want or tuple(scales.shape) != (want[0], -(-want[1] // 128)):
-        raise ValueError(f"q must be {want} and scales {(want[0], -(-want[1] // 128))}, not {tuple(q.shape)} and "
+        index = _dense(rows, "rows", _I32, (rows.numel(),))
+        out_rows = want_r = rows.shape[0]
+    elif transpose:
+        want_r, want_c = N, M
+    blocks = -(-want_c // 128)
+    if q_shape[0] != want_r or q_shape[1] != want_c or s_shape[0] != want_r or s_shape[1] != blocks:
+        raise ValueError(f"q must be {(want_r, want_c)} and scales {(want_r, blocks)}, not {tuple(q.shape)} and "
                          f"{tuple(scales.shape)}")
-    if rows is not None and want[0] == 0:
+    if want_r == 0:
         return
-    o.transpose = int(bool(transpose))
-    o.ldx, o.ldq = _rows_of(x, "x"), _rows_of(q, "q")
-    o.s_row, o.s_blk = scales.stride()
-    _check(_lib.ts_quant_fp8(x.data_ptr(), q.data_ptr(), scales.data_ptr(), M, N, _OUT[x.dtype], _FP8[q.dtype], o,
-                             _stream_handle(stream)))
+    o = QuantOpts(index, out_rows, int(rows_div), 1 if transpose else 0, ldx, ldq, s_stride[0], s_stride[1])
+    st = _lib.ts_quant_fp8(x.data_ptr(), q.data_ptr(), scales.data_ptr(), M, N, x_type, q_type, o, _stream_of(stream))
+    if st:
+        _check(st)
 
 
-def _route_opts(logits, score, renorm, scale, bias=None, groups=1, keep_groups=0, group_best=1):
-    _tensor(logits, "logits", _OUT, 2)
-    o = RouteOpts()
-    o.score = _SCORE[score] if isinstance(score, str) else int(score)
-    o.groups, o.keep_groups, o.group_best = int(groups), int(keep_groups), int(group_best)
-    o.no_renorm = int(not renorm)
-    o.scale = float(scale)
-    if bias is not None:
-        o.bias = _dense(bias, "bias", torch.float32, (logits.shape[1],))
-    o.ldx = _rows_of(logits, "logits")
-    return o
+def _score(score) -> int:
+    return _SCORE[score] if isinstance(score, str) else int(score)
 
 
 def ts_moe_route(logits: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, bias=None, score="softmax",
@@ -707,29 +721,32 @@ def ts_moe_route(logits: torch.Tensor, experts: torch.Tensor, weights: torch.Ten
     ``groups`` equal groups of experts the ``keep_groups`` best (0: all) stay, by the sum of their
     ``group_best`` (1 or 2) best experts.  Equal values go to the lower index; an expert with logit -inf is
     never chosen, and slots without one hold -1 and weight 0.  ``renorm`` divides the weights by their sum."""
-    o = _route_opts(logits, score, renorm, scale, bias, groups, keep_groups, group_best)
-    T, E = logits.shape
-    _tensor(experts, "experts", (torch.int32,), 2)
-    k = experts.shape[1]
-    _check(_lib.ts_moe_route(logits.data_ptr(), _dense(experts, "experts", torch.int32, (T, k)),
-                             _dense(weights, "weights", torch.float32, (T, k)), T, E, k, _OUT[logits.dtype], o,
-                             _stream_handle(stream)))
+    dtype, (T, E), ldx = _matrix_of(logits, "logits", _OUT)
+    k = experts.shape[-1]
+    o = RouteOpts(_dense(bias, "bias", _F32, (E,)) if bias is not None else 0, _score(score), groups, keep_groups,
+                  group_best, 0 if renorm else 1, scale, 0, ldx, 0)
+    st = _lib.ts_moe_route(logits.data_ptr(), _dense(experts, "experts", _I32, (T, k)),
+                           _dense(weights, "weights", _F32, (T, k)), T, E, k, dtype, o, _stream_of(stream))
+    if st:
+        _check(st)
 
 
 def ts_moe_route_grad(logits: torch.Tensor, experts: torch.Tensor, grad_weights: torch.Tensor,
                       grad_logits: torch.Tensor, score="softmax", renorm=True, scale=1.0, stream=None) -> None:
     """grad_logits [T, E] (the logits' type) from grad_weights [T, k], for the experts that ts_moe_route chose."""
-    o = _route_opts(logits, score, renorm, scale)
-    T, E = logits.shape
-    _tensor(experts, "experts", (torch.int32,), 2)
-    k = experts.shape[1]
-    _tensor(grad_logits, "grad_logits", (logits.dtype,), 2)
-    if tuple(grad_logits.shape) != (T, E):
+    dtype, (T, E), ldx = _matrix_of(logits, "logits", _OUT)
+    k = experts.shape[-1]
+    g_dtype, g_shape, ldg = _matrix_of(grad_logits, "grad_logits", _OUT)
+    if g_dtype != dtype:
+        raise TypeError("grad_logits must have the logits' type")
+    if g_shape[0] != T or g_shape[1] != E:
         raise ValueError(f"grad_logits must be {(T, E)}")
-    o.ldg = _rows_of(grad_logits, "grad_logits")
-    _check(_lib.ts_moe_route_grad(logits.data_ptr(), _dense(experts, "experts", torch.int32, (T, k)),
-                                  _dense(grad_weights, "grad_weights", torch.float32, (T, k)), grad_logits.data_ptr(),
-                                  T, E, k, _OUT[logits.dtype], o, _stream_handle(stream)))
+    o = RouteOpts(0, _score(score), 1, 0, 1, 0 if renorm else 1, scale, 0, ldx, ldg)
+    st = _lib.ts_moe_route_grad(logits.data_ptr(), _dense(experts, "experts", _I32, (T, k)),
+                                _dense(grad_weights, "grad_weights", _F32, (T, k)), grad_logits.data_ptr(), T, E, k,
+                                dtype, o, _stream_of(stream))
+    if st:
+        _check(st)
 
 
 def ts_moe_plan_workspace(slots: int, experts: int) -> int:
@@ -746,54 +763,59 @@ def ts_moe_plan(experts: torch.Tensor, offsets: torch.Tensor, order: torch.Tenso
     many slots need is allocated here unless one is passed."""
     n = experts.numel()
     E = offsets.numel() - 1
-    _tensor(experts, "experts", (torch.int32,), experts.dim())
+    shape = experts.shape
+    ptr = size = 0
     need = _lib.ts_moe_plan_workspace(n, E)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=experts.device)
-    if workspace is not None and (not workspace.is_cuda or not workspace.is_contiguous()):
-        raise TypeError("workspace must be a contiguous CUDA tensor")
-    ptr, size = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else (0, 0)
-    _check(_lib.ts_moe_plan(_dense(experts, "experts", torch.int32, experts.shape),
-                            _dense(offsets, "offsets", torch.int64, (E + 1,)),
-                            _dense(order, "order", torch.int32, (n,)),
-                            _dense(position, "position", torch.int32, experts.shape), n, E, ptr, size,
-                            _stream_handle(stream)))
+    if workspace is not None:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise TypeError("workspace must be a contiguous CUDA tensor")
+        ptr, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = _lib.ts_moe_plan(_dense(experts, "experts", _I32, shape), _dense(offsets, "offsets", _I64, (E + 1,)),
+                          _dense(order, "order", _I32, (n,)), _dense(position, "position", _I32, shape), n, E, ptr,
+                          size, _stream_of(stream))
+    if st:
+        _check(st)
 
 
 def ts_moe_combine(y: torch.Tensor, position: torch.Tensor, out: torch.Tensor, weights=None, stream=None) -> None:
     """out[t] = sum_j weights[t, j] * y[position[t, j]] over the slots with position >= 0 (weights None: 1).
 
     y [R, N] and out [T, N] are both bf16 or both fp32; position [T, k] int32; weights [T, k] fp32."""
-    _tensor(y, "y", _OUT, 2)
-    _tensor(out, "out", (y.dtype,), 2)
-    _tensor(position, "position", (torch.int32,), 2)
-    T, k = position.shape
-    R, N = y.shape
-    if tuple(out.shape) != (T, N):
+    dtype, (R, N), ldy = _matrix_of(y, "y", _OUT)
+    o_dtype, o_shape, ldo = _matrix_of(out, "out", _OUT)
+    if o_dtype != dtype:
+        raise TypeError("out must have y's type")
+    T, k = o_shape[0], position.shape[-1]
+    if o_shape[1] != N:
         raise ValueError(f"out must be {(T, N)}")
-    w = _dense(weights, "weights", torch.float32, (T, k)) if weights is not None else 0
-    _check(_lib.ts_moe_combine(y.data_ptr(), _dense(position, "position", torch.int32, (T, k)), w, out.data_ptr(), T,
-                               k, N, R, _OUT[y.dtype], _rows_of(y, "y"), _rows_of(out, "out"), _stream_handle(stream)))
+    st = _lib.ts_moe_combine(y.data_ptr(), _dense(position, "position", _I32, (T, k)),
+                             _dense(weights, "weights", _F32, (T, k)) if weights is not None else 0, out.data_ptr(), T,
+                             k, N, R, dtype, ldy, ldo, _stream_of(stream))
+    if st:
+        _check(st)
 
 
 def ts_moe_combine_grad(grad_out: torch.Tensor, y: torch.Tensor, position: torch.Tensor, weights, grad_y: torch.Tensor,
                         grad_weights=None, stream=None) -> None:
     """The gradient of ts_moe_combine: grad_y[position[t, j]] = weights[t, j] * grad_out[t] and
     grad_weights[t, j] = <grad_out[t], y[position[t, j]]>; rows of grad_y that no slot takes are not written."""
-    _tensor(y, "y", _OUT, 2)
-    _tensor(grad_out, "grad_out", (y.dtype,), 2)
-    _tensor(grad_y, "grad_y", (y.dtype,), 2)
-    _tensor(position, "position", (torch.int32,), 2)
-    T, k = position.shape
-    R, N = y.shape
-    if tuple(grad_out.shape) != (T, N) or tuple(grad_y.shape) != (R, N):
+    dtype, (R, N), ldy = _matrix_of(y, "y", _OUT)
+    o_dtype, o_shape, ldo = _matrix_of(grad_out, "grad_out", _OUT)
+    g_dtype, g_shape, ldg = _matrix_of(grad_y, "grad_y", _OUT)
+    if o_dtype != dtype or g_dtype != dtype:
+        raise TypeError("grad_out and grad_y must have y's type")
+    T, k = o_shape[0], position.shape[-1]
+    if o_shape[1] != N or g_shape != y.shape:
         raise ValueError(f"grad_out must be {(T, N)} and grad_y {(R, N)}")
-    w = _dense(weights, "weights", torch.float32, (T, k)) if weights is not None else 0
-    gw = _dense(grad_weights, "grad_weights", torch.float32, (T, k)) if grad_weights is not None else 0
-    _check(_lib.ts_moe_combine_grad(grad_out.data_ptr(), y.data_ptr(),
-                                    _dense(position, "position", torch.int32, (T, k)), w, grad_y.data_ptr(), gw, T, k,
-                                    N, R, _OUT[y.dtype], _rows_of(y, "y"), _rows_of(grad_out, "grad_out"),
-                                    _rows_of(grad_y, "grad_y"), _stream_handle(stream)))
+    st = _lib.ts_moe_combine_grad(grad_out.data_ptr(), y.data_ptr(), _dense(position, "position", _I32, (T, k)),
+                                  _dense(weights, "weights", _F32, (T, k)) if weights is not None else 0,
+                                  grad_y.data_ptr(),
+                                  _dense(grad_weights, "grad_weights", _F32, (T, k)) if grad_weights is not None else 0,
+                                  T, k, N, R, dtype, ldy, ldo, ldg, _stream_of(stream))
+    if st:
+        _check(st)
 
 
 def ts_spin(ctas: int, duration_ns: int, started: torch.Tensor, stream=None) -> None:

@@ -17,6 +17,9 @@ namespace {
 constexpr int64_t kMaxDim = 0x7fffffffLL;
 constexpr double kDefaultTimeoutS = 2.0;
 constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
+// K split over a cluster: at most the portable cluster size, and not below this many
+// blocks each (a split costs an exchange of partial sums, some 2 us).
+constexpr int64_t kMaxSplit = 8, kMinSplitBlocks = 4;
 constexpr int kRasterGroup = 8;  // tile rows of a raster band, as the bf16 product's default
 
 // K = 0: the rows of D (grouped: of group blockIdx.y) are empty sums.
@@ -126,16 +129,30 @@ ts_status fp8_product(const void *A, const float *SA, const void *B, const float
 
     const int sms = device_sms(current_device());
     if (sms <= 0) return fail(TS_ERR_CUDA, "cannot query the SM count");
+    const int64_t sms_ = sms;  // 64-bit for the products below
+    // K split over a cluster for a product of `units` 128x128 tiles
+    auto split_of = [&](int64_t units) {
+        return std::max<int64_t>(
+            1, std::min<int64_t>(std::min<int64_t>(kMaxSplit, sms_ / std::max<int64_t>(units, 1)), kblocks / kMinSplitBlocks));
+    };
     int tile = o->tile;
-    if (tile == TS_TILE_AUTO) {
-        // the largest tile that still gives every SM work
-        const int64_t g = grouped ? groups : 1, rows_each = cdiv(M, g);
-        if (cdiv(rows_each, 256) * cdiv(N, 256) * g * 2 >= sms)
-            tile = TS_TILE_256x256_2CTA;
-        else if (cdiv(rows_each, 128) * cdiv(N, 256) * g >= sms)
-            tile = TS_TILE_128x256;
-        else
-            tile = TS_TILE_128x128;
+    if (tile == TS_TILE_AUTO && grouped) {
+        // By the mean rows of a group.  Measured, 32 groups of 4096 x 2048, 128x128 /
+        // 128x256 / pair: 32 rows each 49 / 51 / 60 us, 128 62 / 61 / 70, 256 92 / 85 / 91,
+        // 512 157 / 138 / 143.
+        const int64_t mean = M / groups;
+        tile = mean >= 1024 ? TS_TILE_256x256_2CTA : mean >= 96 ? TS_TILE_128x256 : TS_TILE_128x128;
+    } else if (tile == TS_TILE_AUTO) {
+        // The tile with the fewest cycles: waves of workers times what a K block of a tile
+        // takes (the measured steady state; a pair's tiles pay from the second wave on, by
+        // their smaller L2 traffic).  Measured, N = K = 4096, the same order: M = 512 11.4
+        // / 15.9 / 16.9 us, 1024 19.7 / 18.0 / 18.0, 2048 35.7 / 31.4 / 31.0.
+        const int64_t u1 = cdiv(M, 128) * cdiv(N, 128), u2 = cdiv(M, 128) * cdiv(N, 256),
+                      u3 = cdiv(M, 256) * cdiv(N, 256), s1 = split_of(u1);
+        const int64_t c1 = cdiv(u1, sms_) * cdiv(kblocks, s1) * (rows ? 700 : 430) + (s1 > 1 ? 3000 : 0);
+        const int64_t c2 = cdiv(u2, sms_) * kblocks * (rows ? 1300 : 740);
+        const int64_t w3 = cdiv(u3, sms_ / 2), c3 = w3 * kblocks * (rows ? 1400 : w3 > 1 ? 720 : 770);
+        tile = c1 <= c2 && c1 <= c3 ? TS_TILE_128x128 : c2 <= c3 ? TS_TILE_128x256 : TS_TILE_256x256_2CTA;
     }
     const int bn = tile == TS_TILE_128x128 ? 128 : 256, cg = tile == TS_TILE_256x256_2CTA ? 2 : 1;
     const Fp8Variant *v = find_fp8(bn, cg, rows, grouped);
@@ -179,6 +196,10 @@ ts_status fp8_product(const void *A, const float *SA, const void *B, const float
     p.tiles_n = static_cast<int32_t>(tiles_n);
     p.num_kb = static_cast<int32_t>(kblocks);
     p.num_units = static_cast<int32_t>(units);
+    // Few tiles: a cluster of CTAs shares each tile's K blocks, so that the operands (a
+    // single token's weights) stream through the whole GPU.  1 x 4096 x 8192: 19.8 us
+    // without, 12.6 with four CTAs a tile.
+    p.split = !grouped && tile == TS_TILE_128x128 ? static_cast<int32_t>(split_of(units)) : 1;
     p.raster_group = kRasterGroup;
     p.div_group_tiles = fast_div_for(kRasterGroup * tiles_n);
     p.div_group_rows = fast_div_for(kRasterGroup);
@@ -210,7 +231,8 @@ ts_status fp8_product(const void *A, const float *SA, const void *B, const float
     p.status = status;
     int64_t workers = std::min<int64_t>(units, sms / cg);
     if (o->max_workers > 0) workers = std::min<int64_t>(workers, o->max_workers);
-    L.grid = workers * cg;
+    L.grid = p.split > 1 ? units * p.split : workers * cg;
+    L.cluster = p.split > 1 ? p.split : cg;
     L.stream = st;
     cudaError_t e = v->launch(L);
     return e == cudaSuccess ? TS_OK : cuda_fail(e, "8-bit product launch");

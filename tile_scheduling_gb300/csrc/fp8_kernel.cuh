@@ -53,6 +53,7 @@ struct Fp8Cfg {
     // j / 4 = h read slot h of the K block whole; on a CTA pair its MMA takes 64 rows of B
     // from each CTA's tile, so its two 64-column segments lie 128 columns apart.
     static constexpr int SC = SC_;
+    static constexpr bool SPLIT = BN == 128 && CG == 1 && !GROUPED;  // K may be split over a cluster
     static constexpr int SLOTS = 512 / SC;
     static constexpr int H = BN / SC;
     static constexpr int COLS = BN / 2;  // columns of one promotion warp
@@ -94,6 +95,15 @@ struct Fp8Cfg {
 __device__ __forceinline__ uint64_t sw128_nmajor_desc(uint32_t smem_addr) {
     return uint64_t((smem_addr & 0x3FFFFu) >> 4) | (uint64_t(16384 >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
            (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+constexpr int kMaxCluster = 8;
+
+// Where four columns (group g) of row r lie among a CTA's partial sums: rows next to
+// each other for the writers (a lane a row), and the rows of eight groups apart for
+// the readers (a lane a group), so that neither meets bank conflicts.
+__device__ __forceinline__ uint32_t partial_at(int32_t g, int32_t r) {
+    return static_cast<uint32_t>(g * 128 + (r ^ (g & 7))) * 16u;
 }
 
 // One work unit: an output tile.
@@ -227,8 +237,19 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     if constexpr (GROUPED) num_units = prefix[p.groups];
-    const int32_t first = static_cast<int32_t>(blockIdx.x) / CG;
+    int32_t first = static_cast<int32_t>(blockIdx.x) / CG;
     const int32_t step = static_cast<int32_t>(gridDim.x) / CG;
+    // K blocks [kb0, kb0 + num_kb) of every unit; split over a cluster, this CTA's share of
+    // its one unit (step is then at least the number of units)
+    int32_t kb0 = 0, num_kb = p.num_kb, part = 0;
+    if constexpr (C::SPLIT) {
+        if (p.split > 1) {
+            part = static_cast<int32_t>(cluster_ctarank());
+            first = static_cast<int32_t>(blockIdx.x) / p.split;
+            kb0 = static_cast<int32_t>(static_cast<int64_t>(part) * p.num_kb / p.split);
+            num_kb = static_cast<int32_t>(static_cast<int64_t>(part + 1) * p.num_kb / p.split) - kb0;
+        }
+    }
 
     if (warp < kRoleWarps) {
     if constexpr (C::SHIFT_REGS) regs_dec<C::ROLE_REGS>();
@@ -242,7 +263,7 @@ __global__ void __launch_bounds__(384, 1)
                 const Fp8Unit w = fp8_unit<C>(u, p, prefix);
                 const int32_t a_row = w.row0 + static_cast<int32_t>(rank) * C::BM;
                 const int32_t b_row = w.col0 + static_cast<int32_t>(rank) * C::B_ROWS;
-                for (int32_t kb = 0; kb < p.num_kb; ++kb) {
+                for (int32_t kb = 0; kb < num_kb; ++kb) {
                     if (!wait_phase(empty(stage), phase ^ 1u, abort_flag, p, WAIT_PRODUCER_EMPTY)) {
                         alive = false;
                         break;
@@ -251,7 +272,7 @@ __global__ void __launch_bounds__(384, 1)
                     const uint32_t da = s_a + stage * C::A_BYTES;
                     const uint32_t db = s_b + stage * C::B_BYTES;
                     const uint32_t fb = CG == 2 ? mapa(full(stage), 0) : full(stage);
-                    const int32_t k = kb * C::BK;
+                    const int32_t k = (kb0 + kb) * C::BK;
                     auto load_b = [&](uint32_t dst, int32_t x, int32_t y) {
                         if constexpr (CG == 1)
                             tma_load_3d(dst, &tmB, fb, x, y, w.group);
@@ -311,7 +332,7 @@ __global__ void __launch_bounds__(384, 1)
             uint32_t stage = 0, phase = 0, slot = 0, slot_phase = 0;
             bool alive = true;
             for (int32_t u = first; u < num_units && alive; u += step) {
-                for (int32_t kb = 0; kb < p.num_kb && alive; ++kb) {
+                for (int32_t kb = 0; kb < num_kb && alive; ++kb) {
                     if (!wait_phase(full(stage), phase, abort_flag, p, WAIT_MMA_FULL)) {
                         alive = false;
                         break;
@@ -379,12 +400,12 @@ __global__ void __launch_bounds__(384, 1)
         for (int32_t u = first; u < num_units && alive; u += step) {
             const Fp8Unit w = fp8_unit<C>(u, p, prefix);
             const int32_t row = w.row0 + static_cast<int32_t>(rank) * C::BM + lane;
-            const float *pa = p.sa + static_cast<int64_t>(row) * p.sa_row;
+            const float *pa = p.sa + static_cast<int64_t>(row) * p.sa_row + kb0 * p.sa_blk;
             // this lane's first column (ROWS) or block of columns
             const int32_t n = w.col0 + (ROWS ? 1 : kScaleBlock) * lane;
             const bool has_b = ROWS || lane < BN / 128;
-            const float *pb = p.sb + w.group * p.sb_group + static_cast<int64_t>(ROWS ? n : n / kScaleBlock) * p.sb_n;
-            for (int32_t kb = 0; kb < p.num_kb; ++kb) {
+            const float *pb = p.sb + w.group * p.sb_group + static_cast<int64_t>(ROWS ? n : n / kScaleBlock) * p.sb_n + kb0 * p.sb_k;
+            for (int32_t kb = 0; kb < num_kb; ++kb) {
                 const uint32_t buf = chunk % C::CHUNKS;
                 if (kb % C::CHUNK == 0) {
                     const bool ok = wait_inline(sempty(buf), ((chunk / C::CHUNKS) & 1u) ^ 1u, abort_flag, p, WAIT_SCALES);
@@ -406,7 +427,7 @@ __global__ void __launch_bounds__(384, 1)
                     copy_async_f32(at + 512, n < p.N ? pb : p.sb, n < p.N);
                 }
                 pb += p.sb_k;
-                if (kb % C::CHUNK == C::CHUNK - 1 || kb + 1 == p.num_kb) {
+                if (kb % C::CHUNK == C::CHUNK - 1 || kb + 1 == num_kb) {
                     copy_async_arrive(sfull(buf));
                     ++chunk;
                 }
@@ -438,7 +459,7 @@ __global__ void __launch_bounds__(384, 1)
             uint64_t sum[C::COLS / 2];
 #pragma unroll
             for (int i = 0; i < C::COLS / 2; ++i) sum[i] = 0ull;
-            for (int32_t kb = 0; kb < p.num_kb; ++kb) {
+            for (int32_t kb = 0; kb < num_kb; ++kb) {
                 if (kb % C::CHUNK == 0) {
                     const bool ok = wait_inline(sfull(chunk % C::CHUNKS), (chunk / C::CHUNKS) & 1u, abort_flag, p, WAIT_SCALES);
                     if (!__all_sync(0xffffffffu, ok)) {
@@ -457,7 +478,7 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 // the chunk is read: back to the scale warp
                 auto chunk_done = [&] {
-                    if (kb % C::CHUNK == C::CHUNK - 1 || kb + 1 == p.num_kb) {
+                    if (kb % C::CHUNK == C::CHUNK - 1 || kb + 1 == num_kb) {
                         __syncwarp();
                         if (lane == 0) mbar_arrive(sempty(chunk % C::CHUNKS));
                         ++chunk;
@@ -509,6 +530,21 @@ __global__ void __launch_bounds__(384, 1)
                 if (ROWS) chunk_done();
             }
             if (!alive || !work) continue;
+            if constexpr (C::SPLIT) {
+                if (p.split > 1) {
+                    // the partial sums go to shared memory (the ring has been read), for the
+                    // cluster's reduction below: four columns of a row per 16 bytes
+#pragma unroll
+                    for (int i = 0; i < C::COLS / 4; ++i) {
+                        const int g = C::COLS / 4 * h + i, r = 32 * q + lane;
+                        uint32_t x0, x1, x2, x3;
+                        unpair(sum[2 * i], x0, x1);
+                        unpair(sum[2 * i + 1], x2, x3);
+                        st_shared_v4(s_a + partial_at(g, r), x0, x1, x2, x3);
+                    }
+                    continue;
+                }
+            }
             // Store the tile part: 64-byte wide subtiles through swizzled staging and a TMA
             // store where the subtile lies inside D (and, grouped, inside the group), else
             // each lane its own row.
@@ -578,6 +614,61 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
     }
 
+    if constexpr (C::SPLIT) {
+        if (p.split > 1) {
+            // Every CTA sums a share of the tile over the cluster's partial sums, in the
+            // order of their K blocks, so results do not depend on timing.
+            __syncwarp();
+            cluster_sync();
+            const Fp8Unit w = fp8_unit<C>(first, p, prefix);
+            const int32_t rows = min(w.row_end - w.row0, C::BM);
+            for (int32_t i = part * C::THREADS + static_cast<int32_t>(threadIdx.x); i < rows * (BN / 4);
+                 i += p.split * C::THREADS) {
+                const int32_t r = i / (BN / 4), g = i % (BN / 4);
+                const int32_t col = w.col0 + 4 * g;
+                if (col >= p.N) continue;
+                float4 x[kMaxCluster];
+#pragma unroll
+                for (int c = 0; c < kMaxCluster; ++c)
+                    if (c < p.split) x[c] = ld_cluster_f32x4(mapa(s_a + partial_at(g, r), c));
+                float4 t = x[0];
+#pragma unroll
+                for (int c = 1; c < kMaxCluster; ++c)
+                    if (c < p.split) {
+                        t.x += x[c].x;
+                        t.y += x[c].y;
+                        t.z += x[c].z;
+                        t.w += x[c].w;
+                    }
+                const int64_t at = static_cast<int64_t>(w.row0 + r) * p.ldd + col;
+                const bool whole = p.vec_store && col + 4 <= p.N;
+                const float f[4] = {t.x, t.y, t.z, t.w};
+                if (p.out == OUT_F32) {
+                    float *dst = static_cast<float *>(p.D) + at;
+                    if (whole) {
+                        *reinterpret_cast<float4 *>(dst) = t;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (col + k < p.N) dst[k] = f[k];
+                    }
+                } else {
+                    uint16_t *dst = static_cast<uint16_t *>(p.D) + at;
+                    const uint2 o = make_uint2(pack_bf16x2(__float_as_uint(t.x), __float_as_uint(t.y)),
+                                               pack_bf16x2(__float_as_uint(t.z), __float_as_uint(t.w)));
+                    if (whole) {
+                        *reinterpret_cast<uint2 *>(dst) = o;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (col + k < p.N) dst[k] = static_cast<uint16_t>((k < 2 ? o.x : o.y) >> (16 * (k & 1)));
+                    }
+                }
+            }
+            __syncwarp();
+            cluster_sync();  // no CTA leaves while another reads its partial sums
+        }
+    }
     tc_fence_before();
     if constexpr (CG == 2)
         cluster_sync();

@@ -16,6 +16,7 @@ struct Fp8Params {
     int32_t M, N, K;
     int32_t tiles_m, tiles_n, num_kb;  // tiles_m and num_units: plain product only
     int32_t num_units;
+    int32_t split;      // CTAs of a cluster that share a tile's K blocks (1: none; plain 128x128 tiles only)
     int32_t raster_group;
     FastDiv div_group_tiles, div_group_rows, div_last_rows;
     int32_t trans_b;    // 1: B is [K][N]
@@ -41,6 +42,7 @@ struct Fp8Launch {
     CUtensorMap a, b, d;
     Fp8Params p;
     int64_t grid;
+    int cluster;  // CTAs of a cluster
     cudaStream_t stream;
 };
 
