@@ -15,8 +15,7 @@ namespace ts {
 namespace {
 
 constexpr int64_t kMaxDim = 0x7fffffffLL;
-constexpr int kThreads = 256;
-constexpr int kSlots = 8;  // slots whose rows are in flight together
+constexpr int kThreads = 256, kGradThreads = 512, kGradSlots = 4;
 
 struct CombineParams {
     const void *y, *grad_out;
@@ -34,32 +33,29 @@ struct CombineParams {
 template <class T>
 constexpr int kVec = 16 / sizeof(T);
 
+// kVec values at x as they lie in memory; those past n (the row's end) read as 0.
 template <class T>
-__device__ __forceinline__ void load_vec(const T *x, bool vec, int64_t n, float (&v)[kVec<T>]) {
-    if (vec && n >= kVec<T>) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x));
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ uint4 load_raw(const T *x, bool vec, int64_t n) {
+    if (vec && n >= kVec<T>) return __ldcs(reinterpret_cast<const uint4 *>(x));
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (sizeof(T) == 4) {
-                v[i] = __uint_as_float(w[i]);
-            } else {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kVec<T>; ++i) {
-            v[i] = 0.f;
-            if (i < n) {
-                if constexpr (sizeof(T) == 4)
-                    v[i] = x[i];
-                else
-                    v[i] = __uint_as_float(uint32_t(x[i]) << 16);
-            }
+    for (int i = 0; i < kVec<T>; ++i) {
+        if (i < n) {
+            if constexpr (sizeof(T) == 4)
+                w[i] = __float_as_uint(x[i]);
+            else
+                w[i >> 1] |= uint32_t(x[i]) << (16 * (i & 1));
         }
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Value i of a raw vector as fp32.
+template <class T>
+__device__ __forceinline__ float value_at(const uint4 &a, int i) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
 }
 
 template <class T>
@@ -102,91 +98,100 @@ __device__ __forceinline__ int32_t slot_row(const CombineParams &p, int64_t t, i
     return at;
 }
 
-template <class T>
+// One CTA per token and kThreads vectors of its row.  KS: slots whose rows are in
+// flight together (raw, four registers each, so that several CTAs fit an SM).
+template <class T, int KS>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant__ CombineParams p) {
     grid_dep_wait();
     grid_dep_launch();
     constexpr int V = kVec<T>;
     const int64_t t = blockIdx.x;
-    const int64_t c = (static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x) * V;
+    const int64_t c = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * V;
     float sum[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) sum[i] = 0.f;
-    for (int32_t j0 = 0; j0 < p.k; j0 += kSlots) {
-        float v[kSlots][V], w[kSlots];
-        bool has[kSlots];
+    for (int32_t j0 = 0; j0 < p.k; j0 += KS) {
+        uint4 v[KS];
+        float w[KS];
+        int32_t at[KS];
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
-            const int32_t at = slot_row(p, t, j0 + j);
-            has[j] = at >= 0;
-            w[j] = at >= 0 && p.w ? p.w[t * p.k + j0 + j] : 1.f;
-            load_vec(static_cast<const T *>(p.y) + (at >= 0 ? at : 0) * p.ldy + c, p.vec, at >= 0 ? p.N - c : 0, v[j]);
+        for (int j = 0; j < KS; ++j) {
+            at[j] = slot_row(p, t, j0 + j);
+            w[j] = at[j] >= 0 && p.w ? p.w[t * p.k + j0 + j] : 1.f;
         }
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j)
-            if (has[j]) {
+        for (int j = 0; j < KS; ++j)
+            if (at[j] >= 0) v[j] = load_raw(static_cast<const T *>(p.y) + at[j] * p.ldy + c, p.vec, p.N - c);
 #pragma unroll
-                for (int i = 0; i < V; ++i) sum[i] = fmaf(w[j], v[j][i], sum[i]);
+        for (int j = 0; j < KS; ++j)
+            if (at[j] >= 0) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum[i] = fmaf(w[j], value_at<T>(v[j], i), sum[i]);
             }
     }
     if (c < p.N) store_vec(static_cast<T *>(p.out) + t * p.ldo + c, p.vec, p.N - c, sum);
 }
 
-// One CTA per token: grad_out's row is read for each group of kSlots slots (from
-// L2 after the first), the slots' dot products are reduced in fixed order.
+// One CTA per token: grad_out's row is read for each group of four slots (from L2
+// after the first; eight at once would leave room for one CTA on an SM), the slots' dot products are reduced in fixed order.
 template <class T>
-__global__ void __launch_bounds__(kThreads) combine_grad_kernel(const __grid_constant__ CombineParams p) {
-    __shared__ float part[kSlots][kThreads / 32];
+__global__ void __launch_bounds__(kGradThreads, 2) combine_grad_kernel(const __grid_constant__ CombineParams p) {
+    __shared__ float part[kGradSlots][kGradThreads / 32];
     grid_dep_wait();
     grid_dep_launch();
-    constexpr int V = kVec<T>;
+    constexpr int V = kVec<T>, KS = kGradSlots;
     const int64_t t = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int32_t j0 = 0; j0 < p.k; j0 += kSlots) {
-        int32_t at[kSlots];
-        float w[kSlots], dot[kSlots];
+    for (int32_t j0 = 0; j0 < p.k; j0 += KS) {
+        int32_t at[KS];
+        float w[KS], dot[KS];
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
+        for (int j = 0; j < KS; ++j) {
             at[j] = slot_row(p, t, j0 + j);
             w[j] = at[j] >= 0 && p.w ? p.w[t * p.k + j0 + j] : 1.f;
             dot[j] = 0.f;
         }
-        for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < p.N; c += kThreads * V) {
-            float g[V];
-            load_vec(static_cast<const T *>(p.grad_out) + t * p.ldo + c, p.vec, p.N - c, g);
-            float y[kSlots][V];
+#pragma unroll 1
+        for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < p.N; c += static_cast<int64_t>(blockDim.x) * V) {
+            uint4 y[KS];
+            const uint4 g = load_raw(static_cast<const T *>(p.grad_out) + t * p.ldo + c, p.vec, p.N - c);
 #pragma unroll
-            for (int j = 0; j < kSlots; ++j)
-                if (at[j] >= 0) load_vec(static_cast<const T *>(p.y) + at[j] * p.ldy + c, p.vec, p.N - c, y[j]);
+            for (int j = 0; j < KS; ++j)
+                if (at[j] >= 0) y[j] = load_raw(static_cast<const T *>(p.y) + at[j] * p.ldy + c, p.vec, p.N - c);
 #pragma unroll
-            for (int j = 0; j < kSlots; ++j) {
+            for (int j = 0; j < KS; ++j) {
                 if (at[j] < 0) continue;
                 float o[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    dot[j] = fmaf(g[i], y[j][i], dot[j]);
-                    o[i] = w[j] * g[i];
+                    const float x = value_at<T>(g, i);
+                    dot[j] = fmaf(x, value_at<T>(y[j], i), dot[j]);
+                    o[i] = w[j] * x;
                 }
                 store_vec(static_cast<T *>(p.grad_y) + at[j] * p.ldg + c, p.vec, p.N - c, o);
             }
         }
         if (p.grad_w) {
 #pragma unroll
-            for (int j = 0; j < kSlots; ++j) {
+            for (int j = 0; j < KS; ++j) {
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
                 if (lane == 0) part[j][warp] = dot[j];
             }
             __syncthreads();
-            if (threadIdx.x < kSlots && j0 + static_cast<int>(threadIdx.x) < p.k) {
+            if (threadIdx.x < KS && j0 + static_cast<int>(threadIdx.x) < p.k) {
                 float s = 0.f;
-#pragma unroll
-                for (int i = 0; i < kThreads / 32; ++i) s += part[threadIdx.x][i];
+                for (unsigned i = 0; i < blockDim.x / 32; ++i) s += part[threadIdx.x][i];
                 p.grad_w[t * p.k + j0 + threadIdx.x] = s;  // 0 for a dropped slot
             }
             __syncthreads();
         }
     }
+}
+
+// Threads of a CTA: the row's vectors, in warps, up to `most`.
+int cta_threads(int64_t N, int per, int most) {
+    return static_cast<int>(std::min<int64_t>(most, cdiv(cdiv(N, per), 32) * 32));
 }
 
 bool row16(const void *x, int64_t ld, int esize) {
@@ -241,12 +246,13 @@ ts_status ts_moe_combine(const void *y, const int32_t *position, const float *we
     p.ldo = ldo;
     p.k = top_k;
     p.vec = row16(y, ldy, esize) && row16(out, ldo, esize);
-    const int64_t per_cta = kThreads * (16 / esize);
-    if (cdiv(N, per_cta) > 65535) return fail(TS_ERR_UNSUPPORTED, "rows of %lld values", static_cast<long long>(N));
-    const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(cdiv(N, per_cta)));
+    const int per = 16 / esize, threads = cta_threads(N, per, kThreads);
+    if (cdiv(N, threads * per) > 65535) return fail(TS_ERR_UNSUPPORTED, "rows of %lld values", static_cast<long long>(N));
+    const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(cdiv(N, threads * per))), block(threads);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = dtype == TS_OUT_F32 ? launch_pdl(combine_kernel<float>, grid, dim3(kThreads), 0, st, p)
-                                        : launch_pdl(combine_kernel<uint16_t>, grid, dim3(kThreads), 0, st, p);
+    auto go = [&](auto *k4, auto *k8) { return launch_pdl(top_k <= 4 ? k4 : k8, grid, block, 0, st, p); };
+    cudaError_t e = dtype == TS_OUT_F32 ? go(combine_kernel<float, 4>, combine_kernel<float, 8>)
+                                        : go(combine_kernel<uint16_t, 4>, combine_kernel<uint16_t, 8>);
     return e == cudaSuccess ? TS_OK : cuda_fail(e, "combine launch");
 }
 
@@ -290,10 +296,10 @@ ts_status ts_moe_combine_grad(const void *grad_out, const void *y, const int32_t
     p.ldg = ldg;
     p.k = top_k;
     p.vec = row16(y, ldy, esize) && row16(grad_out, ldo, esize) && row16(grad_y, ldg, esize);
-    const dim3 grid(static_cast<unsigned>(T));
+    const dim3 grid(static_cast<unsigned>(T)), block(cta_threads(std::max<int64_t>(N, 1), 16 / esize, kGradThreads));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = dtype == TS_OUT_F32 ? launch_pdl(combine_grad_kernel<float>, grid, dim3(kThreads), 0, st, p)
-                                        : launch_pdl(combine_grad_kernel<uint16_t>, grid, dim3(kThreads), 0, st, p);
+    cudaError_t e = dtype == TS_OUT_F32 ? launch_pdl(combine_grad_kernel<float>, grid, block, 0, st, p)
+                                        : launch_pdl(combine_grad_kernel<uint16_t>, grid, block, 0, st, p);
     return e == cudaSuccess ? TS_OK : cuda_fail(e, "combine gradient launch");
 }
 

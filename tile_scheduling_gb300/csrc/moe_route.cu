@@ -357,9 +357,12 @@ ts_status route_check(RouteParams &p, const void *logits, int64_t T, int32_t E, 
 // kPlanSlots consecutive slots, a warp kWarpSlots of them in order; equal
 // experts of a warp's 32 slots rank by lane.
 constexpr int kPlanWarps = 16;
-constexpr int kWarpSlots = 128;
+constexpr int kWarpSlots = 64;
 constexpr int kPlanSlots = kPlanWarps * kWarpSlots;
-constexpr int kOneCtaSlots = 4 * kPlanSlots;  // up to here one CTA does it all
+constexpr int kOneCtaSlots = 2 * kPlanSlots;  // up to here one CTA does it all
+// Up to here every placing CTA sums the tiles' counts itself (two launches); past it
+// that would read tiles^2 * E counts and a kernel of its own does it (three).
+constexpr int kFusedTiles = 64;
 
 struct PlanParams {
     const int32_t *experts;
@@ -426,8 +429,20 @@ __device__ __forceinline__ void plan_place(const PlanParams &p, int64_t first, i
     __syncthreads();
 }
 
-// Exclusive sum over the experts of tot[e] into offsets and tot itself (one warp's work).
-__device__ __forceinline__ void plan_offsets(const PlanParams &p, int32_t *tot) {
+// Turns a tile's counts of expert e, per warp, into the first row of each warp's slots;
+// returns the row after the last.
+__device__ __forceinline__ int32_t plan_first_rows(const PlanParams &p, int32_t e, int32_t row, int32_t *hist) {
+    for (int w = 0; w < kPlanWarps; ++w) {
+        const int32_t n = hist[w * p.E + e];
+        hist[w * p.E + e] = row;
+        row += n;
+    }
+    return row;
+}
+
+// Exclusive sum over the experts of tot[e] into tot itself and, if `write`, offsets
+// (one warp's work).
+__device__ __forceinline__ void plan_offsets(const PlanParams &p, int32_t *tot, bool write) {
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
         int32_t run = 0;
@@ -442,12 +457,12 @@ __device__ __forceinline__ void plan_offsets(const PlanParams &p, int32_t *tot) 
             }
             if (e < p.E) {
                 tot[e] = run + v - own;
-                p.offsets[e] = run + v - own;
+                if (write) p.offsets[e] = run + v - own;
             }
             run += __shfl_sync(kAll, v, 31);
         }
         if (lane == 0) {
-            p.offsets[p.E] = run;
+            if (write) p.offsets[p.E] = run;
             tot[p.E] = run;
         }
     }
@@ -470,19 +485,11 @@ __global__ void __launch_bounds__(32 * kPlanWarps) plan_one_kernel(const __grid_
         }
         __syncthreads();
     }
-    plan_offsets(p, next);
+    plan_offsets(p, next, true);
     const int32_t valid = next[p.E];
     for (int32_t t = 0; t < p.tiles; ++t) {
         plan_count(p, static_cast<int64_t>(t) * kPlanSlots, hist, false);
-        for (int32_t e = threadIdx.x; e < p.E; e += blockDim.x) {
-            int32_t c = next[e];
-            for (int w = 0; w < kPlanWarps; ++w) {
-                const int32_t n = hist[w * p.E + e];
-                hist[w * p.E + e] = c;
-                c += n;
-            }
-            next[e] = c;
-        }
+        for (int32_t e = threadIdx.x; e < p.E; e += blockDim.x) next[e] = plan_first_rows(p, e, next[e], hist);
         __syncthreads();
         plan_place(p, static_cast<int64_t>(t) * kPlanSlots, hist);
     }
@@ -514,7 +521,7 @@ __global__ void __launch_bounds__(1024) plan_scan_kernel(const __grid_constant__
         tot[e] = c;
     }
     __syncthreads();
-    plan_offsets(p, tot);
+    plan_offsets(p, tot, true);
     if (e < p.E) {
         int32_t c = tot[e];
 #pragma unroll 8
@@ -526,23 +533,44 @@ __global__ void __launch_bounds__(1024) plan_scan_kernel(const __grid_constant__
     }
 }
 
+template <bool FUSED>
 __global__ void __launch_bounds__(32 * kPlanWarps) plan_place_kernel(const __grid_constant__ PlanParams p) {
     extern __shared__ int32_t smem[];
+    // FUSED: slots of each expert in all tiles, then its first row; and in the earlier tiles
+    __shared__ int32_t tot[FUSED ? kMaxRouteExperts + 1 : 1], before[FUSED ? kMaxRouteExperts : 1];
     grid_dep_wait();
     grid_dep_launch();
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kPlanSlots;
-    plan_count(p, first, smem, false);
-    for (int32_t e = threadIdx.x; e < p.E; e += blockDim.x) {
-        int32_t c = p.counts[static_cast<int64_t>(blockIdx.x) * p.E + e];
-        for (int w = 0; w < kPlanWarps; ++w) {
-            const int32_t n = smem[w * p.E + e];
-            smem[w * p.E + e] = c;
-            c += n;
+    if constexpr (FUSED) {
+        for (int32_t e = threadIdx.x; e < p.E; e += blockDim.x) tot[e] = before[e] = 0;
+        __syncthreads();
+        // the CTA's threads share the tiles of an expert, so that a few loads each, in flight
+        // together, cover them
+        const int32_t parts = max(static_cast<int32_t>(blockDim.x) / p.E, 1);
+        for (int32_t i = threadIdx.x; i < parts * p.E; i += blockDim.x) {
+            const int32_t e = i % p.E;
+            int32_t all = 0, bef = 0;
+#pragma unroll 8
+            for (int32_t t = i / p.E; t < p.tiles; t += parts) {
+                const int32_t n = p.counts[static_cast<int64_t>(t) * p.E + e];
+                if (t < static_cast<int32_t>(blockIdx.x)) bef += n;
+                all += n;
+            }
+            atomicAdd(&tot[e], all);
+            atomicAdd(&before[e], bef);
         }
+    }
+    plan_count(p, first, smem, false);
+    if constexpr (FUSED) {
+        plan_offsets(p, tot, blockIdx.x == 0);
+        for (int32_t e = threadIdx.x; e < p.E; e += blockDim.x) plan_first_rows(p, e, tot[e] + before[e], smem);
+    } else {
+        for (int32_t e = threadIdx.x; e < p.E; e += blockDim.x)
+            plan_first_rows(p, e, p.counts[static_cast<int64_t>(blockIdx.x) * p.E + e], smem);
     }
     __syncthreads();
     plan_place(p, first, smem);
-    const int64_t valid = p.offsets[p.E];
+    const int64_t valid = FUSED ? tot[p.E] : p.offsets[p.E];
     for (int64_t r = first + threadIdx.x; r < first + kPlanSlots && r < p.n; r += blockDim.x)
         if (r >= valid) p.order[r] = -1;
 }
@@ -625,7 +653,7 @@ ts_status ts_moe_plan(const int32_t *experts, int64_t *offsets, int32_t *order, 
     const size_t hist = static_cast<size_t>(kPlanWarps) * E * 4;
     // up to 1024 experts take 68 KB: above the default limit
     cudaError_t e = cudaSuccess;
-    for (auto *k : {plan_one_kernel, plan_count_kernel, plan_place_kernel})
+    for (auto *k : {plan_one_kernel, plan_count_kernel, plan_place_kernel<true>, plan_place_kernel<false>})
         if (e == cudaSuccess && hist + 4 * (E + 1) > 48 * 1024)
             e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      kPlanWarps * kMaxRouteExperts * 4 + 4 * (kMaxRouteExperts + 1));
@@ -634,8 +662,12 @@ ts_status ts_moe_plan(const int32_t *experts, int64_t *offsets, int32_t *order, 
     } else if (e == cudaSuccess) {
         const dim3 grid(static_cast<unsigned>(p.tiles));
         e = launch_pdl(plan_count_kernel, grid, block, hist, st, p);
-        if (e == cudaSuccess) e = launch_pdl(plan_scan_kernel, dim3(1), dim3(1024), 0, st, p);
-        if (e == cudaSuccess) e = launch_pdl(plan_place_kernel, grid, block, hist, st, p);
+        if (e == cudaSuccess && p.tiles <= kFusedTiles) {
+            e = launch_pdl(plan_place_kernel<true>, grid, block, hist, st, p);
+        } else if (e == cudaSuccess) {
+            e = launch_pdl(plan_scan_kernel, dim3(1), dim3(1024), 0, st, p);
+            if (e == cudaSuccess) e = launch_pdl(plan_place_kernel<false>, grid, block, hist, st, p);
+        }
     }
     return e == cudaSuccess ? TS_OK : cuda_fail(e, "plan launch");
 }

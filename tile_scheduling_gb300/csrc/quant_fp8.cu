@@ -18,6 +18,7 @@ namespace {
 constexpr int64_t kMaxDim = 0x7fffffffLL;
 constexpr int kBlk = 128;
 constexpr int kQThreads = 256;
+constexpr int kRowBlocks = 2;
 
 struct QuantParams {
     const void *x;
@@ -51,46 +52,51 @@ __device__ __forceinline__ uint32_t pack_f8x4(float a, float b, float c, float d
     return uint32_t(lo) | (uint32_t(hi) << 16);
 }
 
-// Eight values at x[i .. i + 8) as fp32; n: how many of them exist (the rest read as 0).
+// Eight values as they lie in memory (a bf16's stay packed: half the registers).
 template <class T>
-__device__ __forceinline__ void load8(const T *x, bool vec, int64_t n, float (&v)[8]) {
+struct Raw8 {
+    uint32_t w[2 * sizeof(T)];
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+};
+
+// x[0 .. 8); n: how many of them exist (the rest read as 0).
+template <class T>
+__device__ __forceinline__ Raw8<T> load8(const T *x, bool vec, int64_t n) {
+    Raw8<T> r;
     if (vec && n >= 8) {
-        if constexpr (sizeof(T) == 4) {
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(x));
-            const float4 b = __ldg(reinterpret_cast<const float4 *>(x) + 1);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        } else {
-            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x));
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
+        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x) + i);
+            r.w[4 * i] = a.x, r.w[4 * i + 1] = a.y, r.w[4 * i + 2] = a.z, r.w[4 * i + 3] = a.w;
         }
     } else {
 #pragma unroll
+        for (int i = 0; i < 2 * static_cast<int>(sizeof(T)); ++i) r.w[i] = 0u;
+#pragma unroll
         for (int i = 0; i < 8; ++i) {
-            v[i] = 0.f;
             if (i < n) {
                 if constexpr (sizeof(T) == 4)
-                    v[i] = x[i];
+                    r.w[i] = __float_as_uint(x[i]);
                 else
-                    v[i] = __uint_as_float(uint32_t(x[i]) << 16);
+                    r.w[i >> 1] |= uint32_t(x[i]) << (16 * (i & 1));
             }
         }
     }
+    return r;
 }
 
 // Row form.  Sixteen lanes take one block of one row, eight values each; a CTA
-// takes 16 rows and 8 blocks, so a warp reads whole 256-byte (bf16) runs.
-template <class T, bool E5M2>
+// takes 16 rows and BLOCKS blocks, so a warp reads whole 256-byte (bf16) runs.
+template <class T, bool E5M2, int BLOCKS>
 __global__ void __launch_bounds__(kQThreads) quant_rows_kernel(const __grid_constant__ QuantParams p) {
     grid_dep_wait();
     grid_dep_launch();
     const int part = threadIdx.x & 15;
     const int64_t r = static_cast<int64_t>(blockIdx.y) * 16 + (threadIdx.x >> 4);
-    const int64_t kb0 = static_cast<int64_t>(blockIdx.x) * 8;
+    const int64_t kb0 = static_cast<int64_t>(blockIdx.x) * BLOCKS;
     const int64_t blocks = (p.N + kBlk - 1) / kBlk;
     int64_t src = r;
     bool there = r < p.R;
@@ -109,23 +115,25 @@ __global__ void __launch_bounds__(kQThreads) quant_rows_kernel(const __grid_cons
         }
     }
     const T *const x = static_cast<const T *>(p.x) + (there ? src : 0) * p.ldx;
+    Raw8<T> v[BLOCKS];  // every load of this thread is in flight before the first is used
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < BLOCKS; ++i) {
+        const int64_t c = (kb0 + i) * kBlk + part * 8;
+        v[i] = load8(x + c, p.vec, there ? p.N - c : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < BLOCKS; ++i) {
         const int64_t kb = kb0 + i;
         const int64_t c = kb * kBlk + part * 8;
-        float v[8];
-        load8(x + c, p.vec, there ? p.N - c : 0, v);
         float a = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(v[j]));
+        for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(v[i][j]));
 #pragma unroll
         for (int d = 8; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
         a = fmaxf(a, 0x1p-100f);
         const float f = top_of(E5M2) / a;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= f;
-        const uint32_t lo = pack_f8x4<E5M2>(v[0], v[1], v[2], v[3]);
-        const uint32_t hi = pack_f8x4<E5M2>(v[4], v[5], v[6], v[7]);
+        const uint32_t lo = pack_f8x4<E5M2>(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f);
+        const uint32_t hi = pack_f8x4<E5M2>(v[i][4] * f, v[i][5] * f, v[i][6] * f, v[i][7] * f);
         if (r < p.R && kb < blocks) {
             uint8_t *const dst = p.q + r * p.ldq + c;
             if (p.vec && c + 8 <= p.N) {
@@ -144,9 +152,10 @@ __global__ void __launch_bounds__(kQThreads) quant_rows_kernel(const __grid_cons
 // block of 128 rows by 64 columns; each thread holds four consecutive rows of
 // eight columns, so its four values of a column make one 32-bit word of q.
 template <class T, bool E5M2>
-__global__ void __launch_bounds__(kQThreads) quant_trans_kernel(const __grid_constant__ QuantParams p) {
+__global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 6 : 4) quant_trans_kernel(const __grid_constant__ QuantParams p) {
     constexpr int PITCH = kBlk / 4 + 1;  // words of a column's 128 values, padded
     __shared__ float amax[8][64];
+    __shared__ float factor[64];
     __shared__ uint32_t tile[64 * PITCH];
     grid_dep_wait();
     grid_dep_launch();
@@ -156,11 +165,12 @@ __global__ void __launch_bounds__(kQThreads) quant_trans_kernel(const __grid_con
     const int64_t n0 = static_cast<int64_t>(blockIdx.y) * 64;
     const int64_t m0 = mb * kBlk + rg * 4;
     const int64_t n = n0 + cg * 8;
-    float v[4][8], a[8];
+    Raw8<T> v[4];
+    float a[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        load8(static_cast<const T *>(p.x) + (m0 + i < p.M ? m0 + i : 0) * p.ldx + n, p.vec, m0 + i < p.M ? p.N - n : 0,
-              v[i]);
+        v[i] = load8(static_cast<const T *>(p.x) + (m0 + i < p.M ? m0 + i : 0) * p.ldx + n, p.vec,
+                     m0 + i < p.M ? p.N - n : 0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         a[j] = fmaxf(fmaxf(fabsf(v[0][j]), fabsf(v[1][j])), fmaxf(fabsf(v[2][j]), fabsf(v[3][j])));
@@ -172,15 +182,19 @@ __global__ void __launch_bounds__(kQThreads) quant_trans_kernel(const __grid_con
         for (int j = 0; j < 8; ++j) amax[warp][lane * 8 + j] = a[j];
     }
     __syncthreads();
-    float f[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    // one thread a column joins the warps' maxima and divides; every thread doing so for
+    // its eight columns took half of the kernel's time
+    if (threadIdx.x < 64) {
         float t = 0x1p-100f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) t = fmaxf(t, amax[w][cg * 8 + j]);
-        f[j] = top_of(E5M2) / t;
-        if (rg == 0 && n + j < p.N) p.s[(n + j) * p.s_row + mb * p.s_blk] = t / top_of(E5M2);
+        for (int w = 0; w < 8; ++w) t = fmaxf(t, amax[w][threadIdx.x]);
+        factor[threadIdx.x] = top_of(E5M2) / t;
+        if (n0 + threadIdx.x < p.N) p.s[(n0 + threadIdx.x) * p.s_row + mb * p.s_blk] = t / top_of(E5M2);
     }
+    __syncthreads();
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = factor[cg * 8 + j];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         tile[(cg * 8 + j) * PITCH + rg] =
@@ -210,9 +224,10 @@ cudaError_t quant_launch(const QuantParams &p, bool e5m2, bool transpose, cudaSt
         return e5m2 ? launch_pdl(quant_trans_kernel<T, true>, grid, dim3(kQThreads), 0, st, p)
                     : launch_pdl(quant_trans_kernel<T, false>, grid, dim3(kQThreads), 0, st, p);
     }
-    const dim3 grid(static_cast<unsigned>(cdiv(p.N, 8 * kBlk)), static_cast<unsigned>(cdiv(p.R, 16)));
-    return e5m2 ? launch_pdl(quant_rows_kernel<T, true>, grid, dim3(kQThreads), 0, st, p)
-                : launch_pdl(quant_rows_kernel<T, false>, grid, dim3(kQThreads), 0, st, p);
+    // Two blocks a CTA: 256 x 4096 gathered rows 4.8 us with eight (64 CTAs), 2.2 with two.
+    const dim3 grid(static_cast<unsigned>(cdiv(p.N, kRowBlocks * kBlk)), static_cast<unsigned>(cdiv(p.R, 16)));
+    return e5m2 ? launch_pdl(quant_rows_kernel<T, true, kRowBlocks>, grid, dim3(kQThreads), 0, st, p)
+                : launch_pdl(quant_rows_kernel<T, false, kRowBlocks>, grid, dim3(kQThreads), 0, st, p);
 }
 
 }  // namespace
