@@ -57,7 +57,7 @@ struct Fp8Cfg {
     static constexpr int SLOTS = 512 / SC;
     static constexpr int H = BN / SC;
     static constexpr int COLS = BN / 2;  // columns of one promotion warp
-    static constexpr int TEMPTY_ARRIVALS = 8 / H * CG;
+    static constexpr int TEMPTY_ARRIVALS = EPI_WARPS / H * CG;
     static constexpr int TMEM_COLS = 512;
     // First column, within the tile, of a promotion warp's 64-column segment seg.
     static __device__ __forceinline__ int32_t seg_col(int h, int seg) {
@@ -73,9 +73,9 @@ struct Fp8Cfg {
     // Store staging of one warp: three buffers of 32 rows x 64 bytes.
     static constexpr int EPI_ROW = 64, EPI_BUF = 32 * EPI_ROW, EPI_BUFS = 3;
     static constexpr int EPI_BYTES = EPI_WARPS * EPI_BUFS * EPI_BUF;
-    // Scales travel in chunks of four K blocks, two chunks deep: per K block those of the
+    // Scales travel in chunks of four K blocks, four chunks deep: per K block those of the
     // tile's rows, then those of its one or two 128-column blocks (ROWS: its columns).
-    static constexpr int CHUNK = 4, CHUNKS = 2;
+    static constexpr int CHUNK = 4, CHUNKS = 4;
     static constexpr int KB_SCALES = 128 + (ROWS ? BN : 4);
     static constexpr int CHUNK_BYTES = CHUNK * KB_SCALES * 4;
     static constexpr int SCALE_BYTES = CHUNKS * CHUNK_BYTES;
@@ -145,7 +145,7 @@ __device__ __forceinline__ Fp8Unit fp8_unit(int32_t u, const Fp8Params &p, const
 }
 
 template <int BN, int CG, bool ROWS, bool GROUPED, int SC>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC>::THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmD, const __grid_constant__ Fp8Params p) {
     using C = Fp8Cfg<BN, CG, ROWS, GROUPED, SC>;
@@ -399,10 +399,14 @@ __global__ void __launch_bounds__(384, 1)
         bool alive = true;
         for (int32_t u = first; u < num_units && alive; u += step) {
             const Fp8Unit w = fp8_unit<C>(u, p, prefix);
-            const int32_t row = w.row0 + static_cast<int32_t>(rank) * C::BM + lane;
-            const float *pa = p.sa + static_cast<int64_t>(row) * p.sa_row + kb0 * p.sa_blk;
+            // four scales a copy where they lie next to each other on a 16-byte boundary
+            const int32_t row0 = w.row0 + static_cast<int32_t>(rank) * C::BM;
+            const bool vec_a = p.sa_vec && (row0 & 3) == 0, vec_b = ROWS && p.sb_vec;
+            const int32_t row = row0 + (vec_a ? 4 : 1) * lane;  // this lane's first row
+            const int32_t a_bytes = max(0, min(16, 4 * (w.row_end - row)));
+            const float *pa = p.sa + (row < w.row_end ? static_cast<int64_t>(row) * p.sa_row : 0) + kb0 * p.sa_blk;
             // this lane's first column (ROWS) or block of columns
-            const int32_t n = w.col0 + (ROWS ? 1 : kScaleBlock) * lane;
+            const int32_t n = w.col0 + (ROWS ? (vec_b ? 4 : 1) : kScaleBlock) * lane;
             const bool has_b = ROWS || lane < BN / 128;
             const float *pb = p.sb + w.group * p.sb_group + static_cast<int64_t>(ROWS ? n : n / kScaleBlock) * p.sb_n + kb0 * p.sb_k;
             for (int32_t kb = 0; kb < num_kb; ++kb) {
@@ -414,17 +418,30 @@ __global__ void __launch_bounds__(384, 1)
                         break;
                     }
                 }
-                const uint32_t at = s_scale + buf * C::CHUNK_BYTES + (kb % C::CHUNK) * (C::KB_SCALES * 4) + lane * 4;
+                const uint32_t at = s_scale + buf * C::CHUNK_BYTES + (kb % C::CHUNK) * (C::KB_SCALES * 4);
+                if (vec_a) {
+                    copy_async_16(at + 16 * lane, pa, a_bytes);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    copy_async_f32(at + 128 * i, row + 32 * i < w.row_end ? pa + 32 * i * p.sa_row : p.sa, row + 32 * i < w.row_end);
+                    for (int i = 0; i < 4; ++i)
+                        copy_async_f32(at + 4 * lane + 128 * i, row + 32 * i < w.row_end ? pa + 32 * i * p.sa_row : p.sa,
+                                       row + 32 * i < w.row_end);
+                }
                 pa += p.sa_blk;
                 if constexpr (ROWS) {
+                    if (vec_b) {
 #pragma unroll
-                    for (int i = 0; i < BN / 32; ++i)
-                        copy_async_f32(at + 512 + 128 * i, n + 32 * i < p.N ? pb + 32 * i * p.sb_n : p.sb, n + 32 * i < p.N);
+                        for (int i = 0; i < BN / 128; ++i)
+                            copy_async_16(at + 512 + 512 * i + 16 * lane, n + 128 * i < p.N ? pb + 128 * i : p.sb,
+                                          max(0, min(16, 4 * (p.N - n - 128 * i))));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < BN / 32; ++i)
+                            copy_async_f32(at + 512 + 4 * lane + 128 * i, n + 32 * i < p.N ? pb + 32 * i * p.sb_n : p.sb,
+                                           n + 32 * i < p.N);
+                    }
                 } else if (has_b) {
-                    copy_async_f32(at + 512, n < p.N ? pb : p.sb, n < p.N);
+                    copy_async_f32(at + 512 + 4 * lane, n < p.N ? pb : p.sb, n < p.N);
                 }
                 pb += p.sb_k;
                 if (kb % C::CHUNK == C::CHUNK - 1 || kb + 1 == num_kb) {
@@ -510,6 +527,18 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 const uint32_t taddr =
                     tmem_base + (static_cast<uint32_t>(32 * q) << 16) + slot * SC + (C::H == 1 ? C::COLS * h : 0);
+                // ROWS: the scales of sixteen columns, read sixteen columns ahead
+                uint64_t cs[2][8];
+                auto load_cols = [&](int g) {
+                    if constexpr (ROWS) {
+                        if (g < C::COLS / 16) {
+                            const uint32_t at = sc_at + 512 + (C::seg_col(h, g / 4) + 16 * (g % 4)) * 4;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) ld_shared_v2u64(at + 16 * i, cs[g & 1][2 * i], cs[g & 1][2 * i + 1]);
+                        }
+                    }
+                };
+                load_cols(0);
 #pragma unroll
                 for (int c = 0; c < C::COLS / 64; ++c) {
                     uint32_t v[64];
@@ -518,13 +547,21 @@ __global__ void __launch_bounds__(384, 1)
                     // handed back once its last columns are in registers
                     if (c + 1 == C::COLS / 64) release();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const uint64_t x = pair_u32(v[2 * i], v[2 * i + 1]);
-                        if constexpr (ROWS)
-                            fma2(sum[32 * c + i], mul2(x, s2[0]),
-                                 ld_shared_u64(sc_at + 512 + (C::seg_col(h, c) + 2 * i) * 4));
-                        else
-                            fma2(sum[32 * c + i], x, s2[NB == 2 ? c : 0]);
+                    for (int g = 0; g < 4; ++g) {
+                        load_cols(4 * c + g + 1);
+                        if constexpr (ROWS) {
+                            // the products first: each multiply-add waits for none of them
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) cs[g & 1][i] = mul2(cs[g & 1][i], s2[0]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint64_t x = pair_u32(v[16 * g + 2 * i], v[16 * g + 2 * i + 1]);
+                            if constexpr (ROWS)
+                                fma2(sum[32 * c + 8 * g + i], x, cs[g & 1][i]);
+                            else
+                                fma2(sum[32 * c + 8 * g + i], x, s2[NB == 2 ? c : 0]);
+                        }
                     }
                 }
                 if (ROWS) chunk_done();

@@ -28,6 +28,7 @@ struct Fp8Params {
     const int64_t *offsets;
     const float *sa;    // scale of A's row m, K block b: sa[m * sa_row + b * sa_blk]
     int64_t sa_row, sa_blk;
+    int32_t sa_vec, sb_vec;  // four scales along M (row scales: along N) lie on a 16-byte boundary, from a multiple of four
     // scale of B: sb[g * sb_group + i * sb_n + b * sb_k] for K block b and column n of
     // D, i = n / 128 (block scales) or i = n (row scales)
     const float *sb;

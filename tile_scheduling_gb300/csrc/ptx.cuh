@@ -162,6 +162,10 @@ __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol
 __device__ __forceinline__ void copy_async_f32(uint32_t dst, const float *src, bool valid) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
 }
+// The same for 16 bytes, of which the first `bytes` are read and the rest are zero.
+__device__ __forceinline__ void copy_async_16(uint32_t dst, const void *src, int32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 // One arrival on `bar` (counted in its initial count) once this thread's earlier
 // asynchronous copies have landed.
 __device__ __forceinline__ void copy_async_arrive(uint32_t bar) {
@@ -399,12 +403,9 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
 }
-__device__ __forceinline__ uint64_t ld_shared_u64(uint32_t addr) {
-    uint64_t v;
-    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void ld_shared_v2u64(uint32_t addr, uint64_t &a, uint64_t &b) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
 }
-
 // Four fp32 values at a shared::cluster address.
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t cluster_addr) {
     float4 v;
