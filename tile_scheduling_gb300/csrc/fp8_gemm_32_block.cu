@@ -1,0 +1,3 @@
+#include "fp8_launch.cuh"
+
+TS_FP8_VARIANT(fp8_32_block, 128, 1, false, false, 128, 32)

@@ -1,0 +1,3 @@
+#include "fp8_launch.cuh"
+
+TS_FP8_VARIANT(fp8_32_grouped, 128, 1, false, true, 128, 32)

@@ -34,17 +34,20 @@
 
 namespace ts {
 
-template <int BN_, int CG_, bool ROWS_, bool GROUPED_, int SC_>
+template <int BN_, int CG_, bool ROWS_, bool GROUPED_, int SC_, int AR_>
 struct Fp8Cfg {
     static constexpr int BN = BN_, CG = CG_;
     static constexpr bool ROWS = ROWS_, GROUPED = GROUPED_;
     static constexpr int EPI_WARPS = 8;
     static constexpr int THREADS = 32 * (kRoleWarps + EPI_WARPS);
-    static constexpr int BM = 128, TILE_M = BM * CG;
+    // The MMA always takes BM = 128 rows of A.  Tiles of few rows (AR = 32: a batch of
+    // decoded tokens, or experts with a few rows each) load only those; what the MMA reads
+    // past them is whatever lies there, and the rows it makes of it are never read.
+    static constexpr int BM = 128, AR = AR_, TILE_M = AR == BM ? BM * CG : AR;
     static constexpr int BK = kScaleBlock;  // one scale block: a 128-byte swizzle row
     static constexpr int UMMA_K = 32;
     static constexpr int B_ROWS = BN / CG;
-    static constexpr int A_BYTES = BM * BK;
+    static constexpr int A_BYTES = AR * BK;
     static constexpr int B_BYTES = B_ROWS * BK;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int TX_BYTES = STAGE_BYTES * CG;
@@ -70,8 +73,10 @@ struct Fp8Cfg {
     static constexpr bool SHIFT_REGS = BN == 256;
     static constexpr int LAUNCH_REGS = 168, ROLE_REGS = 56, EPI_REGS = 224;
     static_assert(128 * ROLE_REGS + 256 * EPI_REGS == 384 * LAUNCH_REGS, "register split");
-    // Store staging of one warp: three buffers of 32 rows x 64 bytes.
-    static constexpr int EPI_ROW = 64, EPI_BUF = 32 * EPI_ROW, EPI_BUFS = 3;
+    // Store staging of one warp: buffers of 32 rows x 128 bytes, enough for its part of a
+    // bf16 tile, so that the part is written, fenced and stored at once (subtile after
+    // subtile through fewer buffers, the epilogue took 3000 cycles of a pair).
+    static constexpr int EPI_ROW = 128, EPI_BUF = 32 * EPI_ROW, EPI_BUFS = COLS / 64;
     static constexpr int EPI_BYTES = EPI_WARPS * EPI_BUFS * EPI_BUF;
     // Scales travel in chunks of four K blocks, four chunks deep: per K block those of the
     // tile's rows, then those of its one or two 128-column blocks (ROWS: its columns).
@@ -80,11 +85,15 @@ struct Fp8Cfg {
     static constexpr int CHUNK_BYTES = CHUNK * KB_SCALES * 4;
     static constexpr int SCALE_BYTES = CHUNKS * CHUNK_BYTES;
     static constexpr int PREFIX_BYTES = GROUPED ? (kMaxExperts + 8) * 4 : 0;
-    static constexpr int BAR_BYTES = 256;
+    static constexpr int BAR_BYTES = 512;
     static constexpr int FIXED_BYTES = 1024 + EPI_BYTES + SCALE_BYTES + PREFIX_BYTES + BAR_BYTES;
     static constexpr int STAGES = (kSmemLimit - FIXED_BYTES) / STAGE_BYTES;
     static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * STAGE_BYTES;
     static_assert(STAGES >= 2, "ring too shallow");
+    static_assert(AR == BM || (AR == 32 && CG == 1), "tile rows");
+    // the MMA's reads past a short A stage, and the split's partial sums, stay in the ring
+    static_assert((STAGES - 1) * A_BYTES + BM * BK <= STAGES * STAGE_BYTES, "A overrun");
+    static_assert(!SPLIT || STAGES * STAGE_BYTES >= BM * BN * 4, "partial sums");
     static_assert((2 * STAGES + 2 * SLOTS + 2 * CHUNKS + 1) * 8 + 16 <= BAR_BYTES, "barrier region");
 };
 
@@ -108,7 +117,7 @@ __device__ __forceinline__ uint32_t partial_at(int32_t g, int32_t r) {
 
 // One work unit: an output tile.
 struct Fp8Unit {
-    int32_t row0, row_end;  // rows [row0, row_end) of D may be written (row_end: the group's or D's last + 1)
+    int32_t row0, row_end;  // rows [row0, row_end) of D may be written (row_end: past the group's, D's or a short tile's last)
     int32_t col0;
     int32_t group;
 };
@@ -131,24 +140,24 @@ __device__ __forceinline__ Fp8Unit fp8_unit(int32_t u, const Fp8Params &p, const
         const int32_t nb = local / tm;
         w.group = lo;
         w.row0 = static_cast<int32_t>(r0) + (local - nb * tm) * C::TILE_M;
-        w.row_end = static_cast<int32_t>(r1);
+        w.row_end = C::TILE_M < C::BM ? min(static_cast<int32_t>(r1), w.row0 + C::TILE_M) : static_cast<int32_t>(r1);
         w.col0 = nb * C::BN;
     } else {
         int32_t mb, nb;
         raster(u, p, mb, nb);
         w.group = 0;
         w.row0 = mb * C::TILE_M;
-        w.row_end = p.M;
+        w.row_end = C::TILE_M < C::BM ? min(p.M, w.row0 + C::TILE_M) : p.M;
         w.col0 = nb * C::BN;
     }
     return w;
 }
 
-template <int BN, int CG, bool ROWS, bool GROUPED, int SC>
-__global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC>::THREADS, 1)
+template <int BN, int CG, bool ROWS, bool GROUPED, int SC, int AR>
+__global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC, AR>::THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmD, const __grid_constant__ Fp8Params p) {
-    using C = Fp8Cfg<BN, CG, ROWS, GROUPED, SC>;
+    using C = Fp8Cfg<BN, CG, ROWS, GROUPED, SC, AR>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -323,7 +332,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC>::THREADS, 1)
         // took some 630 cycles to issue (8192^3, no promotion: 362 us against 286).
         if (rank == 0) {
             const bool leader = elect_one();
-            const uint32_t idesc = p.idesc | (uint32_t(SC >> 3) << 17) | (uint32_t(C::TILE_M >> 4) << 24);
+            const uint32_t idesc = p.idesc | (uint32_t(SC >> 3) << 17) | (uint32_t((C::BM * CG) >> 4) << 24);
             // steps of B's start address in 16-byte units: one K = 32 MMA (32 bytes along a
             // K-major row, or 32 rows of 128 bytes) and one slot (its rows, or, along a row of
             // n, half of it or the next box)
@@ -412,7 +421,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC>::THREADS, 1)
             for (int32_t kb = 0; kb < num_kb; ++kb) {
                 const uint32_t buf = chunk % C::CHUNKS;
                 if (kb % C::CHUNK == 0) {
-                    const bool ok = wait_inline(sempty(buf), ((chunk / C::CHUNKS) & 1u) ^ 1u, abort_flag, p, WAIT_SCALES);
+                    const bool ok = wait_phase(sempty(buf), ((chunk / C::CHUNKS) & 1u) ^ 1u, abort_flag, p, WAIT_SCALES);
                     if (!__all_sync(0xffffffffu, ok)) {
                         alive = false;
                         break;
@@ -459,7 +468,6 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC>::THREADS, 1)
         const int j = warp - kRoleWarps;
         const int q = j & 3, h = j >> 2;
         const uint32_t stg = s_epi + static_cast<uint32_t>(j) * (C::EPI_BUFS * C::EPI_BUF);
-        uint32_t buf = 0;
         const uint64_t store_policy = policy_evict_first();
         // slots of this warp: count s of its K blocks since the start gives slot and phase
         uint32_t count = C::H == 2 ? h : 0, chunk = 0;
@@ -478,7 +486,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC>::THREADS, 1)
             for (int i = 0; i < C::COLS / 2; ++i) sum[i] = 0ull;
             for (int32_t kb = 0; kb < num_kb; ++kb) {
                 if (kb % C::CHUNK == 0) {
-                    const bool ok = wait_inline(sfull(chunk % C::CHUNKS), (chunk / C::CHUNKS) & 1u, abort_flag, p, WAIT_SCALES);
+                    const bool ok = wait_lean(sfull(chunk % C::CHUNKS), (chunk / C::CHUNKS) & 1u, abort_flag);
                     if (!__all_sync(0xffffffffu, ok)) {
                         alive = false;
                         break;
@@ -503,7 +511,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC>::THREADS, 1)
                 };
                 if (!ROWS || !work) chunk_done();
                 const uint32_t slot = count % C::SLOTS;
-                const bool ok = wait_inline(tfull(slot), (count / C::SLOTS) & 1u, abort_flag, p, WAIT_EPI_TMEM_FULL);
+                const bool ok = wait_lean(tfull(slot), (count / C::SLOTS) & 1u, abort_flag);
                 count += C::H;
                 if (!__all_sync(0xffffffffu, ok)) {
                     alive = false;
@@ -566,6 +574,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC>::THREADS, 1)
                 }
                 if (ROWS) chunk_done();
             }
+            if (!alive) *abort_flag = 1;  // a lean wait that ran out of polls
             if (!alive || !work) continue;
             if constexpr (C::SPLIT) {
                 if (p.split > 1) {
@@ -582,70 +591,80 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC>::THREADS, 1)
                     continue;
                 }
             }
-            // Store the tile part: 64-byte wide subtiles through swizzled staging and a TMA
+            // Store the tile part: 128-byte wide subtiles through swizzled staging and a TMA
             // store where the subtile lies inside D (and, grouped, inside the group), else
             // each lane its own row.
-            auto emit = [&](auto out_tag, int s, const uint64_t *part) {
+            const bool tma = p.tma_store && (!GROUPED || row0 + 32 <= w.row_end);
+            auto emit = [&](auto out_tag) {
                 constexpr int OUT = decltype(out_tag)::value;
                 constexpr int SUB = C::EPI_ROW / (OUT == OUT_F32 ? 4 : 2);  // columns
-                constexpr int W = C::EPI_ROW / 4;                           // words of a row
-                const int32_t col = w.col0 + C::seg_col(h, s * SUB / 64) + s * SUB % 64;
-                if (col >= p.N) return;
-                uint32_t o[W];
+                auto col_of = [&](int s) { return w.col0 + C::seg_col(h, s * SUB / 64) + s * SUB % 64; };
 #pragma unroll
-                for (int i = 0; i < SUB / 2; ++i) {
-                    uint32_t lo, hi;
-                    unpair(part[i], lo, hi);
-                    if constexpr (OUT == OUT_F32) {
-                        o[2 * i] = lo;
-                        o[2 * i + 1] = hi;
-                    } else {
-                        o[i] = pack_bf16x2(lo, hi);
+                for (int s0 = 0; s0 < C::COLS / SUB; s0 += C::EPI_BUFS) {
+                    if (tma) {
+                        if (lane == 0) bulk_wait_read<0>();  // the stores that used the buffers have read them
+                        __syncwarp();
                     }
-                }
-                const bool whole = col + SUB <= p.N;
-                if (p.tma_store && whole && (!GROUPED || row0 + 32 <= w.row_end)) {
-                    if (lane == 0) bulk_wait_read<C::EPI_BUFS - 1>();  // the store that used this buffer has read it
-                    __syncwarp();
-                    const uint32_t at = stg + buf * C::EPI_BUF + static_cast<uint32_t>(lane) * C::EPI_ROW;
 #pragma unroll
-                    for (int i = 0; i < W / 4; ++i)
-                        st_shared_v4(at + ((static_cast<uint32_t>(i) ^ ((lane >> 1) & 3u)) << 4), o[4 * i], o[4 * i + 1],
-                                     o[4 * i + 2], o[4 * i + 3]);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_3d(&tmD, stg + buf * C::EPI_BUF, col, row0, 0, store_policy);
-                        bulk_commit();
+                    for (int s = s0; s < s0 + C::EPI_BUFS; ++s) {
+                        const uint64_t *const part = sum + s * SUB / 2;
+                        uint32_t o[32];
+#pragma unroll
+                        for (int i = 0; i < SUB / 2; ++i) {
+                            uint32_t lo, hi;
+                            unpair(part[i], lo, hi);
+                            if constexpr (OUT == OUT_F32) {
+                                o[2 * i] = lo;
+                                o[2 * i + 1] = hi;
+                            } else {
+                                o[i] = pack_bf16x2(lo, hi);
+                            }
+                        }
+                        const int32_t col = col_of(s);
+                        const bool whole = col + SUB <= p.N;
+                        if (tma && whole) {
+                            const uint32_t at = stg + (s - s0) * C::EPI_BUF + static_cast<uint32_t>(lane) * C::EPI_ROW;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                st_shared_v4(at + ((static_cast<uint32_t>(i) ^ (lane & 7u)) << 4), o[4 * i], o[4 * i + 1],
+                                             o[4 * i + 2], o[4 * i + 3]);
+                        } else if (mine && col < p.N) {
+                            const int64_t at = static_cast<int64_t>(row) * p.ldd + col;
+                            if (p.vec_store && whole) {
+                                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<char *>(p.D) + at * (OUT == OUT_F32 ? 4 : 2));
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            } else if constexpr (OUT == OUT_F32) {
+                                float *dst = static_cast<float *>(p.D) + at;
+#pragma unroll
+                                for (int i = 0; i < SUB; ++i)
+                                    if (col + i < p.N) dst[i] = __uint_as_float(o[i]);
+                            } else {
+                                uint16_t *dst = static_cast<uint16_t *>(p.D) + at;
+#pragma unroll
+                                for (int i = 0; i < SUB; ++i)
+                                    if (col + i < p.N) dst[i] = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
+                            }
+                        }
                     }
-                    buf = buf + 1 == C::EPI_BUFS ? 0 : buf + 1;
-                } else if (mine) {
-                    const int64_t at = static_cast<int64_t>(row) * p.ldd + col;
-                    if (p.vec_store && whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<char *>(p.D) + at * (OUT == OUT_F32 ? 4 : 2));
+                    if (tma) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
 #pragma unroll
-                        for (int i = 0; i < W / 4; ++i)
-                            dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    } else if constexpr (OUT == OUT_F32) {
-                        float *dst = static_cast<float *>(p.D) + at;
-#pragma unroll
-                        for (int i = 0; i < SUB; ++i)
-                            if (col + i < p.N) dst[i] = __uint_as_float(o[i]);
-                    } else {
-                        uint16_t *dst = static_cast<uint16_t *>(p.D) + at;
-#pragma unroll
-                        for (int i = 0; i < SUB; ++i)
-                            if (col + i < p.N) dst[i] = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
+                            for (int s = s0; s < s0 + C::EPI_BUFS; ++s)
+                                if (col_of(s) + SUB <= p.N)
+                                    tma_store_3d(&tmD, stg + (s - s0) * C::EPI_BUF, col_of(s), row0, 0, store_policy);
+                            bulk_commit();
+                        }
                     }
                 }
             };
-            if (p.out == OUT_F32) {
-#pragma unroll
-                for (int s = 0; s < C::COLS / 16; ++s) emit(std::integral_constant<int, OUT_F32>{}, s, sum + 8 * s);
-            } else {
-#pragma unroll
-                for (int s = 0; s < C::COLS / 32; ++s) emit(std::integral_constant<int, OUT_BF16>{}, s, sum + 16 * s);
-            }
+            if (p.out == OUT_F32)
+                emit(std::integral_constant<int, OUT_F32>{});
+            else
+                emit(std::integral_constant<int, OUT_BF16>{});
         }
         if (lane == 0) bulk_wait<0>();
         __syncwarp();

@@ -8,10 +8,10 @@
 namespace ts {
 namespace {
 
-template <int BN, int CG, bool ROWS, bool GROUPED, int SC>
+template <int BN, int CG, bool ROWS, bool GROUPED, int SC, int AR>
 cudaError_t fp8_launch(const Fp8Launch &L) {
-    using C = Fp8Cfg<BN, CG, ROWS, GROUPED, SC>;
-    auto *kernel = fp8_gemm_kernel<BN, CG, ROWS, GROUPED, SC>;
+    using C = Fp8Cfg<BN, CG, ROWS, GROUPED, SC, AR>;
+    auto *kernel = fp8_gemm_kernel<BN, CG, ROWS, GROUPED, SC, AR>;
     static std::atomic<uint64_t> done{0};  // cudaFuncSetAttribute once per device
     const int dev = current_device();
     const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
@@ -50,8 +50,8 @@ cudaError_t fp8_launch(const Fp8Launch &L) {
 }  // namespace
 }  // namespace ts
 
-#define TS_FP8_VARIANT(NAME, BN, CG, ROWS, GROUPED, SC)                                          \
-    namespace ts {                                                                               \
-    extern const Fp8Variant NAME;                                                                \
-    const Fp8Variant NAME = {BN, CG, ROWS, GROUPED, &fp8_launch<BN, CG, ROWS, GROUPED, SC>};         \
+#define TS_FP8_VARIANT(NAME, BN, CG, ROWS, GROUPED, SC, AR)                                          \
+    namespace ts {                                                                                   \
+    extern const Fp8Variant NAME;                                                                    \
+    const Fp8Variant NAME = {BN, CG, ROWS, GROUPED, AR, &fp8_launch<BN, CG, ROWS, GROUPED, SC, AR>}; \
     }

@@ -48,7 +48,7 @@ struct Fp8Launch {
 };
 
 struct Fp8Variant {
-    int bn, cg, rows, grouped;
+    int bn, cg, rows, grouped, a_rows;
     cudaError_t (*launch)(const Fp8Launch &);
 };
 

@@ -42,24 +42,18 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
     return wait_slow(bar, parity, p.timeout_ns, abort_flag, true, p, where);
 }
 
-// The same without a function call, for code whose registers are too many to be
-// kept across one.
-template <class P>
-__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int *abort_flag, const P &p,
-                                            int where) {
+// A wait of few instructions and without a function call, for loops whose registers
+// and instruction-cache lines are scarce.  It gives up when another role of the CTA
+// has (a role that waits with a time limit, and that this wait's end depends on or
+// that depends on it) or after kLeanPolls polls, which take longer than that limit.
+constexpr uint32_t kLeanPolls = 1u << 27;
+__device__ __forceinline__ bool wait_lean(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
     if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer();
-    for (uint32_t n = 1;; ++n) {
+    for (uint32_t n = 0; n < kLeanPolls; ++n) {
         if (mbar_try_wait(bar, parity)) return true;
-        if ((n & 15u) == 0) {
-            if (*abort_flag) return false;
-            if (globaltimer() - t0 > p.timeout_ns) {
-                report_timeout(p, where);
-                *abort_flag = 1;
-                return false;
-            }
-        }
+        if (*abort_flag) return false;
     }
+    return false;
 }
 
 // Bounded wait for roles whose waits last about a tile and whose wake-up is not
