@@ -1,7 +1,8 @@
 /*
  * tsgemm -- persistent, warp-specialised bf16 GEMM with static and Cluster
- * Launch Control tile scheduling, plus a vectorised grid-stride int16 copy,
- * for one NVIDIA GB300 (sm_103a).
+ * Launch Control tile scheduling, plus a vectorised grid-stride int16 copy and
+ * the operators of a mixture-of-experts layer (routing, 8-bit quantisation,
+ * block-scaled 8-bit products, combine), for one NVIDIA GB300 (sm_103a).
  *
  * C ABI: plain pointers and sizes only.  Every device pointer is owned by
  * the caller; the library never allocates device memory on these paths.  The
@@ -514,9 +515,9 @@ typedef struct {
     int32_t max_workers;     /* cap on persistent workers (CTAs or 2-CTA clusters) */
     int64_t lda, ldb, ldd;   /* row strides in elements; 0 = dense rows */
     int64_t b_group;         /* grouped: elements between the groups of B; 0 = dense */
-    int64_t sa_row, sa_blk;  /* strides of SA along M and along the K blocks; 0 = 1 and M (K-block major,
-                                the layout that reads fastest) */
-    int64_t sb_row, sb_blk;  /* strides of SB along its rows and columns; 0 = dense rows */
+    int64_t sa_row, sa_blk;  /* strides of SA along M and along the K blocks; both 0 = 1 and M (K-block
+                                major, the layout that reads fastest); one 0 broadcasts along it */
+    int64_t sb_row, sb_blk;  /* strides of SB along its rows and columns; both 0 = dense rows */
     int64_t sb_group;        /* grouped: elements between the groups of SB; 0 = dense */
     double timeout_s;        /* per-wait limit for every mbarrier wait in the kernel; 0 = 2 s */
 } ts_fp8_opts;

@@ -285,3 +285,27 @@ def test_refusals(lib):
     with pytest.raises(ValueError):
         lib.ts_gemm_fp8_grouped(A, SA, B3, SB3, D, torch.tensor([0, 1, 64], device="cuda"))
     lib.ts_sync_and_check()
+
+
+def test_expanded_tensors(lib):
+    # scales broadcast along one dimension are taken as they are; what cannot be told apart or shares rows is refused
+    M, N, K = 130, 140, 300
+    A, SA, B, SB, a, b = _problem(M, N, K, 13, True)
+    one = SA[:, :1].contiguous()
+    D = torch.empty((M, N), device="cuda")
+    lib.ts_gemm_fp8(A, one.expand(M, 3), B, SB, D)
+    lib.ts_sync_and_check()
+    ref = (A.double().cpu() * one.double().cpu()) @ b
+    assert torch.equal(D.cpu(), ref.float())
+    row = SA[:1].contiguous()
+    lib.ts_gemm_fp8(A, row.expand(M, 3), B, SB, D)
+    lib.ts_sync_and_check()
+    ref = (A.double().cpu() * _expand(row.double().cpu(), 1, K, 1)) @ b
+    assert torch.equal(D.cpu(), ref.float())
+    for bad in (lambda: lib.ts_gemm_fp8(A, SA[:1, :1].expand(M, 3), B, SB, D),
+                lambda: lib.ts_gemm_fp8(A[:1].expand(M, K), SA, B, SB, D),
+                lambda: lib.ts_gemm_fp8(A, SA, B, SB, D[:1].expand(M, N)),
+                lambda: lib.ts_gemm_fp8_grouped(A, SA, B[None].expand(2, N, K), SB[None].repeat(2, 1, 1), D,
+                                                torch.tensor([0, 10, M], device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()

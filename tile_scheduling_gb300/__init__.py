@@ -1,5 +1,6 @@
 """Python binding of libtsgemm (persistent bf16 GEMM with static / Cluster Launch
-Control tile scheduling, and the grid-stride int16 copy) for one GB300.
+Control tile scheduling, the grid-stride int16 copy, and the mixture-of-experts
+operators: routing, 8-bit quantisation and products, combine) for one GB300.
 
 This module only marshals arguments: torch tensors become device pointers and
 sizes, the current torch stream becomes a cudaStream_t, and every computation
@@ -33,7 +34,8 @@ _OUT = {torch.bfloat16: TS_OUT_BF16, torch.float32: TS_OUT_F32}
 EXPORTED = ("ts_gemm_bf16", "ts_gemm_bf16_ex", "ts_gemm_launch_info", "ts_gemm_bf16_checked_noalloc",
             "ts_copy_i16", "ts_spin",
             "ts_spin_wait_started", "ts_sync_and_check", "ts_num_sms", "ts_status_string",
-            "ts_last_error_detail")
+            "ts_last_error_detail", "ts_gemm_fp8", "ts_gemm_fp8_grouped", "ts_quant_fp8", "ts_moe_route",
+            "ts_moe_route_grad", "ts_moe_plan", "ts_moe_plan_workspace", "ts_moe_combine", "ts_moe_combine_grad")
 
 
 class TsError(RuntimeError):
@@ -579,7 +581,11 @@ def _matrix_of(t, name: str, dtypes, dims: int = 2):
     shape, stride = t.shape, t.stride()
     if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must have unit column stride")
-    return dtypes[t.dtype], shape, stride[-2] if shape[-2] > 1 else 0
+    if shape[-2] <= 1:
+        return dtypes[t.dtype], shape, 0
+    if stride[-2] == 0 and shape[-1]:
+        raise ValueError(f"{name} has rows that share memory (an expanded tensor)")
+    return dtypes[t.dtype], shape, stride[-2]
 
 
 def _dense(t, name: str, dtypes, shape) -> int:
@@ -592,10 +598,14 @@ def _dense(t, name: str, dtypes, shape) -> int:
 
 
 def _scales(t, name: str, dims: int):
-    """(shape, strides) of an fp32 scale tensor of any strides."""
+    """(shape, strides) of an fp32 scale tensor of any strides; an expanded one is broadcast along the
+    dimension it is expanded in (both at once cannot be told from the default strides)."""
     if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda or t.dim() != dims:
         _require(t, name, _F32, dims)
-    return t.shape, t.stride()
+    stride = t.stride()
+    if stride[-1] == 0 and stride[-2] == 0 and t.shape[-1] * t.shape[-2] > 1:
+        raise ValueError(f"{name} is one scale expanded in both dimensions")
+    return t.shape, stride
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -638,6 +648,8 @@ def _fp8_opts(A, SA, B, SB, D, dims, trans_b, tile, max_workers, timeout_s):
             raise ValueError(f"SB must hold the scales of {b_shape[0]} groups")
         if b_shape[0] > 1:
             b_group, sb_group = B.stride(0), sb_stride[0]
+            if b_group == 0 or sb_group == 0:
+                raise ValueError("groups of B or SB share memory (an expanded tensor)")
     o = Fp8Opts(a_type, b_type, b_scale, 1 if trans_b else 0, _TILE[tile] if isinstance(tile, str) else int(tile),
                 max_workers, lda, ldb, ldd, b_group, sa_stride[0], sa_stride[1], sb_stride[-2], sb_stride[-1],
                 sb_group, timeout_s)
@@ -687,6 +699,8 @@ def ts_quant_fp8(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, rows=No
     x_type, (M, N), ldx = _matrix_of(x, "x", _OUT)
     q_type, q_shape, ldq = _matrix_of(q, "q", _FP8)
     s_shape, s_stride = _scales(scales, "scales", 2)
+    if 0 in s_stride and scales.numel() > 1:
+        raise ValueError("scales share memory (an expanded tensor)")
     index, out_rows, want_r, want_c = 0, 0, M, N
     if rows is not None:
         if transpose:
@@ -754,20 +768,36 @@ def ts_moe_plan_workspace(slots: int, experts: int) -> int:
     return int(_lib.ts_moe_plan_workspace(int(slots), int(experts)))
 
 
+_SCRATCH: dict = {}
+
+
+def _scratch_for(nbytes: int, device, stream) -> torch.Tensor:
+    """Uninitialised scratch of at least ``nbytes``, kept per device and stream and allocated on the stream
+    it serves, so that calls on different streams never share one."""
+    key = (device, _stream_of(stream))
+    ws = _SCRATCH.get(key)
+    if ws is None or ws.numel() < nbytes:
+        st = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(key[1], device=device)
+        with torch.cuda.stream(st):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        _SCRATCH[key] = ws
+    return ws
+
+
 def ts_moe_plan(experts: torch.Tensor, offsets: torch.Tensor, order: torch.Tensor, position: torch.Tensor,
                 workspace=None, stream=None) -> None:
     """Sort the slots of experts (int32, negative = dropped) by expert, stably.
 
     offsets [E + 1] (int64): the rows of each expert; order [slots] (int32): the slot of each row, -1 past
     the last; position (int32, experts' shape): the row of each slot, -1 if dropped.  The workspace that
-    many slots need is allocated here unless one is passed."""
+    many slots need is one kept for each stream unless one is passed."""
     n = experts.numel()
     E = offsets.numel() - 1
     shape = experts.shape
     ptr = size = 0
     need = _lib.ts_moe_plan_workspace(n, E)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=experts.device)
+        workspace = _scratch_for(need, experts.device, stream)
     if workspace is not None:
         if not workspace.is_cuda or not workspace.is_contiguous():
             raise TypeError("workspace must be a contiguous CUDA tensor")

@@ -68,7 +68,8 @@ ts_status fp8_product(const void *A, const float *SA, const void *B, const float
         return fail(TS_ERR_INVALID_ARG, "b_scale %d", o->b_scale);
     if (o->trans_b != 0 && o->trans_b != 1) return fail(TS_ERR_INVALID_ARG, "trans_b = %d (0 or 1)", o->trans_b);
     if (o->tile < TS_TILE_AUTO || o->tile > TS_TILE_256x256_2CTA) return fail(TS_ERR_INVALID_ARG, "tile %d", o->tile);
-    if (o->max_workers < 0 || o->timeout_s < 0 || o->lda < 0 || o->ldb < 0 || o->ldd < 0 || o->b_group < 0)
+    if (o->max_workers < 0 || o->timeout_s < 0 || o->lda < 0 || o->ldb < 0 || o->ldd < 0 || o->b_group < 0 ||
+        o->sa_row < 0 || o->sa_blk < 0 || o->sb_row < 0 || o->sb_blk < 0 || o->sb_group < 0)
         return fail(TS_ERR_INVALID_ARG, "negative option");
     const bool rows = o->b_scale == TS_SCALE_ROW;
     if (rows && o->trans_b) return fail(TS_ERR_UNSUPPORTED, "row scales need B with K contiguous (trans_b = 0)");
@@ -218,13 +219,14 @@ ts_status fp8_product(const void *A, const float *SA, const void *B, const float
     p.groups = grouped ? static_cast<int32_t>(groups) : 0;
     p.offsets = offsets;
     p.sa = SA;
-    p.sa_row = o->sa_row ? o->sa_row : 1;
-    p.sa_blk = o->sa_blk ? o->sa_blk : M;
+    const bool sa_given = o->sa_row || o->sa_blk, sb_given = o->sb_row || o->sb_blk;
+    p.sa_row = sa_given ? o->sa_row : 1;
+    p.sa_blk = sa_given ? o->sa_blk : M;
     p.sb = SB;
     // strides of SB as it lies ([rows of B / 128][columns of B / 128], or [N][K / 128] for
     // row scales), then along N and along K
-    const int64_t sb_row = o->sb_row ? o->sb_row : (rows ? kblocks : cdiv(b_cols, kScaleBlock));
-    const int64_t sb_blk = o->sb_blk ? o->sb_blk : 1;
+    const int64_t sb_row = sb_given ? o->sb_row : (rows ? kblocks : cdiv(b_cols, kScaleBlock));
+    const int64_t sb_blk = sb_given ? o->sb_blk : 1;
     p.sb_n = o->trans_b ? sb_blk : sb_row;
     p.sb_k = o->trans_b ? sb_row : sb_blk;
     p.sb_group = o->sb_group ? o->sb_group : kblocks * nblocks;

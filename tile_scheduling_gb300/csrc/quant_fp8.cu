@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(kQThreads) quant_rows_kernel(const __grid_cons
     grid_dep_wait();
     grid_dep_launch();
     const int part = threadIdx.x & 15;
-    const int64_t r = static_cast<int64_t>(blockIdx.y) * 16 + (threadIdx.x >> 4);
-    const int64_t kb0 = static_cast<int64_t>(blockIdx.x) * BLOCKS;
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+    const int64_t kb0 = static_cast<int64_t>(blockIdx.y) * BLOCKS;
     const int64_t blocks = (p.N + kBlk - 1) / kBlk;
     int64_t src = r;
     bool there = r < p.R;
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kQThreads) quant_rows_kernel(const __grid_cons
             there = false;  // an empty slot: q and s are zero
             src = -1;
         } else if (src >= p.M) {
-            if (part == 0 && blockIdx.x == 0) {
+            if (part == 0 && blockIdx.y == 0) {
                 if (atomicCAS(&p.status[0], 0ull, 5ull) == 0ull) atomicExch(&p.status[1], static_cast<unsigned long long>(r));
                 atomicAdd(&p.status[2], 1ull);
             }
@@ -225,7 +225,7 @@ cudaError_t quant_launch(const QuantParams &p, bool e5m2, bool transpose, cudaSt
                     : launch_pdl(quant_trans_kernel<T, false>, grid, dim3(kQThreads), 0, st, p);
     }
     // Two blocks a CTA: 256 x 4096 gathered rows 4.8 us with eight (64 CTAs), 2.2 with two.
-    const dim3 grid(static_cast<unsigned>(cdiv(p.N, kRowBlocks * kBlk)), static_cast<unsigned>(cdiv(p.R, 16)));
+    const dim3 grid(static_cast<unsigned>(cdiv(p.R, 16)), static_cast<unsigned>(cdiv(p.N, kRowBlocks * kBlk)));
     return e5m2 ? launch_pdl(quant_rows_kernel<T, true, kRowBlocks>, grid, dim3(kQThreads), 0, st, p)
                 : launch_pdl(quant_rows_kernel<T, false, kRowBlocks>, grid, dim3(kQThreads), 0, st, p);
 }
@@ -264,9 +264,9 @@ extern "C" ts_status ts_quant_fp8(const void *x, void *q, float *scales, int64_t
     const int64_t xbytes = M > 0 ? ((M - 1) * p.ldx + N) * esize : 0;
     if (ranges_overlap(x, xbytes, q, (q_rows - 1) * p.ldq + q_cols))
         return fail(TS_ERR_INVALID_ARG, "q overlaps x");
-    // grid limits: 65535 CTAs along y, 16 rows (64 columns, transposed) each
-    if (cdiv(o->transpose ? N : R, o->transpose ? 64 : 16) > 65535)
-        return fail(TS_ERR_UNSUPPORTED, "too many rows (columns, transposed) for one launch");
+    // the launch grid's second dimension, columns of x, has at most 65535 CTAs
+    if (cdiv(N, o->transpose ? 64 : kRowBlocks * kBlk) > 65535)
+        return fail(TS_ERR_UNSUPPORTED, "N = %lld columns are too many for one launch", static_cast<long long>(N));
     ts_status s;
     p.status = device_status_word(&s);
     if (!p.status) return s;
