@@ -1,0 +1,106 @@
+"""A mixture-of-experts layer on the library's operators, forward and backward.
+
+The layer is a router and one linear map per expert:
+
+    logits = x @ router.T;  experts, weights = the top_k of each token
+    out[t] = sum_j weights[t, j] * W[experts[t, j]] @ x[t]
+
+It shows the operators in the order a user calls them and keeps what the backward
+pass needs.  The experts' products run in 8-bit floating point (weights quantised
+once in 128 x 128 blocks, activations for each row and 128 columns), the router's
+forward product in bf16, its weight gradient in 8 bits along the tokens.
+
+Usage: python -m tile_scheduling_gb300.run_workload moe
+"""
+from __future__ import annotations
+
+import torch
+
+import tile_scheduling_gb300 as ts
+
+BLOCK = 128
+
+
+def quantise_blocks(w: torch.Tensor):
+    """Weights [..., R, C] as e4m3 and one fp32 scale for each 128 x 128 block (rows padded to 16 bytes).
+
+    Done once for weights, in plain torch."""
+    R, C = w.shape[-2:]
+    lead = w.shape[:-2]
+    rb, cb = -(-R // BLOCK), -(-C // BLOCK)
+    v = torch.nn.functional.pad(w.float(), (0, cb * BLOCK - C, 0, rb * BLOCK - R)).view(*lead, rb, BLOCK, cb, BLOCK)
+    amax = v.abs().amax((-3, -1)).clamp_min(2.0 ** -100)
+    q = (v * (448.0 / amax)[..., :, None, :, None]).clamp_(-448.0, 448.0).view(*lead, rb * BLOCK, cb * BLOCK)
+    out = torch.empty((*lead, R, -(-C // 16) * 16), dtype=torch.float8_e4m3fn, device=w.device)[..., :C]
+    out.copy_(q[..., :R, :C])
+    return out, (amax / 448.0).contiguous()
+
+
+def _fp8(rows: int, cols: int, dtype=torch.float8_e4m3fn):
+    """Room for a quantised matrix: rows on 16-byte boundaries, scales with their rows contiguous."""
+    q = torch.empty((rows, -(-cols // 16) * 16), dtype=dtype, device="cuda")[:, :cols]
+    return q, torch.empty((-(-cols // BLOCK), rows), dtype=torch.float32, device="cuda").t()
+
+
+class MoeLayer:
+    """router [E, K] and experts [E, N, K] (bf16 or fp32 CUDA tensors); routing options as ts_moe_route."""
+
+    def __init__(self, router: torch.Tensor, experts: torch.Tensor, top_k: int, score="softmax", bias=None, groups=1,
+                 keep_groups=0, group_best=1, renorm=True, scale=1.0):
+        self.router = router.bfloat16().contiguous()
+        self.w, self.sw = quantise_blocks(experts)
+        self.top_k, self.bias, self.score, self.renorm, self.scale = top_k, bias, score, renorm, scale
+        self.groups = dict(groups=groups, keep_groups=keep_groups, group_best=group_best)
+
+    def forward(self, x: torch.Tensor):
+        """x [T, K] bf16 -> (out [T, N] bf16, what backward needs)."""
+        T, K = x.shape
+        E, N = self.w.shape[0], self.w.shape[1]
+        k = self.top_k
+        dev = dict(device=x.device)
+        s = {"x": x, "logits": torch.empty((T, E), **dev), "experts": torch.empty((T, k), dtype=torch.int32, **dev),
+             "weights": torch.empty((T, k), **dev), "offsets": torch.empty(E + 1, dtype=torch.int64, **dev),
+             "order": torch.empty(T * k, dtype=torch.int32, **dev),
+             "position": torch.empty((T, k), dtype=torch.int32, **dev),
+             "y": torch.empty((T * k, N), dtype=torch.bfloat16, **dev)}
+        ts.ts_gemm_bf16_ex(x, self.router, s["logits"])
+        ts.ts_moe_route(s["logits"], s["experts"], s["weights"], bias=self.bias, score=self.score, renorm=self.renorm,
+                        scale=self.scale, **self.groups)
+        ts.ts_moe_plan(s["experts"], s["offsets"], s["order"], s["position"])
+        # tokens laid out by expert and quantised on the way
+        s["q"], s["sq"] = _fp8(T * k, K)
+        ts.ts_quant_fp8(x, s["q"], s["sq"], rows=s["order"], rows_div=k)
+        ts.ts_gemm_fp8_grouped(s["q"], s["sq"], self.w, self.sw, s["y"], s["offsets"])
+        out = torch.empty((T, N), dtype=torch.bfloat16, **dev)
+        ts.ts_moe_combine(s["y"], s["position"], out, weights=s["weights"])
+        return out, s
+
+    def backward(self, s: dict, grad_out: torch.Tensor):
+        """grad_out [T, N] bf16 -> (grad_x [T, K] bf16, grad_router [E, K] fp32)."""
+        T, K = s["x"].shape
+        E, N = self.w.shape[0], self.w.shape[1]
+        k = self.top_k
+        dev = dict(device=grad_out.device)
+        grad_y = torch.empty((T * k, N), dtype=torch.bfloat16, **dev)
+        grad_w = torch.empty((T, k), **dev)
+        ts.ts_moe_combine_grad(grad_out, s["y"], s["position"], s["weights"], grad_y, grad_w)
+        # the experts' input gradient: gradients in e5m2, the same weights read the other way
+        gq, gs = _fp8(T * k, N, torch.float8_e5m2)
+        ts.ts_quant_fp8(grad_y, gq, gs)
+        grad_rows = torch.empty((T * k, K), dtype=torch.bfloat16, **dev)
+        ts.ts_gemm_fp8_grouped(gq, gs, self.w, self.sw, grad_rows, s["offsets"], trans_b=True)
+        grad_x = torch.empty((T, K), dtype=torch.bfloat16, **dev)
+        ts.ts_moe_combine(grad_rows, s["position"], grad_x)  # the gather's gradient: a sum over the token's slots
+        # the router: through the weights to the logits, then its weights' gradient along the tokens
+        grad_logits = torch.empty_like(s["logits"])
+        ts.ts_moe_route_grad(s["logits"], s["experts"], grad_w, grad_logits, score=self.score, renorm=self.renorm,
+                             scale=self.scale)
+        lq, ls = _fp8(E, T)
+        xq, xs = _fp8(K, T)
+        ts.ts_quant_fp8(grad_logits, lq, ls, transpose=True)
+        ts.ts_quant_fp8(s["x"], xq, xs, transpose=True)
+        grad_router = torch.empty((E, K), **dev)
+        ts.ts_gemm_fp8(lq, ls, xq, xs, grad_router)
+        from_router = torch.empty((T, K), dtype=torch.bfloat16, **dev)
+        ts.ts_gemm_bf16_ex(grad_logits.bfloat16(), self.router.t().contiguous(), from_router)
+        return grad_x.add_(from_router), grad_router

@@ -1,6 +1,7 @@
 """Run one named workload a few times (for profilers such as ncu); prints nothing but a summary line.
 
-Usage: python -m tile_scheduling_gb300.run_workload {gemm256,gemm4096,gemm8192,ragged,smallk,grouped,copy,rows}
+Usage: python -m tile_scheduling_gb300.run_workload {gemm256,gemm4096,gemm8192,ragged,smallk,grouped,copy,rows,
+           moe,fp8}
            [--launches N] [--sched static|clc|nonpersistent] [--tile auto|128x128|128x256|256x256]
 """
 from __future__ import annotations
@@ -26,7 +27,7 @@ GEMMS = {"gemm256": synth.GEMM_256, "gemm4096": synth.GEMM_4096, "gemm8192": syn
 
 def main(argv=None):
     ap = argparse.ArgumentParser()
-    ap.add_argument("workload", choices=sorted(GEMMS) + ["grouped", "copy", "rows"])
+    ap.add_argument("workload", choices=sorted(GEMMS) + ["grouped", "copy", "rows", "moe", "fp8"])
     ap.add_argument("--launches", type=int, default=3)
     ap.add_argument("--sched", default=None, choices=["static", "clc", "nonpersistent"])
     ap.add_argument("--tile", default=None)
@@ -57,6 +58,40 @@ def main(argv=None):
             ts.ts_copy_i16_rows(src, dst, off, sched=sched, chunk=a.chunk, workspace=ws, pack=a.pack)
         ts.ts_sync_and_check()
         print(f"{synth.ROWS.name}: {sched} chunk {a.chunk} pack {a.pack} x{a.launches} ok")
+        return 0
+    if a.workload == "moe":
+        # a mixture-of-experts layer, forward and backward: every operator of one, in its order
+        from tile_scheduling_gb300.moe import MoeLayer
+
+        T, E, N, K, k = 2048, 32, 2048, 2048, 4
+        g = torch.Generator("cuda").manual_seed(1)
+        x = torch.randn((T, K), device="cuda", generator=g).bfloat16()
+        layer = MoeLayer(torch.randn((E, K), device="cuda", generator=g) / K ** 0.5,
+                         torch.randn((E, N, K), device="cuda", generator=g) / K ** 0.5, k)
+        grad_out = torch.randn((T, N), device="cuda", generator=g).bfloat16()
+        for _ in range(a.launches):
+            _, saved = layer.forward(x)
+            layer.backward(saved, grad_out)
+        ts.ts_sync_and_check()
+        rows = saved["offsets"].diff()
+        print(f"moe {T} tokens x {k} of {E} experts, {N} x {K}: {int(rows.min())} to {int(rows.max())} rows each, "
+              f"x{a.launches} ok")
+        return 0
+    if a.workload == "fp8":
+        # one block-scaled 8-bit product (4096^3)
+        from tile_scheduling_gb300.moe import quantise_blocks
+
+        n = 4096
+        g = torch.Generator("cuda").manual_seed(1)
+        x = torch.randn((n, n), device="cuda", generator=g).bfloat16()
+        A, SA = torch.empty((n, n), dtype=torch.float8_e4m3fn, device="cuda"), torch.empty((n // 128, n), device="cuda").t()
+        ts.ts_quant_fp8(x, A, SA)
+        B, SB = quantise_blocks(torch.randn((n, n), device="cuda", generator=g))
+        D = torch.empty((n, n), dtype=torch.bfloat16, device="cuda")
+        for _ in range(a.launches):
+            ts.ts_gemm_fp8(A, SA, B, SB, D, tile=a.tile or "auto")
+        ts.ts_sync_and_check()
+        print(f"fp8 {n}^3 {a.tile or 'auto'} x{a.launches} ok")
         return 0
     if a.workload == "grouped":
         w = synth.GROUPED
