@@ -485,6 +485,32 @@ def test_combine_grad_against_differences(lib):
         assert abs((value(y + d, w) - value(y - d, w)) / (2 * h) - float(gy[r, r % N])) < 2e-3
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,k,N", [(5, 3, 31), (5, 3, 33), (9, 9, 1023), (9, 5, 1025), (3, 8, 2049), (3, 1, 4095)])
+def test_combine_odd_rows(lib, T, k, N, dtype):
+    # rows on no common boundary: dense rows of odd length, and a base off the 16-byte grid
+    y, pos, w, go = _combine_inputs(T, k, N, dtype, N, 0)
+    flat = torch.full((T * N + 2,), 5.0, dtype=dtype, device="cuda")
+    out = flat[1:-1].view(T, N)
+    lib.ts_moe_combine(y, pos, out, weights=w)
+    gy, gw = torch.full_like(y, 7.0), torch.empty_like(w)
+    lib.ts_moe_combine_grad(go, y, pos, w, gy, gw)
+    lib.ts_sync_and_check()
+    there = pos >= 0
+    rows = y.double()[pos.clamp_min(0).long()] * there[:, :, None]
+    terms = rows * w.double()[:, :, None]
+    ref, mag = terms.sum(1), terms.abs().sum(1)
+    # k fused multiply-adds in fp32, then the output's rounding
+    bound = k * 2.0 ** -24 * mag + (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24) * ref.abs() + 1e-37
+    assert bool(((out.double() - ref).abs() <= bound).all())
+    assert flat[0] == 5 and flat[-1] == 5
+    prod = rows * go.double()[:, None, :]
+    assert bool(((gw.double() - prod.sum(2)).abs() <= (N + 16) * 2.0 ** -24 * prod.abs().sum(2) + 1e-37).all())
+    want = torch.full_like(y, 7.0)
+    want[pos[there].long()] = (go.float()[:, None, :] * w[:, :, None])[there].to(dtype)
+    assert torch.equal(gy, want)
+
+
 def test_combine_refusals(lib):
     y, pos, w, go = _combine_inputs(4, 2, 64, torch.float32, 1)
     out = torch.zeros((4, 64), device="cuda")

@@ -26,62 +26,90 @@ struct CombineParams {
     int64_t T, N, R;
     int64_t ldy, ldo, ldg;  // rows of y, of out (or grad_out), of grad_y
     int32_t k;
-    int32_t vec;
     unsigned long long *status;
 };
 
-template <class T>
-constexpr int kVec = 16 / sizeof(T);
-
-// kVec values at x as they lie in memory; those past n (the row's end) read as 0.
-template <class T>
-__device__ __forceinline__ uint4 load_raw(const T *x, bool vec, int64_t n) {
-    if (vec && n >= kVec<T>) return __ldcs(reinterpret_cast<const uint4 *>(x));
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < kVec<T>; ++i) {
-        if (i < n) {
-            if constexpr (sizeof(T) == 4)
-                w[i] = __float_as_uint(x[i]);
-            else
-                w[i >> 1] |= uint32_t(x[i]) << (16 * (i & 1));
-        }
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Value i of a raw vector as fp32.
-template <class T>
-__device__ __forceinline__ float value_at(const uint4 &a, int i) {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
-    return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-}
-
-template <class T>
-__device__ __forceinline__ void store_vec(T *x, bool vec, int64_t n, const float (&v)[kVec<T>]) {
+// A thread's values of a row as they lie in memory.  VEC (the rows start on 16-byte
+// boundaries): the 16 bytes from column c on, in one load.  Else four values 32 columns
+// apart, so that a warp's loads and stores of one value each still fill whole sectors
+// (8192 tokens, eight slots, 4095 bf16 values: 169 us and 290 for the gradient; with eight
+// neighbours a thread 278 and 727; rows of 4096, VEC, 107 and 187).
+template <class T, bool VEC>
+struct Vals {
+    static constexpr int COUNT = VEC ? 16 / sizeof(T) : 4;
     uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 4)
-            w[i] = __float_as_uint(v[i]);
-        else
-            w[i] = pack_bf16x2(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]));
+
+    // a thread's first column among those of its CTA
+    static __device__ __forceinline__ int64_t first(int thread) {
+        return VEC ? int64_t(thread) * COUNT : int64_t(thread & ~31) * COUNT + (thread & 31);
     }
-    if (vec && n >= kVec<T>) {
-        __stcs(reinterpret_cast<uint4 *>(x), make_uint4(w[0], w[1], w[2], w[3]));
-    } else {
+    // those of row x from column c on; the ones past the N-th read as 0
+    __device__ __forceinline__ void load(const T *x, int64_t c, int64_t N) {
+        if constexpr (VEC) {
+            if (c + COUNT <= N) {
+                const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(x + c));
+                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+                return;
+            }
+            w[0] = w[1] = w[2] = w[3] = 0u;
 #pragma unroll
-        for (int i = 0; i < kVec<T>; ++i) {
-            if (i < n) {
+            for (int i = 0; i < COUNT; ++i)
+                if (c + i < N) {
+                    if constexpr (sizeof(T) == 4)
+                        w[i] = __float_as_uint(x[c + i]);
+                    else
+                        w[i >> 1] |= uint32_t(x[c + i]) << (16 * (i & 1));
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < COUNT; ++i) {
+                const T v = c + 32 * i < N ? x[c + 32 * i] : T(0);
                 if constexpr (sizeof(T) == 4)
-                    x[i] = __uint_as_float(w[i]);
+                    w[i] = __float_as_uint(v);
                 else
-                    x[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+                    w[i] = v;
             }
         }
     }
-}
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        if constexpr (!VEC) return __uint_as_float(w[i] << 16);
+        return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+    static __device__ __forceinline__ void store(T *x, int64_t c, int64_t N, const float (&v)[COUNT]) {
+        if constexpr (VEC) {
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (sizeof(T) == 4)
+                    o[i] = __float_as_uint(v[i]);
+                else
+                    o[i] = pack_bf16x2(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]));
+            }
+            if (c + COUNT <= N) {
+                __stcs(reinterpret_cast<uint4 *>(x + c), make_uint4(o[0], o[1], o[2], o[3]));
+                return;
+            }
+#pragma unroll
+            for (int i = 0; i < COUNT; ++i)
+                if (c + i < N) {
+                    if constexpr (sizeof(T) == 4)
+                        x[c + i] = v[i];
+                    else
+                        x[c + i] = static_cast<T>(o[i >> 1] >> (16 * (i & 1)));
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < COUNT; ++i)
+                if (c + 32 * i < N) {
+                    if constexpr (sizeof(T) == 4)
+                        x[c + 32 * i] = v[i];
+                    else
+                        x[c + 32 * i] = static_cast<T>(pack_bf16x2(__float_as_uint(v[i]), 0u));
+                }
+        }
+    }
+};
 
 // The row of y that slot (t, j) takes, or -1.
 __device__ __forceinline__ int32_t slot_row(const CombineParams &p, int64_t t, int32_t j) {
@@ -98,20 +126,20 @@ __device__ __forceinline__ int32_t slot_row(const CombineParams &p, int64_t t, i
     return at;
 }
 
-// One CTA per token and kThreads vectors of its row.  KS: slots whose rows are in
+// One CTA per token and kThreads threads' columns.  KS: slots whose rows are in
 // flight together (raw, four registers each, so that several CTAs fit an SM).
-template <class T, int KS>
+template <class T, int KS, bool VEC>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant__ CombineParams p) {
+    using Row = Vals<T, VEC>;
     grid_dep_wait();
     grid_dep_launch();
-    constexpr int V = kVec<T>;
     const int64_t t = blockIdx.x;
-    const int64_t c = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * V;
-    float sum[V];
+    const int64_t c = static_cast<int64_t>(blockIdx.y) * blockDim.x * Row::COUNT + Row::first(threadIdx.x);
+    float sum[Row::COUNT];
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum[i] = 0.f;
+    for (int i = 0; i < Row::COUNT; ++i) sum[i] = 0.f;
     for (int32_t j0 = 0; j0 < p.k; j0 += KS) {
-        uint4 v[KS];
+        Row v[KS];
         float w[KS];
         int32_t at[KS];
 #pragma unroll
@@ -121,25 +149,27 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
         }
 #pragma unroll
         for (int j = 0; j < KS; ++j)
-            if (at[j] >= 0) v[j] = load_raw(static_cast<const T *>(p.y) + at[j] * p.ldy + c, p.vec, p.N - c);
+            if (at[j] >= 0) v[j].load(static_cast<const T *>(p.y) + at[j] * p.ldy, c, p.N);
 #pragma unroll
         for (int j = 0; j < KS; ++j)
             if (at[j] >= 0) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) sum[i] = fmaf(w[j], value_at<T>(v[j], i), sum[i]);
+                for (int i = 0; i < Row::COUNT; ++i) sum[i] = fmaf(w[j], v[j][i], sum[i]);
             }
     }
-    if (c < p.N) store_vec(static_cast<T *>(p.out) + t * p.ldo + c, p.vec, p.N - c, sum);
+    if (c < p.N) Row::store(static_cast<T *>(p.out) + t * p.ldo, c, p.N, sum);
 }
 
-// One CTA per token: grad_out's row is read for each group of four slots (from L2
-// after the first; eight at once would leave room for one CTA on an SM), the slots' dot products are reduced in fixed order.
-template <class T>
+// One CTA per token: grad_out's row is read for each group of four slots (from L2 after
+// the first; eight at once would leave room for one CTA on an SM), the slots' dot products
+// are reduced in fixed order.
+template <class T, bool VEC>
 __global__ void __launch_bounds__(kGradThreads, 2) combine_grad_kernel(const __grid_constant__ CombineParams p) {
+    using Row = Vals<T, VEC>;
     __shared__ float part[kGradSlots][kGradThreads / 32];
     grid_dep_wait();
     grid_dep_launch();
-    constexpr int V = kVec<T>, KS = kGradSlots;
+    constexpr int KS = kGradSlots;
     const int64_t t = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int32_t j0 = 0; j0 < p.k; j0 += KS) {
@@ -152,23 +182,23 @@ __global__ void __launch_bounds__(kGradThreads, 2) combine_grad_kernel(const __g
             dot[j] = 0.f;
         }
 #pragma unroll 1
-        for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < p.N; c += static_cast<int64_t>(blockDim.x) * V) {
-            uint4 y[KS];
-            const uint4 g = load_raw(static_cast<const T *>(p.grad_out) + t * p.ldo + c, p.vec, p.N - c);
+        for (int64_t c = Row::first(threadIdx.x); c < p.N; c += static_cast<int64_t>(blockDim.x) * Row::COUNT) {
+            Row g, y[KS];
+            g.load(static_cast<const T *>(p.grad_out) + t * p.ldo, c, p.N);
 #pragma unroll
             for (int j = 0; j < KS; ++j)
-                if (at[j] >= 0) y[j] = load_raw(static_cast<const T *>(p.y) + at[j] * p.ldy + c, p.vec, p.N - c);
+                if (at[j] >= 0) y[j].load(static_cast<const T *>(p.y) + at[j] * p.ldy, c, p.N);
 #pragma unroll
             for (int j = 0; j < KS; ++j) {
                 if (at[j] < 0) continue;
-                float o[V];
+                float o[Row::COUNT];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float x = value_at<T>(g, i);
-                    dot[j] = fmaf(x, value_at<T>(y[j], i), dot[j]);
+                for (int i = 0; i < Row::COUNT; ++i) {
+                    const float x = g[i];
+                    dot[j] = fmaf(x, y[j][i], dot[j]);
                     o[i] = w[j] * x;
                 }
-                store_vec(static_cast<T *>(p.grad_y) + at[j] * p.ldg + c, p.vec, p.N - c, o);
+                Row::store(static_cast<T *>(p.grad_y) + at[j] * p.ldg, c, p.N, o);
             }
         }
         if (p.grad_w) {
@@ -245,14 +275,17 @@ ts_status ts_moe_combine(const void *y, const int32_t *position, const float *we
     p.ldy = ldy;
     p.ldo = ldo;
     p.k = top_k;
-    p.vec = row16(y, ldy, esize) && row16(out, ldo, esize);
-    const int per = 16 / esize, threads = cta_threads(N, per, kThreads);
+    const bool vec = row16(y, ldy, esize) && row16(out, ldo, esize);
+    const int per = vec ? 16 / esize : 4, threads = cta_threads(N, per, kThreads);
     if (cdiv(N, threads * per) > 65535) return fail(TS_ERR_UNSUPPORTED, "rows of %lld values", static_cast<long long>(N));
     const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(cdiv(N, threads * per))), block(threads);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     auto go = [&](auto *k4, auto *k8) { return launch_pdl(top_k <= 4 ? k4 : k8, grid, block, 0, st, p); };
-    cudaError_t e = dtype == TS_OUT_F32 ? go(combine_kernel<float, 4>, combine_kernel<float, 8>)
-                                        : go(combine_kernel<uint16_t, 4>, combine_kernel<uint16_t, 8>);
+    cudaError_t e = dtype == TS_OUT_F32
+                        ? (vec ? go(combine_kernel<float, 4, true>, combine_kernel<float, 8, true>)
+                               : go(combine_kernel<float, 4, false>, combine_kernel<float, 8, false>))
+                        : (vec ? go(combine_kernel<uint16_t, 4, true>, combine_kernel<uint16_t, 8, true>)
+                               : go(combine_kernel<uint16_t, 4, false>, combine_kernel<uint16_t, 8, false>));
     return e == cudaSuccess ? TS_OK : cuda_fail(e, "combine launch");
 }
 
@@ -295,11 +328,14 @@ ts_status ts_moe_combine_grad(const void *grad_out, const void *y, const int32_t
     p.ldo = ldo;
     p.ldg = ldg;
     p.k = top_k;
-    p.vec = row16(y, ldy, esize) && row16(grad_out, ldo, esize) && row16(grad_y, ldg, esize);
-    const dim3 grid(static_cast<unsigned>(T)), block(cta_threads(std::max<int64_t>(N, 1), 16 / esize, kGradThreads));
+    const bool vec = row16(y, ldy, esize) && row16(grad_out, ldo, esize) && row16(grad_y, ldg, esize);
+    const dim3 grid(static_cast<unsigned>(T)),
+        block(cta_threads(std::max<int64_t>(N, 1), vec ? 16 / esize : 4, kGradThreads));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = dtype == TS_OUT_F32 ? launch_pdl(combine_grad_kernel<float>, grid, block, 0, st, p)
-                                        : launch_pdl(combine_grad_kernel<uint16_t>, grid, block, 0, st, p);
+    auto go = [&](auto *kernel) { return launch_pdl(kernel, grid, block, 0, st, p); };
+    cudaError_t e = dtype == TS_OUT_F32
+                        ? (vec ? go(combine_grad_kernel<float, true>) : go(combine_grad_kernel<float, false>))
+                        : (vec ? go(combine_grad_kernel<uint16_t, true>) : go(combine_grad_kernel<uint16_t, false>));
     return e == cudaSuccess ? TS_OK : cuda_fail(e, "combine gradient launch");
 }
 
