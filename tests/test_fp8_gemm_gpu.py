@@ -309,3 +309,31 @@ def test_expanded_tensors(lib):
                                                 torch.tensor([0, 10, M], device="cuda"))):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tile", ["128x128", "128x256", "256x256"])
+@pytest.mark.parametrize("N,before,after", [(520, 8, 16), (520, 2, 8), (518, 1, 1), (517, 0, 0), (517, 8, 11), (393, 3, 1)])
+def test_grouped_output_pitches(lib, N, before, after, tile, out):
+    # D's rows and base on 16-, 4- and 2-byte boundaries; groups that end inside a warp's 32 rows
+    off = [2, 70, 71, 71, 230, 262]
+    M, K = off[-1] + 3, 200
+    A, SA, B, SB, a, b = _problem(M, N, K, N + before, True, groups=len(off) - 1)
+    wide = torch.full((M, before + N + after), -777.0, dtype=out, device="cuda")
+    D = wide[:, before:before + N]
+    lib.ts_gemm_fp8_grouped(A, SA, B, SB, D, torch.tensor(off, device="cuda"), tile=tile)
+    lib.ts_sync_and_check()
+    ref = torch.full(wide.shape, -777.0, dtype=torch.float64)
+    ref[off[0]:off[-1], before:before + N] = _grouped_ref(off, a, b, N)[off[0]:off[-1]]
+    assert torch.equal(wide.cpu(), ref.to(out))
+
+
+@pytest.mark.parametrize("workers", [1, 3, 7, 40])
+def test_worker_cap(lib, workers):
+    # few tiles and a long K: without a cap each tile's K blocks are shared by several workers
+    M, N, K = 9, 300, 4096
+    A, SA, B, SB, a, b = _problem(M, N, K, 21, True)
+    D = torch.full((M, N), float("nan"), device="cuda")
+    lib.ts_gemm_fp8(A, SA, B, SB, D, max_workers=workers)
+    lib.ts_sync_and_check()
+    _check(D, a @ b, None, K, True, f"{workers} workers")

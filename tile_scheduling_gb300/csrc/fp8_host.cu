@@ -183,8 +183,13 @@ ts_status fp8_product(const void *A, const float *SA, const void *B, const float
         const int box[3] = {128, o->trans_b ? 128 : bn / cg, 1};
         if ((s = encode_map(&L.b, B, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, dims, strides, box)) != TS_OK) return s;
     }
-    p.vec_store = reinterpret_cast<uintptr_t>(D) % 16 == 0 && (ldd * esize) % 16 == 0;
-    p.tma_store = p.vec_store;
+    p.store_bytes = 2;
+    for (int b : {16, 4})
+        if (reinterpret_cast<uintptr_t>(D) % b == 0 && (ldd * esize) % b == 0) {
+            p.store_bytes = b;
+            break;
+        }
+    p.tma_store = p.store_bytes == 16;
     if (p.tma_store) {
         const int64_t dims[3] = {N, M, 1}, strides[2] = {ldd * esize, M * ldd * esize};
         const int box[3] = {128 / esize, 32, 1};  // a warp's staging buffer
@@ -206,6 +211,8 @@ ts_status fp8_product(const void *A, const float *SA, const void *B, const float
     // single token's weights) stream through the whole GPU.  1 x 4096 x 8192 (128-row
     // tiles): 19.8 us without, 12.6 with four CTAs a tile.
     p.split = !grouped && tile == TS_TILE_128x128 ? static_cast<int32_t>(split_of(units)) : 1;
+    if (o->max_workers > 0 && units * p.split > o->max_workers)
+        p.split = static_cast<int32_t>(std::max<int64_t>(1, o->max_workers / units));
     p.raster_group = kRasterGroup;
     p.div_group_tiles = fast_div_for(kRasterGroup * tiles_n);
     p.div_group_rows = fast_div_for(kRasterGroup);

@@ -22,7 +22,7 @@ struct Fp8Params {
     int32_t trans_b;    // 1: B is [K][N]
     int32_t out;        // OUT_BF16 / OUT_F32
     int32_t tma_store;  // 1: D's rows and base suit a TMA store
-    int32_t vec_store;  // 1: D's rows and base suit 16-byte stores
+    int32_t store_bytes;  // 16, 4 or 2: what D's base and rows are aligned to
     uint32_t idesc;     // MMA instruction descriptor without the tile shape
     int32_t groups;     // grouped product: groups, and their row offsets on the device
     const int64_t *offsets;
