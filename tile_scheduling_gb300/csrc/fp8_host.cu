@@ -151,9 +151,9 @@ ts_status fp8_product(const void *A, const float *SA, const void *B, const float
         // / 15.9 / 16.9 us, 1024 19.7 / 18.0 / 18.0, 2048 35.7 / 31.4 / 31.0.
         const int64_t u1 = cdiv(M, 128) * cdiv(N, 128), u2 = cdiv(M, 128) * cdiv(N, 256),
                       u3 = cdiv(M, 256) * cdiv(N, 256), s1 = split_of(u1);
-        const int64_t c1 = cdiv(u1, sms_) * cdiv(kblocks, s1) * (rows ? 740 : 430) + (s1 > 1 ? 3000 : 0);
-        const int64_t c2 = cdiv(u2, sms_) * kblocks * (rows ? 1280 : 740);
-        const int64_t w3 = cdiv(u3, sms_ / 2), c3 = w3 * kblocks * (rows ? 1240 : w3 > 1 ? 720 : 770);
+        const int64_t c1 = cdiv(u1, sms_) * cdiv(kblocks, s1) * (rows ? 660 : 430) + (s1 > 1 ? 3000 : 0);
+        const int64_t c2 = cdiv(u2, sms_) * kblocks * (rows ? 1230 : 740);
+        const int64_t w3 = cdiv(u3, sms_ / 2), c3 = w3 * kblocks * (rows ? 1195 : w3 > 1 ? 720 : 770);
         tile = c1 <= c2 && c1 <= c3 ? TS_TILE_128x128 : c2 <= c3 ? TS_TILE_128x256 : TS_TILE_256x256_2CTA;
     }
     const int bn = tile == TS_TILE_128x128 ? 128 : 256, cg = tile == TS_TILE_256x256_2CTA ? 2 : 1;

@@ -60,6 +60,13 @@ struct Fp8Cfg {
     static constexpr int SLOTS = 512 / SC;
     static constexpr int H = BN / SC;
     static constexpr int COLS = BN / 2;  // columns of one promotion warp
+    // Columns of one TMEM load; PIPE: the next load is issued before a load's columns are
+    // added.  Row scales, 4096 x 4096 x 8191 on 128x128 / 128x256 / pair: 157 / 170 / 162 us,
+    // without 176 / 177 / 168.  Block scales, 8192 x 8192 x 2048: 128x128 134 us, without
+    // 138; but 155 and 117 on the wider tiles against 120 and 112, and 256
+    // rows over 64 experts of 2048 x 2048 (32-row tiles) 44.0 against 43.6.
+    static constexpr bool PIPE = ROWS || (BN == 128 && AR == BM);
+    static constexpr int LD = PIPE ? 32 : 64;
     static constexpr int TEMPTY_ARRIVALS = EPI_WARPS / H * CG;
     static constexpr int TMEM_COLS = 512;
     // First column, within the tile, of a promotion warp's 64-column segment seg.
@@ -582,28 +589,33 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC, AR>::THREADS
                     }
                 };
                 load_cols(0);
+                constexpr int NC = C::COLS / C::LD;
+                uint32_t v[C::PIPE ? 2 : 1][C::LD];
 #pragma unroll
-                for (int c = 0; c < C::COLS / 64; ++c) {
-                    uint32_t v[64];
-                    tmem_ld(taddr + 64 * c, v);
+                for (int c = 0; c < NC; ++c) {
+                    if (!C::PIPE || c == 0) tmem_ld(taddr + C::LD * c, v[0]);
                     tmem_ld_wait();
-                    // handed back once its last columns are in registers
-                    if (c + 1 == C::COLS / 64) release();
+                    if (c + 1 == NC)
+                        release();  // the slot's last columns are in registers
+                    else if constexpr (C::PIPE)
+                        tmem_ld(taddr + C::LD * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        load_cols(4 * c + g + 1);
+                    for (int g = 0; g < C::LD / 16; ++g) {
+                        const int gg = C::LD / 16 * c + g;
+                        load_cols(gg + 1);
                         if constexpr (ROWS) {
                             // the products first: each multiply-add waits for none of them
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) cs[g & 1][i] = mul2(cs[g & 1][i], s2[0]);
+                            for (int i = 0; i < 8; ++i) cs[gg & 1][i] = mul2(cs[gg & 1][i], s2[0]);
                         }
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const uint64_t x = pair_u32(v[16 * g + 2 * i], v[16 * g + 2 * i + 1]);
+                            const uint32_t *const at = v[C::PIPE ? c & 1 : 0] + 16 * g + 2 * i;
+                            const uint64_t x = pair_u32(at[0], at[1]);
                             if constexpr (ROWS)
-                                fma2(sum[32 * c + 8 * g + i], x, cs[g & 1][i]);
+                                fma2(sum[8 * gg + i], x, cs[gg & 1][i]);
                             else
-                                fma2(sum[32 * c + 8 * g + i], x, s2[NB == 2 ? c : 0]);
+                                fma2(sum[8 * gg + i], x, s2[NB == 2 ? gg / 4 : 0]);
                         }
                     }
                 }
