@@ -17,9 +17,6 @@ namespace {
 constexpr int64_t kMaxDim = 0x7fffffffLL;
 constexpr double kDefaultTimeoutS = 2.0;
 constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
-// K split over a cluster: at most the portable cluster size, and not below this many
-// blocks each (a split costs an exchange of partial sums, some 2 us).
-constexpr int64_t kMaxSplit = 8, kMinSplitBlocks = 4;
 constexpr int kRasterGroup = 8;  // tile rows of a raster band, as the bf16 product's default
 
 // K = 0: the rows of D (grouped: of group blockIdx.y) are empty sums.
@@ -132,42 +129,60 @@ ts_status fp8_product(const void *A, const float *SA, const void *B, const float
     const int sms = device_sms(current_device());
     if (sms <= 0) return fail(TS_ERR_CUDA, "cannot query the SM count");
     const int64_t sms_ = sms;  // 64-bit for the products below
-    // K split over a cluster for a product of `units` 128x128 tiles
-    auto split_of = [&](int64_t units) {
-        return std::max<int64_t>(
-            1, std::min<int64_t>(std::min<int64_t>(kMaxSplit, sms_ / std::max<int64_t>(units, 1)), kblocks / kMinSplitBlocks));
+    // Few rows: tiles of 32 (of which the MMA makes 128), so that the ring holds nine
+    // stages of weights instead of five: 1 x 4096 x 8192 12.6 -> 9.6 us.
+    const bool few = !rows && (grouped ? M / groups <= 16 : M <= 32);
+    // CTAs of a cluster that share the K blocks of each of `units` 128x128 tiles, and the
+    // cycles that a tile then takes: 430 a K block (660 with row scales) and, from two CTAs
+    // on, the exchange of their partial sums.  Measured, 128 x 4096 x 4096 (32 tiles) by 1 /
+    // 2 / 4 CTAs 10.2 / 9.1 / 7.9 us, 128 x 512 x 8192 (4 tiles) by 1 / 2 / 4 / 8 16.9 / 12.2
+    // / 8.9 / 7.7; but 128 x 2048 x 8192 by 4 / 8 9.2 / 15.4: its 16 clusters of eight do
+    // not run at once.
+    auto split_of = [&](int64_t units, int64_t &cycles) {
+        int64_t best = 1;
+        cycles = kblocks * (rows ? 660 : 430);
+        const Fp8Variant *v1 = find_fp8(128, 1, rows, false, few ? 32 : 128);
+        for (int64_t c = 2; c <= kMaxCluster && c <= kblocks && units * c <= sms_; ++c) {
+            if (o->max_workers > 0 && units * c > o->max_workers) break;
+            const int64_t t = cdiv(kblocks, c) * (rows ? 660 : 430) + 3000 + 16 * std::min<int64_t>(M, 128) + 150 * c;
+            if (t >= cycles || (v1 && v1->clusters(static_cast<int>(c)) < units)) continue;
+            best = c;
+            cycles = t;
+        }
+        return best;
     };
     int tile = o->tile;
     if (tile == TS_TILE_AUTO && grouped) {
-        // By the mean rows of a group.  Measured, 32 groups of 4096 x 2048, 128x128 /
-        // 128x256 / pair: 32 rows each 49 / 51 / 60 us, 128 62 / 61 / 70, 256 92 / 85 / 91,
-        // 512 157 / 138 / 143.
-        const int64_t mean = M / groups;
-        tile = mean >= 1024 ? TS_TILE_256x256_2CTA : mean >= 96 ? TS_TILE_128x256 : TS_TILE_128x128;
+        // By the mean rows of a group.  Measured, 32 groups of 4096 x 2048, 128x128 / 128x256
+        // / pair: 64 rows each 48 / 50 / 60 us, 128 62 / 60 / 69, 256 89 / 82 / 85, 512 162 /
+        // 139 / 145; 8 groups of 2048 rows 142 / 119 / 120.
+        tile = M / groups >= 96 ? TS_TILE_128x256 : TS_TILE_128x128;
     } else if (tile == TS_TILE_AUTO) {
         // The tile with the fewest cycles: waves of workers times what a K block of a tile
-        // takes (the measured steady state; a pair's tiles pay from the second wave on, by
-        // their smaller L2 traffic).  Measured, N = K = 4096, the same order: M = 512 11.4
-        // / 15.9 / 16.9 us, 1024 19.7 / 18.0 / 18.0, 2048 35.7 / 31.4 / 31.0.
+        // takes (measured steady states; a pair's, with its smaller L2 traffic, is shorter
+        // while a wave is the only one, but it starts later).  Measured, N = K = 4096,
+        // 128x128 / 128x256 / pair: M = 512 10.9 / 15.0 / 15.6 us, 1024 19.2 / 17.7 / 16.6,
+        // 1536 26.7 / 30.0 / 28.7, 2048 34.8 / 30.8 / 29.1; 2048^3 11.5 / 9.9 / 10.6; row
+        // scales, M = 512 14.1 / 22.7 / 23.2, 1024 25.6 / 25.1 / 23.6, 2048 48.2 / 44.8 / 43.2.
         const int64_t u1 = cdiv(M, 128) * cdiv(N, 128), u2 = cdiv(M, 128) * cdiv(N, 256),
-                      u3 = cdiv(M, 256) * cdiv(N, 256), s1 = split_of(u1);
-        const int64_t c1 = cdiv(u1, sms_) * cdiv(kblocks, s1) * (rows ? 660 : 430) + (s1 > 1 ? 3000 : 0);
+                      u3 = cdiv(M, 256) * cdiv(N, 256);
+        int64_t c1;
+        split_of(u1, c1);
+        c1 *= cdiv(u1, sms_);
         const int64_t c2 = cdiv(u2, sms_) * kblocks * (rows ? 1230 : 740);
-        const int64_t w3 = cdiv(u3, sms_ / 2), c3 = w3 * kblocks * (rows ? 1195 : w3 > 1 ? 720 : 770);
+        const int64_t w3 = cdiv(u3, sms_ / 2);
+        const int64_t c3 = w3 > 1 ? w3 * kblocks * (rows ? 1195 : 720) : kblocks * (rows ? 1120 : 640) + 2000;
         tile = c1 <= c2 && c1 <= c3 ? TS_TILE_128x128 : c2 <= c3 ? TS_TILE_128x256 : TS_TILE_256x256_2CTA;
     }
     const int bn = tile == TS_TILE_128x128 ? 128 : 256, cg = tile == TS_TILE_256x256_2CTA ? 2 : 1;
-    // Few rows: tiles of 32 (of which the MMA makes 128), so that the ring holds nine
-    // stages of weights instead of five: 1 x 4096 x 8192 12.6 -> 9.6 us.
-    const bool few = tile == TS_TILE_128x128 && !rows && (grouped ? M / groups <= 16 : M <= 32);
-    const int a_rows = few ? 32 : 128;
+    const int a_rows = few && tile == TS_TILE_128x128 ? 32 : 128;
     const Fp8Variant *v = find_fp8(bn, cg, rows, grouped, a_rows);
     if (!v) return fail(TS_ERR_UNSUPPORTED, "no compiled variant");
 
     Fp8Launch L;
     std::memset(&L, 0, sizeof L);
     Fp8Params &p = L.p;
-    const int64_t tile_m = few ? a_rows : 128 * cg;
+    const int64_t tile_m = a_rows < 128 ? a_rows : 128 * cg;
     const int64_t tiles_m = cdiv(M, tile_m), tiles_n = cdiv(N, bn);
     // grouped: every group may end in a partial tile
     const int64_t units = grouped ? (tiles_m + groups) * tiles_n : tiles_m * tiles_n;
@@ -207,12 +222,8 @@ ts_status fp8_product(const void *A, const float *SA, const void *B, const float
     p.tiles_n = static_cast<int32_t>(tiles_n);
     p.num_kb = static_cast<int32_t>(kblocks);
     p.num_units = static_cast<int32_t>(units);
-    // Few tiles: a cluster of CTAs shares each tile's K blocks, so that the operands (a
-    // single token's weights) stream through the whole GPU.  1 x 4096 x 8192 (128-row
-    // tiles): 19.8 us without, 12.6 with four CTAs a tile.
-    p.split = !grouped && tile == TS_TILE_128x128 ? static_cast<int32_t>(split_of(units)) : 1;
-    if (o->max_workers > 0 && units * p.split > o->max_workers)
-        p.split = static_cast<int32_t>(std::max<int64_t>(1, o->max_workers / units));
+    int64_t tile_cycles;
+    p.split = !grouped && tile == TS_TILE_128x128 ? static_cast<int32_t>(split_of(units, tile_cycles)) : 1;
     p.raster_group = kRasterGroup;
     p.div_group_tiles = fast_div_for(kRasterGroup * tiles_n);
     p.div_group_rows = fast_div_for(kRasterGroup);

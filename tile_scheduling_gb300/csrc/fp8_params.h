@@ -10,6 +10,7 @@
 namespace ts {
 
 constexpr int kScaleBlock = 128;   // elements of K (and, for block scales, rows of B) that share a scale
+constexpr int kMaxCluster = 8;      // most CTAs that share a tile's K blocks: the portable cluster size
 constexpr int kMaxExperts = 1024;  // most groups of a grouped product: their tile counts are scanned in shared memory
 
 struct Fp8Params {
@@ -50,6 +51,7 @@ struct Fp8Launch {
 struct Fp8Variant {
     int bn, cg, rows, grouped, a_rows;
     cudaError_t (*launch)(const Fp8Launch &);
+    int (*clusters)(int size);  // clusters of so many CTAs that run at once
 };
 
 }  // namespace ts
