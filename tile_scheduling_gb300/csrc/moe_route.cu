@@ -15,6 +15,11 @@
 // halving sum is first a tree over a lane's slots, then a butterfly over lanes,
 // and a round of the choice is one scan of a lane's slots and two warp
 // reductions on order-preserving integer keys.
+//
+// A token's logits are a few hundred bytes, so instructions and their latencies bound
+// it: 16384 tokens of 256 fp32 logits, eight choices, 18.3 us (18.7 MB, 1 TB/s), the
+// gradient 14.7; 8191 of 128 in bf16, six choices, 6.9 and 5.5; one token of 256 in
+// eight groups 4.0.
 #include <algorithm>
 #include <type_traits>
 
@@ -43,6 +48,7 @@ struct RouteParams {
     int32_t E, k;
     int32_t softmax, renorm;
     int32_t groups, keep, best, group_size;
+    uint32_t group_div;  // e / group_size = e * group_div >> 22, exact for e < 1024
     float scale;
     unsigned long long *status;
 };
@@ -65,27 +71,39 @@ __device__ __forceinline__ float value_of(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
+// What a token's softmax scores share.
+struct Norm {
+    float top, sum;
+};
+
+// The score of one logit (x: not NaN, at most the largest number; -inf where masked).
+__device__ __forceinline__ float score_of(float x, const Norm &n, bool softmax) {
+    if (softmax) return n.sum > 0.f ? expf(x - n.top) / n.sum : 0.f;
+    return 1.f / (1.f + expf(-x));
+}
+__device__ __forceinline__ float clean(float x) { return x > -INFINITY ? fminf(x, 3.402823466e38f) : -INFINITY; }
+
 // Scores of one token: x[i] becomes s of expert i * 32 + lane; masked[i] tells the
 // experts that cannot be chosen.  Returns whether any logit of the row is NaN.
 template <int NS>
-__device__ __forceinline__ bool scores(float (&x)[NS], bool (&masked)[NS], bool softmax) {
+__device__ __forceinline__ bool scores(float (&x)[NS], bool (&masked)[NS], Norm &norm, bool softmax) {
     bool nan = false;
-    float top = -3.402823466e38f;
+    norm.top = -3.402823466e38f;
+    norm.sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
         nan |= isnan(x[i]);
         masked[i] = !(x[i] > -INFINITY);
-        if (masked[i]) x[i] = -INFINITY;
-        x[i] = fminf(x[i], 3.402823466e38f);  // +inf as the largest number
-        top = fmaxf(top, x[i]);
+        x[i] = clean(x[i]);  // (+inf as the largest number)
+        norm.top = fmaxf(norm.top, x[i]);
     }
     if (softmax) {
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+        for (int d = 16; d > 0; d >>= 1) norm.top = fmaxf(norm.top, __shfl_xor_sync(kAll, norm.top, d));
         float sum[NS];
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            x[i] = expf(x[i] - top);
+            x[i] = expf(x[i] - norm.top);
             sum[i] = x[i];
         }
 #pragma unroll
@@ -95,11 +113,12 @@ __device__ __forceinline__ bool scores(float (&x)[NS], bool (&masked)[NS], bool 
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum[0] += __shfl_xor_sync(kAll, sum[0], d);
+        norm.sum = sum[0];
 #pragma unroll
         for (int i = 0; i < NS; ++i) x[i] = sum[0] > 0.f ? x[i] / sum[0] : 0.f;
     } else {
 #pragma unroll
-        for (int i = 0; i < NS; ++i) x[i] = 1.f / (1.f + expf(-x[i]));
+        for (int i = 0; i < NS; ++i) x[i] = score_of(x[i], norm, false);
     }
     return __any_sync(kAll, nan);
 }
@@ -119,7 +138,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
         const int e = i * 32 + lane;
         s[i] = e < p.E ? load_logit(row + e) : -INFINITY;
     }
-    const bool nan = scores<NS>(s, masked, p.softmax);
+    Norm norm;
+    const bool nan = scores<NS>(s, masked, norm, p.softmax);
     uint32_t key[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
@@ -131,24 +151,36 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
     if (p.groups > 1) {
         // lane g holds the key of group g's score
         uint32_t gkey = 0;
-        for (int g = 0; g < p.groups; ++g) {
-            const int lo = g * p.group_size, hi = lo + p.group_size;
-            uint32_t k1 = 0, k2 = 0;  // this lane's two largest of the group
-#pragma unroll
-            for (int i = 0; i < NS; ++i) {
-                const int e = i * 32 + lane;
-                const uint32_t k = e >= lo && e < hi ? key[i] : 0u;
-                k2 = max(k2, min(k1, k));
-                k1 = max(k1, k);
-            }
+        // the score's key, from this lane's two largest of the group
+        auto group_key = [&](uint32_t k1, uint32_t k2) {
             const uint32_t m1 = __reduce_max_sync(kAll, k1);
-            uint32_t score = m1;
-            if (p.best == 2 && m1) {
-                const int owner = __ffs(__ballot_sync(kAll, k1 == m1)) - 1;
-                const uint32_t m2 = __reduce_max_sync(kAll, lane == owner ? k2 : k1);
-                if (m2) score = key_of(value_of(m1) + value_of(m2));
+            if (p.best != 2) return m1;
+            const uint32_t owner = __reduce_min_sync(kAll, k1 == m1 ? static_cast<uint32_t>(lane) : kAll);
+            const uint32_t m2 = __reduce_max_sync(kAll, lane == owner ? k2 : k1);
+            return m2 ? key_of(value_of(m1) + value_of(m2)) : m1;
+        };
+        if (p.group_size == 32) {
+            // a lane has one expert of each group: nothing to search, and the groups' reductions
+            // overlap (one token, 256 experts in eight groups: 4.8 us, through the search 5.3)
+#pragma unroll
+            for (int g = 0; g < NS; ++g) {
+                const uint32_t k = group_key(key[g], 0u);
+                if (lane == g) gkey = k;
             }
-            if (lane == g) gkey = score;
+        } else {
+            for (int g = 0; g < p.groups; ++g) {
+                const int lo = g * p.group_size, hi = lo + p.group_size;
+                uint32_t k1 = 0, k2 = 0;  // this lane's two largest of the group
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    const int e = i * 32 + lane;
+                    const uint32_t k = e >= lo && e < hi ? key[i] : 0u;
+                    k2 = max(k2, min(k1, k));
+                    k1 = max(k1, k);
+                }
+                const uint32_t k = group_key(k1, k2);
+                if (lane == g) gkey = k;
+            }
         }
         uint32_t kept = 0;  // bit g: group g stays
         for (int r = 0; r < p.keep; ++r) {
@@ -161,36 +193,28 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const int e = i * 32 + lane;
-            if (e < p.E && !((kept >> (e / p.group_size)) & 1u)) key[i] = 0;
+            if (e < p.E && !((kept >> (e * p.group_div >> 22)) & 1u)) key[i] = 0;
         }
     }
     int32_t mine = -1;  // lane j: choice j
-    float w = 0.f;
     for (int j = 0; j < p.k; ++j) {
         uint32_t best = 0;
-        int at = 0;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) best = max(best, key[i]);
+        best = __reduce_max_sync(kAll, best);
+        if (!best) break;
+        uint32_t at = kAll;  // the lowest of this lane's experts with that key
+#pragma unroll
+        for (int i = NS - 1; i >= 0; --i)
+            if (key[i] == best) at = i * 32 + lane;
+        const uint32_t e = __reduce_min_sync(kAll, at);
 #pragma unroll
         for (int i = 0; i < NS; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = i;
-            }
-        const uint32_t m = __reduce_max_sync(kAll, best);
-        if (!m) break;
-        const int e = static_cast<int>(__reduce_min_sync(kAll, best == m ? static_cast<uint32_t>(at * 32 + lane) : kAll));
-        float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < NS; ++i)
-            if (i * 32 + lane == e) {
-                key[i] = 0;
-                v = s[i];
-            }
-        v = __shfl_sync(kAll, v, e & 31);
-        if (lane == j) {
-            mine = e;
-            w = v;
-        }
+            if (i * 32 + lane == e) key[i] = 0;
+        if (lane == j) mine = static_cast<int32_t>(e);
     }
+    // its score once more, from its logit: one load for a search through the lanes a choice
+    float w = mine >= 0 ? score_of(clean(load_logit(row + mine)), norm, p.softmax) : 0.f;
     if (p.renorm) {
         float sum = w;
 #pragma unroll
@@ -223,7 +247,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const __gr
         s[i] = e < p.E ? load_logit(row + e) : -INFINITY;
         x[i] = s[i];
     }
-    const bool nan = scores<NS>(s, masked, p.softmax);
+    Norm norm;
+    const bool nan = scores<NS>(s, masked, norm, p.softmax);
     int32_t mine = -1;
     float g = 0.f;
     if (lane < p.k) {
@@ -236,17 +261,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const __gr
         }
         if (mine >= 0) g = p.grad_w[t * p.k + lane] * p.scale;
     }
-    float sj = 0.f;  // lane j: the score of choice j
-    for (int j = 0; j < p.k; ++j) {
-        const int e = __shfl_sync(kAll, mine, j);
-        float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < NS; ++i)
-            if (i * 32 + lane == e) v = s[i];
-        v = __shfl_sync(kAll, v, e & 31);
-        if (lane == j) sj = v;
-    }
-    if (mine < 0) sj = 0.f;
+    // lane j: the score of choice j, from its logit
+    const float sj = mine >= 0 ? score_of(clean(load_logit(row + mine)), norm, p.softmax) : 0.f;
     float ds = g;
     if (p.renorm) {
         float sum = sj, dot = g * sj;
@@ -345,6 +361,7 @@ ts_status route_check(RouteParams &p, const void *logits, int64_t T, int32_t E, 
     p.keep = keep;
     p.best = best;
     p.group_size = E / groups;
+    p.group_div = ((1u << 22) + p.group_size - 1) / p.group_size;
     p.scale = o->scale != 0.f ? o->scale : 1.f;
     p.bias = o->bias;
     ts_status s = TS_OK;
@@ -355,7 +372,8 @@ ts_status route_check(RouteParams &p, const void *logits, int64_t T, int32_t E, 
 // ------------------------------------------------------------------- plan
 // A stable counting sort of the slots by expert.  A CTA takes tiles of
 // kPlanSlots consecutive slots, a warp kWarpSlots of them in order; equal
-// experts of a warp's 32 slots rank by lane.
+// experts of a warp's 32 slots rank by lane.  Latencies bound it (three integers move
+// for a slot): 8 slots 2.9 us, 49146 of 128 experts 9.3, 131072 of 256 15.9.
 constexpr int kPlanWarps = 16;
 constexpr int kWarpSlots = 64;
 constexpr int kPlanSlots = kPlanWarps * kWarpSlots;
