@@ -6,18 +6,31 @@
 // 128 elements of K, and for each 128 x 128 block (or each row) of B.
 //
 // The scales change every 128 elements of K, so the tensor core cannot carry one
-// accumulator through the K loop.  Each K block of 128 columns of the tile is a
-// chain of four MMAs (K = 32 each) into one of four TMEM slots; promotion warps
-// read it back, scale it, and add it to fp32 registers that hold the tile's
-// running sum, while the MMAs fill the other slots.  From the commit of a slot to
-// its hand-back some 1000 cycles pass, most of them latencies, and its MMAs take
-// 256: with two 256-column accumulators that round trip bounded the kernel
-// (8192^3: 560 us on 128x256 tiles, 603 us on pairs); four slots hide it.
+// accumulator through the K loop.  Each K block of a tile is a chain of four MMAs (K = 32
+// each) into a TMEM slot; promotion warps read the slot back, scale it, and add it to fp32
+// registers that hold the tile's running sum, while the MMAs fill the other slots.
+//
+// What bounds it.  A K block of 128 x 256 outputs takes the tensor core 512 cycles; the
+// promotion reads 128 KB of TMEM and issues 512 two-wide multiply-adds (1024 with row
+// scales) beside it.  The steady state is 720 to 760 cycles a K block, 1200 with row scales.
+// On a pair it is the promotion warps that share the MMA warp's scheduler (in the CTA that
+// issues, they run 1.8 times slower than in the other); on 128x256 tiles the operands'
+// traffic through shared memory, 96 KB a K block written and read, is close to its
+// bandwidth as well.  From the commit of a slot to its hand-back some 1000 cycles pass,
+// most of them latencies: 128-column slots (four of them) hide it on a pair (8192^3 603 us
+// with two of 256 columns); two 256-column slots are enough where both halves of the
+// promotion warps read every slot (128x256).
+//
+// Measured: 8192^3, e4m3, bf16 out, 363 to 400 us by the power cap's state (2750 to 3030
+// TFLOP/s; a pair); 4096 x 4096 x 8191 with row scales 157 us (1750; 128x128); 2047 x 4096
+// x 6144 41 us (2510; a pair); 16384 rows over 32 groups of 4096 x 2048, ragged, 132 us
+// (2080; 128x256); 1 x 4096 x 8192 8.3 us (4 TB/s; split over four CTAs a tile).
 //
 // Warp roles (384 threads, one CTA per SM):
 //   warp 0       TMA producer of the operand ring
 //   warp 1       TMEM allocator and MMA issuer
 //   warp 2       scales: copies them to shared memory, a chunk of four K blocks at a time
+//   warp 3       initialises the barriers
 //   warps 4..11  promotion and epilogue: warp 4 + j holds rows 32 * (j % 4) of the
 //                tile, one row per lane; j / 4 picks the columns (see Fp8Cfg)
 #pragma once
