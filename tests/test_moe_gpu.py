@@ -289,6 +289,34 @@ def test_plan_reports_an_expert_past_the_last(lib):
     assert off.tolist() == [0, 2, 3] and order.tolist() == [0, 3, 2, -1] and pos.tolist() == [[0, -1], [2, 1]]
 
 
+def test_plan_in_graphs_that_replay_at_once(lib):
+    # many slots, no workspace passed: each graph has its own
+    T, E = 30000, 64
+    runs = []
+    for i in range(2):
+        e = torch.randint(0, E, (T, 2), generator=torch.Generator().manual_seed(i), dtype=torch.int32).cuda()
+        off = torch.empty(E + 1, dtype=torch.int64, device="cuda")
+        order = torch.empty(T * 2, dtype=torch.int32, device="cuda")
+        pos = torch.empty((T, 2), dtype=torch.int32, device="cuda")
+        lib.ts_moe_plan(e, off, order, pos)
+        lib.ts_sync_and_check()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            lib.ts_moe_plan(e, off, order, pos)
+        runs.append((graph, order, order.clone(), torch.cuda.Stream(), e, off, pos))
+    for _, order, *_ in runs:
+        order.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, _, _, stream, *_ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    lib.ts_sync_and_check(runs[0][3])
+    torch.cuda.synchronize()
+    for _, order, want, *_ in runs:
+        assert torch.equal(order, want)
+
+
 # ----------------------------------------------------------------- quantise
 TOPS = {torch.float8_e4m3fn: 448.0, torch.float8_e5m2: 57344.0}
 

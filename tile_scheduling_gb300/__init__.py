@@ -773,7 +773,9 @@ _SCRATCH: dict = {}
 
 def _scratch_for(nbytes: int, device, stream) -> torch.Tensor:
     """Uninitialised scratch of at least ``nbytes``, kept per device and stream and allocated on the stream
-    it serves, so that calls on different streams never share one."""
+    it serves, so that calls on different streams never share one (nor do graphs, which may replay at once)."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)  # the graph's own
     key = (device, _stream_of(stream))
     ws = _SCRATCH.get(key)
     if ws is None or ws.numel() < nbytes:
