@@ -119,6 +119,14 @@ def test_binding_structs_match_the_header_layout(ts, tmp_path):
             assert got[(name, f)] == getattr(cls, f).offset, f"{name}.{f}"
 
 
+@pytest.mark.parametrize("name,cls", [("_PACK_FP8", "Fp8Opts"), ("_PACK_QUANT", "QuantOpts"), ("_PACK_ROUTE", "RouteOpts")])
+def test_packed_options_are_the_structures(ts, name, cls):
+    cls, packer = getattr(ts, cls), getattr(ts, name)
+    values = [i + 1 for i in range(len(cls._fields_))]
+    o = cls.from_buffer_copy(packer.pack(*values))
+    assert [getattr(o, f) for f, _ in cls._fields_] == values
+
+
 @pytest.mark.parametrize("name,value", [("TS_FP8_E4M3", 0), ("TS_FP8_E5M2", 1), ("TS_SCALE_BLOCK", 0), ("TS_SCALE_ROW", 1),
                                         ("TS_SCORE_SOFTMAX", 0), ("TS_SCORE_SIGMOID", 1)])
 def test_constants(ts, name, value):

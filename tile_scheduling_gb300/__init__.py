@@ -13,7 +13,9 @@ the same names.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -93,6 +95,12 @@ class RouteOpts(ctypes.Structure):
                 ("ldg", ctypes.c_int64)]
 
 
+# The same layouts packed into bytes: a quarter of the time of filling a Structure, in calls of a few microseconds.
+_PACK_FP8 = struct.Struct("6i9qd")
+_PACK_QUANT = struct.Struct("Pqiiqqqq")
+_PACK_ROUTE = struct.Struct("P5ifiqq")
+
+
 class GemmProtocol(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "cluster", "stages", "tx_bytes", "full_arrivals", "empty_arrivals", "accumulators", "tmem_full_arrivals",
@@ -152,6 +160,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                  "ts_gemm_grouped_order", "ts_copy_i16", "ts_copy_i16_rows", "ts_copy_rows_launch_info", "ts_spin",
                  "ts_spin_wait_started", "ts_sync_and_check"):
         getattr(lib, name).restype = ctypes.c_int
+    for name in ("ts_gemm_fp8", "ts_gemm_fp8_grouped", "ts_quant_fp8", "ts_moe_route", "ts_moe_route_grad"):
+        packed = lib[name]  # a handle of its own, whose options are packed bytes
+        packed.argtypes = [P if t in (F8, QO, RO) else t for t in getattr(lib, name).argtypes]
+        packed.restype = ctypes.c_int
+        setattr(lib, name + "_packed", packed)
     return lib
 
 
@@ -575,22 +588,32 @@ _I64 = {torch.int64: 0}
 
 def _matrix_of(t, name: str, dtypes, dims: int = 2):
     """(dtype code, shape, row stride) of a CUDA tensor with dense last dimension; the stride is 0, for
-    the default, with a single row."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or not t.is_cuda or t.dim() != dims:
+    the default, with a single row.  (Each attribute of a tensor costs some 0.1 us: no more are read than
+    the checks need.)"""
+    try:
+        code, shape, stride, cuda = dtypes[t.dtype], t.shape, t.stride(), t.is_cuda
+    except (AttributeError, KeyError, TypeError):
+        cuda = False
+    if not cuda or len(shape) != dims:
         _require(t, name, dtypes, dims)
-    shape, stride = t.shape, t.stride()
-    if stride[-1] != 1 and shape[-1] > 1:
+    cols = shape[-1]
+    if stride[-1] != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
     if shape[-2] <= 1:
-        return dtypes[t.dtype], shape, 0
-    if stride[-2] == 0 and shape[-1]:
+        return code, shape, 0
+    pitch = stride[-2]
+    if pitch == 0 and cols:
         raise ValueError(f"{name} has rows that share memory (an expanded tensor)")
-    return dtypes[t.dtype], shape, stride[-2]
+    return code, shape, pitch
 
 
 def _dense(t, name: str, dtypes, shape) -> int:
     """Address of a contiguous CUDA tensor of the given type and shape."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or not t.is_cuda or t.dim() != len(shape):
+    try:
+        ok = t.dtype in dtypes and t.is_cuda
+    except AttributeError:
+        ok = False
+    if not ok:
         _require(t, name, dtypes, len(shape))
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}")
@@ -600,12 +623,16 @@ def _dense(t, name: str, dtypes, shape) -> int:
 def _scales(t, name: str, dims: int):
     """(shape, strides) of an fp32 scale tensor of any strides; an expanded one is broadcast along the
     dimension it is expanded in (both at once cannot be told from the default strides)."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda or t.dim() != dims:
+    try:
+        ok = t.dtype is torch.float32 and t.is_cuda
+        shape, stride = t.shape, t.stride()
+    except (AttributeError, TypeError):
+        ok = False
+    if not ok or len(shape) != dims:
         _require(t, name, _F32, dims)
-    stride = t.stride()
-    if stride[-1] == 0 and stride[-2] == 0 and t.shape[-1] * t.shape[-2] > 1:
+    if stride[-1] == 0 and stride[-2] == 0 and shape[-1] * shape[-2] > 1:
         raise ValueError(f"{name} is one scale expanded in both dimensions")
-    return t.shape, stride
+    return shape, stride
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -650,9 +677,9 @@ def _fp8_opts(A, SA, B, SB, D, dims, trans_b, tile, max_workers, timeout_s):
             b_group, sb_group = B.stride(0), sb_stride[0]
             if b_group == 0 or sb_group == 0:
                 raise ValueError("groups of B or SB share memory (an expanded tensor)")
-    o = Fp8Opts(a_type, b_type, b_scale, 1 if trans_b else 0, _TILE[tile] if isinstance(tile, str) else int(tile),
-                max_workers, lda, ldb, ldd, b_group, sa_stride[0], sa_stride[1], sb_stride[-2], sb_stride[-1],
-                sb_group, timeout_s)
+    o = _PACK_FP8.pack(a_type, b_type, b_scale, 1 if trans_b else 0,
+                       _TILE[tile] if isinstance(tile, str) else int(tile), max_workers, lda, ldb, ldd, b_group,
+                       sa_stride[0], sa_stride[1], sb_stride[-2], sb_stride[-1], sb_group, timeout_s)
     return o, M, N, K, out
 
 
@@ -667,8 +694,8 @@ def ts_gemm_fp8(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch.Te
     [K, N] with block scales [ceil(K / 128), ceil(N / 128)].  Rows may be strided; rows of A and B start
     on 16-byte boundaries.  Asynchronous on ``stream`` (default: torch's current stream)."""
     o, M, N, K, out = _fp8_opts(A, SA, B, SB, D, 2, trans_b, tile, max_workers, timeout_s)
-    st = _lib.ts_gemm_fp8(A.data_ptr(), SA.data_ptr(), B.data_ptr(), SB.data_ptr(), D.data_ptr(), M, N, K, out, o,
-                          _stream_of(stream))
+    st = _lib.ts_gemm_fp8_packed(A.data_ptr(), SA.data_ptr(), B.data_ptr(), SB.data_ptr(), D.data_ptr(), M, N, K, out,
+                                 o, _stream_of(stream))
     if st:
         _check(st)
 
@@ -682,8 +709,9 @@ def ts_gemm_fp8_grouped(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: 
     everything else as ts_gemm_fp8.  Rows outside every group are not written."""
     o, M, N, K, out = _fp8_opts(A, SA, B, SB, D, 3, trans_b, tile, max_workers, timeout_s)
     G = B.shape[0]
-    st = _lib.ts_gemm_fp8_grouped(A.data_ptr(), SA.data_ptr(), B.data_ptr(), SB.data_ptr(), D.data_ptr(),
-                                  _dense(offsets, "offsets", _I64, (G + 1,)), G, M, N, K, out, o, _stream_of(stream))
+    st = _lib.ts_gemm_fp8_grouped_packed(A.data_ptr(), SA.data_ptr(), B.data_ptr(), SB.data_ptr(), D.data_ptr(),
+                                         _dense(offsets, "offsets", _I64, (G + 1,)), G, M, N, K, out, o,
+                                         _stream_of(stream))
     if st:
         _check(st)
 
@@ -717,8 +745,9 @@ def ts_quant_fp8(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, rows=No
                          f"{tuple(scales.shape)}")
     if want_r == 0:
         return
-    o = QuantOpts(index, out_rows, int(rows_div), 1 if transpose else 0, ldx, ldq, s_stride[0], s_stride[1])
-    st = _lib.ts_quant_fp8(x.data_ptr(), q.data_ptr(), scales.data_ptr(), M, N, x_type, q_type, o, _stream_of(stream))
+    o = _PACK_QUANT.pack(index, out_rows, int(rows_div), 1 if transpose else 0, ldx, ldq, s_stride[0], s_stride[1])
+    st = _lib.ts_quant_fp8_packed(x.data_ptr(), q.data_ptr(), scales.data_ptr(), M, N, x_type, q_type, o,
+                                  _stream_of(stream))
     if st:
         _check(st)
 
@@ -737,10 +766,10 @@ def ts_moe_route(logits: torch.Tensor, experts: torch.Tensor, weights: torch.Ten
     never chosen, and slots without one hold -1 and weight 0.  ``renorm`` divides the weights by their sum."""
     dtype, (T, E), ldx = _matrix_of(logits, "logits", _OUT)
     k = experts.shape[-1]
-    o = RouteOpts(_dense(bias, "bias", _F32, (E,)) if bias is not None else 0, _score(score), groups, keep_groups,
-                  group_best, 0 if renorm else 1, scale, 0, ldx, 0)
-    st = _lib.ts_moe_route(logits.data_ptr(), _dense(experts, "experts", _I32, (T, k)),
-                           _dense(weights, "weights", _F32, (T, k)), T, E, k, dtype, o, _stream_of(stream))
+    o = _PACK_ROUTE.pack(_dense(bias, "bias", _F32, (E,)) if bias is not None else 0, _score(score), groups,
+                         keep_groups, group_best, 0 if renorm else 1, scale, 0, ldx, 0)
+    st = _lib.ts_moe_route_packed(logits.data_ptr(), _dense(experts, "experts", _I32, (T, k)),
+                                  _dense(weights, "weights", _F32, (T, k)), T, E, k, dtype, o, _stream_of(stream))
     if st:
         _check(st)
 
@@ -755,10 +784,10 @@ def ts_moe_route_grad(logits: torch.Tensor, experts: torch.Tensor, grad_weights:
         raise TypeError("grad_logits must have the logits' type")
     if g_shape[0] != T or g_shape[1] != E:
         raise ValueError(f"grad_logits must be {(T, E)}")
-    o = RouteOpts(0, _score(score), 1, 0, 1, 0 if renorm else 1, scale, 0, ldx, ldg)
-    st = _lib.ts_moe_route_grad(logits.data_ptr(), _dense(experts, "experts", _I32, (T, k)),
-                                _dense(grad_weights, "grad_weights", _F32, (T, k)), grad_logits.data_ptr(), T, E, k,
-                                dtype, o, _stream_of(stream))
+    o = _PACK_ROUTE.pack(0, _score(score), 1, 0, 1, 0 if renorm else 1, scale, 0, ldx, ldg)
+    st = _lib.ts_moe_route_grad_packed(logits.data_ptr(), _dense(experts, "experts", _I32, (T, k)),
+                                       _dense(grad_weights, "grad_weights", _F32, (T, k)), grad_logits.data_ptr(), T,
+                                       E, k, dtype, o, _stream_of(stream))
     if st:
         _check(st)
 
@@ -766,6 +795,11 @@ def ts_moe_route_grad(logits: torch.Tensor, experts: torch.Tensor, grad_weights:
 def ts_moe_plan_workspace(slots: int, experts: int) -> int:
     """Bytes of workspace that ts_moe_plan needs for that many slots and experts."""
     return int(_lib.ts_moe_plan_workspace(int(slots), int(experts)))
+
+
+@functools.lru_cache(maxsize=64)
+def _plan_need(slots: int, experts: int) -> int:
+    return _lib.ts_moe_plan_workspace(slots, experts)
 
 
 _SCRATCH: dict = {}
@@ -797,7 +831,7 @@ def ts_moe_plan(experts: torch.Tensor, offsets: torch.Tensor, order: torch.Tenso
     E = offsets.numel() - 1
     shape = experts.shape
     ptr = size = 0
-    need = _lib.ts_moe_plan_workspace(n, E)
+    need = _plan_need(n, E)
     if need and workspace is None:
         workspace = _scratch_for(need, experts.device, stream)
     if workspace is not None:
