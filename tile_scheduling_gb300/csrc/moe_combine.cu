@@ -221,9 +221,12 @@ __global__ void __launch_bounds__(kGradThreads, 2) combine_grad_kernel(const __g
     }
 }
 
-// Threads of a CTA: the row's vectors, in warps, up to `most`.
+// Threads of a CTA: the row's vectors shared evenly by as few rounds (or CTAs) as `most`
+// threads need, in warps: 1795 tokens, four slots of 2360 bf16 8.9 us; with `most` threads
+// and a last CTA that is mostly idle 13.4.
 int cta_threads(int64_t N, int per, int most) {
-    return static_cast<int>(std::min<int64_t>(most, cdiv(cdiv(N, per), 32) * 32));
+    const int64_t vectors = cdiv(N, per);
+    return static_cast<int>(cdiv(cdiv(vectors, cdiv(vectors, most)), 32) * 32);
 }
 
 bool row16(const void *x, int64_t ld, int esize) {

@@ -403,41 +403,43 @@ __device__ __forceinline__ int32_t plan_expert(const PlanParams &p, int64_t i, b
     return -1;
 }
 
+// A thread's slots of a tile: their experts, and the lanes whose slot has the same one.
+struct PlanSlots {
+    int32_t e[kWarpSlots / 32];
+    uint32_t same[kWarpSlots / 32];
+};
+
 // Per-warp counts of one tile's slots in hist[warp][E].
-__device__ __forceinline__ void plan_count(const PlanParams &p, int64_t first, int32_t *hist, bool report) {
+__device__ __forceinline__ PlanSlots plan_count(const PlanParams &p, int64_t first, int32_t *hist, bool report) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int32_t i = threadIdx.x; i < kPlanWarps * p.E; i += blockDim.x) hist[i] = 0;
     __syncthreads();
     int32_t *const h = hist + warp * p.E;
-    int32_t e[kWarpSlots / 32];
+    PlanSlots s;
 #pragma unroll
     for (int r = 0; r < kWarpSlots / 32; ++r)
-        e[r] = plan_expert(p, first + warp * kWarpSlots + r * 32 + lane, report);
+        s.e[r] = plan_expert(p, first + warp * kWarpSlots + r * 32 + lane, report);
 #pragma unroll
     for (int r = 0; r < kWarpSlots / 32; ++r) {
-        const uint32_t same = __match_any_sync(kAll, e[r]);
-        if (e[r] >= 0 && lane == __ffs(same) - 1) h[e[r]] += __popc(same);
+        s.same[r] = __match_any_sync(kAll, s.e[r]);
+        if (s.e[r] >= 0 && lane == __ffs(s.same[r]) - 1) h[s.e[r]] += __popc(s.same[r]);
         __syncwarp();
     }
     __syncthreads();
+    return s;
 }
 
 // Rows of one tile's slots: hist[warp][e] holds the first row of the warp's slots of e.
-__device__ __forceinline__ void plan_place(const PlanParams &p, int64_t first, int32_t *hist) {
+__device__ __forceinline__ void plan_place(const PlanParams &p, int64_t first, int32_t *hist, const PlanSlots &s) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t *const h = hist + warp * p.E;
-    int32_t e[kWarpSlots / 32];
-#pragma unroll
-    for (int r = 0; r < kWarpSlots / 32; ++r)
-        e[r] = plan_expert(p, first + warp * kWarpSlots + r * 32 + lane, false);
 #pragma unroll
     for (int r = 0; r < kWarpSlots / 32; ++r) {
         const int64_t i = first + warp * kWarpSlots + r * 32 + lane;
-        const uint32_t same = __match_any_sync(kAll, e[r]);
         int32_t row = -1;
-        if (e[r] >= 0) row = h[e[r]] + __popc(same & ((1u << lane) - 1u));
+        if (s.e[r] >= 0) row = h[s.e[r]] + __popc(s.same[r] & ((1u << lane) - 1u));
         __syncwarp();
-        if (e[r] >= 0 && lane == __ffs(same) - 1) h[e[r]] += __popc(same);
+        if (s.e[r] >= 0 && lane == __ffs(s.same[r]) - 1) h[s.e[r]] += __popc(s.same[r]);
         __syncwarp();
         if (i < p.n) {
             p.position[i] = row;
@@ -450,38 +452,43 @@ __device__ __forceinline__ void plan_place(const PlanParams &p, int64_t first, i
 // Turns a tile's counts of expert e, per warp, into the first row of each warp's slots;
 // returns the row after the last.
 __device__ __forceinline__ int32_t plan_first_rows(const PlanParams &p, int32_t e, int32_t row, int32_t *hist) {
+    int32_t n[kPlanWarps];  // all read first: a read behind a write would wait for it
+#pragma unroll
+    for (int w = 0; w < kPlanWarps; ++w) n[w] = hist[w * p.E + e];
+#pragma unroll
     for (int w = 0; w < kPlanWarps; ++w) {
-        const int32_t n = hist[w * p.E + e];
         hist[w * p.E + e] = row;
-        row += n;
+        row += n[w];
     }
     return row;
 }
 
 // Exclusive sum over the experts of tot[e] into tot itself and, if `write`, offsets
-// (one warp's work).
+// (one warp's work: a lane sums its share of the experts, the lanes scan once).
 __device__ __forceinline__ void plan_offsets(const PlanParams &p, int32_t *tot, bool write) {
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        int32_t run = 0;
-        for (int32_t e0 = 0; e0 < p.E; e0 += 32) {
-            const int32_t e = e0 + lane;
-            const int32_t own = e < p.E ? tot[e] : 0;
-            int32_t v = own;
+        const int32_t share = (p.E + 31) / 32, e0 = min(lane * share, p.E), e1 = min(e0 + share, p.E);
+        int32_t own = 0;
+#pragma unroll 4
+        for (int32_t e = e0; e < e1; ++e) own += tot[e];
+        int32_t run = own;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int32_t o = __shfl_up_sync(kAll, v, d);
-                if (lane >= d) v += o;
-            }
-            if (e < p.E) {
-                tot[e] = run + v - own;
-                if (write) p.offsets[e] = run + v - own;
-            }
-            run += __shfl_sync(kAll, v, 31);
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t o = __shfl_up_sync(kAll, run, d);
+            if (lane >= d) run += o;
+        }
+        const int32_t all = __shfl_sync(kAll, run, 31);
+        run -= own;
+        for (int32_t e = e0; e < e1; ++e) {
+            const int32_t n = tot[e];
+            tot[e] = run;
+            if (write) p.offsets[e] = run;
+            run += n;
         }
         if (lane == 0) {
-            if (write) p.offsets[p.E] = run;
-            tot[p.E] = run;
+            if (write) p.offsets[p.E] = all;
+            tot[p.E] = all;
         }
     }
     __syncthreads();
@@ -506,10 +513,10 @@ __global__ void __launch_bounds__(32 * kPlanWarps) plan_one_kernel(const __grid_
     plan_offsets(p, next, true);
     const int32_t valid = next[p.E];
     for (int32_t t = 0; t < p.tiles; ++t) {
-        plan_count(p, static_cast<int64_t>(t) * kPlanSlots, hist, false);
+        const PlanSlots s = plan_count(p, static_cast<int64_t>(t) * kPlanSlots, hist, false);
         for (int32_t e = threadIdx.x; e < p.E; e += blockDim.x) next[e] = plan_first_rows(p, e, next[e], hist);
         __syncthreads();
-        plan_place(p, static_cast<int64_t>(t) * kPlanSlots, hist);
+        plan_place(p, static_cast<int64_t>(t) * kPlanSlots, hist, s);
     }
     for (int64_t r = valid + threadIdx.x; r < p.n; r += blockDim.x) p.order[r] = -1;
 }
@@ -578,7 +585,7 @@ __global__ void __launch_bounds__(32 * kPlanWarps) plan_place_kernel(const __gri
             atomicAdd(&before[e], bef);
         }
     }
-    plan_count(p, first, smem, false);
+    const PlanSlots s = plan_count(p, first, smem, false);
     if constexpr (FUSED) {
         plan_offsets(p, tot, blockIdx.x == 0);
         for (int32_t e = threadIdx.x; e < p.E; e += blockDim.x) plan_first_rows(p, e, tot[e] + before[e], smem);
@@ -587,7 +594,7 @@ __global__ void __launch_bounds__(32 * kPlanWarps) plan_place_kernel(const __gri
             plan_first_rows(p, e, p.counts[static_cast<int64_t>(blockIdx.x) * p.E + e], smem);
     }
     __syncthreads();
-    plan_place(p, first, smem);
+    plan_place(p, first, smem, s);
     const int64_t valid = FUSED ? tot[p.E] : p.offsets[p.E];
     for (int64_t r = first + threadIdx.x; r < first + kPlanSlots && r < p.n; r += blockDim.x)
         if (r >= valid) p.order[r] = -1;
