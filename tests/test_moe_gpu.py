@@ -255,7 +255,8 @@ def test_route_refusals(lib):
 
 # --------------------------------------------------------------------- plan
 @pytest.mark.parametrize("T,k,E", [(0, 2, 4), (1, 1, 1), (1, 8, 256), (100, 3, 5), (2048, 1, 7), (1000, 8, 64),
-                                   (1025, 8, 1024), (8191, 6, 128), (20000, 2, 3), (70001, 1, 300)])
+                                   (1025, 8, 1024), (8191, 6, 128), (20000, 2, 3), (70001, 1, 300),
+                                   (1200, 2, 700), (40000, 2, 760), (70000, 1, 640), (66000, 1, 1024), (300000, 1, 33)])
 def test_plan(lib, T, k, E):
     g = torch.Generator().manual_seed(T + E)
     e = torch.randint(-1, E, (T, k), generator=g, dtype=torch.int32)

@@ -373,20 +373,22 @@ ts_status route_check(RouteParams &p, const void *logits, int64_t T, int32_t E, 
 // A stable counting sort of the slots by expert.  A CTA takes tiles of
 // kPlanSlots consecutive slots, a warp kWarpSlots of them in order; equal
 // experts of a warp's 32 slots rank by lane.  Latencies bound it (three integers move
-// for a slot): 8 slots 2.9 us, 49146 of 128 experts 9.3, 131072 of 256 15.9.
+// for a slot): 8 slots 2.8 us, 49146 of 128 experts 7.8, 131072 of 256 12.0, 1048576 of
+// 256 34.6.
 constexpr int kPlanWarps = 16;
 constexpr int kWarpSlots = 64;
 constexpr int kPlanSlots = kPlanWarps * kWarpSlots;
 constexpr int kOneCtaSlots = 2 * kPlanSlots;  // up to here one CTA does it all
-// Up to here every placing CTA sums the tiles' counts itself (two launches); past it
-// that would read tiles^2 * E counts and a kernel of its own does it (three).
+// Up to here every placing CTA sums the tiles' counts itself (two launches); past it that
+// reads tiles^2 * E counts and a kernel of its own does it (three).  Two / three launches:
+// 128 tiles of 256 experts 11.1 / 12.0 us, of 512 14.9 / 13.0, 256 tiles of 256 24.6 / 14.2.
 constexpr int kFusedTiles = 64;
 
 struct PlanParams {
     const int32_t *experts;
     int64_t *offsets;
     int32_t *order, *position;
-    int32_t *counts;  // [tiles][E] workspace: counts, then first rows
+    int32_t *counts;  // workspace: [tiles][E] counts, then (many tiles) those of the earlier tiles, and [E] sums
     int64_t n;
     int32_t E, tiles;
     unsigned long long *status;
@@ -533,27 +535,35 @@ __global__ void __launch_bounds__(32 * kPlanWarps) plan_count_kernel(const __gri
     }
 }
 
-// One CTA: each expert's running sum over the tiles, then over the experts.
+// Many tiles: a CTA turns the counts of 32 experts into the slots of each in the earlier
+// tiles, and sums them.  A lane takes an expert, a warp a run of tiles.
 __global__ void __launch_bounds__(1024) plan_scan_kernel(const __grid_constant__ PlanParams p) {
-    __shared__ int32_t tot[kMaxRouteExperts + 1];
+    __shared__ int32_t part[32][33];
     grid_dep_wait();
     grid_dep_launch();
-    const int32_t e = threadIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t e = static_cast<int32_t>(blockIdx.x) * 32 + lane;
+    const int32_t run = (p.tiles + 31) / 32, t0 = min(warp * run, p.tiles), t1 = min(t0 + run, p.tiles);
+    int32_t *const column = p.counts + e;
+    int32_t c = 0;
     if (e < p.E) {
-        int32_t c = 0;
 #pragma unroll 8
-        for (int32_t t = 0; t < p.tiles; ++t) c += p.counts[static_cast<int64_t>(t) * p.E + e];
-        tot[e] = c;
+        for (int32_t t = t0; t < t1; ++t) c += column[static_cast<int64_t>(t) * p.E];
     }
+    part[warp][lane] = c;
     __syncthreads();
-    plan_offsets(p, tot, true);
-    if (e < p.E) {
-        int32_t c = tot[e];
-#pragma unroll 8
-        for (int32_t t = 0; t < p.tiles; ++t) {
-            const int32_t n = p.counts[static_cast<int64_t>(t) * p.E + e];
-            p.counts[static_cast<int64_t>(t) * p.E + e] = c;
-            c += n;
+    if (e >= p.E) return;
+    c = 0;
+    for (int w = 0; w < warp; ++w) c += part[w][lane];
+    if (warp == 31) column[static_cast<int64_t>(p.tiles) * p.E] = c + part[31][lane];
+    for (int32_t t = t0; t < t1; t += 8) {
+        int32_t n[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n[i] = t + i < t1 ? column[static_cast<int64_t>(t + i) * p.E] : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (t + i < t1) column[static_cast<int64_t>(t + i) * p.E] = c;
+            c += n[i];
         }
     }
 }
@@ -561,8 +571,8 @@ __global__ void __launch_bounds__(1024) plan_scan_kernel(const __grid_constant__
 template <bool FUSED>
 __global__ void __launch_bounds__(32 * kPlanWarps) plan_place_kernel(const __grid_constant__ PlanParams p) {
     extern __shared__ int32_t smem[];
-    // FUSED: slots of each expert in all tiles, then its first row; and in the earlier tiles
-    __shared__ int32_t tot[FUSED ? kMaxRouteExperts + 1 : 1], before[FUSED ? kMaxRouteExperts : 1];
+    // slots of each expert in all tiles, then its first row; and in the earlier tiles
+    __shared__ int32_t tot[kMaxRouteExperts + 1], before[kMaxRouteExperts];
     grid_dep_wait();
     grid_dep_launch();
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kPlanSlots;
@@ -584,18 +594,18 @@ __global__ void __launch_bounds__(32 * kPlanWarps) plan_place_kernel(const __gri
             atomicAdd(&tot[e], all);
             atomicAdd(&before[e], bef);
         }
+    } else {
+        for (int32_t e = threadIdx.x; e < p.E; e += blockDim.x) {
+            tot[e] = p.counts[static_cast<int64_t>(p.tiles) * p.E + e];
+            before[e] = p.counts[static_cast<int64_t>(blockIdx.x) * p.E + e];
+        }
     }
     const PlanSlots s = plan_count(p, first, smem, false);
-    if constexpr (FUSED) {
-        plan_offsets(p, tot, blockIdx.x == 0);
-        for (int32_t e = threadIdx.x; e < p.E; e += blockDim.x) plan_first_rows(p, e, tot[e] + before[e], smem);
-    } else {
-        for (int32_t e = threadIdx.x; e < p.E; e += blockDim.x)
-            plan_first_rows(p, e, p.counts[static_cast<int64_t>(blockIdx.x) * p.E + e], smem);
-    }
+    plan_offsets(p, tot, blockIdx.x == 0);
+    for (int32_t e = threadIdx.x; e < p.E; e += blockDim.x) plan_first_rows(p, e, tot[e] + before[e], smem);
     __syncthreads();
     plan_place(p, first, smem, s);
-    const int64_t valid = FUSED ? tot[p.E] : p.offsets[p.E];
+    const int64_t valid = tot[p.E];
     for (int64_t r = first + threadIdx.x; r < first + kPlanSlots && r < p.n; r += blockDim.x)
         if (r >= valid) p.order[r] = -1;
 }
@@ -643,7 +653,7 @@ ts_status ts_moe_route_grad(const void *logits, const int32_t *experts, const fl
 int64_t ts_moe_plan_workspace(int64_t slots, int32_t E) {
     using namespace ts;
     if (slots <= kOneCtaSlots || E < 1) return 0;
-    return cdiv(slots, kPlanSlots) * E * static_cast<int64_t>(sizeof(int32_t));
+    return (cdiv(slots, kPlanSlots) + 1) * E * static_cast<int64_t>(sizeof(int32_t));
 }
 
 ts_status ts_moe_plan(const int32_t *experts, int64_t *offsets, int32_t *order, int32_t *position, int64_t slots,
@@ -676,10 +686,10 @@ ts_status ts_moe_plan(const int32_t *experts, int64_t *offsets, int32_t *order, 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const dim3 block(32 * kPlanWarps);
     const size_t hist = static_cast<size_t>(kPlanWarps) * E * 4;
-    // up to 1024 experts take 68 KB: above the default limit
+    // up to 1024 experts take 68 KB, with 8 KB of static arrays: above the default limit of 48
     cudaError_t e = cudaSuccess;
     for (auto *k : {plan_one_kernel, plan_count_kernel, plan_place_kernel<true>, plan_place_kernel<false>})
-        if (e == cudaSuccess && hist + 4 * (E + 1) > 48 * 1024)
+        if (e == cudaSuccess && hist > 32 * 1024)
             e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      kPlanWarps * kMaxRouteExperts * 4 + 4 * (kMaxRouteExperts + 1));
     if (e == cudaSuccess && need == 0) {
@@ -690,7 +700,7 @@ ts_status ts_moe_plan(const int32_t *experts, int64_t *offsets, int32_t *order, 
         if (e == cudaSuccess && p.tiles <= kFusedTiles) {
             e = launch_pdl(plan_place_kernel<true>, grid, block, hist, st, p);
         } else if (e == cudaSuccess) {
-            e = launch_pdl(plan_scan_kernel, dim3(1), dim3(1024), 0, st, p);
+            e = launch_pdl(plan_scan_kernel, dim3(static_cast<unsigned>(cdiv(E, 32))), dim3(1024), 0, st, p);
             if (e == cudaSuccess) e = launch_pdl(plan_place_kernel<false>, grid, block, hist, st, p);
         }
     }
