@@ -24,7 +24,7 @@
 // Measured: 8192^3, e4m3, bf16 out, 363 to 400 us by the power cap's state (2750 to 3030
 // TFLOP/s; a pair); 4096 x 4096 x 8191 with row scales 157 us (1750; 128x128); 2047 x 4096
 // x 6144 41 us (2510; a pair); 16384 rows over 32 groups of 4096 x 2048, ragged, 132 us
-// (2080; 128x256); 1 x 4096 x 8192 8.3 us (4 TB/s; split over four CTAs a tile).
+// (2080; 128x256); 1 x 4096 x 8192 8.1 to 8.9 us (4 TB/s; split over four CTAs a tile).
 //
 // Warp roles (384 threads, one CTA per SM):
 //   warp 0       TMA producer of the operand ring
