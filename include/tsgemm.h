@@ -511,7 +511,7 @@ typedef struct {
     int32_t b_scale;         /* ts_scale; TS_SCALE_ROW: plain product, trans_b = 0 only */
     int32_t trans_b;         /* 0: B is [N][K]; 1: B is [K][N] (the product with the transposed matrix, read in
                                 place: the input gradient of a layer whose weights are B) */
-    int32_t tile;            /* ts_tile; results do not depend on it */
+    int32_t tile;            /* ts_tile; see below for what results depend on */
     int32_t max_workers;     /* cap on persistent workers (CTAs or 2-CTA clusters) */
     int64_t lda, ldb, ldd;   /* row strides in elements; 0 = dense rows */
     int64_t b_group;         /* grouped: elements between the groups of B; 0 = dense */
@@ -536,7 +536,11 @@ typedef struct {
  *   M, N, K  sizes, each in [0, 2^31 - 1]; K need not be a multiple of 128
  *
  * Each K block's sum is accumulated by the tensor cores in fp32, scaled, and added
- * in fp32.  A scale is fp32 of any value; an infinity or NaN in an operand or a
+ * in fp32, the K blocks in order; where a plain product has few 128x128 tiles, their
+ * K blocks are shared by up to eight CTAs, whose sums are then added in order.  So
+ * results are the same on every run, and the order of the sums (the last bits of fp32)
+ * depends on M, N, K, tile and max_workers through that sharing alone; a grouped
+ * product has none, and a row's result does not depend on its neighbours.  A scale is fp32 of any value; an infinity or NaN in an operand or a
  * scale shows in the rows and columns that use it.
  * M == 0 or N == 0: no-op.  K == 0: D is filled with zeros.  A, B and their rows
  * must start on 16-byte boundaries (lda and ldb multiples of 16), or the call

@@ -337,3 +337,21 @@ def test_worker_cap(lib, workers):
     lib.ts_gemm_fp8(A, SA, B, SB, D, max_workers=workers)
     lib.ts_sync_and_check()
     _check(D, a @ b, None, K, True, f"{workers} workers")
+
+
+def test_unsplit_results_are_the_same_on_every_tile_and_for_every_batch(lib):
+    # (random values: the order of the fp32 sums is the K blocks' on every tile)
+    off = [0, 30, 30, 211, 611]
+    A, SA, B, SB, _, _ = _problem(off[-1], 520, 1000, 4, False, groups=4)
+    o = torch.tensor(off, device="cuda")
+    D = [torch.empty((off[-1], 520), device="cuda") for _ in range(4)]
+    for d, tile in zip(D, ("128x128", "128x256", "256x256")):
+        lib.ts_gemm_fp8_grouped(A, SA, B, SB, d, o, tile=tile)
+    for g in range(4):  # eleven rows at a time, on short tiles
+        for i in range(off[g], off[g + 1], 11):
+            j = min(i + 11, off[g + 1])
+            lib.ts_gemm_fp8_grouped(A[i:j], SA[i:j], B[g:g + 1], SB[g:g + 1], D[3][i:j],
+                                    torch.tensor([0, j - i], device="cuda"))
+    lib.ts_sync_and_check()
+    for d in D[1:]:
+        assert torch.equal(D[0], d)

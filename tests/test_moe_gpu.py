@@ -244,6 +244,10 @@ def test_route_refusals(lib):
         lib.ts_moe_route(x, e, w[:3])
     with pytest.raises(TypeError):
         lib.ts_moe_route(x, e.long(), w)
+    with pytest.raises(ValueError):
+        lib.ts_moe_route(x, e, w, scale=0.0)
+    with pytest.raises(ValueError):
+        lib.ts_moe_route_grad(x, e, w, x, scale=0.0)
     # an expert index past the last is reported, and gives nothing
     e[1, 0] = 32
     gx = torch.full((4, 32), 1.0, device="cuda")
