@@ -153,10 +153,15 @@ ts_status fp8_product(const void *A, const float *SA, const void *B, const float
     };
     int tile = o->tile;
     if (tile == TS_TILE_AUTO && grouped) {
-        // By the mean rows of a group.  Measured, 32 groups of 4096 x 2048, 128x128 / 128x256
-        // / pair: 64 rows each 48 / 50 / 60 us, 128 62 / 60 / 69, 256 89 / 82 / 85, 512 162 /
-        // 139 / 145; 8 groups of 2048 rows 142 / 119 / 120.
-        tile = M / groups >= 96 ? TS_TILE_128x256 : TS_TILE_128x128;
+        // By the mean rows of a group, and the waves that its tiles make: tiles / workers and
+        // half a wave, as their number is an estimate (a group ends in half a tile).  Measured,
+        // 32 groups of 4096 x 2048, 128x128 / 128x256 / pair: 64 rows each 48 / 50 / 60 us, 128
+        // 62 / 60 / 69, 256 89 / 82 / 85, 512 162 / 139 / 145; 8 groups of 2048 rows 142 / 119
+        // / 120, of 128 rows 20.6 / 23.4 / 21.6; 20 groups of 300 rows, 1000 x 1500, 25.6 /
+        // 21.3 / 25.7.
+        const int64_t row_tiles = cdiv(M, 128) + groups / 2;
+        const int64_t t1 = row_tiles * cdiv(N, 128), t2 = row_tiles * cdiv(N, 256);
+        tile = M / groups >= 96 && (2 * t2 + sms_) * 740 < (2 * t1 + sms_) * 430 ? TS_TILE_128x256 : TS_TILE_128x128;
     } else if (tile == TS_TILE_AUTO) {
         // The tile with the fewest cycles: waves of workers times what a K block of a tile
         // takes (measured steady states; a pair's, with its smaller L2 traffic, is shorter

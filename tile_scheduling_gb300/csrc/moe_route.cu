@@ -21,6 +21,7 @@
 // gradient 14.7; 8191 of 128 in bf16, six choices, 6.9 and 5.5; one token of 256 in
 // eight groups 4.0.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "common.h"
@@ -687,11 +688,17 @@ ts_status ts_moe_plan(const int32_t *experts, int64_t *offsets, int32_t *order, 
     const dim3 block(32 * kPlanWarps);
     const size_t hist = static_cast<size_t>(kPlanWarps) * E * 4;
     // up to 1024 experts take 68 KB, with 8 KB of static arrays: above the default limit of 48
+    static std::atomic<uint64_t> raised{0};  // devices
+    const int dev = current_device();
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
     cudaError_t e = cudaSuccess;
-    for (auto *k : {plan_one_kernel, plan_count_kernel, plan_place_kernel<true>, plan_place_kernel<false>})
-        if (e == cudaSuccess && hist > 32 * 1024)
-            e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     kPlanWarps * kMaxRouteExperts * 4 + 4 * (kMaxRouteExperts + 1));
+    if (hist > 32 * 1024 && !(raised.load(std::memory_order_acquire) & bit)) {
+        for (auto *k : {plan_one_kernel, plan_count_kernel, plan_place_kernel<true>, plan_place_kernel<false>})
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kPlanWarps * kMaxRouteExperts * 4 + 4 * (kMaxRouteExperts + 1));
+        if (e == cudaSuccess) raised.fetch_or(bit, std::memory_order_acq_rel);
+    }
     if (e == cudaSuccess && need == 0) {
         e = launch_pdl(plan_one_kernel, dim3(1), block, hist + 4 * (E + 1), st, p);
     } else if (e == cudaSuccess) {
