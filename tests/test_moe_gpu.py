@@ -519,13 +519,17 @@ def test_combine_grad_against_differences(lib):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("T,k,N", [(5, 3, 31), (5, 3, 33), (9, 9, 1023), (9, 5, 1025), (3, 8, 2049), (3, 1, 4095)])
+@pytest.mark.parametrize("T,k,N", [(5, 3, 31), (5, 3, 33), (9, 9, 1023), (9, 5, 1025), (3, 8, 2049), (3, 1, 4095),
+                                   (9, 5, 1026), (7, 9, 444), (5, 2, 36), (5, 2, 6), (4, 3, 4092)])
 def test_combine_odd_rows(lib, T, k, N, dtype):
-    # rows on no common boundary: dense rows of odd length, and a base off the 16-byte grid
+    # rows off the 16-byte grid: dense rows of odd length, of 2 or 4 values more, and a base off it
     y, pos, w, go = _combine_inputs(T, k, N, dtype, N, 0)
     flat = torch.full((T * N + 2,), 5.0, dtype=dtype, device="cuda")
     out = flat[1:-1].view(T, N)
     lib.ts_moe_combine(y, pos, out, weights=w)
+    aligned = torch.empty((T, N), dtype=dtype, device="cuda")
+    lib.ts_moe_combine(y, pos, aligned, weights=w)
+    assert torch.equal(out, aligned)
     gy, gw = torch.full_like(y, 7.0), torch.empty_like(w)
     lib.ts_moe_combine_grad(go, y, pos, w, gy, gw)
     lib.ts_sync_and_check()

@@ -9,6 +9,7 @@
 // eight slots 2.7 us.  Sums run in fp32, a token's slots in order, so results do not depend
 // on timing.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "ptx.cuh"
@@ -31,84 +32,102 @@ struct CombineParams {
     unsigned long long *status;
 };
 
-// A thread's values of a row as they lie in memory.  VEC (the rows start on 16-byte
-// boundaries): the 16 bytes from column c on, in one load.  Else four values 32 columns
-// apart, so that a warp's loads and stores of one value each still fill whole sectors
-// (8192 tokens, eight slots, 4095 bf16 values: 169 us and 290 for the gradient; with eight
-// neighbours a thread 278 and 727; rows of 4096, VEC, 107 and 187).
-template <class T, bool VEC>
+// A thread's values of a row as they lie in memory, in units of U bytes: what the rows'
+// starts are aligned to.  Units of 16 bytes: one.  Smaller: several, 32 units apart, so
+// that a warp's loads and stores of one unit each still fill whole sectors (8192 tokens,
+// eight slots of bf16, combine and gradient: 4096 values 107 and 182 us, 4092 128 and 203,
+// 4094 141 and 221, 4095 167 and 282; 4095 with eight neighbours a thread 278 and 727).
+template <class T, int U>
 struct Vals {
-    static constexpr int COUNT = VEC ? 16 / sizeof(T) : 4;
-    uint32_t w[4];
+    static constexpr int UE = U / sizeof(T), COUNT = U == 2 ? 4 : 16 / sizeof(T), UNITS = COUNT / UE;
+    static constexpr bool PACKED = sizeof(T) == 2 && UE > 1;  // two bf16 a word, else a value a word
+    static constexpr int UW = PACKED ? UE / 2 : UE;           // words of a unit
+    uint32_t w[UNITS * UW];
 
     // a thread's first column among those of its CTA
     static __device__ __forceinline__ int64_t first(int thread) {
-        return VEC ? int64_t(thread) * COUNT : int64_t(thread & ~31) * COUNT + (thread & 31);
+        return int64_t(thread & ~31) * COUNT + (thread & 31) * UE;
     }
     // those of row x from column c on; the ones past the N-th read as 0
     __device__ __forceinline__ void load(const T *x, int64_t c, int64_t N) {
-        if constexpr (VEC) {
-            if (c + COUNT <= N) {
-                const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(x + c));
-                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-                return;
-            }
-            w[0] = w[1] = w[2] = w[3] = 0u;
 #pragma unroll
-            for (int i = 0; i < COUNT; ++i)
-                if (c + i < N) {
-                    if constexpr (sizeof(T) == 4)
-                        w[i] = __float_as_uint(x[c + i]);
-                    else
-                        w[i >> 1] |= uint32_t(x[c + i]) << (16 * (i & 1));
-                }
-        } else {
-#pragma unroll
-            for (int i = 0; i < COUNT; ++i) {
-                const T v = c + 32 * i < N ? x[c + 32 * i] : T(0);
+        for (int u = 0; u < UNITS; ++u) {
+            const int64_t at = c + u * (32 * UE);
+            uint32_t *const o = w + u * UW;
+            if constexpr (UE == 1) {
+                const T v = at < N ? x[at] : T(0);
                 if constexpr (sizeof(T) == 4)
-                    w[i] = __float_as_uint(v);
+                    o[0] = __float_as_uint(v);
                 else
-                    w[i] = v;
+                    o[0] = v;
+            } else if (at + UE <= N) {
+                if constexpr (U == 16) {
+                    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(x + at));
+                    o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+                } else if constexpr (U == 8) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(x + at);
+                    o[0] = v.x, o[1] = v.y;
+                } else {
+                    o[0] = *reinterpret_cast<const uint32_t *>(x + at);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < UW; ++i) o[i] = 0u;
+#pragma unroll
+                for (int i = 0; i < UE; ++i)
+                    if (at + i < N) {
+                        if constexpr (sizeof(T) == 4)
+                            o[i] = __float_as_uint(x[at + i]);
+                        else
+                            o[i >> 1] |= uint32_t(x[at + i]) << (16 * (i & 1));
+                    }
             }
         }
     }
     __device__ __forceinline__ float operator[](int i) const {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
-        if constexpr (!VEC) return __uint_as_float(w[i] << 16);
+        if constexpr (!PACKED) return __uint_as_float(w[i] << 16);
         return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
     }
     static __device__ __forceinline__ void store(T *x, int64_t c, int64_t N, const float (&v)[COUNT]) {
-        if constexpr (VEC) {
-            uint32_t o[4];
+        uint32_t r[UNITS * UW];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (sizeof(T) == 4)
-                    o[i] = __float_as_uint(v[i]);
+        for (int i = 0; i < UNITS * UW; ++i) {
+            if constexpr (sizeof(T) == 4)
+                r[i] = __float_as_uint(v[i]);
+            else if constexpr (PACKED)
+                r[i] = pack_bf16x2(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]));
+            else
+                r[i] = pack_bf16x2(__float_as_uint(v[i]), 0u);
+        }
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            const int64_t at = c + u * (32 * UE);
+            const uint32_t *const o = r + u * UW;
+            if constexpr (UE == 1) {
+                if (at < N) {
+                    if constexpr (sizeof(T) == 4)
+                        x[at] = __uint_as_float(o[0]);
+                    else
+                        x[at] = static_cast<T>(o[0]);
+                }
+            } else if (at + UE <= N) {
+                if constexpr (U == 16)
+                    __stcs(reinterpret_cast<uint4 *>(x + at), make_uint4(o[0], o[1], o[2], o[3]));
+                else if constexpr (U == 8)
+                    *reinterpret_cast<uint2 *>(x + at) = make_uint2(o[0], o[1]);
                 else
-                    o[i] = pack_bf16x2(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]));
-            }
-            if (c + COUNT <= N) {
-                __stcs(reinterpret_cast<uint4 *>(x + c), make_uint4(o[0], o[1], o[2], o[3]));
-                return;
-            }
+                    *reinterpret_cast<uint32_t *>(x + at) = o[0];
+            } else {
 #pragma unroll
-            for (int i = 0; i < COUNT; ++i)
-                if (c + i < N) {
-                    if constexpr (sizeof(T) == 4)
-                        x[c + i] = v[i];
-                    else
-                        x[c + i] = static_cast<T>(o[i >> 1] >> (16 * (i & 1)));
-                }
-        } else {
-#pragma unroll
-            for (int i = 0; i < COUNT; ++i)
-                if (c + 32 * i < N) {
-                    if constexpr (sizeof(T) == 4)
-                        x[c + 32 * i] = v[i];
-                    else
-                        x[c + 32 * i] = static_cast<T>(pack_bf16x2(__float_as_uint(v[i]), 0u));
-                }
+                for (int i = 0; i < UE; ++i)
+                    if (at + i < N) {
+                        if constexpr (sizeof(T) == 4)
+                            x[at + i] = __uint_as_float(o[i]);
+                        else
+                            x[at + i] = static_cast<T>(o[i >> 1] >> (16 * (i & 1)));
+                    }
+            }
         }
     }
 };
@@ -130,9 +149,9 @@ __device__ __forceinline__ int32_t slot_row(const CombineParams &p, int64_t t, i
 
 // One CTA per token and kThreads threads' columns.  KS: slots whose rows are in
 // flight together (raw, four registers each, so that several CTAs fit an SM).
-template <class T, int KS, bool VEC>
+template <class T, int KS, int U>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant__ CombineParams p) {
-    using Row = Vals<T, VEC>;
+    using Row = Vals<T, U>;
     grid_dep_wait();
     grid_dep_launch();
     const int64_t t = blockIdx.x;
@@ -165,9 +184,12 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
 // One CTA per token: grad_out's row is read for each group of four slots (from L2 after
 // the first; eight at once would leave room for one CTA on an SM), the slots' dot products
 // are reduced in fixed order.
-template <class T, bool VEC>
-__global__ void __launch_bounds__(kGradThreads, 2) combine_grad_kernel(const __grid_constant__ CombineParams p) {
-    using Row = Vals<T, VEC>;
+//
+// Registers: 56 (three CTAs of 384 threads: 4096 tokens, four slots of 2880 36.1 us, 43.5
+// with 64); with a limit of 64 single values take 56 too, and less time (4095: 282 us, 368).
+template <class T, int U>
+__global__ void __maxnreg__(U == 2 ? 64 : 56) combine_grad_kernel(const __grid_constant__ CombineParams p) {
+    using Row = Vals<T, U>;
     __shared__ float part[kGradSlots][kGradThreads / 32];
     grid_dep_wait();
     grid_dep_launch();
@@ -229,8 +251,40 @@ int cta_threads(int64_t N, int per, int most) {
     return static_cast<int>(cdiv(cdiv(vectors, cdiv(vectors, most)), 32) * 32);
 }
 
-bool row16(const void *x, int64_t ld, int esize) {
-    return reinterpret_cast<uintptr_t>(x) % 16 == 0 && (ld * esize) % 16 == 0;
+// Bytes (16, 8, 4 or the element) that both the base and the pitch of rows are multiples of.
+int row_unit(const void *x, int64_t ld, int esize) {
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(x) | static_cast<uintptr_t>(ld * esize);
+    int u = 16;
+    while (u > esize && bits % u) u /= 2;
+    return u;
+}
+int values_of(int unit, int esize) { return unit == 2 ? 4 : 16 / esize; }
+
+// Calls f with the unit as a compile-time constant.
+template <class F>
+cudaError_t with_unit(int unit, F &&f) {
+    switch (unit) {
+        case 16: return f(std::integral_constant<int, 16>{});
+        case 8: return f(std::integral_constant<int, 8>{});
+        case 4: return f(std::integral_constant<int, 4>{});
+        default: return f(std::integral_constant<int, 2>{});
+    }
+}
+
+template <class T>
+cudaError_t combine_launch(const CombineParams &p, int unit, dim3 grid, dim3 block, cudaStream_t st) {
+    return with_unit(unit, [&](auto u) {
+        constexpr int U = decltype(u)::value < static_cast<int>(sizeof(T)) ? static_cast<int>(sizeof(T)) : decltype(u)::value;
+        return launch_pdl(p.k <= 4 ? combine_kernel<T, 4, U> : combine_kernel<T, 8, U>, grid, block, 0, st, p);
+    });
+}
+
+template <class T>
+cudaError_t combine_grad_launch(const CombineParams &p, int unit, dim3 grid, dim3 block, cudaStream_t st) {
+    return with_unit(unit, [&](auto u) {
+        constexpr int U = decltype(u)::value < static_cast<int>(sizeof(T)) ? static_cast<int>(sizeof(T)) : decltype(u)::value;
+        return launch_pdl(combine_grad_kernel<T, U>, grid, block, 0, st, p);
+    });
 }
 
 ts_status combine_check(int64_t T, int32_t k, int64_t N, int64_t R, int32_t dtype, int64_t ldy, int64_t ldo,
@@ -280,17 +334,13 @@ ts_status ts_moe_combine(const void *y, const int32_t *position, const float *we
     p.ldy = ldy;
     p.ldo = ldo;
     p.k = top_k;
-    const bool vec = row16(y, ldy, esize) && row16(out, ldo, esize);
-    const int per = vec ? 16 / esize : 4, threads = cta_threads(N, per, kThreads);
+    const int unit = std::min(row_unit(y, ldy, esize), row_unit(out, ldo, esize));
+    const int per = values_of(unit, esize), threads = cta_threads(N, per, kThreads);
     if (cdiv(N, threads * per) > 65535) return fail(TS_ERR_UNSUPPORTED, "rows of %lld values", static_cast<long long>(N));
     const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(cdiv(N, threads * per))), block(threads);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    auto go = [&](auto *k4, auto *k8) { return launch_pdl(top_k <= 4 ? k4 : k8, grid, block, 0, st, p); };
-    cudaError_t e = dtype == TS_OUT_F32
-                        ? (vec ? go(combine_kernel<float, 4, true>, combine_kernel<float, 8, true>)
-                               : go(combine_kernel<float, 4, false>, combine_kernel<float, 8, false>))
-                        : (vec ? go(combine_kernel<uint16_t, 4, true>, combine_kernel<uint16_t, 8, true>)
-                               : go(combine_kernel<uint16_t, 4, false>, combine_kernel<uint16_t, 8, false>));
+    cudaError_t e = dtype == TS_OUT_F32 ? combine_launch<float>(p, unit, grid, block, st)
+                                        : combine_launch<uint16_t>(p, unit, grid, block, st);
     return e == cudaSuccess ? TS_OK : cuda_fail(e, "combine launch");
 }
 
@@ -333,14 +383,13 @@ ts_status ts_moe_combine_grad(const void *grad_out, const void *y, const int32_t
     p.ldo = ldo;
     p.ldg = ldg;
     p.k = top_k;
-    const bool vec = row16(y, ldy, esize) && row16(grad_out, ldo, esize) && row16(grad_y, ldg, esize);
+    const int unit =
+        std::min({row_unit(y, ldy, esize), row_unit(grad_out, ldo, esize), row_unit(grad_y, ldg, esize)});
     const dim3 grid(static_cast<unsigned>(T)),
-        block(cta_threads(std::max<int64_t>(N, 1), vec ? 16 / esize : 4, kGradThreads));
+        block(cta_threads(std::max<int64_t>(N, 1), values_of(unit, esize), kGradThreads));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    auto go = [&](auto *kernel) { return launch_pdl(kernel, grid, block, 0, st, p); };
-    cudaError_t e = dtype == TS_OUT_F32
-                        ? (vec ? go(combine_grad_kernel<float, true>) : go(combine_grad_kernel<float, false>))
-                        : (vec ? go(combine_grad_kernel<uint16_t, true>) : go(combine_grad_kernel<uint16_t, false>));
+    cudaError_t e = dtype == TS_OUT_F32 ? combine_grad_launch<float>(p, unit, grid, block, st)
+                                        : combine_grad_launch<uint16_t>(p, unit, grid, block, st);
     return e == cudaSuccess ? TS_OK : cuda_fail(e, "combine gradient launch");
 }
 
