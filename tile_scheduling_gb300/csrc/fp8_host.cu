@@ -129,9 +129,12 @@ ts_status fp8_product(const void *A, const float *SA, const void *B, const float
     const int sms = device_sms(current_device());
     if (sms <= 0) return fail(TS_ERR_CUDA, "cannot query the SM count");
     const int64_t sms_ = sms;  // 64-bit for the products below
-    // Few rows: tiles of 32 (of which the MMA makes 128), so that the ring holds nine
-    // stages of weights instead of five: 1 x 4096 x 8192 12.6 -> 9.6 us.
-    const bool few = !rows && (grouped ? M / groups <= 16 : M <= 32);
+    // Few rows: tiles of 32 (of which the MMA makes 128).  A 128-row box that lies mostly past
+    // A's end is slow to load, and the ring holds nine stages of weights instead of five: 1 x
+    // 4096 x 8192 8.9 us for 13.8, 8 x 8192 x 8192 14.7 for 22.1; 40 rows over 32 groups of
+    // 4096 x 2048 32.8 for 46.4.  With more rows there is no gain (256 over 64 groups of 2048 x
+    // 2048 43.4 and 43.2, 1024 49.5 and 46.5).
+    const bool few = !rows && (grouped ? M < 128 && M / groups <= 16 : M <= 32);
     // CTAs of a cluster that share the K blocks of each of `units` 128x128 tiles, and the
     // cycles that a tile then takes: 430 a K block (660 with row scales) and, from two CTAs
     // on, the exchange of their partial sums.  Measured, 128 x 4096 x 4096 (32 tiles) by 1 /
