@@ -504,6 +504,7 @@ __global__ void __launch_bounds__(32 * kPlanWarps) plan_one_kernel(const __grid_
     grid_dep_wait();
     grid_dep_launch();
     for (int32_t e = threadIdx.x; e <= p.E; e += blockDim.x) next[e] = 0;
+    __syncthreads();  // without a slot there is no tile, and no other barrier before the sums
     for (int32_t t = 0; t < p.tiles; ++t) {
         plan_count(p, static_cast<int64_t>(t) * kPlanSlots, hist, true);
         for (int32_t e = threadIdx.x; e < p.E; e += blockDim.x) {
