@@ -23,3 +23,30 @@ def test_plan_without_slots_after_one_with_some(lib, E):
         lib.ts_moe_plan(empty, *b)
     lib.ts_sync_and_check()
     assert all(not off.any() for off, _, _ in offs)
+
+
+@pytest.mark.parametrize("pitch", [0, 256, 400])
+@pytest.mark.parametrize("trans", [False, True])
+def test_groups_of_one_row_through_the_c_entry(lib, trans, pitch):
+    # B [groups][1][128] (or, K = 1, its transpose), the groups one after another at the row's pitch
+    G, R, L = 5, 3, 128
+    rng = torch.Generator().manual_seed(pitch + trans)
+    step = pitch or L
+    M, N, K = G * R, (L if trans else 1), (1 if trans else L)
+    buf = torch.randint(-4, 5, (G, step), generator=rng).float()  # what lies between the groups is not zero
+    B = buf.to(torch.float8_e4m3fn).cuda()
+    a = torch.randint(-4, 5, (M, K), generator=rng).float()
+    A = torch.zeros((M, -(-K // 16) * 16), dtype=torch.float8_e4m3fn, device="cuda")
+    A[:, :K] = a.to(torch.float8_e4m3fn).cuda()
+    SA, SB = torch.ones((1, M), device="cuda"), torch.full((G,), 2.0, device="cuda")
+    off = torch.arange(0, M + 1, R, device="cuda")
+    D = torch.full((M, N), float("nan"), device="cuda")
+    o = lib.Fp8Opts(trans_b=int(trans), lda=A.shape[1], ldb=pitch)
+    st = lib._lib.ts_gemm_fp8_grouped(A.data_ptr(), SA.data_ptr(), B.data_ptr(), SB.data_ptr(), D.data_ptr(),
+                                      off.data_ptr(), G, M, N, K, lib.TS_OUT_F32, o,
+                                      torch.cuda.current_stream().cuda_stream)
+    assert st == lib.TS_OK, lib.ts_last_error_detail()
+    lib.ts_sync_and_check()
+    rows = buf[:, :L].repeat_interleave(R, 0)
+    want = 2 * (a * rows if trans else (a * rows).sum(1, keepdim=True))
+    assert torch.equal(D.cpu(), want)

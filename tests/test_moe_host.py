@@ -131,3 +131,16 @@ def test_packed_options_are_the_structures(ts, name, cls):
                                         ("TS_SCORE_SOFTMAX", 0), ("TS_SCORE_SIGMOID", 1)])
 def test_constants(ts, name, value):
     assert getattr(ts, name) == value
+
+
+@pytest.mark.parametrize("trans", [0, 1])
+def test_groups_of_one_row_keep_the_callers_pitch(ts, trans):
+    # B's groups of a single row, one after another: the default distance is that row's length (or ldb)
+    U, E = ts.TS_ERR_UNSUPPORTED, ts.TS_ERR_INVALID_ARG
+    one = dict(N=100, K=1, trans_b=1, lda=16) if trans else dict(N=1, K=100, lda=112)
+    assert _fp8(ts, groups=2, **one) == U and "b_group" in ts.ts_last_error_detail()
+    assert _fp8(ts, groups=2, ldb=104, **one) == U and _fp8(ts, groups=2, ldb=96, **one) == E
+    assert _fp8(ts, groups=2, b_group=1 << 40, **one) == E and _fp8(ts, groups=2, ldb=1 << 40, **one) == E
+    assert _fp8(ts, groups=2, b_group=120, ldb=96, **one) == U  # given, it leaves a single row's pitch unused
+    # a padded row: the second group ends 1024 + 100 bytes behind B's start
+    assert _fp8(ts, groups=2, D=2 * P + 1024 + 96, ldb=1024, **one) == E and "overlap" in ts.ts_last_error_detail()

@@ -74,14 +74,17 @@ ts_status fp8_product(const void *A, const float *SA, const void *B, const float
 
     const int64_t b_rows = o->trans_b ? K : N, b_cols = o->trans_b ? N : K;
     const int64_t kblocks = cdiv(K, kScaleBlock), nblocks = cdiv(N, kScaleBlock);
-    // a single row's pitch is never used: take one that suits a tensor map
+    // a single row's pitch is never used, but for the default distance of B's groups: take one
+    // that suits a tensor map
+    const bool b_pitched = b_rows > 1 || (groups > 1 && !o->b_group);
+    const int64_t b_pitch = b_pitched && o->ldb ? o->ldb : b_cols;
     const int64_t lda = M > 1 ? (o->lda ? o->lda : K) : cdiv(K, 16) * 16;
-    const int64_t ldb = b_rows > 1 ? (o->ldb ? o->ldb : b_cols) : cdiv(b_cols, 16) * 16;
+    const int64_t ldb = b_rows > 1 ? b_pitch : cdiv(b_cols, 16) * 16;
     const int64_t ldd = o->ldd ? o->ldd : N;
-    if (lda < K || ldb < b_cols || ldd < N || lda > (int64_t(1) << 38) || ldb > (int64_t(1) << 38) ||
+    if (lda < K || b_pitch < b_cols || ldd < N || lda > (int64_t(1) << 38) || b_pitch > (int64_t(1) << 38) ||
         ldd > (int64_t(1) << 37))
         return fail(TS_ERR_INVALID_ARG, "leading dimensions must cover a row (lda=%lld ldb=%lld ldd=%lld)",
-                    static_cast<long long>(lda), static_cast<long long>(ldb), static_cast<long long>(ldd));
+                    static_cast<long long>(lda), static_cast<long long>(b_pitch), static_cast<long long>(ldd));
     if (M == 0 || N == 0 || groups == 0) return TS_OK;
     if (!D) return fail(TS_ERR_INVALID_ARG, "D is NULL");
     if (grouped && !offsets) return fail(TS_ERR_INVALID_ARG, "offsets is NULL");
@@ -117,7 +120,10 @@ ts_status fp8_product(const void *A, const float *SA, const void *B, const float
     if (lda % 16 || ldb % 16)
         return fail(TS_ERR_UNSUPPORTED, "rows of A and B must start on 16-byte boundaries (lda, ldb multiples of 16)");
     const int64_t depth = grouped ? groups : 1;
-    const int64_t b_group = o->b_group ? o->b_group : b_rows * ldb;
+    if (depth > 1 && (b_pitch > (int64_t(1) << 39) / b_rows || o->b_group > (int64_t(1) << 39)))
+        return fail(TS_ERR_INVALID_ARG, "groups of B are too far apart (ldb=%lld b_group=%lld)",
+                    static_cast<long long>(b_pitch), static_cast<long long>(o->b_group));
+    const int64_t b_group = o->b_group ? o->b_group : b_rows * b_pitch;
     if (depth > 1 && b_group % 16)
         return fail(TS_ERR_UNSUPPORTED, "groups of B must start on 16-byte boundaries (b_group a multiple of 16)");
     if (depth > 1 && b_group < (b_rows - 1) * ldb + b_cols)
