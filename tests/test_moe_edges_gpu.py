@@ -50,3 +50,33 @@ def test_groups_of_one_row_through_the_c_entry(lib, trans, pitch):
     rows = buf[:, :L].repeat_interleave(R, 0)
     want = 2 * (a * rows if trans else (a * rows).sum(1, keepdim=True))
     assert torch.equal(D.cpu(), want)
+
+
+def test_plans_of_threads_on_one_stream(lib):
+    # more slots than one CTA sorts: each call is two launches that share the scratch it keeps
+    import threading
+
+    T, E, threads, calls = 9000, 64, 4, 30
+    start, errors = threading.Barrier(threads), []
+
+    def work(seed):
+        try:
+            g = torch.Generator().manual_seed(seed)
+            e = [torch.randint(0, E, (T, 2), generator=g, dtype=torch.int32) for _ in range(calls)]
+            dev = [x.cuda() for x in e]
+            bufs = [_plan_buffers(T, 2, E) for _ in range(calls)]
+            torch.cuda.synchronize()
+            start.wait()
+            for x, b in zip(dev, bufs):
+                lib.ts_moe_plan(x, *b)  # all on the default stream
+            torch.cuda.synchronize()
+            for x, (_, order, _) in zip(e, bufs):
+                assert torch.equal(order.cpu().long(), x.flatten().sort(stable=True).indices)
+        except Exception as err:  # noqa: BLE001
+            errors.append(err)
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(threads)]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    lib.ts_sync_and_check()
+    assert not errors, errors[0]

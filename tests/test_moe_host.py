@@ -144,3 +144,49 @@ def test_groups_of_one_row_keep_the_callers_pitch(ts, trans):
     assert _fp8(ts, groups=2, b_group=120, ldb=96, **one) == U  # given, it leaves a single row's pitch unused
     # a padded row: the second group ends 1024 + 100 bytes behind B's start
     assert _fp8(ts, groups=2, D=2 * P + 1024 + 96, ldb=1024, **one) == E and "overlap" in ts.ts_last_error_detail()
+
+
+@pytest.fixture
+def no_cuda_scratch(ts, monkeypatch):
+    """The plan's scratch on the CPU: its streams are integers, and `capturing` says which of them capture."""
+    import contextlib
+
+    import torch
+
+    current, capturing = [0], set()
+
+    @contextlib.contextmanager
+    def on(stream):
+        current.append(stream)
+        try:
+            yield
+        finally:
+            current.pop()
+
+    class Stream(int):
+        cuda_stream = property(int)
+
+        def __new__(cls, handle, device=None):
+            return int.__new__(cls, handle)
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: int(current[-1]) in capturing)
+    monkeypatch.setattr(ts, "_stream_of", lambda s: int(current[-1] if s is None else s))
+    made = []
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: made.append(int(current[-1])) or empty(*a, **kw))
+    return current, capturing, made, lambda stream=None, n=1000: ts._scratch_for(n, torch.device("cpu"), stream)
+
+
+def test_threads_on_one_stream_do_not_share_a_plans_scratch(no_cuda_scratch):
+    import threading
+
+    *_, scratch = no_cuda_scratch
+    mine = scratch(7)
+    assert scratch(7) is mine, "kept from call to call"
+    got = []
+    t = threading.Thread(target=lambda: got.append(scratch(7)))
+    t.start()
+    t.join()
+    assert got[0].data_ptr() != mine.data_ptr()

@@ -16,6 +16,7 @@ import ctypes
 import functools
 import os
 import struct
+import threading
 
 import torch
 
@@ -806,21 +807,28 @@ def _plan_need(slots: int, experts: int) -> int:
     return _lib.ts_moe_plan_workspace(slots, experts)
 
 
-_SCRATCH: dict = {}
+class _Scratch(threading.local):
+    def __init__(self):
+        self.kept: dict = {}
+
+
+_SCRATCH = _Scratch()
 
 
 def _scratch_for(nbytes: int, device, stream) -> torch.Tensor:
     """Uninitialised scratch of at least ``nbytes``, kept per device and stream and allocated on the stream
-    it serves, so that calls on different streams never share one (nor do graphs, which may replay at once)."""
+    it serves, so that calls on different streams never share one (nor do graphs, which may replay at once).
+    Each thread keeps its own: a call launches several kernels that hand counts on through the scratch, and
+    on a stream that threads share another's may come between them."""
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)  # the graph's own
     key = (device, _stream_of(stream))
-    ws = _SCRATCH.get(key)
+    ws = _SCRATCH.kept.get(key)
     if ws is None or ws.numel() < nbytes:
         st = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(key[1], device=device)
         with torch.cuda.stream(st):
             ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        _SCRATCH[key] = ws
+        _SCRATCH.kept[key] = ws
     return ws
 
 
