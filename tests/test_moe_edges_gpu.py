@@ -57,7 +57,7 @@ def test_plans_of_threads_on_one_stream(lib):
     import threading
 
     T, E, threads, calls = 9000, 64, 4, 30
-    start, errors = threading.Barrier(threads), []
+    start, errors = threading.Barrier(threads, timeout=60), []
 
     def work(seed):
         try:
@@ -80,3 +80,42 @@ def test_plans_of_threads_on_one_stream(lib):
     [t.join() for t in ts]
     lib.ts_sync_and_check()
     assert not errors, errors[0]
+
+
+def _captured_plan(lib, e, bufs, fork):
+    """A graph of one plan, on a side stream that the capture forks to or that captures alone; then an
+    allocation on the capturing stream, filled before the fork joins."""
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    main = torch.cuda.Stream()
+    if fork:
+        with torch.cuda.graph(graph, stream=main):
+            side.wait_stream(main)
+            lib.ts_moe_plan(e, *bufs, stream=side)
+            other = [torch.empty(lib.ts_moe_plan_workspace(e.numel(), bufs[0].numel() - 1), dtype=torch.uint8,
+                                 device="cuda").fill_(255) for _ in range(4)]
+            main.wait_stream(side)
+        return graph, other
+    with torch.cuda.stream(main):
+        graph.capture_begin(capture_error_mode="relaxed")
+    with torch.cuda.stream(side):
+        lib.ts_moe_plan(e, *bufs, stream=main)
+    with torch.cuda.stream(main):
+        graph.capture_end()
+    return graph, None
+
+
+@pytest.mark.parametrize("fork", [True, False])
+def test_captured_plan_on_a_stream_that_is_passed(lib, fork):
+    T, E = 20000, 64
+    e = torch.randint(0, E, (T, 2), dtype=torch.int32, device="cuda")
+    bufs, eager = _plan_buffers(T, 2, E), _plan_buffers(T, 2, E)
+    lib.ts_moe_plan(e, *eager)
+    torch.cuda.synchronize()
+    graph, other = _captured_plan(lib, e, bufs, fork)
+    for _ in range(10):
+        bufs[1].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(bufs, eager))
+    lib.ts_sync_and_check()
+    assert other is None or all((o == 255).all() for o in other)

@@ -190,3 +190,23 @@ def test_threads_on_one_stream_do_not_share_a_plans_scratch(no_cuda_scratch):
     t.start()
     t.join()
     assert got[0].data_ptr() != mine.data_ptr()
+
+
+def test_a_captured_plans_scratch_is_its_graphs(no_cuda_scratch):
+    current, capturing, made, scratch = no_cuda_scratch
+    kept = scratch(7)
+    made.clear()
+    # a capture that forks: the current stream (0) captures too, and the plan runs on 7
+    capturing |= {0, 7}
+    first = scratch(7)
+    assert made == [7] and first.data_ptr() != kept.data_ptr(), "allocated on the stream that uses it"
+    assert scratch().data_ptr() != first.data_ptr() and made == [7, 0]
+    # only the plan's stream captures: the graph must not record the kept scratch
+    capturing.discard(0)
+    assert scratch(7).data_ptr() not in (kept.data_ptr(), first.data_ptr())
+    # and nothing of a graph is kept for later calls
+    capturing.clear()
+    assert scratch(7) is kept
+    # only the current stream captures: the call is no part of the graph
+    capturing.add(0)
+    assert scratch(7) is kept

@@ -820,15 +820,19 @@ def _scratch_for(nbytes: int, device, stream) -> torch.Tensor:
     it serves, so that calls on different streams never share one (nor do graphs, which may replay at once).
     Each thread keeps its own: a call launches several kernels that hand counts on through the scratch, and
     on a stream that threads share another's may come between them."""
+    handle = _stream_of(stream)
+    if stream is not None and handle != _stream_of(None):
+        # as on that stream: whether it captures, and where memory that the call returns is used next
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(handle, device=device)
+        with torch.cuda.stream(stream):
+            return _scratch_for(nbytes, device, None)
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)  # the graph's own
-    key = (device, _stream_of(stream))
+    key = (device, handle)
     ws = _SCRATCH.kept.get(key)
     if ws is None or ws.numel() < nbytes:
-        st = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(key[1], device=device)
-        with torch.cuda.stream(st):
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        _SCRATCH.kept[key] = ws
+        ws = _SCRATCH.kept[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return ws
 
 
