@@ -119,3 +119,26 @@ def test_captured_plan_on_a_stream_that_is_passed(lib, fork):
         assert all(torch.equal(a, b) for a, b in zip(bufs, eager))
     lib.ts_sync_and_check()
     assert other is None or all((o == 255).all() for o in other)
+
+
+@pytest.mark.parametrize("form", ["block", "row"])
+def test_scales_of_more_than_2_29_rows(lib, form):
+    # four bytes a scale: the distance to the last one, in bytes, passes 2^31
+    n = 2 ** 29 + 256
+    codes = torch.tensor([1.0, 2.0, 3.0, 4.0], device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+    long = torch.zeros((n, 16), dtype=torch.uint8, device="cuda")
+    long.view(-1, 4, 16)[:, :, 0] = codes
+    long = long.view(torch.float8_e4m3fn)
+    scales = torch.empty((1, n), device="cuda")
+    scales.view(-1, 8)[:] = torch.tensor([1.0, 1.0, 1.0, 1.0, 2.0, 2.0, 2.0, 2.0], device="cuda")
+    one = torch.ones((1, 16), device="cuda").to(torch.float8_e4m3fn)
+    unit = torch.ones((1, 1), device="cuda")
+    if form == "block":
+        D = torch.full((n, 1), float("nan"), device="cuda")
+        lib.ts_gemm_fp8(long, scales.t(), one, unit, D)
+    else:
+        D = torch.full((1, n), float("nan"), device="cuda")
+        lib.ts_gemm_fp8(one, unit, long, scales.t(), D)
+    lib.ts_sync_and_check()
+    want = torch.tensor([1.0, 2.0, 3.0, 4.0, 2.0, 4.0, 6.0, 8.0], device="cuda")
+    assert bool((D.view(-1, 8) == want).all())
