@@ -555,8 +555,8 @@ ts_status ts_gemm_fp8(const void *A, const float *SA, const void *B, const float
  *
  *   D[m][n] = as ts_gemm_fp8 with B and SB of group g,   offsets[g] <= m < offsets[g + 1]
  *
- *   A, SA, D  as for ts_gemm_fp8, M rows in all; rows of D outside every group are
- *             not written
+ *   A, SA, D  as for ts_gemm_fp8, M rows in all (at most 2^31 - 256, or the call returns
+ *             TS_ERR_UNSUPPORTED); rows of D outside every group are not written
  *   B, SB     device, `groups` matrices (and their block scales) one after another
  *   offsets   DEVICE int64 array of groups + 1 non-decreasing row offsets in [0, M],
  *             8-byte aligned, read by the kernel: the host need not know them.  A

@@ -210,3 +210,12 @@ def test_a_captured_plans_scratch_is_its_graphs(no_cuda_scratch):
     # only the current stream captures: the call is no part of the graph
     capturing.add(0)
     assert scratch(7) is kept
+
+
+def test_grouped_rows_stay_below_2_31(ts):
+    # a group may start at any row, and its tiles reach up to 255 rows past its last one
+    U, top = ts.TS_ERR_UNSUPPORTED, (1 << 31) - 256
+    assert _fp8(ts, M=top + 1, groups=2, D=1 << 50) == U and "rows" in ts.ts_last_error_detail()
+    assert _fp8(ts, M=(1 << 31) - 1, groups=2, D=1 << 50) == U
+    # at the limit, the next check answers
+    assert _fp8(ts, M=top, groups=2, D=0) == ts.TS_ERR_INVALID_ARG

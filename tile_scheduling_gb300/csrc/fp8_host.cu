@@ -58,6 +58,10 @@ ts_status fp8_product(const void *A, const float *SA, const void *B, const float
     if (grouped && groups > kMaxExperts)
         return fail(TS_ERR_UNSUPPORTED, "%lld groups exceed the %d-group limit", static_cast<long long>(groups),
                     kMaxExperts);
+    // a group starts at any row, and the last row of its last tile must be a 32-bit coordinate
+    if (grouped && M > kMaxDim - 255)
+        return fail(TS_ERR_UNSUPPORTED, "M = %lld: a grouped product takes at most 2^31 - 256 rows",
+                    static_cast<long long>(M));
     if (out != TS_OUT_BF16 && out != TS_OUT_F32) return fail(TS_ERR_INVALID_ARG, "out_dtype %d", out);
     if (o->a_type != TS_FP8_E4M3 && o->a_type != TS_FP8_E5M2) return fail(TS_ERR_INVALID_ARG, "a_type %d", o->a_type);
     if (o->b_type != TS_FP8_E4M3 && o->b_type != TS_FP8_E5M2) return fail(TS_ERR_INVALID_ARG, "b_type %d", o->b_type);
