@@ -561,7 +561,9 @@ ts_status ts_gemm_fp8(const void *A, const float *SA, const void *B, const float
  *   offsets   DEVICE int64 array of groups + 1 non-decreasing row offsets in [0, M],
  *             8-byte aligned, read by the kernel: the host need not know them.  A
  *             group whose offsets are not ordered in [0, M] is not computed and is
- *             reported by ts_sync_and_check.  An empty group costs nothing.
+ *             reported by ts_sync_and_check; of the groups behind one that decreases,
+ *             whose rows may overlap earlier ones, no more tiles are computed than M
+ *             rows in so many groups have.  An empty group costs nothing.
  *   groups    0 .. 1024
  */
 ts_status ts_gemm_fp8_grouped(const void *A, const float *SA, const void *B, const float *SB, void *D,

@@ -142,3 +142,25 @@ def test_scales_of_more_than_2_29_rows(lib, form):
     lib.ts_sync_and_check()
     want = torch.tensor([1.0, 2.0, 3.0, 4.0, 2.0, 4.0, 6.0, 8.0], device="cuda")
     assert bool((D.view(-1, 8) == want).all())
+
+
+@pytest.mark.parametrize("M,G,N", [(1280, 64, 300), (2 ** 29, 1024, 1)])
+def test_disordered_groups_make_no_more_tiles_than_ordered_ones(lib, M, G, N):
+    # offsets 0, M, 0, M, ...: every other group is all rows, and 512 of those have 2^31 tiles.  All groups
+    # have the same weights, so it does not matter which of them writes a row.
+    codes = torch.tensor([1.0, 2.0, 3.0, 4.0], device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+    A = torch.zeros((M, 16), dtype=torch.uint8, device="cuda")
+    A.view(-1, 4, 16)[:, :, 0] = codes
+    A = A.view(torch.float8_e4m3fn)
+    SA = torch.full((1, M), 0.5, device="cuda").t()
+    B = torch.ones((G, N, 16), device="cuda").to(torch.float8_e4m3fn)
+    SB = torch.ones((G, -(-N // 128), 1), device="cuda")
+    off = torch.zeros(G + 1, dtype=torch.int64, device="cuda")
+    off[1::2] = M
+    D = torch.full((M, N), float("nan"), device="cuda")
+    lib.ts_gemm_fp8_grouped(A, SA, B, SB, D, off)
+    with pytest.raises(lib.TsError) as err:
+        lib.ts_sync_and_check()
+    assert "offsets" in err.value.detail
+    want = torch.tensor([[0.5], [1.0], [1.5], [2.0]], device="cuda")
+    assert bool((D.view(-1, 4, N) == want).all())

@@ -272,7 +272,9 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC, AR>::THREADS
     grid_dep_launch();
     int32_t num_units = p.num_units;
     if constexpr (GROUPED) {
-        // Units per group, then their running sum (warp 2, 32 groups at a time).
+        // Units per group, then their running sum (warp 2, 32 groups at a time).  Ordered offsets
+        // make at most p.num_units in all; disordered ones may leave groups whose ranges overlap
+        // and whose sum passes 32 bits: it is formed in 64 and cut there.
         for (int32_t g = threadIdx.x; g < p.groups; g += C::THREADS) {
             int64_t lo, hi;
             if (!group_rows(p, g, lo, hi) && blockIdx.x == 0) report_group(p, g);
@@ -281,16 +283,16 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC, AR>::THREADS
         if (threadIdx.x == 0) prefix[0] = 0;
         __syncthreads();
         if (warp == 2) {
-            int32_t run = 0;
+            int64_t run = 0;
             for (int32_t g0 = 0; g0 < p.groups; g0 += 32) {
                 const int32_t g = g0 + lane;
-                int32_t v = g < p.groups ? prefix[g + 1] : 0;
+                int64_t v = g < p.groups ? prefix[g + 1] : 0;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
-                    const int32_t o = __shfl_up_sync(0xffffffffu, v, d);
+                    const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
                     if (lane >= d) v += o;
                 }
-                if (g < p.groups) prefix[g + 1] = run + v;
+                if (g < p.groups) prefix[g + 1] = static_cast<int32_t>(min(run + v, static_cast<int64_t>(p.num_units)));
                 run += __shfl_sync(0xffffffffu, v, 31);
             }
         }
