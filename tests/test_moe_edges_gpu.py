@@ -164,3 +164,11 @@ def test_disordered_groups_make_no_more_tiles_than_ordered_ones(lib, M, G, N):
     assert "offsets" in err.value.detail
     want = torch.tensor([[0.5], [1.0], [1.5], [2.0]], device="cuda")
     assert bool((D.view(-1, 4, N) == want).all())
+
+
+def test_routing_scale_of_the_smallest_normal_number(lib):
+    x = torch.zeros((1, 4), device="cuda")
+    e, w = torch.empty((1, 2), dtype=torch.int32, device="cuda"), torch.empty((1, 2), device="cuda")
+    lib.ts_moe_route(x, e, w, scale=2.0 ** -126)
+    lib.ts_sync_and_check()
+    assert w.tolist() == [[2.0 ** -127] * 2]

@@ -219,3 +219,13 @@ def test_grouped_rows_stay_below_2_31(ts):
     assert _fp8(ts, M=(1 << 31) - 1, groups=2, D=1 << 50) == U
     # at the limit, the next check answers
     assert _fp8(ts, M=top, groups=2, D=0) == ts.TS_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("scale", [0, -0.0, 1e-50, -1e-50, 2.0 ** -150])
+def test_a_routing_scale_that_is_zero_in_32_bits(ts, scale):
+    # the options hold it in fp32, where 0 stands for the default of 1
+    with pytest.raises(ValueError, match="scale"):
+        ts.ts_moe_route(None, None, None, scale=scale)
+    with pytest.raises(ValueError, match="scale"):
+        ts.ts_moe_route_grad(None, None, None, None, scale=scale)
+    assert ts._PACK_ROUTE.unpack(ts._PACK_ROUTE.pack(*[0] * 6, 2.0 ** -149, 0, 0, 0))[6] == 2.0 ** -149

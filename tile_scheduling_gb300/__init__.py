@@ -753,6 +753,9 @@ def ts_quant_fp8(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, rows=No
         _check(st)
 
 
+_SCALE_ZERO = 2.0 ** -150  # up to here a routing scale is 0 in fp32, as the options hold it, and 0 is the default
+
+
 def _score(score) -> int:
     return _SCORE[score] if isinstance(score, str) else int(score)
 
@@ -765,8 +768,8 @@ def ts_moe_route(logits: torch.Tensor, experts: torch.Tensor, weights: torch.Ten
     ``groups`` equal groups of experts the ``keep_groups`` best (0: all) stay, by the sum of their
     ``group_best`` (1 or 2) best experts.  Equal values go to the lower index; an expert with logit -inf is
     never chosen, and slots without one hold -1 and weight 0.  ``renorm`` divides the weights by their sum."""
-    if scale == 0:
-        raise ValueError("scale must not be 0")
+    if -_SCALE_ZERO <= scale <= _SCALE_ZERO:
+        raise ValueError("scale must not be 0 in fp32")
     dtype, (T, E), ldx = _matrix_of(logits, "logits", _OUT)
     k = experts.shape[-1]
     o = _PACK_ROUTE.pack(_dense(bias, "bias", _F32, (E,)) if bias is not None else 0, _score(score), groups,
@@ -780,8 +783,8 @@ def ts_moe_route(logits: torch.Tensor, experts: torch.Tensor, weights: torch.Ten
 def ts_moe_route_grad(logits: torch.Tensor, experts: torch.Tensor, grad_weights: torch.Tensor,
                       grad_logits: torch.Tensor, score="softmax", renorm=True, scale=1.0, stream=None) -> None:
     """grad_logits [T, E] (the logits' type) from grad_weights [T, k], for the experts that ts_moe_route chose."""
-    if scale == 0:
-        raise ValueError("scale must not be 0")
+    if -_SCALE_ZERO <= scale <= _SCALE_ZERO:
+        raise ValueError("scale must not be 0 in fp32")
     dtype, (T, E), ldx = _matrix_of(logits, "logits", _OUT)
     k = experts.shape[-1]
     g_dtype, g_shape, ldg = _matrix_of(grad_logits, "grad_logits", _OUT)
