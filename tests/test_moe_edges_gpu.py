@@ -172,3 +172,31 @@ def test_routing_scale_of_the_smallest_normal_number(lib):
     lib.ts_moe_route(x, e, w, scale=2.0 ** -126)
     lib.ts_sync_and_check()
     assert w.tolist() == [[2.0 ** -127] * 2]
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_gradient_of_chosen_scores_whose_reciprocal_overflows(lib, score):
+    # chosen scores of some 6e-39 (softmax: experts that a bias chose, far below the largest logit)
+    x = torch.full((3, 40), -88.0, device="cuda")
+    x[:, 1::2] = -88.2
+    if score == "softmax":
+        x += 88.0
+        x[:, 7] = 88.0 - 8.0 / 1024
+    e = torch.tensor([[0, 1], [5, 38], [-1, 3]], dtype=torch.int32, device="cuda")
+    gw = torch.tensor([[30.0, -20.0], [-5.0, 40.0], [3.0, 7.0]], device="cuda")
+    gx = torch.full_like(x, float("nan"))
+    lib.ts_moe_route_grad(x, e, gw, gx, score=score)
+    lib.ts_sync_and_check()
+    there = (e >= 0).double()
+    xd = x.double()
+    s = torch.sigmoid(xd) if score == "sigmoid" else torch.softmax(xd, 1)
+    share = s.gather(1, e.clamp_min(0).long()) * there
+    share = share / share.sum(1, keepdim=True)
+    g = gw.double() * there
+    v = (g - (g * share).sum(1, keepdim=True)) * share
+    want = torch.zeros_like(xd).scatter_add_(1, e.clamp_min(0).long(), v)
+    if score == "sigmoid":
+        want *= torch.sigmoid(-xd)
+    # a score: two units of expf and of the subnormal grid here (2^-22 each), a rounding or two; its share
+    # twice that, the difference twice again
+    assert bool(((gx.double() - want).abs() <= 2.0 ** -18 * gw.double().abs().amax()).all())

@@ -228,10 +228,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
     }
 }
 
-// The gradient recomputes the scores.  With g_j = scale * grad_w_j:
-//   d s_j = (g_j - sum_i g_i s_i / S) / S with S = sum_j s_j (renorm), else g_j
-//   sigmoid: dx = ds * s * (1 - s);   softmax: dx_e = s_e * (ds_e - sum_i ds_i s_i)
-// 1 - s is sigmoid(-x), which keeps its digits where s is close to 1.
+// The gradient recomputes the scores.  With g_j = scale * grad_w_j and p_j = s_j / S, S = sum_j s_j:
+//   v_j = s_j * d s_j = (g_j - sum_i g_i p_i) * p_j (renorm), else g_j * s_j
+//   sigmoid: dx = v * (1 - s);   softmax: dx_e = v_e - s_e * sum_i v_i   (renorm: the sum is 0)
+// 1 - s is sigmoid(-x), which keeps its digits where s is close to 1.  Dividing s by S before
+// anything multiplies it keeps v finite where S is so small that 1 / S would not be.
 template <class T, int NS>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const __grid_constant__ RouteParams p) {
     grid_dep_wait();
@@ -264,19 +265,18 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const __gr
     }
     // lane j: the score of choice j, from its logit
     const float sj = mine >= 0 ? score_of(clean(load_logit(row + mine)), norm, p.softmax) : 0.f;
-    float ds = g;
+    float dsj = g * sj, mean = 0.f;
     if (p.renorm) {
-        float sum = sj, dot = g * sj;
+        float sum = sj;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) {
-            sum += __shfl_xor_sync(kAll, sum, d);
-            dot += __shfl_xor_sync(kAll, dot, d);
-        }
-        ds = mine >= 0 && sum > 0.f ? (g - dot / sum) / sum : 0.f;
-    }
-    float mean = 0.f;
-    if (p.softmax) {
-        mean = ds * sj;
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+        const float share = sum > 0.f ? sj / sum : 0.f;
+        float dot = g * share;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(kAll, dot, d);
+        dsj = mine >= 0 ? (g - dot) * share : 0.f;
+    } else if (p.softmax) {
+        mean = dsj;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) mean += __shfl_xor_sync(kAll, mean, d);
     }
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const __gr
     for (int i = 0; i < NS; ++i) dx[i] = 0.f;
     for (int j = 0; j < p.k; ++j) {
         const int e = __shfl_sync(kAll, mine, j);
-        const float v = __shfl_sync(kAll, ds, j);
+        const float v = __shfl_sync(kAll, dsj, j);
 #pragma unroll
         for (int i = 0; i < NS; ++i)
             if (i * 32 + lane == e) dx[i] += v;
@@ -294,9 +294,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const __gr
     for (int i = 0; i < NS; ++i) {
         const int e = i * 32 + lane;
         if (p.softmax)
-            dx[i] = s[i] * (dx[i] - mean);
+            dx[i] = dx[i] - s[i] * mean;
         else
-            dx[i] = masked[i] ? 0.f : dx[i] * s[i] * (1.f / (1.f + expf(fminf(x[i], 3.402823466e38f))));
+            dx[i] = masked[i] ? 0.f : dx[i] * (1.f / (1.f + expf(fminf(x[i], 3.402823466e38f))));
         if (nan) dx[i] = __int_as_float(0x7fffffff);
         if (e < p.E) {
             if constexpr (sizeof(T) == 4)
