@@ -42,18 +42,30 @@ def _fp8(rows: int, cols: int, dtype=torch.float8_e4m3fn):
     return q, torch.empty((-(-cols // BLOCK), rows), dtype=torch.float32, device="cuda").t()
 
 
+def _bf16_rows(x: torch.Tensor) -> torch.Tensor:
+    """A matrix as bf16 with its rows on 16-byte boundaries, where the bf16 products take them (x itself if it is)."""
+    rows, cols = x.shape
+    if x.dtype is torch.bfloat16 and x.stride(1) == 1 and x.data_ptr() % 16 == 0 and \
+            (rows <= 1 or (x.stride(0) >= cols and x.stride(0) % 8 == 0)):
+        return x
+    out = torch.empty((rows, -(-cols // 8) * 8), dtype=torch.bfloat16, device=x.device)[:, :cols]
+    return out.copy_(x)
+
+
 class MoeLayer:
     """router [E, K] and experts [E, N, K] (bf16 or fp32 CUDA tensors); routing options as ts_moe_route."""
 
     def __init__(self, router: torch.Tensor, experts: torch.Tensor, top_k: int, score="softmax", bias=None, groups=1,
                  keep_groups=0, group_best=1, renorm=True, scale=1.0):
-        self.router = router.bfloat16().contiguous()
+        self.router = _bf16_rows(router)
         self.w, self.sw = quantise_blocks(experts)
         self.top_k, self.bias, self.score, self.renorm, self.scale = top_k, bias, score, renorm, scale
         self.groups = dict(groups=groups, keep_groups=keep_groups, group_best=group_best)
 
     def forward(self, x: torch.Tensor):
         """x [T, K] bf16 -> (out [T, N] bf16, what backward needs)."""
+        if x.dtype is not torch.bfloat16:
+            raise TypeError("x must be a torch.bfloat16 tensor")
         T, K = x.shape
         E, N = self.w.shape[0], self.w.shape[1]
         k = self.top_k
@@ -63,7 +75,7 @@ class MoeLayer:
              "order": torch.empty(T * k, dtype=torch.int32, **dev),
              "position": torch.empty((T, k), dtype=torch.int32, **dev),
              "y": torch.empty((T * k, N), dtype=torch.bfloat16, **dev)}
-        ts.ts_gemm_bf16_ex(x, self.router, s["logits"])
+        ts.ts_gemm_bf16_ex(_bf16_rows(x), self.router, s["logits"])
         ts.ts_moe_route(s["logits"], s["experts"], s["weights"], bias=self.bias, score=self.score, renorm=self.renorm,
                         scale=self.scale, **self.groups)
         ts.ts_moe_plan(s["experts"], s["offsets"], s["order"], s["position"])
@@ -102,5 +114,5 @@ class MoeLayer:
         grad_router = torch.empty((E, K), **dev)
         ts.ts_gemm_fp8(lq, ls, xq, xs, grad_router)
         from_router = torch.empty((T, K), dtype=torch.bfloat16, **dev)
-        ts.ts_gemm_bf16_ex(grad_logits.bfloat16(), self.router.t().contiguous(), from_router)
+        ts.ts_gemm_bf16_ex(_bf16_rows(grad_logits), _bf16_rows(self.router.t()), from_router)
         return grad_x.add_(from_router), grad_router
