@@ -85,3 +85,15 @@ def test_rows_off_the_16_byte_grid(lib, T, E, N, K, k, score):
     grads = layer.backward(s, grad_out)
     lib.ts_sync_and_check()
     _check_layer(lib, layer, x, grad_out, out, s, *grads)
+
+
+def test_default_dtype_does_not_reach_the_layers_buffers(lib):
+    layer, x, grad_out = _layer(40, 8, 64, 128, 2)
+    try:
+        torch.set_default_dtype(torch.float64)
+        out, s = layer.forward(x)
+        grads = layer.backward(s, grad_out)
+        lib.ts_sync_and_check()
+    finally:
+        torch.set_default_dtype(torch.float32)
+    _check_layer(lib, layer, x, grad_out, out, s, *grads)

@@ -36,10 +36,10 @@ def quantise_blocks(w: torch.Tensor):
     return out, (amax / 448.0).contiguous()
 
 
-def _fp8(rows: int, cols: int, dtype=torch.float8_e4m3fn):
+def _fp8(rows: int, cols: int, device, dtype=torch.float8_e4m3fn):
     """Room for a quantised matrix: rows on 16-byte boundaries, scales with their rows contiguous."""
-    q = torch.empty((rows, -(-cols // 16) * 16), dtype=dtype, device="cuda")[:, :cols]
-    return q, torch.empty((-(-cols // BLOCK), rows), dtype=torch.float32, device="cuda").t()
+    q = torch.empty((rows, -(-cols // 16) * 16), dtype=dtype, device=device)[:, :cols]
+    return q, torch.empty((-(-cols // BLOCK), rows), dtype=torch.float32, device=device).t()
 
 
 def _bf16_rows(x: torch.Tensor) -> torch.Tensor:
@@ -69,21 +69,20 @@ class MoeLayer:
         T, K = x.shape
         E, N = self.w.shape[0], self.w.shape[1]
         k = self.top_k
-        dev = dict(device=x.device)
-        s = {"x": x, "logits": torch.empty((T, E), **dev), "experts": torch.empty((T, k), dtype=torch.int32, **dev),
-             "weights": torch.empty((T, k), **dev), "offsets": torch.empty(E + 1, dtype=torch.int64, **dev),
-             "order": torch.empty(T * k, dtype=torch.int32, **dev),
-             "position": torch.empty((T, k), dtype=torch.int32, **dev),
-             "y": torch.empty((T * k, N), dtype=torch.bfloat16, **dev)}
+        f32, i32, bf16 = (dict(dtype=t, device=x.device) for t in (torch.float32, torch.int32, torch.bfloat16))
+        s = {"x": x, "logits": torch.empty((T, E), **f32), "experts": torch.empty((T, k), **i32),
+             "weights": torch.empty((T, k), **f32), "offsets": torch.empty(E + 1, dtype=torch.int64, device=x.device),
+             "order": torch.empty(T * k, **i32), "position": torch.empty((T, k), **i32),
+             "y": torch.empty((T * k, N), **bf16)}
         ts.ts_gemm_bf16_ex(_bf16_rows(x), self.router, s["logits"])
         ts.ts_moe_route(s["logits"], s["experts"], s["weights"], bias=self.bias, score=self.score, renorm=self.renorm,
                         scale=self.scale, **self.groups)
         ts.ts_moe_plan(s["experts"], s["offsets"], s["order"], s["position"])
         # tokens laid out by expert and quantised on the way
-        s["q"], s["sq"] = _fp8(T * k, K)
+        s["q"], s["sq"] = _fp8(T * k, K, x.device)
         ts.ts_quant_fp8(x, s["q"], s["sq"], rows=s["order"], rows_div=k)
         ts.ts_gemm_fp8_grouped(s["q"], s["sq"], self.w, self.sw, s["y"], s["offsets"])
-        out = torch.empty((T, N), dtype=torch.bfloat16, **dev)
+        out = torch.empty((T, N), **bf16)
         ts.ts_moe_combine(s["y"], s["position"], out, weights=s["weights"])
         return out, s
 
@@ -92,27 +91,28 @@ class MoeLayer:
         T, K = s["x"].shape
         E, N = self.w.shape[0], self.w.shape[1]
         k = self.top_k
-        dev = dict(device=grad_out.device)
-        grad_y = torch.empty((T * k, N), dtype=torch.bfloat16, **dev)
-        grad_w = torch.empty((T, k), **dev)
+        device = grad_out.device
+        f32, bf16 = (dict(dtype=t, device=device) for t in (torch.float32, torch.bfloat16))
+        grad_y = torch.empty((T * k, N), **bf16)
+        grad_w = torch.empty((T, k), **f32)
         ts.ts_moe_combine_grad(grad_out, s["y"], s["position"], s["weights"], grad_y, grad_w)
         # the experts' input gradient: gradients in e5m2, the same weights read the other way
-        gq, gs = _fp8(T * k, N, torch.float8_e5m2)
+        gq, gs = _fp8(T * k, N, device, torch.float8_e5m2)
         ts.ts_quant_fp8(grad_y, gq, gs)
-        grad_rows = torch.empty((T * k, K), dtype=torch.bfloat16, **dev)
+        grad_rows = torch.empty((T * k, K), **bf16)
         ts.ts_gemm_fp8_grouped(gq, gs, self.w, self.sw, grad_rows, s["offsets"], trans_b=True)
-        grad_x = torch.empty((T, K), dtype=torch.bfloat16, **dev)
+        grad_x = torch.empty((T, K), **bf16)
         ts.ts_moe_combine(grad_rows, s["position"], grad_x)  # the gather's gradient: a sum over the token's slots
         # the router: through the weights to the logits, then its weights' gradient along the tokens
         grad_logits = torch.empty_like(s["logits"])
         ts.ts_moe_route_grad(s["logits"], s["experts"], grad_w, grad_logits, score=self.score, renorm=self.renorm,
                              scale=self.scale)
-        lq, ls = _fp8(E, T)
-        xq, xs = _fp8(K, T)
+        lq, ls = _fp8(E, T, device)
+        xq, xs = _fp8(K, T, device)
         ts.ts_quant_fp8(grad_logits, lq, ls, transpose=True)
         ts.ts_quant_fp8(s["x"], xq, xs, transpose=True)
-        grad_router = torch.empty((E, K), **dev)
+        grad_router = torch.empty((E, K), **f32)
         ts.ts_gemm_fp8(lq, ls, xq, xs, grad_router)
-        from_router = torch.empty((T, K), dtype=torch.bfloat16, **dev)
+        from_router = torch.empty((T, K), **bf16)
         ts.ts_gemm_bf16_ex(_bf16_rows(grad_logits), _bf16_rows(self.router.t()), from_router)
         return grad_x.add_(from_router), grad_router
