@@ -97,3 +97,16 @@ def test_default_dtype_does_not_reach_the_layers_buffers(lib):
     finally:
         torch.set_default_dtype(torch.float32)
     _check_layer(lib, layer, x, grad_out, out, s, *grads)
+
+
+@pytest.mark.parametrize("how", ["sum", "column", "transposed"])
+def test_gradients_that_are_not_dense(lib, how):
+    # what out.sum().backward() and friends hand over: one value, or one row, expanded; columns first
+    T, N = 40, 64
+    layer, x, grad_out = _layer(T, 8, N, 128, 2)
+    grad_out = {"sum": torch.ones((), dtype=torch.bfloat16, device="cuda").expand(T, N),
+                "column": grad_out[:1].expand(T, N), "transposed": grad_out.t().contiguous().t()}[how]
+    out, s = layer.forward(x)
+    grads = layer.backward(s, grad_out)
+    lib.ts_sync_and_check()
+    _check_layer(lib, layer, x, grad_out, out, s, *grads)

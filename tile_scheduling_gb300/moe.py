@@ -93,6 +93,7 @@ class MoeLayer:
         k = self.top_k
         device = grad_out.device
         f32, bf16 = (dict(dtype=t, device=device) for t in (torch.float32, torch.bfloat16))
+        grad_out = grad_out.contiguous()  # a sum's gradient is one value expanded to [T, N]
         grad_y = torch.empty((T * k, N), **bf16)
         grad_w = torch.empty((T, k), **f32)
         ts.ts_moe_combine_grad(grad_out, s["y"], s["position"], s["weights"], grad_y, grad_w)
