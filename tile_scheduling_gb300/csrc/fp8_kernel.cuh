@@ -471,7 +471,9 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC, AR>::THREADS
             const int32_t row0 = w.row0 + static_cast<int32_t>(rank) * C::BM;
             const bool vec_a = p.sa_vec && (row0 & 3) == 0, vec_b = ROWS && p.sb_vec;
             const int32_t row = row0 + (vec_a ? 4 : 1) * lane;  // this lane's first row
-            const int32_t a_bytes = 4 * max(0, min(4, w.row_end - row));
+            // bytes of rows and columns that exist, from those left in the tile (times four they stay in 32 bits)
+            const int32_t row_left = min(w.row_end - row0, C::BM), col_left = min(p.N - w.col0, BN);
+            const int32_t a_bytes = max(0, min(16, 4 * (row_left - 4 * lane)));
             const float *pa = p.sa + (row < w.row_end ? static_cast<int64_t>(row) * p.sa_row : 0) + kb0 * p.sa_blk;
             // this lane's first column (ROWS) or block of columns
             const int32_t n = w.col0 + (ROWS ? (vec_b ? 4 : 1) : kScaleBlock) * lane;
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC, AR>::THREADS
 #pragma unroll
                         for (int i = 0; i < BN / 128; ++i)
                             copy_async_16(at + 512 + 512 * i + 16 * lane, n + 128 * i < p.N ? pb + 128 * i : p.sb,
-                                          4 * max(0, min(4, p.N - n - 128 * i)));
+                                          max(0, min(16, 4 * (col_left - 4 * lane - 128 * i))));
                     } else {
 #pragma unroll
                         for (int i = 0; i < BN / 32; ++i)
