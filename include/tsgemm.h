@@ -519,7 +519,8 @@ typedef struct {
                                 major, the layout that reads fastest); one 0 broadcasts along it */
     int64_t sb_row, sb_blk;  /* strides of SB along its rows and columns; both 0 = dense rows */
     int64_t sb_group;        /* grouped: elements between the groups of SB; 0 = dense */
-    double timeout_s;        /* per-wait limit for every mbarrier wait in the kernel; 0 = 2 s */
+    double timeout_s;        /* limit of an mbarrier wait in the kernel, at most 60; 0 = 2 s.  The promotion
+                                warps wait as long as the others do, but for no more than 2^27 polls */
 } ts_fp8_opts;
 
 /*

@@ -273,9 +273,6 @@ ts_status fp8_product(const void *A, const float *SA, const void *B, const float
     const double tmo = o->timeout_s > 0 ? o->timeout_s : kDefaultTimeoutS;
     p.timeout_ns = std::max<uint64_t>(1, static_cast<uint64_t>(std::min(tmo, 60.0) * 1e9));
     p.drain_ns = kDrainNs;
-    // a poll tries the barrier and reads the abort flag, two dependent loads: more than 16 ns
-    p.lean_polls = static_cast<uint32_t>(
-        std::min<uint64_t>(std::max<uint64_t>(p.timeout_ns / 16, uint64_t(1) << 27), 0xffffffffu));
     p.status = status;
     int64_t workers = std::min<int64_t>(units, sms / cg);
     if (o->max_workers > 0) workers = std::min<int64_t>(workers, o->max_workers);

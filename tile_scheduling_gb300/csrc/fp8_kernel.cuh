@@ -532,8 +532,8 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC, AR>::THREADS
         const uint64_t store_policy = policy_evict_first();
         // slots of this warp: count s of its K blocks since the start gives slot and phase
         uint32_t count = C::H == 2 ? h : 0, chunk = 0;
-        int32_t gave_up = 0;  // the wait that ended without its barrier
-        for (int32_t u = first; u < num_units && !gave_up; u += step) {
+        bool alive = true;
+        for (int32_t u = first; u < num_units && alive; u += step) {
             const Fp8Unit w = fp8_unit<C>(u, p, prefix);
             const int32_t row0 = w.row0 + static_cast<int32_t>(rank) * C::BM + 32 * q;
             const int32_t col0 = w.col0 + C::seg_col(h, 0);
@@ -545,9 +545,9 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC, AR>::THREADS
             for (int i = 0; i < C::COLS / 2; ++i) sum[i] = 0ull;
             for (int32_t kb = 0; kb < num_kb; ++kb) {
                 if (kb % C::CHUNK == 0) {
-                    const bool ok = wait_lean(sfull(chunk % C::CHUNKS), (chunk / C::CHUNKS) & 1u, abort_flag, p.lean_polls);
+                    const bool ok = wait_lean(sfull(chunk % C::CHUNKS), (chunk / C::CHUNKS) & 1u, abort_flag);
                     if (!__all_sync(0xffffffffu, ok)) {
-                        gave_up = WAIT_SCALES;
+                        alive = false;
                         break;
                     }
                 }
@@ -570,10 +570,10 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC, AR>::THREADS
                 };
                 if (!ROWS || !work) chunk_done();
                 const uint32_t slot = count % C::SLOTS;
-                const bool ok = wait_lean(tfull(slot), (count / C::SLOTS) & 1u, abort_flag, p.lean_polls);
+                const bool ok = wait_lean(tfull(slot), (count / C::SLOTS) & 1u, abort_flag);
                 count += C::H;
                 if (!__all_sync(0xffffffffu, ok)) {
-                    gave_up = WAIT_EPI_TMEM_FULL;
+                    alive = false;
                     break;
                 }
                 tc_fence_after();
@@ -638,11 +638,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC, AR>::THREADS
                 }
                 if (ROWS) chunk_done();
             }
-            if (gave_up && lane == 0 && !*abort_flag) {  // no other role has: the polls ran out
-                report_timeout(p, gave_up);
-                *abort_flag = 1;
-            }
-            if (gave_up || !work) continue;
+            if (!alive || !work) continue;
             if constexpr (C::SPLIT) {
                 if (p.split > 1) {
                     // the partial sums go to shared memory (the ring has been read), for the
@@ -714,6 +710,10 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, ROWS, GROUPED, SC, AR>::THREADS
                 emit(std::integral_constant<int, OUT_F32>{});
             else
                 emit(std::integral_constant<int, OUT_BF16>{});
+        }
+        if (!alive && lane == 0 && !*abort_flag) {  // no other role gave up: the polls ran out
+            report_timeout(p, WAIT_PROMOTION);
+            *abort_flag = 1;
         }
         if (lane == 0) bulk_wait<0>();
         __syncwarp();

@@ -37,7 +37,6 @@ struct Fp8Params {
     void *D;
     int64_t ldd;
     uint64_t timeout_ns, drain_ns;
-    uint32_t lean_polls;  // polls of a wait without a time limit of its own; they take longer than timeout_ns
     unsigned long long *status;
 };
 

@@ -19,6 +19,7 @@ enum : int32_t {
     WAIT_ROWS_CLC = 8,
     WAIT_SCHED_PRODUCER = 9,
     WAIT_SCALES = 10,
+    WAIT_PROMOTION = 11,
 };
 
 // Device status word (library-owned, one per device):

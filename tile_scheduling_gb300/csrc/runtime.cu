@@ -29,7 +29,8 @@ const char *wait_name(int where) {
         case WAIT_DRAIN: return "waiting for in-flight copies at exit";
         case WAIT_ROWS_CLC: return "row copy waiting for a CLC response";
         case WAIT_SCHED_PRODUCER: return "CLC scheduler waiting for the producer to begin its unit";
-        case WAIT_SCALES: return "waiting for a chunk of scales, or for its buffer";
+        case WAIT_SCALES: return "waiting for the buffer of a chunk of scales";
+        case WAIT_PROMOTION: return "promotion warp waiting for scales or for a finished K block";
         default: return "unknown wait";
     }
 }

@@ -45,10 +45,13 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
 // A wait of few instructions and without a function call, for loops whose registers
 // and instruction-cache lines are scarce.  It gives up when another role of the CTA
 // has (a role that waits with a time limit, and that this wait's end depends on or
-// that depends on it) or, should none, after `polls` polls; the caller then reports it.
-__device__ __forceinline__ bool wait_lean(uint32_t bar, uint32_t parity, volatile int *abort_flag, uint32_t polls) {
+// that depends on it) or, should none, after kLeanPolls polls, whatever that limit: a few
+// seconds at least (a poll tries the barrier and reads the abort flag, two dependent loads
+// of shared memory).  The caller reports it then.
+constexpr uint32_t kLeanPolls = 1u << 27;
+__device__ __forceinline__ bool wait_lean(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
     if (mbar_try_wait(bar, parity)) return true;
-    for (uint32_t n = 0; n < polls; ++n) {
+    for (uint32_t n = 0; n < kLeanPolls; ++n) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
     }
