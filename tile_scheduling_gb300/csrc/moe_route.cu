@@ -84,10 +84,11 @@ __device__ __forceinline__ float score_of(float x, const Norm &n, bool softmax) 
 }
 __device__ __forceinline__ float clean(float x) { return x > -INFINITY ? fminf(x, 3.402823466e38f) : -INFINITY; }
 
-// Scores of one token: x[i] becomes s of expert i * 32 + lane; masked[i] tells the
-// experts that cannot be chosen.  Returns whether any logit of the row is NaN.
+// Scores of one token: x[i] becomes s of expert i * 32 + lane (if `all`; else only what they
+// share is formed); masked[i] tells the experts that cannot be chosen.  Returns whether any
+// logit of the row is NaN.
 template <int NS>
-__device__ __forceinline__ bool scores(float (&x)[NS], bool (&masked)[NS], Norm &norm, bool softmax) {
+__device__ __forceinline__ bool scores(float (&x)[NS], bool (&masked)[NS], Norm &norm, bool softmax, bool all = true) {
     bool nan = false;
     norm.top = -3.402823466e38f;
     norm.sum = 0.f;
@@ -115,9 +116,11 @@ __device__ __forceinline__ bool scores(float (&x)[NS], bool (&masked)[NS], Norm 
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum[0] += __shfl_xor_sync(kAll, sum[0], d);
         norm.sum = sum[0];
+        if (all) {
 #pragma unroll
-        for (int i = 0; i < NS; ++i) x[i] = sum[0] > 0.f ? x[i] / sum[0] : 0.f;
-    } else {
+            for (int i = 0; i < NS; ++i) x[i] = sum[0] > 0.f ? x[i] / sum[0] : 0.f;
+        }
+    } else if (all) {
 #pragma unroll
         for (int i = 0; i < NS; ++i) x[i] = score_of(x[i], norm, false);
     }
@@ -250,7 +253,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const __gr
         x[i] = s[i];
     }
     Norm norm;
-    const bool nan = scores<NS>(s, masked, norm, p.softmax);
+    const bool every = p.softmax && !p.renorm;  // every expert's score stands in the gradient
+    const bool nan = scores<NS>(s, masked, norm, p.softmax, every);
     int32_t mine = -1;
     float g = 0.f;
     if (lane < p.k) {
@@ -293,9 +297,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const __gr
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
         const int e = i * 32 + lane;
-        if (p.softmax)
-            dx[i] = dx[i] - s[i] * mean;
-        else
+        if (every)
+            dx[i] -= s[i] * mean;
+        else if (!p.softmax)
             dx[i] = masked[i] ? 0.f : dx[i] * (1.f / (1.f + expf(fminf(x[i], 3.402823466e38f))));
         if (nan) dx[i] = __int_as_float(0x7fffffff);
         if (e < p.E) {
