@@ -541,7 +541,10 @@ typedef struct {
  * K blocks are shared by up to eight CTAs, whose sums are then added in order.  So
  * results are the same on every run, and the order of the sums (the last bits of fp32)
  * depends on M, N, K, tile and max_workers through that sharing alone; a grouped
- * product has none, and a row's result does not depend on its neighbours.  A scale is fp32 of any value; an infinity or NaN in an operand or a
+ * product has none, and a row's result does not depend on its neighbours.
+ * SA[m][b] * SB(n, b) is formed first, in fp32, and multiplies the block's sum: where the
+ * product of two finite scales overflows, that output is infinite or NaN even if the sum
+ * is 0, and a subnormal one has a subnormal's bits.  An infinity or NaN in an operand or a
  * scale shows in the rows and columns that use it.
  * M == 0 or N == 0: no-op.  K == 0: D is filled with zeros.  A, B and their rows
  * must start on 16-byte boundaries (lda and ldb multiples of 16), or the call

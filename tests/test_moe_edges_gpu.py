@@ -200,3 +200,19 @@ def test_route_gradient_of_chosen_scores_whose_reciprocal_overflows(lib, score):
     # a score: two units of expf and of the subnormal grid here (2^-22 each), a rounding or two; its share
     # twice that, the difference twice again
     assert bool(((gx.double() - want).abs() <= 2.0 ** -18 * gw.double().abs().amax()).all())
+
+
+@pytest.mark.parametrize("form", ["block", "row"])
+@pytest.mark.parametrize("a,b", [(100, -100), (-120, 126), (-100, -40), (60, 60), (0, -149)])
+def test_scales_far_apart(lib, form, a, b):
+    # powers of two whose product fp32 holds (a subnormal one too): the small whole numbers' sums stay exact
+    M, N, K = 40, 200, 384
+    g = torch.Generator().manual_seed(a)
+    x, y = (torch.randint(-2, 3, s, generator=g).float() for s in ((M, K), (N, K)))
+    A, B = x.to(torch.float8_e4m3fn).cuda(), y.to(torch.float8_e4m3fn).cuda()
+    SA = torch.full((M, 3), 2.0 ** a, device="cuda")
+    SB = torch.full((2 if form == "block" else N, 3), 2.0 ** b, device="cuda")
+    D = torch.full((M, N), float("nan"), device="cuda")
+    lib.ts_gemm_fp8(A, SA, B, SB, D)
+    lib.ts_sync_and_check()
+    assert torch.equal(D.double().cpu(), (x.double() @ y.double().t()) * 2.0 ** (a + b))
