@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 8 : 4) quant_trans
         }
     } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 8; ++j) {
             a[j] = fmaxf(fmaxf(fabsf(v[0][j]), fabsf(v[1][j])), fmaxf(fabsf(v[2][j]), fabsf(v[3][j])));
             a[j] = fmaxf(a[j], __shfl_xor_sync(0xffffffffu, a[j], 8));
             a[j] = fmaxf(a[j], __shfl_xor_sync(0xffffffffu, a[j], 16));
