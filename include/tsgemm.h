@@ -628,7 +628,8 @@ typedef struct {
  *
  * Equal values go to the lower index.  An expert whose logit is -inf (or whose c is
  * -inf or NaN) cannot be chosen; where fewer than top_k are left the last slots hold
- * expert -1 and weight 0 (a fully masked token holds nothing else).  A row with a NaN
+ * expert -1 and weight 0 (a fully masked token holds nothing else).  Scores are fp32:
+ * where every chosen one is 0, so are the weights and their gradient.  A row with a NaN
  * logit chooses among its other experts and all its weights are NaN.  The softmax's
  * denominator is summed by halving the zero-padded expert axis (to a power of two of
  * at least 32), so the choice is the same on every run and for every batch.

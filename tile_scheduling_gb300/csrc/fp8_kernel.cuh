@@ -21,10 +21,12 @@
 // with two of 256 columns); two 256-column slots are enough where both halves of the
 // promotion warps read every slot (128x256).
 //
-// Measured: 8192^3, e4m3, bf16 out, 363 to 400 us by the power cap's state (2750 to 3030
-// TFLOP/s; a pair); 4096 x 4096 x 8191 with row scales 157 us (1750; 128x128); 2047 x 4096
-// x 6144 41 us (2510; a pair); 16384 rows over 32 groups of 4096 x 2048, ragged, 132 us
-// (2080; 128x256); 1 x 4096 x 8192 8.1 to 8.9 us (4 TB/s; split over four CTAs a tile).
+// Measured, launches back to back: 8192^3, e4m3, bf16 out, 361 us at the full clock and 400
+// once the power cap lowers it, after some 40 ms (3050 and 2750 TFLOP/s; a pair); 4096 x
+// 4096 x 8191 with row scales 158 to 161 us (1740; 128x128); 2047 x 4096 x 6144 41 us (2530;
+// a pair); 16384 rows over 32 groups of 4096 x 2048, ragged, 131 us and 147 under the cap
+// (2100 and 1870; 128x256); 1 x 4096 x 8192 7.7 to 8.9 us (4 TB/s; split over four CTAs a
+// tile).
 //
 // Warp roles (384 threads, one CTA per SM):
 //   warp 0       TMA producer of the operand ring

@@ -16,10 +16,11 @@
 // and a round of the choice is one scan of a lane's slots and two warp
 // reductions on order-preserving integer keys.
 //
-// A token's logits are a few hundred bytes, so instructions and their latencies bound
-// it: 16384 tokens of 256 fp32 logits, eight choices, 18.3 us (18.7 MB, 1 TB/s), the
-// gradient 14.7; 8191 of 128 in bf16, six choices, 6.9 and 5.5; one token of 256 in
-// eight groups 4.0.
+// A token's logits are a few hundred bytes, so instructions bound a batch: at 8191 tokens of
+// 128 in bf16, six choices, a scheduler issues in 68 % of its cycles (the gradient: 50 %)
+// and memory is at 3 % of its rate.  Launches back to back: that batch 6.2 us and its
+// gradient 4.7; 16384 tokens of 256 fp32 logits, eight choices, softmax 16.5 us (18.7 MB,
+// 1.1 TB/s) and 10.4, sigmoid 15.9 and 12.2; one token of 256 in eight groups 3.4.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -378,8 +379,9 @@ ts_status route_check(RouteParams &p, const void *logits, int64_t T, int32_t E, 
 // A stable counting sort of the slots by expert.  A CTA takes tiles of
 // kPlanSlots consecutive slots, a warp kWarpSlots of them in order; equal
 // experts of a warp's 32 slots rank by lane.  Latencies bound it (three integers move
-// for a slot): 8 slots 2.8 us, 49146 of 128 experts 7.8, 131072 of 256 12.0, 1048576 of
-// 256 34.6.
+// for a slot, and at 49146 slots the two kernels issue in 9 and 18 % of the cycles): 8
+// slots 2.7 us, 49146 of 128 experts 7.5, 131072 of 256 12.0, 1048576 of 256 34.5, where
+// a tile's 16 x E counts, cleared and walked twice for 1024 slots, add to it.
 constexpr int kPlanWarps = 16;
 constexpr int kWarpSlots = 64;
 constexpr int kPlanSlots = kPlanWarps * kWarpSlots;
