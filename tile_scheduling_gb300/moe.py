@@ -6,9 +6,15 @@ The layer is a router and one linear map per expert:
     out[t] = sum_j weights[t, j] * W[experts[t, j]] @ x[t]
 
 It shows the operators in the order a user calls them and keeps what the backward
-pass needs.  The experts' products run in 8-bit floating point (weights quantised
-once in 128 x 128 blocks, activations for each row and 128 columns), the router's
-forward product in bf16, its weight gradient in 8 bits along the tokens.
+pass needs.  backward gives the gradients of the input and of the router; the experts'
+weights stay as they are (no operator forms their gradient from a plan).
+
+Rounded to fewer bits, in this order: the experts' weights (once, e4m3 in 128 x 128
+blocks), x (e4m3 for each row and 128 columns, for the experts; bf16 for the router),
+y and the output (bf16); backward, grad_y (bf16, then e5m2, whose range gradients need),
+the rows' gradients (bf16), grad_logits (bf16 for the input's gradient; e4m3 along the
+tokens, with x, for the router's weights, whose sum over the tokens averages the
+rounding) and grad_x (bf16).
 
 Usage: python -m tile_scheduling_gb300.run_workload moe
 """
