@@ -2,7 +2,9 @@
  * tsgemm -- persistent, warp-specialised bf16 GEMM with static and Cluster
  * Launch Control tile scheduling, plus a vectorised grid-stride int16 copy and
  * the operators of a mixture-of-experts layer (routing, 8-bit quantisation,
- * block-scaled 8-bit products, combine), for one NVIDIA GB300 (sm_103a).
+ * block-scaled 8-bit products, combine) and of a linear layer (the product with its
+ * bias, activation and residual, its gradients, orthogonalised updates), for one
+ * NVIDIA GB300 (sm_103a).
  *
  * C ABI: plain pointers and sizes only.  Every device pointer is owned by
  * the caller; the library never allocates device memory on these paths.  The
@@ -691,6 +693,146 @@ ts_status ts_moe_combine(const void *y, const int32_t *position, const float *we
 ts_status ts_moe_combine_grad(const void *grad_out, const void *y, const int32_t *position, const float *weights,
                               void *grad_y, float *grad_weights, int64_t T, int32_t top_k, int64_t N, int64_t R,
                               int32_t dtype, int64_t ldy, int64_t ldo, int64_t ldg, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Operators of a linear layer: the product with its bias, activation and residual, the
+ * gradients, and the orthogonalised update of its weights.  Every call is asynchronous on
+ * `stream`, allocates nothing and launches programmatic dependents, as the calls above.
+ * ---------------------------------------------------------------------- */
+typedef enum {
+    TS_ACT_NONE = 0,
+    TS_ACT_RELU = 1,      /* max(z, 0) */
+    TS_ACT_GELU = 2,      /* z Phi(z), by the error function */
+    TS_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+    TS_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+} ts_act;
+
+/* Optional knobs for ts_linear; zero means "default" for every field. */
+typedef struct {
+    const void *bias;       /* device [N] or NULL: bf16 (bias_type = TS_OUT_BF16) or fp32 (TS_OUT_F32) */
+    const void *residual;   /* device [M][N] of y's type or NULL; may be y itself */
+    void *preact;           /* device [M][N] of y's type or NULL: receives z, which the backward pass needs */
+    int64_t ldx, ldw, ldy, ld_residual, ld_preact;  /* row strides in elements; 0 = dense rows */
+    int32_t act;            /* ts_act */
+    int32_t bias_type;      /* ts_out_dtype of bias */
+    int32_t tile;           /* ts_tile */
+    int32_t max_workers;    /* cap on persistent workers (CTAs or 2-CTA clusters) */
+    double timeout_s;       /* limit of an mbarrier wait in the kernel, at most 60; 0 = 2 s */
+} ts_linear_opts;
+
+/*
+ * ts_linear -- a linear layer's product with everything that follows it:
+ *
+ *   z[m][n] = sum_k x[m][k] * w[n][k] + bias[n]
+ *   y[m][n] = act(z[m][n]) + residual[m][n]
+ *
+ *   x   device, bf16 [M][K] row-major, 16-byte aligned rows
+ *   w   device, bf16 [N][K] row-major, 16-byte aligned rows
+ *   y   device, [M][N] row-major, bf16 (out_dtype = TS_OUT_BF16) or fp32 (TS_OUT_F32), any row pitch
+ *   M, N, K  sizes, each in [0, 2^31 - 512]
+ *
+ * Sums, bias, activation and residual are fp32; y and preact are rounded once, to nearest even
+ * (the activation takes z before that rounding).  Results are the same on every run.  Which sums
+ * are formed in which order depends on the sizes, tile and max_workers; a NaN or infinity shows in
+ * the rows and columns that use it.
+ * M == 0 or N == 0: no-op.  K == 0: y = act(bias) + residual.  Rows of x and w must start on
+ * 16-byte boundaries (strides multiples of 8), or the call returns TS_ERR_UNSUPPORTED.  y must not
+ * overlap x, w or bias, nor the residual unless it is the residual; preact overlaps nothing.
+ */
+ts_status ts_linear(const void *x, const void *w, void *y, int64_t M, int64_t N, int64_t K, int32_t out_dtype,
+                    const ts_linear_opts *opts, void *stream);
+
+/* Optional knobs for the two gradient products; zero means "default" for every field. */
+typedef struct {
+    const void *aux;        /* ts_linear_grad_input: pre-activations [M][K] of grad_x's type, given with act;
+                               ts_linear_grad_weight: the sum so far [N][K] of grad_w's type, which may be
+                               grad_w itself.  Or NULL. */
+    int64_t ldg, ldb, ldd, ld_aux;  /* row strides of grad_z, of w or x, of the output and of aux; 0 = dense rows */
+    int32_t act;            /* ts_act whose slope at aux multiplies grad_x (ts_linear_grad_weight: TS_ACT_NONE) */
+    int32_t tile;           /* ts_tile */
+    int32_t max_workers;
+    int32_t reserved;
+    double timeout_s;       /* limit of an mbarrier wait in the kernel, at most 60; 0 = 2 s */
+} ts_linear_grad_opts;
+
+/*
+ * ts_linear_grad_input -- the gradient by a linear layer's input, back through the activation
+ * that made that input:
+ *
+ *   grad_x[m][k] = sum_n grad_z[m][n] * w[n][k] * act'(aux[m][k])        (without act: the sum alone)
+ *
+ *   grad_z  device, bf16 [M][N];  w  device, bf16 [N][K], read in place;  grad_x  device, bf16 or fp32 [M][K]
+ *
+ * Types, rounding, alignment, aliases and errors as for ts_linear (grad_x may be aux itself).
+ */
+ts_status ts_linear_grad_input(const void *grad_z, const void *w, void *grad_x, int64_t M, int64_t N, int64_t K,
+                               int32_t out_dtype, const ts_linear_grad_opts *opts, void *stream);
+
+/*
+ * ts_linear_grad_weight -- the gradient by a linear layer's weights, added to what aux holds:
+ *
+ *   grad_w[n][k] = aux[n][k] + sum_m grad_z[m][n] * x[m][k]
+ *
+ *   grad_z  device, bf16 [M][N];  x  device, bf16 [M][K];  grad_w  device, bf16 or fp32 [N][K]
+ *
+ * Both operands are read in place.  M == 0: grad_w = aux, or zeros.
+ */
+ts_status ts_linear_grad_weight(const void *grad_z, const void *x, void *grad_w, int64_t M, int64_t N, int64_t K,
+                                int32_t out_dtype, const ts_linear_grad_opts *opts, void *stream);
+
+/*
+ * ts_act_grad -- the gradient through a linear layer's activation, and by its bias:
+ *
+ *   grad_z[m][n] = grad_y[m][n] * act'(preact[m][n]),   grad_bias[n] = sum_m grad_z[m][n]
+ *
+ *   grad_y, preact, grad_z  device, [M][N], all bf16 or all fp32 (dtype) with row strides ldy, ldp
+ *             and ldg (0 = N); preact is NULL with TS_ACT_NONE and only then; grad_z may be NULL
+ *             (the bias gradient alone), or grad_y or preact itself
+ *   grad_bias device fp32 [N] or NULL: the sum of the values before they are rounded to grad_z's
+ *             type, in fp32 and in an order that depends on M and the rows' alignment alone
+ *
+ * Any alignment and pitch is taken; rows on 16-byte boundaries move in vectors.
+ */
+ts_status ts_act_grad(const void *grad_y, const void *preact, void *grad_z, float *grad_bias, int64_t M, int64_t N,
+                      int32_t dtype, int32_t act, int64_t ldy, int64_t ldp, int64_t ldg, void *stream);
+
+/* Optional knobs for ts_orthogonalise; zero means "default" for every field. */
+typedef struct {
+    int32_t steps;               /* 0 = 5, at most 64; negative: none, the normalised matrix itself */
+    float a, b, c;               /* coefficients; all 0 = 3.4445, -4.7750, 2.0315 */
+    float eps;                   /* 0 = 1e-7 */
+    int32_t reserved;
+    int64_t ldg, ldo;            /* row strides of G and O in elements; 0 = C */
+    int64_t g_matrix, o_matrix;  /* elements between the matrices of G and of O; 0 = R rows */
+    double timeout_s;            /* limit of an mbarrier wait in a kernel, at most 60; 0 = 2 s */
+} ts_orth_opts;
+
+/*
+ * ts_orthogonalise -- the orthogonalised update of weight matrices by a quintic Newton-Schulz
+ * iteration (as the Muon optimiser takes it), for each of `batch` matrices:
+ *
+ *   X = G / (|G|_F + eps);   steps times:  A = X X^T,  X = a X + (b A + c A^2) X;   O = X
+ *
+ * (R > C: A = X^T X, X = a X + X (b A + c A^2), which is the same).
+ *
+ *   G  device, [batch][R][C], bf16 (g_type = TS_OUT_BF16) or fp32 (TS_OUT_F32), any alignment and pitch
+ *   O  device, bf16 [batch][R][C], any alignment and pitch; must not overlap G
+ *   workspace  device scratch of ts_orthogonalise_workspace(batch, R, C, steps) bytes (steps as they
+ *              run), 256-byte aligned, no initialisation; launches that may overlap on the GPU
+ *              need separate workspaces
+ *   R, C  0 .. 2^20;  batch  0 .. 65535
+ *
+ * The norm's squares are summed in fp32 in three ranges, so that no finite G overflows or is lost.
+ * Between the products X, A and b A + c A^2 are held as 4096 times their value in fp16; with the
+ * default coefficients nothing overflows there, and other coefficients must keep every |entry| of
+ * the three below 15.  Entries of X below 2^-36 round to 0 (a G whose norm is far below eps).  A
+ * matrix of zeros gives zeros; one that holds an infinity or a NaN gives NaNs, and the other
+ * matrices of the batch are not affected.
+ */
+ts_status ts_orthogonalise(const void *G, void *O, int64_t batch, int64_t R, int64_t C, int32_t g_type,
+                           const ts_orth_opts *opts, void *workspace, int64_t workspace_bytes, void *stream);
+/* 0 for sizes that ts_orthogonalise does not take, or with nothing to do. */
+int64_t ts_orthogonalise_workspace(int64_t batch, int64_t R, int64_t C, int32_t steps);
 
 /*
  * ts_spin -- occupy `ctas` SMs for `duration_ns` nanoseconds (measured with

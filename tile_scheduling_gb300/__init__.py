@@ -1,6 +1,7 @@
 """Python binding of libtsgemm (persistent bf16 GEMM with static / Cluster Launch
 Control tile scheduling, the grid-stride int16 copy, and the mixture-of-experts
-operators: routing, 8-bit quantisation and products, combine) for one GB300.
+operators: routing, 8-bit quantisation and products, combine; a linear layer's
+operators: fused product, gradients, orthogonalised updates) for one GB300.
 
 This module only marshals arguments: torch tensors become device pointers and
 sizes, the current torch stream becomes a cudaStream_t, and every computation
@@ -38,7 +39,9 @@ EXPORTED = ("ts_gemm_bf16", "ts_gemm_bf16_ex", "ts_gemm_launch_info", "ts_gemm_b
             "ts_copy_i16", "ts_spin",
             "ts_spin_wait_started", "ts_sync_and_check", "ts_num_sms", "ts_status_string",
             "ts_last_error_detail", "ts_gemm_fp8", "ts_gemm_fp8_grouped", "ts_quant_fp8", "ts_moe_route",
-            "ts_moe_route_grad", "ts_moe_plan", "ts_moe_plan_workspace", "ts_moe_combine", "ts_moe_combine_grad")
+            "ts_moe_route_grad", "ts_moe_plan", "ts_moe_plan_workspace", "ts_moe_combine", "ts_moe_combine_grad",
+            "ts_linear", "ts_linear_grad_input", "ts_linear_grad_weight", "ts_act_grad", "ts_orthogonalise",
+            "ts_orthogonalise_workspace")
 
 
 class TsError(RuntimeError):
@@ -96,10 +99,34 @@ class RouteOpts(ctypes.Structure):
                 ("ldg", ctypes.c_int64)]
 
 
+class LinearOpts(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("preact", ctypes.c_void_p),
+                ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("ld_residual", ctypes.c_int64), ("ld_preact", ctypes.c_int64), ("act", ctypes.c_int32),
+                ("bias_type", ctypes.c_int32), ("tile", ctypes.c_int32), ("max_workers", ctypes.c_int32),
+                ("timeout_s", ctypes.c_double)]
+
+
+class LinearGradOpts(ctypes.Structure):
+    _fields_ = [("aux", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("ldb", ctypes.c_int64), ("ldd", ctypes.c_int64),
+                ("ld_aux", ctypes.c_int64), ("act", ctypes.c_int32), ("tile", ctypes.c_int32),
+                ("max_workers", ctypes.c_int32), ("reserved", ctypes.c_int32), ("timeout_s", ctypes.c_double)]
+
+
+class OrthOpts(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_int32), ("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float),
+                ("eps", ctypes.c_float), ("reserved", ctypes.c_int32), ("ldg", ctypes.c_int64),
+                ("ldo", ctypes.c_int64), ("g_matrix", ctypes.c_int64), ("o_matrix", ctypes.c_int64),
+                ("timeout_s", ctypes.c_double)]
+
+
 # The same layouts packed into bytes: a quarter of the time of filling a Structure, in calls of a few microseconds.
 _PACK_FP8 = struct.Struct("6i9qd")
 _PACK_QUANT = struct.Struct("Pqiiqqqq")
 _PACK_ROUTE = struct.Struct("P5ifiqq")
+_PACK_LINEAR = struct.Struct("3P5q4id")
+_PACK_LINEAR_GRAD = struct.Struct("P4q4id")
+_PACK_ORTH = struct.Struct("i4fi4qd")
 
 
 class GemmProtocol(ctypes.Structure):
@@ -155,15 +182,25 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ts_moe_plan_workspace.restype = I64
     lib.ts_moe_combine.argtypes = [P, P, P, P, I64, I32, I64, I64, I32, I64, I64, P]
     lib.ts_moe_combine_grad.argtypes = [P, P, P, P, P, P, I64, I32, I64, I64, I32, I64, I64, I64, P]
-    for name in ("ts_gemm_fp8", "ts_gemm_fp8_grouped", "ts_quant_fp8", "ts_moe_route", "ts_moe_route_grad",
+    LO, LG, OO = ctypes.POINTER(LinearOpts), ctypes.POINTER(LinearGradOpts), ctypes.POINTER(OrthOpts)
+    lib.ts_linear.argtypes = [P, P, P, I64, I64, I64, I32, LO, P]
+    lib.ts_linear_grad_input.argtypes = [P, P, P, I64, I64, I64, I32, LG, P]
+    lib.ts_linear_grad_weight.argtypes = [P, P, P, I64, I64, I64, I32, LG, P]
+    lib.ts_act_grad.argtypes = [P, P, P, P, I64, I64, I32, I32, I64, I64, I64, P]
+    lib.ts_orthogonalise.argtypes = [P, P, I64, I64, I64, I32, OO, P, I64, P]
+    lib.ts_orthogonalise_workspace.argtypes = [I64, I64, I64, I32]
+    lib.ts_orthogonalise_workspace.restype = I64
+    for name in ("ts_linear", "ts_linear_grad_input", "ts_linear_grad_weight", "ts_act_grad", "ts_orthogonalise",
+                 "ts_gemm_fp8", "ts_gemm_fp8_grouped", "ts_quant_fp8", "ts_moe_route", "ts_moe_route_grad",
                  "ts_moe_plan", "ts_moe_combine", "ts_moe_combine_grad", "ts_gemm_bf16", "ts_gemm_bf16_ex", "ts_gemm_launch_info", "ts_gemm_bf16_checked_noalloc",
                  "ts_gemm_tile_coords", "ts_gemm_protocol_info", "ts_gemm_bf16_grouped", "ts_gemm_grouped_launch_info",
                  "ts_gemm_grouped_order", "ts_copy_i16", "ts_copy_i16_rows", "ts_copy_rows_launch_info", "ts_spin",
                  "ts_spin_wait_started", "ts_sync_and_check"):
         getattr(lib, name).restype = ctypes.c_int
-    for name in ("ts_gemm_fp8", "ts_gemm_fp8_grouped", "ts_quant_fp8", "ts_moe_route", "ts_moe_route_grad"):
+    for name in ("ts_gemm_fp8", "ts_gemm_fp8_grouped", "ts_quant_fp8", "ts_moe_route", "ts_moe_route_grad", "ts_linear",
+                 "ts_linear_grad_input", "ts_linear_grad_weight", "ts_orthogonalise"):
         packed = lib[name]  # a handle of its own, whose options are packed bytes
-        packed.argtypes = [P if t in (F8, QO, RO) else t for t in getattr(lib, name).argtypes]
+        packed.argtypes = [P if t in (F8, QO, RO, LO, LG, OO) else t for t in getattr(lib, name).argtypes]
         packed.restype = ctypes.c_int
         setattr(lib, name + "_packed", packed)
     return lib
@@ -899,6 +936,149 @@ def ts_moe_combine_grad(grad_out: torch.Tensor, y: torch.Tensor, position: torch
                                   grad_y.data_ptr(),
                                   _dense(grad_weights, "grad_weights", _F32, (T, k)) if grad_weights is not None else 0,
                                   T, k, N, R, dtype, ldy, ldo, ldg, _stream_of(stream))
+    if st:
+        _check(st)
+
+
+TS_ACT_NONE, TS_ACT_RELU, TS_ACT_GELU, TS_ACT_GELU_TANH, TS_ACT_SILU = range(5)
+_ACT = {"none": TS_ACT_NONE, "relu": TS_ACT_RELU, "gelu": TS_ACT_GELU, "gelu_tanh": TS_ACT_GELU_TANH,
+        "silu": TS_ACT_SILU}
+_BF16 = {torch.bfloat16: TS_OUT_BF16}
+
+
+def _like(t, name: str, other: str, code: int, shape):
+    """(address, row stride) of an optional matrix of the output's type and shape."""
+    if t is None:
+        return 0, 0
+    c, s, ld = _matrix_of(t, name, _OUT)
+    if c != code:
+        raise TypeError(f"{name} must have the type of {other}")
+    if s != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(s)}")
+    return t.data_ptr(), ld
+
+
+def ts_linear(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, bias=None, act="none", residual=None, preact=None,
+              tile="auto", max_workers=0, timeout_s=0.0, stream=None) -> None:
+    """y = act(x @ w.T + bias) + residual for bf16 x [M, K] and w [N, K]; y [M, N] is bf16 or fp32.
+
+    ``bias`` [N] is bf16 or fp32; ``act``: "none", "relu", "gelu", "gelu_tanh" or "silu"; ``residual``
+    and ``preact`` are [M, N] of y's type, and preact receives x @ w.T + bias.  residual may be y
+    itself.  Rows may be strided; rows of x and w start on 16-byte boundaries.  Asynchronous on
+    ``stream`` (default: torch's current stream)."""
+    _, (M, K), ldx = _matrix_of(x, "x", _BF16)
+    _, (N, K2), ldw = _matrix_of(w, "w", _BF16)
+    out, shape, ldy = _matrix_of(y, "y", _OUT)
+    if K2 != K or shape[0] != M or shape[1] != N:
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, w {tuple(w.shape)}, y {tuple(y.shape)}")
+    b = b_type = 0
+    if bias is not None:
+        b = _dense(bias, "bias", _OUT, (N,))
+        b_type = _OUT[bias.dtype]
+    r, ldr = _like(residual, "residual", "y", out, shape)
+    z, ldz = _like(preact, "preact", "y", out, shape)
+    o = _PACK_LINEAR.pack(b, r, z, ldx, ldw, ldy, ldr, ldz, _ACT[act] if isinstance(act, str) else int(act), b_type,
+                          _TILE[tile] if isinstance(tile, str) else int(tile), max_workers, timeout_s)
+    st = _lib.ts_linear_packed(x.data_ptr(), w.data_ptr(), y.data_ptr(), M, N, K, out, o, _stream_of(stream))
+    if st:
+        _check(st)
+
+
+def ts_linear_grad_input(grad_z: torch.Tensor, w: torch.Tensor, grad_x: torch.Tensor, act="none", preact=None,
+                         tile="auto", max_workers=0, timeout_s=0.0, stream=None) -> None:
+    """grad_x = (grad_z @ w) * act'(preact) for bf16 grad_z [M, N] and w [N, K]; grad_x [M, K] is bf16 or fp32.
+
+    ``act`` and ``preact`` ([M, K] of grad_x's type) are those of the layer that made this one's input;
+    without them grad_x is the gradient by that input.  w is read in place."""
+    _, (M, N), ldg = _matrix_of(grad_z, "grad_z", _BF16)
+    _, (N2, K), ldw = _matrix_of(w, "w", _BF16)
+    out, shape, ldd = _matrix_of(grad_x, "grad_x", _OUT)
+    if N2 != N or shape[0] != M or shape[1] != K:
+        raise ValueError(f"shape mismatch: grad_z {tuple(grad_z.shape)}, w {tuple(w.shape)}, grad_x {tuple(grad_x.shape)}")
+    z, ldz = _like(preact, "preact", "grad_x", out, shape)
+    o = _PACK_LINEAR_GRAD.pack(z, ldg, ldw, ldd, ldz, _ACT[act] if isinstance(act, str) else int(act),
+                               _TILE[tile] if isinstance(tile, str) else int(tile), max_workers, 0, timeout_s)
+    st = _lib.ts_linear_grad_input_packed(grad_z.data_ptr(), w.data_ptr(), grad_x.data_ptr(), M, N, K, out, o,
+                                          _stream_of(stream))
+    if st:
+        _check(st)
+
+
+def ts_linear_grad_weight(grad_z: torch.Tensor, x: torch.Tensor, grad_w: torch.Tensor, base=None, tile="auto",
+                          max_workers=0, timeout_s=0.0, stream=None) -> None:
+    """grad_w = base + grad_z.T @ x for bf16 grad_z [M, N] and x [M, K]; grad_w [N, K] is bf16 or fp32.
+
+    ``base`` ([N, K] of grad_w's type, which may be grad_w itself) is what has been accumulated so far."""
+    _, (M, N), ldg = _matrix_of(grad_z, "grad_z", _BF16)
+    _, (M2, K), ldx = _matrix_of(x, "x", _BF16)
+    out, shape, ldd = _matrix_of(grad_w, "grad_w", _OUT)
+    if M2 != M or shape[0] != N or shape[1] != K:
+        raise ValueError(f"shape mismatch: grad_z {tuple(grad_z.shape)}, x {tuple(x.shape)}, grad_w {tuple(grad_w.shape)}")
+    r, ldr = _like(base, "base", "grad_w", out, shape)
+    o = _PACK_LINEAR_GRAD.pack(r, ldg, ldx, ldd, ldr, TS_ACT_NONE, _TILE[tile] if isinstance(tile, str) else int(tile),
+                               max_workers, 0, timeout_s)
+    st = _lib.ts_linear_grad_weight_packed(grad_z.data_ptr(), x.data_ptr(), grad_w.data_ptr(), M, N, K, out, o,
+                                           _stream_of(stream))
+    if st:
+        _check(st)
+
+
+def ts_act_grad(grad_y: torch.Tensor, preact, grad_z, grad_bias=None, act="none", stream=None) -> None:
+    """grad_z = grad_y * act'(preact) and grad_bias = the sum of its rows (before rounding, fp32 [N]).
+
+    grad_y, preact and grad_z are [M, N], all bf16 or all fp32.  preact is None with act "none"; grad_z
+    may be None (the bias gradient alone), or grad_y or preact itself."""
+    dtype, shape, ldy = _matrix_of(grad_y, "grad_y", _OUT)
+    z, ldz = _like(preact, "preact", "grad_y", dtype, shape)
+    g, ldg = _like(grad_z, "grad_z", "grad_y", dtype, shape)
+    st = _lib.ts_act_grad(grad_y.data_ptr(), z, g, _dense(grad_bias, "grad_bias", _F32, (shape[1],)) if grad_bias is not None else 0,
+                          shape[0], shape[1], dtype, _ACT[act] if isinstance(act, str) else int(act), ldy, ldz, ldg,
+                          _stream_of(stream))
+    if st:
+        _check(st)
+
+
+def ts_orthogonalise_workspace(batch: int, R: int, C: int, steps: int = 5) -> int:
+    """Bytes of workspace that ts_orthogonalise needs for ``batch`` matrices [R, C]."""
+    return int(_lib.ts_orthogonalise_workspace(int(batch), int(R), int(C), int(steps)))
+
+
+def ts_orthogonalise(g: torch.Tensor, out: torch.Tensor, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7,
+                     workspace=None, timeout_s=0.0, stream=None) -> None:
+    """out = the Newton-Schulz orthogonalisation of g [R, C], or of each matrix of g [batch, R, C].
+
+    g is bf16 or fp32, out bf16 of the same shape; ``steps`` times X = a X + (b A + c A A) X with A = X X^T
+    and (a, b, c) = ``coefficients``, from X = g / (norm(g) + eps).  The workspace is one kept for each
+    stream unless one is passed (ts_orthogonalise_workspace bytes, 256-byte aligned)."""
+    dims = 3 if g.dim() == 3 else 2
+    g_type, shape, ldg = _matrix_of(g, "g", _OUT, dims)
+    _, o_shape, ldo = _matrix_of(out, "out", _BF16, dims)
+    if o_shape != shape:
+        raise ValueError(f"out must be {tuple(shape)}, not {tuple(o_shape)}")
+    steps = int(steps)
+    if steps < 0:
+        raise ValueError("steps must not be negative")
+    if not eps > _SCALE_ZERO:
+        raise ValueError("eps must be above 0 in fp32")
+    a, b, c = coefficients
+    if a == b == c == 0:
+        raise ValueError("the coefficients must not all be 0")
+    n, R, C = (1, *shape) if dims == 2 else shape
+    gm = om = 0
+    if n > 1:
+        gm, om = g.stride(0), out.stride(0)
+        if gm <= 0 or om <= 0:
+            raise ValueError("matrices of g or out share memory (an expanded tensor)")
+    need = _lib.ts_orthogonalise_workspace(n, R, C, steps)
+    if need and workspace is None:
+        workspace = _scratch_for(need, g.device, stream)
+    ptr = size = 0
+    if workspace is not None:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise TypeError("workspace must be a contiguous CUDA tensor")
+        ptr, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    o = _PACK_ORTH.pack(steps or -1, a, b, c, eps, 0, ldg, ldo, gm, om, timeout_s)
+    st = _lib.ts_orthogonalise_packed(g.data_ptr(), out.data_ptr(), n, R, C, g_type, o, ptr, size, _stream_of(stream))
     if st:
         _check(st)
 

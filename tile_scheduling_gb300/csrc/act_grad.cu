@@ -1,0 +1,250 @@
+// The gradient of a linear layer's activation and bias:
+//
+//   grad_z = grad_y * act'(preact),   grad_bias[n] = sum_m grad_z[m][n]
+//
+// One pass over the data.  A cluster takes a strip of columns, 128 bytes of a row, and its CTAs
+// share the rows; each thread holds the fp32 sums of its columns, which the CTA adds up through
+// shared memory and the cluster's first CTA over the cluster, in a fixed order.  The sums take the
+// values before they are rounded to grad_z's type.  Bound by memory.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "act.cuh"
+#include "common.h"
+#include "ptx.cuh"
+
+namespace ts {
+namespace {
+
+constexpr int kActThreads = 256, kStripLanes = 8, kStripRows = kActThreads / kStripLanes;
+constexpr int kActUnroll = 4;      // rows of a thread in flight
+constexpr int kMaxActCluster = 8;
+
+struct ActParams {
+    const void *gy, *z;
+    void *gz;
+    float *gb;
+    int64_t ldy, ldz, ldg;
+    int64_t M, N;
+    int32_t act, cluster;
+};
+
+template <class T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32(uint16_t v) { return __uint_as_float(uint32_t(v) << 16); }
+
+// V values at p, V * sizeof(T) bytes in one access
+template <class T, int V>
+__device__ __forceinline__ void load_v(const T *p, float (&f)[V]) {
+    if constexpr (V == 1) {
+        f[0] = to_f32(*p);
+    } else {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                f[i] = __uint_as_float(w[i]);
+            } else {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
+}
+template <class T, int V>
+__device__ __forceinline__ void store_v(T *p, const float (&f)[V]) {
+    if constexpr (V == 1) {
+        if constexpr (sizeof(T) == 4)
+            *p = f[0];
+        else
+            *p = static_cast<uint16_t>(pack_bf16x2(__float_as_uint(f[0]), 0u));
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4)
+                w[i] = __float_as_uint(f[i]);
+            else
+                w[i] = pack_bf16x2(__float_as_uint(f[2 * i]), __float_as_uint(f[2 * i + 1]));
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// T: uint16_t (bf16) or float; VEC: rows start on 16-byte boundaries.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kActThreads) act_grad_kernel(const __grid_constant__ ActParams p) {
+    constexpr int V = VEC ? 16 / sizeof(T) : 1;
+    constexpr int STRIP = kStripLanes * V;
+    __shared__ __align__(16) float part[kStripRows][STRIP];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int rank = static_cast<int>(blockIdx.x) % p.cluster;
+    const int64_t strip = blockIdx.x / p.cluster;
+    const int tx = threadIdx.x % kStripLanes, ty = threadIdx.x / kStripLanes;
+    const int64_t col = strip * STRIP + tx * V;
+    const int64_t m0 = p.M * rank / p.cluster, m1 = p.M * (rank + 1) / p.cluster;
+    const int count = static_cast<int>(max(int64_t(0), min(static_cast<int64_t>(V), p.N - col)));  // columns of this thread
+    const T *gy = static_cast<const T *>(p.gy) + col, *z = static_cast<const T *>(p.z) + col;
+    T *gz = static_cast<T *>(p.gz) + col;
+    float sum[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum[i] = 0.f;
+    auto rows = [&](auto tag) {
+        constexpr int A = decltype(tag)::value;
+        if (count == V) {
+            for (int64_t m = m0 + ty; m < m1; m += kActUnroll * kStripRows) {
+                float g[kActUnroll][V], zz[kActUnroll][V];
+#pragma unroll
+                for (int k = 0; k < kActUnroll; ++k) {
+                    const int64_t r = m + k * kStripRows;
+                    if (r < m1) {
+                        load_v<T, V>(gy + r * p.ldy, g[k]);
+                        if constexpr (A != ACT_NONE) load_v<T, V>(z + r * p.ldz, zz[k]);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kActUnroll; ++k) {
+                    const int64_t r = m + k * kStripRows;
+                    if (r < m1) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            if constexpr (A != ACT_NONE) g[k][i] *= act_slope<A>(zz[k][i]);
+                            sum[i] += g[k][i];
+                        }
+                        if (p.gz) store_v<T, V>(gz + r * p.ldg, g[k]);
+                    }
+                }
+            }
+        } else if (count > 0) {  // the last, shorter vector of the rows
+            for (int64_t m = m0 + ty; m < m1; m += kStripRows) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    if (i < count) {
+                        float g = to_f32(gy[m * p.ldy + i]);
+                        if constexpr (A != ACT_NONE) g *= act_slope<A>(to_f32(z[m * p.ldz + i]));
+                        sum[i] += g;
+                        if (p.gz) {
+                            const float one[1] = {g};
+                            store_v<T, 1>(gz + m * p.ldg + i, one);
+                        }
+                    }
+                }
+            }
+        }
+    };
+    if (p.act == ACT_NONE)
+        rows(ActTag<ACT_NONE>{});
+    else
+        with_act(p.act, rows);
+    if (!p.gb) return;
+#pragma unroll
+    for (int i = 0; i < V; ++i) part[ty][tx * V + i] = sum[i];
+    __syncthreads();
+    if (threadIdx.x < STRIP) {
+        float t = 0.f;
+        for (int r = 0; r < kStripRows; ++r) t += part[r][threadIdx.x];
+        sum[0] = t;
+        part[0][threadIdx.x] = t;  // only this thread reads the column
+    }
+    if (p.cluster > 1) {
+        cluster_sync();
+        if (rank == 0 && threadIdx.x < STRIP) {
+            const uint32_t at = smem_u32(&part[0][threadIdx.x]);
+            float t = sum[0];
+            for (int c = 1; c < p.cluster; ++c) t += ld_cluster_f32(mapa(at, c));
+            sum[0] = t;
+        }
+        cluster_sync();  // no CTA leaves while the first reads its sums
+    }
+    if (rank == 0 && threadIdx.x < STRIP && strip * STRIP + threadIdx.x < p.N) p.gb[strip * STRIP + threadIdx.x] = sum[0];
+}
+
+template <class T, bool VEC>
+cudaError_t launch_act_grad(const ActParams &p, cudaStream_t st) {
+    constexpr int64_t STRIP = kStripLanes * (VEC ? 16 / sizeof(T) : 1);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(cdiv(p.N, STRIP) * p.cluster), 1, 1);
+    cfg.blockDim = dim3(kActThreads, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, act_grad_kernel<T, VEC>, p);
+}
+
+}  // namespace
+}  // namespace ts
+
+extern "C" ts_status ts_act_grad(const void *grad_y, const void *preact, void *grad_z, float *grad_bias, int64_t M,
+                                 int64_t N, int32_t dtype, int32_t act, int64_t ldy, int64_t ldp, int64_t ldg,
+                                 void *stream) {
+    using namespace ts;
+    constexpr int64_t kMax = 0x7fffffffLL - 511, kPitch = int64_t(1) << 37;
+    if (M < 0 || N < 0 || M > kMax || N > kMax)
+        return fail(TS_ERR_INVALID_ARG, "sizes must be in [0, 2^31 - 512] (M=%lld N=%lld)", static_cast<long long>(M),
+                    static_cast<long long>(N));
+    if (dtype != TS_OUT_BF16 && dtype != TS_OUT_F32) return fail(TS_ERR_INVALID_ARG, "dtype %d", dtype);
+    if (act < 0 || act >= kActs) return fail(TS_ERR_INVALID_ARG, "act %d", act);
+    if ((act != TS_ACT_NONE) != (preact != nullptr))
+        return fail(TS_ERR_INVALID_ARG, "an activation and its pre-activations are given together");
+    if (!grad_z && !grad_bias) return fail(TS_ERR_INVALID_ARG, "neither grad_z nor grad_bias is given");
+    ldy = ldy ? ldy : N;
+    ldp = ldp ? ldp : N;
+    ldg = ldg ? ldg : N;
+    if (ldy < N || ldp < N || ldg < N || ldy > kPitch || ldp > kPitch || ldg > kPitch)
+        return fail(TS_ERR_INVALID_ARG, "row strides must cover a row (%lld, %lld, %lld)", static_cast<long long>(ldy),
+                    static_cast<long long>(ldp), static_cast<long long>(ldg));
+    if (N == 0 || (M == 0 && !grad_bias)) return TS_OK;
+    if (M > 0 && !grad_y) return fail(TS_ERR_INVALID_ARG, "grad_y is NULL");
+    const int esize = dtype == TS_OUT_F32 ? 4 : 2;
+    bool vec = true;
+    for (const void *q : {grad_y, preact, static_cast<const void *>(grad_z)}) {
+        if (reinterpret_cast<uintptr_t>(q) % esize) return fail(TS_ERR_INVALID_ARG, "a matrix is not aligned to its element size");
+        vec &= reinterpret_cast<uintptr_t>(q) % 16 == 0;
+    }
+    if (reinterpret_cast<uintptr_t>(grad_bias) % 4) return fail(TS_ERR_INVALID_ARG, "grad_bias is not aligned to 4 bytes");
+    if (M > 1) vec &= (ldy * esize) % 16 == 0 && (!preact || (ldp * esize) % 16 == 0) && (!grad_z || (ldg * esize) % 16 == 0);
+    const int64_t ybytes = M > 0 ? ((M - 1) * ldy + N) * esize : 0, zbytes = M > 0 ? ((M - 1) * ldp + N) * esize : 0,
+                  gbytes = M > 0 ? ((M - 1) * ldg + N) * esize : 0;
+    // each element of grad_z is written by the thread that has read the others at its place
+    auto clash = [&](const void *q, int64_t bytes, int64_t ld) {
+        return grad_z && q && bytes && ranges_overlap(grad_z, gbytes, q, bytes) && !(q == grad_z && (ld == ldg || M <= 1));
+    };
+    if (clash(grad_y, ybytes, ldy) || clash(preact, zbytes, ldp))
+        return fail(TS_ERR_INVALID_ARG, "grad_z overlaps an input, and is not that input");
+    if (grad_bias && M > 0 &&
+        (ranges_overlap(grad_bias, 4 * N, grad_y, ybytes) || (preact && ranges_overlap(grad_bias, 4 * N, preact, zbytes)) ||
+         (grad_z && ranges_overlap(grad_bias, 4 * N, grad_z, gbytes))))
+        return fail(TS_ERR_INVALID_ARG, "grad_bias overlaps a matrix");
+    ActParams p;
+    std::memset(&p, 0, sizeof p);
+    p.gy = grad_y;
+    p.z = preact;
+    p.gz = grad_z;
+    p.gb = grad_bias;
+    p.ldy = ldy;
+    p.ldz = ldp;
+    p.ldg = ldg;
+    p.M = M;
+    p.N = N;
+    p.act = act;
+    p.cluster = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(kMaxActCluster, M / (2 * kStripRows))));
+    if (cdiv(N, kStripLanes) * p.cluster > 0x7fffffffLL) return fail(TS_ERR_UNSUPPORTED, "too many columns");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == TS_OUT_F32 ? (vec ? launch_act_grad<float, true>(p, st) : launch_act_grad<float, false>(p, st))
+                                              : (vec ? launch_act_grad<uint16_t, true>(p, st) : launch_act_grad<uint16_t, false>(p, st));
+    return e == cudaSuccess ? TS_OK : cuda_fail(e, "activation gradient launch");
+}

@@ -20,6 +20,7 @@ enum : int32_t {
     WAIT_SCHED_PRODUCER = 9,
     WAIT_SCALES = 10,
     WAIT_PROMOTION = 11,
+    WAIT_AUX = 12,
 };
 
 // Device status word (library-owned, one per device):

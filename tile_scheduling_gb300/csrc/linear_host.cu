@@ -1,0 +1,358 @@
+// Host side of the fused-epilogue products: argument checks, planning, tensor maps, launch.
+#include <algorithm>
+#include <cstring>
+
+#include "common.h"
+#include "linear_params.h"
+
+namespace ts {
+
+extern const LinVariant linear_128_1, linear_128_1_pre, linear_256_1, linear_256_1_pre, linear_256_2, linear_256_2_pre;
+
+namespace {
+
+constexpr int64_t kMaxSize = 0x7fffffffLL - 511;  // the last tile's coordinates stay in 32 bits
+constexpr int64_t kMaxPitch = int64_t(1) << 37;
+constexpr double kDefaultTimeoutS = 2.0;
+constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
+constexpr int kRasterGroup = 8;
+
+const LinVariant *find_linear(int bn, int cg, int pre) {
+    static const LinVariant *const all[] = {&linear_128_1,     &linear_128_1_pre, &linear_256_1,
+                                            &linear_256_1_pre, &linear_256_2,     &linear_256_2_pre};
+    for (const LinVariant *v : all)
+        if (v->bn == bn && v->cg == cg && v->pre == pre) return v;
+    return nullptr;
+}
+
+int64_t aligned_pitch(int64_t ld, int64_t rows, int64_t cols, int unit) {
+    return rows > 1 ? ld : cdiv(cols, unit) * unit;  // a single row's pitch is never used
+}
+
+// Tensor map of an operand of `rows` rows of D by K, in boxes of 64 of K by box_rows, or (mn) of 64 rows by 64 of K.
+ts_status operand_map(CUtensorMap *m, const void *ptr, int mn, int64_t rows, int64_t K, int64_t batch, int64_t ld,
+                      int64_t matrix, int box_rows) {
+    const int64_t outer = mn ? K : rows, inner = mn ? rows : K;
+    const int64_t pitch = aligned_pitch(ld, outer, inner, 8);
+    const int64_t dims[3] = {inner, outer, batch};
+    const int64_t strides[2] = {pitch * 2, (batch > 1 ? matrix : outer * pitch) * 2};
+    const int box[3] = {64, mn ? 64 : box_rows, 1};
+    return encode_map(m, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dims, strides, box);
+}
+
+ts_status output_map(CUtensorMap *m, const void *ptr, int esize, int64_t M, int64_t N, int64_t batch, int64_t ld,
+                     int64_t matrix) {
+    const int64_t pitch = aligned_pitch(ld, M, N, 16 / esize);
+    const int64_t dims[3] = {N, M, batch}, strides[2] = {pitch * esize, (batch > 1 ? matrix : M * pitch) * esize};
+    const int box[3] = {128 / esize, 32, 1};  // a warp's staging buffer
+    return encode_map(m, ptr, esize == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dims,
+                      strides, box);
+}
+
+}  // namespace
+
+ts_status linear_product(const LinCall &c) {
+    const int sms_ = device_sms(current_device());
+    if (sms_ <= 0) return fail(TS_ERR_CUDA, "cannot query the SM count");
+    const int64_t sms = sms_, nkb = cdiv(c.K, 64);
+    int tile = c.tile;
+    auto tri = [](int64_t n) { return n * (n + 1) / 2; };
+    const int64_t m1 = cdiv(c.M, 128), m2 = cdiv(c.M, 256), n1 = cdiv(c.N, 128), n2 = cdiv(c.N, 256);
+    const int64_t u1 = c.batch * (c.sym ? tri(n1) : m1 * n1), u2 = c.batch * m1 * n2,
+                  u3 = c.batch * (c.sym ? tri(n2) : m2 * n2);
+    if (tile == TS_TILE_AUTO) {
+        // The tile with the fewest cycles: waves of workers times what a tile takes.
+        const int64_t c1 = cdiv(u1, sms) * (nkb * 300 + 300) + 2500;
+        const int64_t c2 = cdiv(u2, sms) * (nkb * 540 + 300) + 4000;
+        const int64_t c3 = cdiv(u3, sms / 2) * (nkb * 520 + 300) + 4500;
+        if (c.sym)
+            tile = c1 <= c3 ? TS_TILE_128x128 : TS_TILE_256x256_2CTA;
+        else
+            tile = c1 <= c2 && c1 <= c3 ? TS_TILE_128x128 : c2 < c3 ? TS_TILE_128x256 : TS_TILE_256x256_2CTA;
+    }
+    const int bn = tile == TS_TILE_128x128 ? 128 : 256, cg = tile == TS_TILE_256x256_2CTA ? 2 : 1;
+    const LinVariant *v = find_linear(bn, cg, c.pre ? 1 : 0);
+    if (!v) return fail(TS_ERR_UNSUPPORTED, "no compiled variant");
+
+    LinLaunch L;
+    std::memset(&L, 0, sizeof L);
+    LinParams &p = L.p;
+    const int64_t tiles_m = cdiv(c.M, 128 * cg), tiles_n = cdiv(c.N, bn);
+    const int64_t per = c.sym ? tri(tiles_n) : tiles_m * tiles_n, units = per * c.batch;
+    if (units * cg > 0x7fffffffLL) return fail(TS_ERR_UNSUPPORTED, "too many output tiles");
+    const int esize = c.out == OUT_F32 ? 4 : 2;
+    p.store_bytes = 2;
+    for (int b : {16, 4}) {
+        auto fits = [&](const void *ptr, int64_t ld, int64_t matrix) {
+            return !ptr || (reinterpret_cast<uintptr_t>(ptr) % b == 0 && (c.M <= 1 || (ld * esize) % b == 0) &&
+                            (c.batch <= 1 || (matrix * esize) % b == 0));
+        };
+        if (fits(c.D, c.ldd, c.d_matrix) && fits(c.aux, c.ld_aux, c.aux_matrix) && fits(c.pre, c.ld_pre, 0)) {
+            p.store_bytes = b;
+            break;
+        }
+    }
+    ts_status s = TS_OK;
+    if (c.K > 0) {
+        if ((s = operand_map(&L.a, c.A, c.a_mn, c.M, c.K, c.batch, c.lda, c.a_matrix, 128)) != TS_OK) return s;
+        if ((s = operand_map(&L.b, c.B, c.b_mn, c.N, c.K, c.batch, c.ldb, c.b_matrix, bn / cg)) != TS_OK) return s;
+    }
+    if (p.store_bytes == 16) {
+        if ((s = output_map(&L.d, c.D, esize, c.M, c.N, c.batch, c.ldd, c.d_matrix)) != TS_OK) return s;
+        if (c.aux && (s = output_map(&L.aux, c.aux, esize, c.M, c.N, c.batch, c.ld_aux, c.aux_matrix)) != TS_OK) return s;
+        if (c.pre && (s = output_map(&L.pre, c.pre, esize, c.M, c.N, 1, c.ld_pre, 0)) != TS_OK) return s;
+    }
+    unsigned long long *status = device_status_word(&s);
+    if (!status) return s;
+
+    p.M = static_cast<int32_t>(c.M);
+    p.N = static_cast<int32_t>(c.N);
+    p.tiles_m = static_cast<int32_t>(tiles_m);
+    p.tiles_n = static_cast<int32_t>(tiles_n);
+    p.num_kb = static_cast<int32_t>(nkb);
+    p.num_units = static_cast<int32_t>(units);
+    p.tiles_per_matrix = static_cast<int32_t>(per);
+    p.raster_group = kRasterGroup;
+    p.div_group_tiles = fast_div_for(c.sym ? tiles_n + 1 : kRasterGroup * tiles_n);
+    p.div_group_rows = fast_div_for(kRasterGroup);
+    p.div_last_rows = fast_div_for(tiles_m - (cdiv(tiles_m, kRasterGroup) - 1) * kRasterGroup);
+    p.div_matrix = fast_div_for(per);
+    p.a_mn = c.a_mn;
+    p.b_mn = c.b_mn;
+    // Instruction descriptor, kind::f16: D fp32 (bits 4-5 = 1), A and B bf16 (bits 7-9 and 10-12 = 1)
+    // or fp16 (0), A and B K-major (bits 15 and 16 = 0) or not; the kernel adds N and M of its tile.
+    const uint32_t type = c.f16 ? 0u : 1u;
+    p.idesc = (1u << 4) | (type << 7) | (type << 10) | (uint32_t(c.a_mn) << 15) | (uint32_t(c.b_mn) << 16);
+    p.out = c.out;
+    p.aux_type = c.aux_type;
+    p.act = c.act;
+    p.slope = c.slope;
+    p.sym = c.sym;
+    p.alpha = c.alpha;
+    p.beta = c.beta;
+    p.bias = c.bias;
+    p.bias_f32 = c.bias_f32;
+    p.aux = c.aux;
+    p.ld_aux = c.ld_aux;
+    p.aux_matrix = c.aux_matrix;
+    p.pre = c.pre;
+    p.ld_pre = c.ld_pre;
+    p.D = c.D;
+    p.ldd = c.ldd;
+    p.d_matrix = c.d_matrix;
+    const double tmo = c.timeout_s > 0 ? c.timeout_s : kDefaultTimeoutS;
+    p.timeout_ns = std::max<uint64_t>(1, static_cast<uint64_t>(std::min(tmo, 60.0) * 1e9));
+    p.drain_ns = kDrainNs;
+    p.status = status;
+    int64_t workers = std::min<int64_t>(units, sms / cg);
+    if (c.max_workers > 0) workers = std::min<int64_t>(workers, c.max_workers);
+    L.grid = workers * cg;
+    L.stream = c.stream;
+    const cudaError_t e = v->launch(L);
+    return e == cudaSuccess ? TS_OK : cuda_fail(e, "linear product launch");
+}
+
+namespace {
+
+struct Matrix {
+    const void *ptr;
+    int64_t rows, cols, ld;
+    int esize;
+    int64_t bytes() const { return rows > 0 && cols > 0 ? ((rows - 1) * ld + cols) * esize : 0; }
+};
+
+bool overlap(const Matrix &a, const Matrix &b) {
+    return a.ptr && b.ptr && a.bytes() && b.bytes() && ranges_overlap(a.ptr, a.bytes(), b.ptr, b.bytes());
+}
+
+ts_status check_sizes(int64_t M, int64_t N, int64_t K, int32_t out, int32_t act, int32_t tile, int32_t max_workers,
+                      double timeout_s) {
+    if (M < 0 || N < 0 || K < 0 || M > kMaxSize || N > kMaxSize || K > kMaxSize)
+        return fail(TS_ERR_INVALID_ARG, "sizes must be in [0, 2^31 - 512] (M=%lld N=%lld K=%lld)",
+                    static_cast<long long>(M), static_cast<long long>(N), static_cast<long long>(K));
+    if (out != TS_OUT_BF16 && out != TS_OUT_F32) return fail(TS_ERR_INVALID_ARG, "out_dtype %d", out);
+    if (act < 0 || act >= kActs) return fail(TS_ERR_INVALID_ARG, "act %d", act);
+    if (tile < TS_TILE_AUTO || tile > TS_TILE_256x256_2CTA) return fail(TS_ERR_INVALID_ARG, "tile %d", tile);
+    if (max_workers < 0 || !(timeout_s >= 0)) return fail(TS_ERR_INVALID_ARG, "negative option");
+    return TS_OK;
+}
+
+ts_status check_pitch(const char *name, int64_t ld, int64_t cols) {
+    if (ld < cols || ld > kMaxPitch)
+        return fail(TS_ERR_INVALID_ARG, "the row stride of %s (%lld) must cover a row of %lld elements", name,
+                    static_cast<long long>(ld), static_cast<long long>(cols));
+    return TS_OK;
+}
+
+ts_status check_operand(const char *name, const Matrix &m) {
+    if (!m.ptr) return fail(TS_ERR_INVALID_ARG, "%s is NULL", name);
+    if (reinterpret_cast<uintptr_t>(m.ptr) % 16)
+        return fail(TS_ERR_UNSUPPORTED, "%s must start on a 16-byte boundary", name);
+    if (m.rows > 1 && m.ld % 8)
+        return fail(TS_ERR_UNSUPPORTED, "rows of %s must start on 16-byte boundaries (a stride that is a multiple of 8)",
+                    name);
+    return TS_OK;
+}
+
+ts_status check_output(const char *name, const Matrix &m) {
+    if (reinterpret_cast<uintptr_t>(m.ptr) % m.esize)
+        return fail(TS_ERR_INVALID_ARG, "%s is not aligned to its element size", name);
+    return TS_OK;
+}
+
+// `aux` may be D itself, element for element, and overlaps it in no other way.
+ts_status check_aliases(const Matrix &A, const Matrix &B, const Matrix &D, const Matrix &aux, const Matrix &pre) {
+    if (overlap(D, A) || overlap(D, B)) return fail(TS_ERR_INVALID_ARG, "the output overlaps an operand");
+    if (overlap(D, aux) && !(D.ptr == aux.ptr && (D.ld == aux.ld || D.rows <= 1)))
+        return fail(TS_ERR_INVALID_ARG, "the output overlaps the matrix its epilogue reads, and is not that matrix");
+    if (overlap(pre, A) || overlap(pre, B) || overlap(pre, D) || overlap(pre, aux))
+        return fail(TS_ERR_INVALID_ARG, "preact overlaps another matrix");
+    return TS_OK;
+}
+
+#define TS_TRY(call)                       \
+    do {                                   \
+        const ts_status s_ = (call);       \
+        if (s_ != TS_OK) return s_;        \
+    } while (0)
+
+// The two gradient products: D (rows x cols) from A and B, contracted over K.
+ts_status grad_product(const char *b_name, const char *d_name, const Matrix &A, const Matrix &B, const Matrix &D,
+                       const Matrix &aux, bool a_mn, bool slope, int64_t K, int32_t out, const ts_linear_grad_opts *o,
+                       void *stream) {
+    TS_TRY(check_pitch("grad_z", A.ld, A.cols));
+    TS_TRY(check_pitch(b_name, B.ld, B.cols));
+    TS_TRY(check_pitch(d_name, D.ld, D.cols));
+    if (aux.ptr) TS_TRY(check_pitch(slope ? "preact" : "base", aux.ld, aux.cols));
+    if (D.rows == 0 || D.cols == 0) return TS_OK;
+    if (!D.ptr) return fail(TS_ERR_INVALID_ARG, "%s is NULL", d_name);
+    TS_TRY(check_output(d_name, D));
+    TS_TRY(check_output(slope ? "preact" : "base", aux));
+    if (K > 0) {
+        TS_TRY(check_operand("grad_z", A));
+        TS_TRY(check_operand(b_name, B));
+    }
+    TS_TRY(check_aliases(A, B, D, aux, Matrix{nullptr, 0, 0, 0, 1}));
+    LinCall c;
+    std::memset(&c, 0, sizeof c);
+    c.A = A.ptr;
+    c.lda = A.ld;
+    c.a_mn = a_mn;
+    c.B = B.ptr;
+    c.ldb = B.ld;
+    c.b_mn = 1;
+    c.D = const_cast<void *>(D.ptr);
+    c.ldd = D.ld;
+    c.aux = aux.ptr;
+    c.ld_aux = aux.ld;
+    c.M = D.rows;
+    c.N = D.cols;
+    c.K = K;
+    c.batch = 1;
+    c.out = c.aux_type = out;
+    c.act = slope ? o->act : ACT_NONE;
+    c.slope = slope;
+    c.alpha = c.beta = 1.f;
+    c.tile = o->tile;
+    c.max_workers = o->max_workers;
+    c.timeout_s = o->timeout_s;
+    c.stream = static_cast<cudaStream_t>(stream);
+    return linear_product(c);
+}
+
+}  // namespace
+}  // namespace ts
+
+extern "C" {
+
+ts_status ts_linear(const void *x, const void *w, void *y, int64_t M, int64_t N, int64_t K, int32_t out_dtype,
+                    const ts_linear_opts *opts, void *stream) {
+    using namespace ts;
+    ts_linear_opts z;
+    std::memset(&z, 0, sizeof z);
+    const ts_linear_opts *o = opts ? opts : &z;
+    TS_TRY(check_sizes(M, N, K, out_dtype, o->act, o->tile, o->max_workers, o->timeout_s));
+    if (o->bias && o->bias_type != TS_OUT_BF16 && o->bias_type != TS_OUT_F32)
+        return fail(TS_ERR_INVALID_ARG, "bias_type %d", o->bias_type);
+    const int esize = out_dtype == TS_OUT_F32 ? 4 : 2, bsize = o->bias_type == TS_OUT_F32 ? 4 : 2;
+    const Matrix A{x, M, K, o->ldx ? o->ldx : K, 2}, B{w, N, K, o->ldw ? o->ldw : K, 2};
+    const Matrix D{y, M, N, o->ldy ? o->ldy : N, esize};
+    const Matrix R{o->residual, M, N, o->ld_residual ? o->ld_residual : N, esize};
+    const Matrix Z{o->preact, M, N, o->ld_preact ? o->ld_preact : N, esize};
+    TS_TRY(check_pitch("x", A.ld, K));
+    TS_TRY(check_pitch("w", B.ld, K));
+    TS_TRY(check_pitch("y", D.ld, N));
+    if (R.ptr) TS_TRY(check_pitch("residual", R.ld, N));
+    if (Z.ptr) TS_TRY(check_pitch("preact", Z.ld, N));
+    if (M == 0 || N == 0) return TS_OK;
+    if (!y) return fail(TS_ERR_INVALID_ARG, "y is NULL");
+    TS_TRY(check_output("y", D));
+    TS_TRY(check_output("residual", R));
+    TS_TRY(check_output("preact", Z));
+    if (K > 0) {
+        TS_TRY(check_operand("x", A));
+        TS_TRY(check_operand("w", B));
+    }
+    TS_TRY(check_aliases(A, B, D, R, Z));
+    const Matrix bias{o->bias, 1, N, N, bsize};
+    if (reinterpret_cast<uintptr_t>(o->bias) % bsize)
+        return fail(TS_ERR_INVALID_ARG, "bias is not aligned to its element size");
+    if (overlap(bias, D) || overlap(bias, Z)) return fail(TS_ERR_INVALID_ARG, "an output overlaps the bias");
+    LinCall c;
+    std::memset(&c, 0, sizeof c);
+    c.A = x;
+    c.lda = A.ld;
+    c.B = w;
+    c.ldb = B.ld;
+    c.D = y;
+    c.ldd = D.ld;
+    c.aux = R.ptr;
+    c.ld_aux = R.ld;
+    c.pre = o->preact;
+    c.ld_pre = Z.ld;
+    c.bias = o->bias;
+    c.bias_f32 = o->bias_type == TS_OUT_F32;
+    c.M = M;
+    c.N = N;
+    c.K = K;
+    c.batch = 1;
+    c.out = c.aux_type = out_dtype;
+    c.act = o->act;
+    c.alpha = c.beta = 1.f;
+    c.tile = o->tile;
+    c.max_workers = o->max_workers;
+    c.timeout_s = o->timeout_s;
+    c.stream = static_cast<cudaStream_t>(stream);
+    return linear_product(c);
+}
+
+ts_status ts_linear_grad_input(const void *grad_z, const void *w, void *grad_x, int64_t M, int64_t N, int64_t K,
+                               int32_t out_dtype, const ts_linear_grad_opts *opts, void *stream) {
+    using namespace ts;
+    ts_linear_grad_opts z;
+    std::memset(&z, 0, sizeof z);
+    const ts_linear_grad_opts *o = opts ? opts : &z;
+    TS_TRY(check_sizes(M, N, K, out_dtype, o->act, o->tile, o->max_workers, o->timeout_s));
+    if ((o->act != TS_ACT_NONE) != (o->aux != nullptr))
+        return fail(TS_ERR_INVALID_ARG, "an activation and its pre-activations are given together");
+    const int esize = out_dtype == TS_OUT_F32 ? 4 : 2;
+    return grad_product("w", "grad_x", Matrix{grad_z, M, N, o->ldg ? o->ldg : N, 2},
+                        Matrix{w, N, K, o->ldb ? o->ldb : K, 2}, Matrix{grad_x, M, K, o->ldd ? o->ldd : K, esize},
+                        Matrix{o->aux, M, K, o->ld_aux ? o->ld_aux : K, esize}, false, true, N, out_dtype, o, stream);
+}
+
+ts_status ts_linear_grad_weight(const void *grad_z, const void *x, void *grad_w, int64_t M, int64_t N, int64_t K,
+                                int32_t out_dtype, const ts_linear_grad_opts *opts, void *stream) {
+    using namespace ts;
+    ts_linear_grad_opts z;
+    std::memset(&z, 0, sizeof z);
+    const ts_linear_grad_opts *o = opts ? opts : &z;
+    TS_TRY(check_sizes(M, N, K, out_dtype, o->act, o->tile, o->max_workers, o->timeout_s));
+    if (o->act != TS_ACT_NONE) return fail(TS_ERR_INVALID_ARG, "a weight gradient passes no activation");
+    const int esize = out_dtype == TS_OUT_F32 ? 4 : 2;
+    return grad_product("x", "grad_w", Matrix{grad_z, M, N, o->ldg ? o->ldg : N, 2},
+                        Matrix{x, M, K, o->ldb ? o->ldb : K, 2}, Matrix{grad_w, N, K, o->ldd ? o->ldd : K, esize},
+                        Matrix{o->aux, N, K, o->ld_aux ? o->ld_aux : K, esize}, true, false, M, out_dtype, o, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,591 @@
+// Products with a fused epilogue for sm_103a: a linear layer's forward and backward products and
+// the products of an orthogonalised update.
+//
+//   D[z] = act(alpha * A[z] B[z]^T + bias) + beta * aux[z]        (forward; optionally the sum before act too)
+//   D[z] = alpha * A[z] B[z]^T * act'(aux[z])                     (backward through the activation before)
+//
+// with 16-bit operands (bf16, or fp16 inside the library), fp32 accumulation in Tensor Memory and
+// an epilogue in fp32.  Either operand may lie with K contiguous or with its rows of D contiguous:
+// a layer's input gradient reads the weights, its weight gradient both operands, the other way
+// around, in place.  With `sym` D is symmetric: the tiles on and above the diagonal are computed
+// and those above it stored twice.
+//
+// Warp roles (384 threads, one CTA per SM):
+//   warp 0       TMA producer of the operand ring
+//   warp 1       TMEM allocator and MMA issuer
+//   warp 3       initialises the barriers
+//   warps 4..11  epilogue: warp 4 + j holds rows 32 * (j % 4) of the tile, one row per lane, and
+//                half j / 4 of its columns, in subtiles of 128 bytes of D
+//
+// Two accumulators in TMEM: the epilogue of a tile overlaps the mainloop of the next.  The epilogue
+// fetches aux by TMA into the staging buffer that the result leaves from, before it waits for the
+// accumulator, so that neither the fetch nor its latency is on the path from one tile to the next.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "act.cuh"
+#include "gemm_kernel.cuh"
+#include "linear_params.h"
+#include "ptx.cuh"
+#include "waits.cuh"
+
+namespace ts {
+
+template <int BN_, int CG_, int PRE_>
+struct LinCfg {
+    static constexpr int BN = BN_, CG = CG_, PRE = PRE_;
+    static constexpr int EPI_WARPS = 8;
+    static constexpr int THREADS = 32 * (kRoleWarps + EPI_WARPS);
+    static constexpr int BM = 128, TILE_M = BM * CG;
+    static constexpr int BK = 64, UMMA_K = 16;
+    static constexpr int B_ROWS = BN / CG;
+    static constexpr int A_BYTES = BM * BK * 2, B_BYTES = B_ROWS * BK * 2;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES, TX_BYTES = STAGE_BYTES * CG;
+    static constexpr int BOX_BYTES = 64 * BK * 2;  // operand with its rows contiguous: 64 of them by BK
+    static constexpr int COLS = BN / 2;            // columns of an epilogue warp
+    // Staging of a warp: buffers of 32 rows x 128 bytes for D (and aux before it), enough for its
+    // part of a 16-bit tile, and one for the sum before the activation.
+    static constexpr int EPI_BUF = 32 * 128, BUFS = BN / 128;
+    static constexpr int WARP_BYTES = (BUFS + PRE) * EPI_BUF;
+    static constexpr int EPI_BYTES = EPI_WARPS * WARP_BYTES;
+    static constexpr int BIAS_BYTES = EPI_WARPS * COLS * 4;
+    static constexpr int TMEM_COLS = 2 * BN;
+    static constexpr int BAR_BYTES = 512;
+    static constexpr int FIXED_BYTES = 1024 + EPI_BYTES + BIAS_BYTES + BAR_BYTES;
+    static constexpr int STAGES = (kSmemLimit - FIXED_BYTES) / STAGE_BYTES;
+    static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * STAGE_BYTES;
+    static_assert(STAGES >= 2, "ring too shallow");
+    static_assert((2 * STAGES + 5 + EPI_WARPS * BUFS) * 8 + 16 <= BAR_BYTES, "barrier region");
+};
+
+// Shared-memory descriptor of an operand tile with its rows (columns of D for B) contiguous: boxes
+// of 64 of them by 64 of K, rows of 128 bytes along the first for consecutive k, 8-row atoms 1024
+// bytes apart along K (stride byte offset), the next 64 rows in the next 8 KB box (leading byte
+// offset).
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t smem_addr) {
+    return uint64_t((smem_addr & 0x3FFFFu) >> 4) | (uint64_t(8192 >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
+           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+__device__ __forceinline__ float f16_to_f32(uint16_t h) {
+    float f;
+    asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(h));
+    return f;
+}
+
+// Byte b of staged row r: 16-byte units permuted within the row as the TMA's 128-byte swizzle does.
+__device__ __forceinline__ uint32_t staged(uint32_t stage, int r, int b) {
+    return stage + r * 128 + (((b >> 4) ^ (r & 7)) << 4) + (b & 15);
+}
+
+// A warp moves `rows` rows of `left` <= 128 bytes between global memory (pitch in bytes) and swizzled
+// staging, lanes along the rows, in units of `unit` = 4 or 2 bytes (the alignment of the rows).
+// Where TMA cannot: a subtile that crosses N, rows that start off 16-byte boundaries.
+__device__ __forceinline__ void stage_rows_in(const char *src, int64_t pitch, int rows, int left, int unit,
+                                              uint32_t stage, int lane) {
+    if (unit >= 4) {
+        const int b = lane * 4;
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r) {
+            uint32_t v = 0;
+            if (b + 4 <= left)
+                v = __ldcg(reinterpret_cast<const uint32_t *>(src + r * pitch + b));
+            else if (b + 2 <= left)
+                v = __ldcg(reinterpret_cast<const uint16_t *>(src + r * pitch + b));
+            st_shared_u32(staged(stage, r, b), v);
+        }
+    } else {
+        const int b = lane * 2;
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r) {
+            const uint16_t v0 = b + 2 <= left ? __ldcg(reinterpret_cast<const uint16_t *>(src + r * pitch + b)) : 0;
+            const uint16_t v1 = b + 66 <= left ? __ldcg(reinterpret_cast<const uint16_t *>(src + r * pitch + b + 64)) : 0;
+            st_shared_u16(staged(stage, r, b), v0);
+            st_shared_u16(staged(stage, r, b + 64), v1);
+        }
+    }
+}
+__device__ __forceinline__ void stage_rows_out(char *dst, int64_t pitch, int rows, int left, int unit, uint32_t stage,
+                                               int lane) {
+    if (unit >= 4) {
+        const int b = lane * 4;
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r) {
+            const uint32_t v = ld_shared_u32(staged(stage, r, b));
+            if (b + 4 <= left)
+                *reinterpret_cast<uint32_t *>(dst + r * pitch + b) = v;
+            else if (b + 2 <= left)
+                *reinterpret_cast<uint16_t *>(dst + r * pitch + b) = static_cast<uint16_t>(v);
+        }
+    } else {
+        const int b = lane * 2;
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r) {
+            const uint16_t v0 = ld_shared_u16(staged(stage, r, b)), v1 = ld_shared_u16(staged(stage, r, b + 64));
+            if (b + 2 <= left) *reinterpret_cast<uint16_t *>(dst + r * pitch + b) = v0;
+            if (b + 66 <= left) *reinterpret_cast<uint16_t *>(dst + r * pitch + b + 64) = v1;
+        }
+    }
+}
+
+struct LinUnit {
+    int32_t mb, nb, z;  // tile and matrix
+};
+
+template <class C>
+__device__ __forceinline__ LinUnit lin_unit(int32_t u, const LinParams &p) {
+    LinUnit w;
+    w.z = fast_div(u, p.div_matrix);
+    const int32_t t = u - w.z * p.tiles_per_matrix;
+    if (p.sym) {
+        // rows i and n - 1 - i of the triangle together hold n + 1 tiles (the middle row alone, half)
+        const int32_t n = p.tiles_n, i = fast_div(t, p.div_group_tiles), r = t - i * (n + 1);
+        w.mb = r < n - i ? i : n - 1 - i;
+        w.nb = r < n - i ? i + r : w.mb + (r - (n - i));
+    } else {
+        raster(t, p, w.mb, w.nb);
+    }
+    return w;
+}
+
+template <int BN, int CG, int PRE>
+__global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
+    linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                  const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmAux,
+                  const __grid_constant__ CUtensorMap tmPre, const __grid_constant__ LinParams p) {
+    using C = LinCfg<BN, CG, PRE>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *const gbase = smem_raw + (base - raw);
+    const uint32_t s_a = base;
+    const uint32_t s_b = s_a + C::STAGES * C::A_BYTES;
+    const uint32_t s_epi = s_b + C::STAGES * C::B_BYTES;
+    const uint32_t s_bias = s_epi + C::EPI_BYTES;
+    const uint32_t s_bar = s_bias + C::BIAS_BYTES;
+    auto full = [&](uint32_t s) { return s_bar + 8u * s; };
+    auto empty = [&](uint32_t s) { return s_bar + 8u * (C::STAGES + s); };
+    auto tfull = [&](uint32_t a) { return s_bar + 8u * (2 * C::STAGES + a); };
+    auto tempty = [&](uint32_t a) { return s_bar + 8u * (2 * C::STAGES + 2 + a); };
+    const uint32_t mma_done = s_bar + 8u * (2 * C::STAGES + 4);
+    auto aux_full = [&](uint32_t j, uint32_t b) { return s_bar + 8u * (2 * C::STAGES + 5 + j * C::BUFS + b); };
+    const uint32_t tail = s_bar + 8u * (2 * C::STAGES + 5 + C::EPI_WARPS * C::BUFS);
+    volatile uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(gbase + (tail - base));
+    volatile int *const abort_flag = reinterpret_cast<volatile int *>(gbase + (tail - base) + 4);
+
+    // uniform across the warp, and known to be: the role loops then run on uniform registers
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+    const bool tma_d = p.store_bytes == 16;
+
+    if (warp == 0 && lane == 0 && p.num_kb > 0) {
+        prefetch_tmap(&tmA);
+        prefetch_tmap(&tmB);
+    }
+    if (warp == 3 && lane == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(tfull(a), 1);
+            mbar_init(tempty(a), C::EPI_WARPS * CG);
+        }
+        mbar_init(mma_done, 1);
+        for (int i = 0; i < C::EPI_WARPS * C::BUFS; ++i) mbar_init(aux_full(0, i), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc<CG>(tail, C::TMEM_COLS);
+        tmem_relinquish<CG>();
+    }
+    tc_fence_before();
+    if constexpr (CG == 2)
+        cluster_sync();
+    else
+        __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int32_t first = static_cast<int32_t>(blockIdx.x) / CG;
+    const int32_t step = static_cast<int32_t>(gridDim.x) / CG;
+
+    if (warp == 0) {
+        // ------------------------------------------------------ TMA producer
+        const bool leader = elect_one();
+        uint32_t stage = 0, phase = 0, issued = 0;
+        bool alive = true;
+        for (int32_t u = first; u < p.num_units && alive; u += step) {
+            const LinUnit w = lin_unit<C>(u, p);
+            const int32_t a_row = w.mb * C::TILE_M + static_cast<int32_t>(rank) * C::BM;
+            const int32_t b_row = w.nb * BN + static_cast<int32_t>(rank) * C::B_ROWS;
+            for (int32_t kb = 0; kb < p.num_kb; ++kb) {
+                if (!wait_phase(empty(stage), phase ^ 1u, abort_flag, p, WAIT_PRODUCER_EMPTY)) {
+                    alive = false;
+                    break;
+                }
+                if (rank == 0 && leader) mbar_arrive_expect_tx(full(stage), C::TX_BYTES);
+                const uint32_t fb = CG == 2 ? mapa(full(stage), 0) : full(stage);
+                auto load = [&](uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y) {
+                    if constexpr (CG == 1)
+                        tma_load_3d(dst, m, fb, x, y, w.z);
+                    else
+                        tma_load_3d_pair(dst, m, fb, x, y, w.z);
+                };
+                if (leader) {
+                    const uint32_t da = s_a + stage * C::A_BYTES, db = s_b + stage * C::B_BYTES;
+                    const int32_t k = kb * C::BK;
+                    if (p.a_mn) {
+#pragma unroll
+                        for (int c = 0; c < C::BM / 64; ++c) load(da + c * C::BOX_BYTES, &tmA, a_row + 64 * c, k);
+                    } else {
+                        load(da, &tmA, k, a_row);
+                    }
+                    if (p.b_mn) {
+#pragma unroll
+                        for (int c = 0; c < C::B_ROWS / 64; ++c) load(db + c * C::BOX_BYTES, &tmB, b_row + 64 * c, k);
+                    } else {
+                        load(db, &tmB, k, b_row);
+                    }
+                }
+                __syncwarp();
+                ++issued;
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        // every load has landed (seen on the even CTA's barriers) and every stage is released
+        if (rank == 0) {
+            const uint32_t n = issued < C::STAGES ? issued : C::STAGES;
+            for (uint32_t i = 1; i <= n; ++i) {
+                const uint32_t b = issued - i;
+                wait_drain(full(b % C::STAGES), (b / C::STAGES) & 1u, abort_flag, p);
+            }
+        }
+        for (int i = 0; i < C::STAGES; ++i) {
+            if (!wait_drain(empty(stage), phase ^ 1u, abort_flag, p)) break;
+            if (++stage == C::STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------- MMA issuer
+        // The whole warp runs the loop, one elected lane issues.
+        if (rank == 0) {
+            const bool leader = elect_one();
+            const uint32_t idesc = p.idesc | (uint32_t(BN >> 3) << 17) | (uint32_t((C::BM * CG) >> 4) << 24);
+            // steps of a start address for K = 16, in 16-byte units: 32 bytes along a K-major row, or
+            // 16 rows of 128 bytes
+            const uint32_t a_step = p.a_mn ? (16 * 128) >> 4 : 32 >> 4, b_step = p.b_mn ? (16 * 128) >> 4 : 32 >> 4;
+            uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+            bool alive = true;
+            for (int32_t u = first; u < p.num_units && alive; u += step) {
+                if (!wait_phase(tempty(acc), acc_phase ^ 1u, abort_flag, p, WAIT_MMA_TMEM_EMPTY)) break;
+                tc_fence_after();
+                for (int32_t kb = 0; kb < p.num_kb; ++kb) {
+                    if (!wait_phase(full(stage), phase, abort_flag, p, WAIT_MMA_FULL)) {
+                        alive = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (leader) {
+                        const uint32_t at_a = s_a + stage * C::A_BYTES, at_b = s_b + stage * C::B_BYTES;
+                        const uint64_t da = p.a_mn ? sw128_mn_desc(at_a) : sw128_kmajor_desc(at_a);
+                        const uint64_t db = p.b_mn ? sw128_mn_desc(at_b) : sw128_kmajor_desc(at_b);
+#pragma unroll
+                        for (int kk = 0; kk < C::BK / C::UMMA_K; ++kk)
+                            mma_bf16<CG>(tmem_base + acc * BN, da + a_step * kk, db + b_step * kk, idesc,
+                                         kb != 0 || kk != 0);
+                        if constexpr (CG == 1)
+                            mma_commit(empty(stage));
+                        else
+                            mma_commit_pair(empty(stage), 0x3);
+                    }
+                    __syncwarp();
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!alive) break;
+                if (leader) {
+                    if constexpr (CG == 1)
+                        mma_commit(tfull(acc));
+                    else
+                        mma_commit_pair(tfull(acc), 0x3);
+                }
+                __syncwarp();
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+            }
+            // every MMA has completed before TMEM is freed
+            if (leader) {
+                if constexpr (CG == 1)
+                    mma_commit(mma_done);
+                else
+                    mma_commit_pair(mma_done, 0x1);
+            }
+            __syncwarp();
+            wait_drain(mma_done, 0, abort_flag, p);
+        }
+        __syncwarp();
+    } else if (warp >= kRoleWarps) {
+        // --------------------------------------------------------- epilogue
+        const int j = warp - kRoleWarps;
+        const int q = j & 3, h = j >> 2;
+        const uint32_t stg = s_epi + static_cast<uint32_t>(j) * C::WARP_BYTES;
+        const uint32_t stg_pre = stg + C::BUFS * C::EPI_BUF;
+        const uint32_t bias_at = s_bias + static_cast<uint32_t>(j) * (C::COLS * 4);
+        const bool f32 = p.out == OUT_F32;
+        const int sub = f32 ? 32 : 64, subs = C::COLS / sub, esize = f32 ? 4 : 2;
+        const bool aux_tma = p.aux != nullptr && tma_d;
+        uint32_t acc = 0, acc_phase = 0, aux_phase = 0;  // aux_phase: bit b, parity of buffer b's next load
+        uint32_t aux_pending = 0;                        // bit b: a load into buffer b has not been waited for
+        bool alive = true;
+        for (int32_t u = first; u < p.num_units && alive; u += step) {
+            const LinUnit w = lin_unit<C>(u, p);
+            const int32_t row0 = w.mb * C::TILE_M + static_cast<int32_t>(rank) * C::BM + 32 * q;
+            const int32_t col0 = w.nb * BN + C::COLS * h;
+            const bool work = row0 < p.M && col0 < p.N;
+            auto load_aux = [&](int s) {  // lane 0, by TMA; the buffer is free
+                mbar_arrive_expect_tx(aux_full(j, s % C::BUFS), C::EPI_BUF);
+                tma_load_3d(stg + (s % C::BUFS) * C::EPI_BUF, &tmAux, aux_full(j, s % C::BUFS), col0 + s * sub, row0, w.z);
+            };
+            if (work) {
+                if (p.bias) {
+                    // the columns' bias, for reads that all lanes make at once; zeros without one
+                    __syncwarp();  // the last tile's have been read
+#pragma unroll
+                    for (int i = 0; i < C::COLS / 32; ++i) {
+                        const int32_t c = col0 + 32 * i + lane;
+                        float b = 0.f;
+                        if (c < p.N)
+                            b = p.bias_f32 ? __ldg(static_cast<const float *>(p.bias) + c)
+                                           : __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t *>(p.bias) + c)) << 16);
+                        st_shared_f32(bias_at + (32 * i + lane) * 4, b);
+                    }
+                }
+                if (aux_tma) {
+                    __syncwarp();
+                    if (lane == 0) {
+                        bulk_wait_read<0>();  // the stores that used the buffers have read them
+                        fence_proxy_async_smem();
+                        for (int s = 0; s < C::BUFS && s < subs; ++s)
+                            if (col0 + s * sub < p.N) load_aux(s);
+                    }
+                    for (int s = 0; s < C::BUFS && s < subs; ++s)
+                        if (col0 + s * sub < p.N) aux_pending |= 1u << s;
+                }
+                __syncwarp();
+            }
+            int ok = 1;
+            if (lane == 0) ok = wait_long(tfull(acc), acc_phase, abort_flag, p, WAIT_EPI_TMEM_FULL);
+            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * BN + C::COLS * h;
+            const int chunks = !work ? 0 : min(C::COLS, p.N - col0 + 31) / 32;
+            // the accumulator is read: back to the MMA issuer
+            auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 1)
+                        mbar_arrive(tempty(acc));
+                    else
+                        mbar_arrive_cluster(mapa(tempty(acc), 0));
+                }
+            };
+            if (chunks == 0) release();
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(taddr + 32 * c, v);
+                const int s = 32 * c / sub;
+                const uint32_t buf = s % C::BUFS, at = stg + buf * C::EPI_BUF;
+                const int32_t col = col0 + s * sub;  // of the subtile
+                const int piece = f32 ? 0 : (c & 1) * 4;  // 16-byte units of the chunk within the staged row
+                const bool head = f32 || (c & 1) == 0, done = f32 || (c & 1) == 1 || c + 1 == chunks;
+                const bool tma = tma_d && col + sub <= p.N;
+                const int rows = min(32, p.M - row0), left = min(p.N - col, sub) * esize;
+                if (head) {
+                    // the subtile's buffer: free, or holding aux
+                    if (aux_tma) {
+                        if (s >= C::BUFS) {
+                            __syncwarp();
+                            if (lane == 0) {
+                                bulk_wait_read<0>();
+                                fence_proxy_async_smem();
+                                load_aux(s);
+                            }
+                            aux_pending |= 1u << buf;
+                        }
+                        const bool got = wait_phase(aux_full(j, buf), (aux_phase >> buf) & 1u, abort_flag, p, WAIT_AUX);
+                        if (!__all_sync(0xffffffffu, got)) {
+                            alive = false;
+                            break;
+                        }
+                        aux_phase ^= 1u << buf;
+                        aux_pending &= ~(1u << buf);
+                    } else {
+                        if (lane == 0) bulk_wait_read<C::BUFS - 1>();
+                        __syncwarp();
+                        if (p.aux) {
+                            stage_rows_in(static_cast<const char *>(p.aux) +
+                                              (w.z * p.aux_matrix + static_cast<int64_t>(row0) * p.ld_aux + col) * esize,
+                                          p.ld_aux * esize, rows, left, p.store_bytes, at, lane);
+                            __syncwarp();
+                        }
+                    }
+                    if (PRE && aux_tma) {
+                        if (lane == 0) bulk_wait_read<C::BUFS - 1>();  // the other buffer's store, and pre's before it
+                        __syncwarp();
+                    }
+                }
+                tmem_ld_wait();
+                if (c + 1 == chunks) release();
+                float x[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = p.num_kb > 0 ? p.alpha * __uint_as_float(v[i]) : 0.f;
+                if (p.bias) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 b = ld_shared_v4(bias_at + (32 * c + 4 * i) * 4);
+                        x[4 * i] += __uint_as_float(b.x);
+                        x[4 * i + 1] += __uint_as_float(b.y);
+                        x[4 * i + 2] += __uint_as_float(b.z);
+                        x[4 * i + 3] += __uint_as_float(b.w);
+                    }
+                }
+                // x into this lane's row of a staging buffer
+                auto put = [&](uint32_t buffer) {
+                    const uint32_t row_at = buffer + lane * 128;
+                    if (f32) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            st_shared_v4(row_at + ((i ^ (lane & 7)) << 4), __float_as_uint(x[4 * i]),
+                                         __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]),
+                                         __float_as_uint(x[4 * i + 3]));
+                    } else {
+                        uint32_t o[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            o[i] = p.out == OUT_BF16 ? pack_bf16x2(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]))
+                                                     : pack_f16x2(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            st_shared_v4(row_at + (((piece + i) ^ (lane & 7)) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2],
+                                         o[4 * i + 3]);
+                        if (p.sym && w.nb > w.mb) {
+                            // the entry's mirror image: a column of this warp's is 32 consecutive values there
+                            uint16_t *const m = static_cast<uint16_t *>(p.D) + w.z * p.d_matrix + row0 + lane;
+                            const int32_t c0 = col0 + 32 * c;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (row0 + lane < p.M && c0 + i < p.N)
+                                    m[static_cast<int64_t>(c0 + i) * p.ldd] = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
+                        }
+                    }
+                };
+                // the staged subtile leaves for `dst`
+                auto leave = [&](uint32_t buffer, const CUtensorMap *map, void *dst, int64_t matrix, int64_t ld) {
+                    if (tma) fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (tma) tma_store_3d(map, buffer, col, row0, w.z, policy_evict_first());
+                        bulk_commit();
+                    }
+                    if (!tma)
+                        stage_rows_out(static_cast<char *>(dst) +
+                                           (w.z * matrix + static_cast<int64_t>(row0) * ld + col) * esize,
+                                       ld * esize, rows, left, p.store_bytes, buffer, lane);
+                };
+                if (PRE) {
+                    put(stg_pre);
+                    if (done) leave(stg_pre, &tmPre, p.pre, 0, p.ld_pre);
+                }
+                float a[32];
+                if (p.aux) {
+                    const uint32_t row_at = at + lane * 128;
+                    if (f32) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint4 t = ld_shared_v4(row_at + ((i ^ (lane & 7)) << 4));
+                            a[4 * i] = __uint_as_float(t.x);
+                            a[4 * i + 1] = __uint_as_float(t.y);
+                            a[4 * i + 2] = __uint_as_float(t.z);
+                            a[4 * i + 3] = __uint_as_float(t.w);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 t = ld_shared_v4(row_at + (((piece + i) ^ (lane & 7)) << 4));
+                            const uint32_t w4[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                a[8 * i + 2 * e] = p.aux_type == OUT_BF16 ? __uint_as_float(w4[e] << 16)
+                                                                          : f16_to_f32(static_cast<uint16_t>(w4[e]));
+                                a[8 * i + 2 * e + 1] = p.aux_type == OUT_BF16 ? __uint_as_float(w4[e] & 0xffff0000u)
+                                                                              : f16_to_f32(static_cast<uint16_t>(w4[e] >> 16));
+                            }
+                        }
+                    }
+                }
+                if (p.slope) {
+                    with_act(p.act, [&](auto tag) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] *= act_slope<decltype(tag)::value>(a[i]);
+                    });
+                } else {
+                    with_act(p.act, [&](auto tag) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = act_of<decltype(tag)::value>(x[i]);
+                    });
+                    if (p.aux) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = fmaf(p.beta, a[i], x[i]);
+                    }
+                }
+                put(at);
+                if (done) leave(at, &tmD, p.D, p.d_matrix, p.ldd);
+            }
+            if (++acc == 2) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+        // loads of aux that a given-up wait left in flight
+        for (uint32_t b = 0; b < C::BUFS; ++b)
+            if ((aux_pending >> b) & 1u) wait_drain(aux_full(j, b), (aux_phase >> b) & 1u, abort_flag, p);
+        if (lane == 0) bulk_wait<0>();
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    if constexpr (CG == 2)
+        cluster_sync();
+    else
+        __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc<CG>(tmem_base, C::TMEM_COLS);
+}
+
+}  // namespace ts
