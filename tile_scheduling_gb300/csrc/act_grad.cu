@@ -10,6 +10,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "act.cuh"
 #include "common.h"
@@ -18,7 +19,7 @@
 namespace ts {
 namespace {
 
-constexpr int kActThreads = 256, kStripLanes = 8, kStripRows = kActThreads / kStripLanes;
+constexpr int kActThreads = 512, kStripLanes = 8, kStripRows = kActThreads / kStripLanes;
 constexpr int kActUnroll = 4;      // rows of a thread in flight
 constexpr int kMaxActCluster = 8;
 
@@ -38,25 +39,23 @@ __device__ __forceinline__ float to_f32(float v) { return v; }
 template <>
 __device__ __forceinline__ float to_f32(uint16_t v) { return __uint_as_float(uint32_t(v) << 16); }
 
-// V values at p, V * sizeof(T) bytes in one access
+// V values, one access: as they lie, and unpacked
 template <class T, int V>
-__device__ __forceinline__ void load_v(const T *p, float (&f)[V]) {
-    if constexpr (V == 1) {
-        f[0] = to_f32(*p);
-    } else {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (sizeof(T) == 4) {
-                f[i] = __uint_as_float(w[i]);
-            } else {
-                f[2 * i] = __uint_as_float(w[i] << 16);
-                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
-        }
+struct Vec {
+    uint4 u;
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (V == 1)
+            u.x = sizeof(T) == 4 ? *reinterpret_cast<const uint32_t *>(p) : *reinterpret_cast<const uint16_t *>(p);
+        else
+            u = *reinterpret_cast<const uint4 *>(p);
     }
-}
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w);
+        const uint32_t w = i / 2 == 0 ? u.x : i / 2 == 1 ? u.y : i / 2 == 2 ? u.z : u.w;
+        return __uint_as_float(i % 2 ? w & 0xffff0000u : w << 16);
+    }
+};
 template <class T, int V>
 __device__ __forceinline__ void store_v(T *p, const float (&f)[V]) {
     if constexpr (V == 1) {
@@ -79,7 +78,7 @@ __device__ __forceinline__ void store_v(T *p, const float (&f)[V]) {
 
 // T: uint16_t (bf16) or float; VEC: rows start on 16-byte boundaries.
 template <class T, bool VEC>
-__global__ void __launch_bounds__(kActThreads) act_grad_kernel(const __grid_constant__ ActParams p) {
+__global__ void __launch_bounds__(kActThreads, 2) act_grad_kernel(const __grid_constant__ ActParams p) {
     constexpr int V = VEC ? 16 / sizeof(T) : 1;
     constexpr int STRIP = kStripLanes * V;
     __shared__ __align__(16) float part[kStripRows][STRIP];
@@ -100,25 +99,27 @@ __global__ void __launch_bounds__(kActThreads) act_grad_kernel(const __grid_cons
         constexpr int A = decltype(tag)::value;
         if (count == V) {
             for (int64_t m = m0 + ty; m < m1; m += kActUnroll * kStripRows) {
-                float g[kActUnroll][V], zz[kActUnroll][V];
+                Vec<T, V> g[kActUnroll], zz[kActUnroll];
 #pragma unroll
                 for (int k = 0; k < kActUnroll; ++k) {
                     const int64_t r = m + k * kStripRows;
                     if (r < m1) {
-                        load_v<T, V>(gy + r * p.ldy, g[k]);
-                        if constexpr (A != ACT_NONE) load_v<T, V>(z + r * p.ldz, zz[k]);
+                        g[k].load(gy + r * p.ldy);
+                        if constexpr (A != ACT_NONE) zz[k].load(z + r * p.ldz);
                     }
                 }
 #pragma unroll
                 for (int k = 0; k < kActUnroll; ++k) {
                     const int64_t r = m + k * kStripRows;
                     if (r < m1) {
+                        float o[V];
 #pragma unroll
                         for (int i = 0; i < V; ++i) {
-                            if constexpr (A != ACT_NONE) g[k][i] *= act_slope<A>(zz[k][i]);
-                            sum[i] += g[k][i];
+                            o[i] = g[k].get(i);
+                            if constexpr (A != ACT_NONE) o[i] *= act_slope<A>(zz[k].get(i));
+                            sum[i] += o[i];
                         }
-                        if (p.gz) store_v<T, V>(gz + r * p.ldg, g[k]);
+                        if (p.gz) store_v<T, V>(gz + r * p.ldg, o);
                     }
                 }
             }
@@ -147,23 +148,21 @@ __global__ void __launch_bounds__(kActThreads) act_grad_kernel(const __grid_cons
 #pragma unroll
     for (int i = 0; i < V; ++i) part[ty][tx * V + i] = sum[i];
     __syncthreads();
+    static_assert(STRIP <= kActThreads, "a thread sums a column");
+    float total = 0.f;
     if (threadIdx.x < STRIP) {
-        float t = 0.f;
-        for (int r = 0; r < kStripRows; ++r) t += part[r][threadIdx.x];
-        sum[0] = t;
-        part[0][threadIdx.x] = t;  // only this thread reads the column
+        for (int r = 0; r < kStripRows; ++r) total += part[r][threadIdx.x];
+        part[0][threadIdx.x] = total;  // only this thread reads the column
     }
     if (p.cluster > 1) {
         cluster_sync();
         if (rank == 0 && threadIdx.x < STRIP) {
             const uint32_t at = smem_u32(&part[0][threadIdx.x]);
-            float t = sum[0];
-            for (int c = 1; c < p.cluster; ++c) t += ld_cluster_f32(mapa(at, c));
-            sum[0] = t;
+            for (int c = 1; c < p.cluster; ++c) total += ld_cluster_f32(mapa(at, c));
         }
         cluster_sync();  // no CTA leaves while the first reads its sums
     }
-    if (rank == 0 && threadIdx.x < STRIP && strip * STRIP + threadIdx.x < p.N) p.gb[strip * STRIP + threadIdx.x] = sum[0];
+    if (rank == 0 && threadIdx.x < STRIP && strip * STRIP + threadIdx.x < p.N) p.gb[strip * STRIP + threadIdx.x] = total;
 }
 
 template <class T, bool VEC>
@@ -241,10 +240,11 @@ extern "C" ts_status ts_act_grad(const void *grad_y, const void *preact, void *g
     p.M = M;
     p.N = N;
     p.act = act;
-    p.cluster = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(kMaxActCluster, M / (2 * kStripRows))));
-    if (cdiv(N, kStripLanes) * p.cluster > 0x7fffffffLL) return fail(TS_ERR_UNSUPPORTED, "too many columns");
+    p.cluster = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(kMaxActCluster, M / 64)));
+    if (cdiv(N, 8) * p.cluster > 0x7fffffffLL) return fail(TS_ERR_UNSUPPORTED, "too many columns");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == TS_OUT_F32 ? (vec ? launch_act_grad<float, true>(p, st) : launch_act_grad<float, false>(p, st))
-                                              : (vec ? launch_act_grad<uint16_t, true>(p, st) : launch_act_grad<uint16_t, false>(p, st));
+    auto pick = [&](auto t, auto v) { return launch_act_grad<decltype(t), decltype(v)::value>(p, st); };
+    const cudaError_t e = dtype == TS_OUT_F32 ? (vec ? pick(float(), std::true_type()) : pick(float(), std::false_type()))
+                                              : (vec ? pick(uint16_t(), std::true_type()) : pick(uint16_t(), std::false_type()));
     return e == cudaSuccess ? TS_OK : cuda_fail(e, "activation gradient launch");
 }

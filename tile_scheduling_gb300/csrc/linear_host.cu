@@ -7,6 +7,7 @@
 
 namespace ts {
 
+extern const SplitVariant split_128, split_swap_64, split_swap_32;
 extern const LinVariant linear_128_1, linear_128_1_pre, linear_256_1, linear_256_1_pre, linear_256_2, linear_256_2_pre;
 
 namespace {
@@ -60,15 +61,35 @@ ts_status linear_product(const LinCall &c) {
     const int64_t m1 = cdiv(c.M, 128), m2 = cdiv(c.M, 256), n1 = cdiv(c.N, 128), n2 = cdiv(c.N, 256);
     const int64_t u1 = c.batch * (c.sym ? tri(n1) : m1 * n1), u2 = c.batch * m1 * n2,
                   u3 = c.batch * (c.sym ? tri(n2) : m2 * n2);
+    // Few tiles: K shared by a cluster, the fewest cycles of a cluster size whose clusters all run at once.
+    const SplitVariant *sv = nullptr;
+    int split = 1, split_ctas = 1;
+    int64_t best = INT64_MAX;
+    if (tile == TS_TILE_AUTO && nkb > 0 && c.max_workers == 0) {
+        // Measured, cycles of a K block with all of a CTA's loads in flight and what is left without one:
+        // 512 x 512 x 768 with a bf16 output by 1 / 2 / 4 CTAs a tile 8.1 / 6.8 / 6.1 us, by a persistent
+        // CTA 6.5; 257 x 1023 x 777 9.6 / 7.5 / 6.8 and 8.2.
+        auto consider = [&](const SplitVariant &v, int64_t units, int64_t fixed) {
+            for (int k = v.swap ? 1 : 2; k <= kMaxSplit && k <= nkb; k *= 2) {
+                const int ctas = v.swap && units * k > sms ? 2 : 1;
+                if (units * k > ctas * sms || (k > 1 && v.clusters(k, ctas) < units)) break;
+                const int64_t t = cdiv(nkb, k) * 340 * ctas + fixed;
+                if (t < best) best = t, sv = &v, split = k, split_ctas = ctas;
+            }
+        };
+        consider(split_128, u1, 10700);
+        // an operand with its rows contiguous comes in boxes of 64
+        if (!c.sym && c.batch == 1 && c.M <= 64)
+            consider(c.M <= 32 && !c.a_mn ? split_swap_32 : split_swap_64, n1, 8000);
+    }
     if (tile == TS_TILE_AUTO) {
         // The tile with the fewest cycles: waves of workers times what a tile takes.
-        const int64_t c1 = cdiv(u1, sms) * (nkb * 300 + 300) + 2500;
-        const int64_t c2 = cdiv(u2, sms) * (nkb * 540 + 300) + 4000;
-        const int64_t c3 = cdiv(u3, sms / 2) * (nkb * 520 + 300) + 4500;
-        if (c.sym)
-            tile = c1 <= c3 ? TS_TILE_128x128 : TS_TILE_256x256_2CTA;
-        else
-            tile = c1 <= c2 && c1 <= c3 ? TS_TILE_128x128 : c2 < c3 ? TS_TILE_128x256 : TS_TILE_256x256_2CTA;
+        const int64_t c1 = cdiv(u1, sms) * (nkb * 340) + 8300;
+        const int64_t c2 = cdiv(u2, sms) * (nkb * 540) + 9100;
+        const int64_t c3 = cdiv(u3, sms / 2) * (nkb * 520) + 9800;
+        const int64_t least = std::min(c1, std::min(c.sym ? c1 : c2, c3));
+        if (best >= least) sv = nullptr;
+        tile = least == c1 ? TS_TILE_128x128 : least == c3 ? TS_TILE_256x256_2CTA : TS_TILE_128x256;
     }
     const int bn = tile == TS_TILE_128x128 ? 128 : 256, cg = tile == TS_TILE_256x256_2CTA ? 2 : 1;
     const LinVariant *v = find_linear(bn, cg, c.pre ? 1 : 0);
@@ -77,7 +98,8 @@ ts_status linear_product(const LinCall &c) {
     LinLaunch L;
     std::memset(&L, 0, sizeof L);
     LinParams &p = L.p;
-    const int64_t tiles_m = cdiv(c.M, 128 * cg), tiles_n = cdiv(c.N, bn);
+    const bool swap = sv && sv->swap;
+    const int64_t tiles_m = swap ? 1 : cdiv(c.M, sv ? 128 : 128 * cg), tiles_n = cdiv(c.N, sv ? 128 : bn);
     const int64_t per = c.sym ? tri(tiles_n) : tiles_m * tiles_n, units = per * c.batch;
     if (units * cg > 0x7fffffffLL) return fail(TS_ERR_UNSUPPORTED, "too many output tiles");
     const int esize = c.out == OUT_F32 ? 4 : 2;
@@ -94,10 +116,13 @@ ts_status linear_product(const LinCall &c) {
     }
     ts_status s = TS_OK;
     if (c.K > 0) {
-        if ((s = operand_map(&L.a, c.A, c.a_mn, c.M, c.K, c.batch, c.lda, c.a_matrix, 128)) != TS_OK) return s;
-        if ((s = operand_map(&L.b, c.B, c.b_mn, c.N, c.K, c.batch, c.ldb, c.b_matrix, bn / cg)) != TS_OK) return s;
+        // swapped, the rows of D are the instruction's columns
+        CUtensorMap &a = swap ? L.b : L.a, &b = swap ? L.a : L.b;
+        const int a_box = swap ? sv->bn : 128, b_box = sv ? 128 : bn / cg;
+        if ((s = operand_map(&a, c.A, c.a_mn, c.M, c.K, c.batch, c.lda, c.a_matrix, a_box)) != TS_OK) return s;
+        if ((s = operand_map(&b, c.B, c.b_mn, c.N, c.K, c.batch, c.ldb, c.b_matrix, b_box)) != TS_OK) return s;
     }
-    if (p.store_bytes == 16) {
+    if (p.store_bytes == 16 && !sv) {
         if ((s = output_map(&L.d, c.D, esize, c.M, c.N, c.batch, c.ldd, c.d_matrix)) != TS_OK) return s;
         if (c.aux && (s = output_map(&L.aux, c.aux, esize, c.M, c.N, c.batch, c.ld_aux, c.aux_matrix)) != TS_OK) return s;
         if (c.pre && (s = output_map(&L.pre, c.pre, esize, c.M, c.N, 1, c.ld_pre, 0)) != TS_OK) return s;
@@ -117,12 +142,12 @@ ts_status linear_product(const LinCall &c) {
     p.div_group_rows = fast_div_for(kRasterGroup);
     p.div_last_rows = fast_div_for(tiles_m - (cdiv(tiles_m, kRasterGroup) - 1) * kRasterGroup);
     p.div_matrix = fast_div_for(per);
-    p.a_mn = c.a_mn;
-    p.b_mn = c.b_mn;
+    p.a_mn = swap ? c.b_mn : c.a_mn;
+    p.b_mn = swap ? c.a_mn : c.b_mn;
     // Instruction descriptor, kind::f16: D fp32 (bits 4-5 = 1), A and B bf16 (bits 7-9 and 10-12 = 1)
     // or fp16 (0), A and B K-major (bits 15 and 16 = 0) or not; the kernel adds N and M of its tile.
     const uint32_t type = c.f16 ? 0u : 1u;
-    p.idesc = (1u << 4) | (type << 7) | (type << 10) | (uint32_t(c.a_mn) << 15) | (uint32_t(c.b_mn) << 16);
+    p.idesc = (1u << 4) | (type << 7) | (type << 10) | (uint32_t(p.a_mn) << 15) | (uint32_t(p.b_mn) << 16);
     p.out = c.out;
     p.aux_type = c.aux_type;
     p.act = c.act;
@@ -132,6 +157,7 @@ ts_status linear_product(const LinCall &c) {
     p.beta = c.beta;
     p.bias = c.bias;
     p.bias_f32 = c.bias_f32;
+    p.bias_vec = reinterpret_cast<uintptr_t>(c.bias) % 16 == 0;
     p.aux = c.aux;
     p.ld_aux = c.ld_aux;
     p.aux_matrix = c.aux_matrix;
@@ -144,10 +170,17 @@ ts_status linear_product(const LinCall &c) {
     p.timeout_ns = std::max<uint64_t>(1, static_cast<uint64_t>(std::min(tmo, 60.0) * 1e9));
     p.drain_ns = kDrainNs;
     p.status = status;
+    L.stream = c.stream;
+    if (sv) {
+        p.split = split;
+        p.stages = sv->stages(split, split_ctas);
+        L.grid = units * split;
+        const cudaError_t e = sv->launch(L);
+        return e == cudaSuccess ? TS_OK : cuda_fail(e, "split product launch");
+    }
     int64_t workers = std::min<int64_t>(units, sms / cg);
     if (c.max_workers > 0) workers = std::min<int64_t>(workers, c.max_workers);
     L.grid = workers * cg;
-    L.stream = c.stream;
     const cudaError_t e = v->launch(L);
     return e == cudaSuccess ? TS_OK : cuda_fail(e, "linear product launch");
 }
@@ -323,7 +356,7 @@ ts_status ts_linear(const void *x, const void *w, void *y, int64_t M, int64_t N,
     c.max_workers = o->max_workers;
     c.timeout_s = o->timeout_s;
     c.stream = static_cast<cudaStream_t>(stream);
-    return linear_product(c);
+    return linear_few_takes(c) ? linear_few(c) : linear_product(c);
 }
 
 ts_status ts_linear_grad_input(const void *grad_z, const void *w, void *grad_x, int64_t M, int64_t N, int64_t K,

@@ -29,11 +29,12 @@ struct LinParams {
     int32_t aux_type;                 // of aux, of the same size as out
     int32_t act;                      // of the forward epilogue, or whose slope the backward one multiplies by
     int32_t slope;                    // 0: D = act(alpha * acc + bias) + beta * aux; 1: D = alpha * acc * act'(aux)
+    int32_t split, stages;            // the split kernel: CTAs of a cluster that share K, operand stages
     int32_t sym;                      // 1: D is symmetric: tiles above the diagonal are stored twice
     int32_t store_bytes;              // 16, 4 or 2: what the bases and rows of D, aux and pre are aligned to
     float alpha, beta;
     const void *bias;                 // N values added to every row, or NULL
-    int32_t bias_f32;
+    int32_t bias_f32, bias_vec;       // bias_vec: it starts on a 16-byte boundary
     const void *aux;                  // residual or pre-activation [M][N], or NULL
     int64_t ld_aux, aux_matrix;
     void *pre;                        // alpha * acc + bias, or NULL
@@ -54,6 +55,15 @@ struct LinLaunch {
 struct LinVariant {
     int bn, cg, pre;
     cudaError_t (*launch)(const LinLaunch &);
+};
+
+constexpr int kMaxSplit = 8;  // most CTAs that share a tile's K: the portable cluster size
+
+struct SplitVariant {
+    int bn, swap;
+    cudaError_t (*launch)(const LinLaunch &);
+    int (*clusters)(int size, int ctas);  // clusters of so many CTAs that run at once, with so many on an SM
+    int (*stages)(int split, int ctas);   // operand stages of a CTA
 };
 
 // One product as its callers describe it: D[z] = epilogue(A[z] B[z]^T), z < batch.
@@ -79,5 +89,10 @@ struct LinCall {
 };
 // Plans and launches a product whose arguments have been checked.
 ts_status linear_product(const LinCall &c);
+
+// The forward product of at most so many rows of x runs in a kernel of its own.
+constexpr int kFewTokens = 8;
+bool linear_few_takes(const LinCall &c);
+ts_status linear_few(const LinCall &c);
 
 }  // namespace ts

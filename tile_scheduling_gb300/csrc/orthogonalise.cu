@@ -28,7 +28,7 @@ namespace {
 
 constexpr float kOrthScale = 4096.f;
 constexpr int kOrthThreads = 256;
-constexpr int64_t kOrthChunks = 128;  // CTAs that share the sum of a matrix's squares
+constexpr int64_t kOrthChunks = 608;  // CTAs that share a matrix, at most: four for each SM
 
 struct OrthParams {
     const void *G;
@@ -37,6 +37,7 @@ struct OrthParams {
     int64_t ldx, x_matrix;
     float *partial;       // [batch][chunks][3]
     int64_t R, C, vecs;   // vecs: vectors of a row
+    FastDiv div_vecs;
     int32_t chunks, to_bf16;
     float eps;
 };
@@ -69,6 +70,58 @@ __device__ __forceinline__ void load_row(const T *p, int count, float (&f)[V]) {
     }
 }
 
+// f(values, row, first column, how many) for the vectors of rows [r0, r1), four of a thread in flight.
+template <class T, int V, class F>
+__device__ __forceinline__ void each_vector(const OrthParams &p, const T *g, int64_t r0, int64_t r1, F &&f) {
+    constexpr int UN = 4;
+    const int64_t total = (r1 - r0) * p.vecs;
+    for (int64_t i0 = threadIdx.x; i0 < total; i0 += UN * kOrthThreads) {
+        float v[UN][V];
+        int64_t r[UN], c[UN];
+        int count[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const int64_t i = i0 + u * kOrthThreads;
+            count[u] = 0;
+            if (i < total) {
+                // a CTA's share has fewer than 2^31 vectors (checked on the host)
+                const int32_t row = fast_div(static_cast<int32_t>(i), p.div_vecs);
+                r[u] = r0 + row;
+                c[u] = (i - row * p.vecs) * V;
+                count[u] = static_cast<int>(min(static_cast<int64_t>(V), p.C - c[u]));
+                load_row<T, V>(g + r[u] * p.ldg + c[u], count[u], v[u]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+            if (count[u]) f(v[u], r[u], c[u], count[u]);
+    }
+}
+
+// The block's sums of three values, in thread 0, in a fixed order.
+template <class T>
+__device__ __forceinline__ void block_sum3(T &a, T &b, T &c) {
+    __shared__ T s[3][kOrthThreads / 32];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, d);
+        b += __shfl_xor_sync(0xffffffffu, b, d);
+        c += __shfl_xor_sync(0xffffffffu, c, d);
+    }
+    if (threadIdx.x % 32 == 0) {
+        s[0][threadIdx.x / 32] = a;
+        s[1][threadIdx.x / 32] = b;
+        s[2][threadIdx.x / 32] = c;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int w = 1; w < kOrthThreads / 32; ++w) {
+            a += s[0][w];
+            b += s[1][w];
+            c += s[2][w];
+        }
+}
+
 // Sums of squares in three ranges, after Blue ("A Portable Fortran Program to Find the Euclidean
 // Norm of a Vector", 1978): as they are, and scaled by 2^-70 and 2^70 for values whose squares
 // leave fp32's range.
@@ -79,12 +132,8 @@ __global__ void __launch_bounds__(kOrthThreads) orth_norm_kernel(const __grid_co
     grid_dep_launch();
     const T *g = static_cast<const T *>(p.G) + blockIdx.y * p.g_matrix;
     float mid = 0.f, big = 0.f, tiny = 0.f;
-    const int64_t total = p.R * p.vecs;
-    for (int64_t i = blockIdx.x * static_cast<int64_t>(kOrthThreads) + threadIdx.x; i < total;
-         i += static_cast<int64_t>(p.chunks) * kOrthThreads) {
-        const int64_t r = i / p.vecs, c = (i - r * p.vecs) * V;
-        float f[V];
-        load_row<T, V>(g + r * p.ldg + c, static_cast<int>(min(static_cast<int64_t>(V), p.C - c)), f);
+    const int64_t r0 = p.R * blockIdx.x / p.chunks, r1 = p.R * (blockIdx.x + 1) / p.chunks;
+    each_vector<T, V>(p, g, r0, r1, [&](const float (&f)[V], int64_t, int64_t, int) {
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const float b = f[k] * 0x1p-70f, t = f[k] * 0x1p70f;
@@ -92,24 +141,13 @@ __global__ void __launch_bounds__(kOrthThreads) orth_norm_kernel(const __grid_co
             big = fmaf(b, b, big);
             tiny = fmaf(t, t, tiny);
         }
-    }
-    __shared__ float s[3][kOrthThreads / 32];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        mid += __shfl_xor_sync(0xffffffffu, mid, d);
-        big += __shfl_xor_sync(0xffffffffu, big, d);
-        tiny += __shfl_xor_sync(0xffffffffu, tiny, d);
-    }
-    if (threadIdx.x % 32 == 0) {
-        s[0][threadIdx.x / 32] = mid;
-        s[1][threadIdx.x / 32] = big;
-        s[2][threadIdx.x / 32] = tiny;
-    }
-    __syncthreads();
-    if (threadIdx.x < 3) {
-        float t = 0.f;
-        for (int w = 0; w < kOrthThreads / 32; ++w) t += s[threadIdx.x][w];
-        p.partial[(static_cast<int64_t>(blockIdx.y) * p.chunks + blockIdx.x) * 3 + threadIdx.x] = t;
+    });
+    block_sum3(mid, big, tiny);
+    if (threadIdx.x == 0) {
+        float *const q = p.partial + (static_cast<int64_t>(blockIdx.y) * p.chunks + blockIdx.x) * 3;
+        q[0] = mid;
+        q[1] = big;
+        q[2] = tiny;
     }
 }
 
@@ -120,13 +158,22 @@ __global__ void __launch_bounds__(kOrthThreads) orth_scale_kernel(const __grid_c
     grid_dep_wait();
     grid_dep_launch();
     __shared__ double sums[3];
-    if (threadIdx.x < 3) {
-        double t = 0.0;
-        const float *q = p.partial + static_cast<int64_t>(blockIdx.y) * p.chunks * 3 + threadIdx.x;
-        for (int c = 0; c < p.chunks; ++c) t += static_cast<double>(q[3 * c]);
-        sums[threadIdx.x] = t;
+    {
+        double mid = 0.0, big = 0.0, tiny = 0.0;
+        const float *q = p.partial + static_cast<int64_t>(blockIdx.y) * p.chunks * 3;
+        for (int c = threadIdx.x; c < p.chunks; c += kOrthThreads) {
+            mid += static_cast<double>(q[3 * c]);
+            big += static_cast<double>(q[3 * c + 1]);
+            tiny += static_cast<double>(q[3 * c + 2]);
+        }
+        block_sum3(mid, big, tiny);
+        if (threadIdx.x == 0) {
+            sums[0] = mid;
+            sums[1] = big;
+            sums[2] = tiny;
+        }
+        __syncthreads();
     }
-    __syncthreads();
     // the middle sum where it neither overflowed (then it is infinite) nor lost what is below
     // 2^-75 (then it is small); a NaN stays one
     double sq = sums[0];
@@ -143,13 +190,8 @@ __global__ void __launch_bounds__(kOrthThreads) orth_scale_kernel(const __grid_c
     const T *g = static_cast<const T *>(p.G) + blockIdx.y * p.g_matrix;
     uint16_t *x = static_cast<uint16_t *>(p.X) + blockIdx.y * p.x_matrix;
     const bool whole = (p.ldx % V) == 0 && (p.x_matrix % V) == 0 && reinterpret_cast<uintptr_t>(p.X) % (2 * V) == 0;
-    const int64_t total = p.R * p.vecs;
-    for (int64_t i = blockIdx.x * static_cast<int64_t>(kOrthThreads) + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * kOrthThreads) {
-        const int64_t r = i / p.vecs, c = (i - r * p.vecs) * V;
-        const int count = static_cast<int>(min(static_cast<int64_t>(V), p.C - c));
-        float f[V];
-        load_row<T, V>(g + r * p.ldg + c, count, f);
+    const int64_t r0 = p.R * blockIdx.x / gridDim.x, r1 = p.R * (blockIdx.x + 1) / gridDim.x;
+    each_vector<T, V>(p, g, r0, r1, [&](const float (&f)[V], int64_t r, int64_t c, int count) {
         uint16_t o[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) {
@@ -171,7 +213,7 @@ __global__ void __launch_bounds__(kOrthThreads) orth_scale_kernel(const __grid_c
             for (int k = 0; k < V; ++k)
                 if (k < count) at[k] = o[k];
         }
-    }
+    });
 }
 
 // Where the iteration's matrices lie in the workspace, in bytes.
@@ -192,7 +234,7 @@ OrthPlan plan_orth(int64_t batch, int64_t R, int64_t C, int steps) {
     o.ldn = cdiv(o.n, 8) * 8;
     o.x_bytes = steps > 0 ? round(batch * R * o.ldx * 2) : 0;
     o.n_bytes = steps > 0 ? round(batch * o.n * o.ldn * 2) : 0;
-    o.chunks = std::max<int64_t>(1, std::min<int64_t>(kOrthChunks, R * C / 8192));
+    o.chunks = std::max<int64_t>(1, std::min<int64_t>({kOrthChunks, R, cdiv(R * C, 8192)}));
     o.partial_bytes = round(batch * o.chunks * 3 * 4);
     return o;
 }
@@ -275,17 +317,16 @@ ts_status ts_orthogonalise(const void *G, void *O, int64_t batch, int64_t R, int
     p.R = R;
     p.C = C;
     p.vecs = cdiv(C, V);
+    p.div_vecs = fast_div_for(p.vecs);
     p.chunks = static_cast<int32_t>(plan.chunks);
     p.to_bf16 = steps == 0;
     p.eps = o->eps > 0.f ? o->eps : 1e-7f;
     const dim3 norm_grid(static_cast<unsigned>(plan.chunks), static_cast<unsigned>(batch));
-    const dim3 scale_grid(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(1024, cdiv(R * p.vecs, 2 * kOrthThreads)))),
-                          static_cast<unsigned>(batch));
     const dim3 block(kOrthThreads);
     cudaError_t e;
     auto prepare = [&](auto norm, auto scale) {
         e = launch_pdl(norm, norm_grid, block, 0, st, p);
-        if (e == cudaSuccess) e = launch_pdl(scale, scale_grid, block, 0, st, p);
+        if (e == cudaSuccess) e = launch_pdl(scale, norm_grid, block, 0, st, p);
     };
     if (gsize == 4)
         vec ? prepare(orth_norm_kernel<float, true>, orth_scale_kernel<float, true>)
