@@ -17,6 +17,8 @@ constexpr int64_t kMaxPitch = int64_t(1) << 37;
 constexpr double kDefaultTimeoutS = 2.0;
 constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
 constexpr int kRasterGroup = 8;
+// What a tile takes beside its columns, as columns: the loads and barriers of a K block.
+constexpr int64_t kWidthOverhead = 16;
 
 const LinVariant *find_linear(int bn, int cg, int pre) {
     static const LinVariant *const all[] = {&linear_128_1,     &linear_128_1_pre, &linear_256_1,
@@ -82,17 +84,33 @@ ts_status linear_product(const LinCall &c) {
         if (!c.sym && c.batch == 1 && c.M <= 64)
             consider(c.M <= 32 && !c.a_mn ? split_swap_32 : split_swap_64, n1, 8000);
     }
+    // Columns of a 256-column tile: the width whose waves of workers take the fewest cycles in all.
+    // With B's rows contiguous only whole boxes of 64 of them for each CTA: 4096 x 2048 x 2048 on pairs
+    // 24.6 us with 256 columns, 30.1 with 240 (which take as many waves, and K-major 24.6 as well).
+    auto width = [&](int64_t rows, int64_t workers, int64_t pair, int64_t &waves) {
+        int64_t bn = 256;
+        waves = cdiv(rows * n2 * c.batch, workers);
+        for (int64_t b = 240; !c.sym && b > 128; b -= 16) {
+            if (c.b_mn && b % (64 * pair) != 0) continue;
+            const int64_t w = cdiv(rows * cdiv(c.N, b) * c.batch, workers);
+            if (w * (b + kWidthOverhead) < waves * (bn + kWidthOverhead)) bn = b, waves = w;
+        }
+        return bn;
+    };
+    int64_t w2, w3;
+    const int64_t bn2 = width(m1, sms, 1, w2), bn3 = width(m2, sms / 2, 2, w3);
     if (tile == TS_TILE_AUTO) {
         // The tile with the fewest cycles: waves of workers times what a tile takes.
         const int64_t c1 = cdiv(u1, sms) * (nkb * 340) + 8300;
-        const int64_t c2 = cdiv(u2, sms) * (nkb * 540) + 9100;
-        const int64_t c3 = cdiv(u3, sms / 2) * (nkb * 520) + 9800;
+        const int64_t c2 = w2 * nkb * 540 * (bn2 + kWidthOverhead) / (256 + kWidthOverhead) + 9100;
+        const int64_t c3 = (c.sym ? cdiv(u3, sms / 2) * nkb * 520 : w3 * nkb * 520 * (bn3 + kWidthOverhead) / (256 + kWidthOverhead)) + 9800;
         const int64_t least = std::min(c1, std::min(c.sym ? c1 : c2, c3));
         if (best >= least) sv = nullptr;
         tile = least == c1 ? TS_TILE_128x128 : least == c3 ? TS_TILE_256x256_2CTA : TS_TILE_128x256;
     }
-    const int bn = tile == TS_TILE_128x128 ? 128 : 256, cg = tile == TS_TILE_256x256_2CTA ? 2 : 1;
-    const LinVariant *v = find_linear(bn, cg, c.pre ? 1 : 0);
+    const int cg = tile == TS_TILE_256x256_2CTA ? 2 : 1;
+    int bn = tile == TS_TILE_128x128 ? 128 : static_cast<int>(cg == 2 ? bn3 : bn2);
+    const LinVariant *v = find_linear(bn > 128 ? 256 : 128, cg, c.pre ? 1 : 0);
     if (!v) return fail(TS_ERR_UNSUPPORTED, "no compiled variant");
 
     LinLaunch L;
@@ -178,6 +196,13 @@ ts_status linear_product(const LinCall &c) {
         const cudaError_t e = sv->launch(L);
         return e == cudaSuccess ? TS_OK : cuda_fail(e, "split product launch");
     }
+    p.bn = bn;
+    // boxes of 64 rows where an operand's rows are contiguous, which may pass the tile's columns
+    p.tx_bytes = cg * (128 * 128 + (c.b_mn ? cdiv(bn / cg, 64) * 64 : bn / cg) * 128);
+    // Short K loops leave the epilogue as the bound: 4096 x 4096 x 256 14.7 us with two buffers, 15.7 with
+    // one; x 1024 23.9 both.  Long ones need the ring: 2047 x 4096 x 6144 59.0 and 57.3.
+    p.bufs = nkb <= 8 ? 2 : 1;
+    p.stages = v->stages(p.bufs);
     int64_t workers = std::min<int64_t>(units, sms / cg);
     if (c.max_workers > 0) workers = std::min<int64_t>(workers, c.max_workers);
     L.grid = workers * cg;

@@ -17,6 +17,9 @@
 //   warps 4..11  epilogue: warp 4 + j holds rows 32 * (j % 4) of the tile, one row per lane, and
 //                half j / 4 of its columns, in subtiles of 128 bytes of D
 //
+// A 256-column tile may be used with fewer columns (LinParams::bn, a multiple of 16 above 128): the
+// host picks the width whose tiles fill their waves of workers best.
+//
 // Two accumulators in TMEM: the epilogue of a tile overlaps the mainloop of the next.  The epilogue
 // fetches aux by TMA into the staging buffer that the result leaves from, before it waits for the
 // accumulator, so that neither the fetch nor its latency is on the path from one tile to the next.
@@ -44,19 +47,21 @@ struct LinCfg {
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES, TX_BYTES = STAGE_BYTES * CG;
     static constexpr int BOX_BYTES = 64 * BK * 2;  // operand with its rows contiguous: 64 of them by BK
     static constexpr int COLS = BN / 2;            // columns of an epilogue warp
-    // Staging of a warp: buffers of 32 rows x 128 bytes for D (and aux before it), enough for its
-    // part of a 16-bit tile, and one for the sum before the activation.
-    static constexpr int EPI_BUF = 32 * 128, BUFS = BN / 128;
-    static constexpr int WARP_BYTES = (BUFS + PRE) * EPI_BUF;
-    static constexpr int EPI_BYTES = EPI_WARPS * WARP_BYTES;
-    static constexpr int BIAS_BYTES = EPI_WARPS * COLS * 4;
+    // Staging of a warp: one or two buffers of 32 rows x 128 bytes for D (and aux before it), and one
+    // for the sum before the activation.  A buffer for all warps costs the ring a stage: two pay off
+    // with short K loops alone, where the epilogue's latency shows (see the host).
+    static constexpr int EPI_BUF = 32 * 128, MAX_BUFS = 2;
     static constexpr int TMEM_COLS = 2 * BN;
     static constexpr int BAR_BYTES = 512;
-    static constexpr int FIXED_BYTES = 1024 + EPI_BYTES + BIAS_BYTES + BAR_BYTES;
-    static constexpr int STAGES = (kSmemLimit - FIXED_BYTES) / STAGE_BYTES;
-    static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * STAGE_BYTES;
-    static_assert(STAGES >= 2, "ring too shallow");
-    static_assert((2 * STAGES + 5 + EPI_WARPS * BUFS) * 8 + 16 <= BAR_BYTES, "barrier region");
+    static constexpr int MAX_STAGES = 8;
+    static constexpr int smem_bytes(int stages, int bufs) {
+        return 1024 + stages * STAGE_BYTES + EPI_WARPS * (bufs + PRE) * EPI_BUF + BAR_BYTES;
+    }
+    static constexpr int stages(int bufs) {
+        const int n = (kSmemLimit - smem_bytes(0, bufs)) / STAGE_BYTES;
+        return n < MAX_STAGES ? n : MAX_STAGES;
+    }
+    static_assert((2 * MAX_STAGES + 5 + EPI_WARPS * MAX_BUFS) * 8 + 8 <= BAR_BYTES, "barrier region");
 };
 
 // Shared-memory descriptor of an operand tile with its rows (columns of D for B) contiguous: boxes
@@ -89,11 +94,19 @@ __device__ __forceinline__ uint32_t staged(uint32_t stage, int r, int b) {
 }
 
 // A warp moves `rows` rows of `left` <= 128 bytes between global memory (pitch in bytes) and swizzled
-// staging, lanes along the rows, in units of `unit` = 4 or 2 bytes (the alignment of the rows).
-// Where TMA cannot: a subtile that crosses N, rows that start off 16-byte boundaries.
+// staging, lanes along the rows, in units of `unit` = 16, 4 or 2 bytes (the alignment of the rows; 16
+// where `left` is a multiple too).  Where TMA cannot: a subtile that is cut off by N or by the tile's
+// width, rows that start off 16-byte boundaries.
 __device__ __forceinline__ void stage_rows_in(const char *src, int64_t pitch, int rows, int left, int unit,
                                               uint32_t stage, int lane) {
-    if (unit >= 4) {
+    if (unit == 16 && left % 16 == 0) {
+        const int per = left / 16;
+        for (int i = lane; i < rows * per; i += 32) {
+            const int r = i / per, b = (i - r * per) * 16;
+            const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(src + r * pitch + b));
+            st_shared_v4(staged(stage, r, b), v.x, v.y, v.z, v.w);
+        }
+    } else if (unit >= 4) {
         const int b = lane * 4;
 #pragma unroll 8
         for (int r = 0; r < rows; ++r) {
@@ -117,7 +130,13 @@ __device__ __forceinline__ void stage_rows_in(const char *src, int64_t pitch, in
 }
 __device__ __forceinline__ void stage_rows_out(char *dst, int64_t pitch, int rows, int left, int unit, uint32_t stage,
                                                int lane) {
-    if (unit >= 4) {
+    if (unit == 16 && left % 16 == 0) {
+        const int per = left / 16;
+        for (int i = lane; i < rows * per; i += 32) {
+            const int r = i / per, b = (i - r * per) * 16;
+            *reinterpret_cast<uint4 *>(dst + r * pitch + b) = ld_shared_v4(staged(stage, r, b));
+        }
+    } else if (unit >= 4) {
         const int b = lane * 4;
 #pragma unroll 8
         for (int r = 0; r < rows; ++r) {
@@ -168,18 +187,18 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *const gbase = smem_raw + (base - raw);
+    const uint32_t stages = static_cast<uint32_t>(p.stages), bufs = static_cast<uint32_t>(p.bufs);
     const uint32_t s_a = base;
-    const uint32_t s_b = s_a + C::STAGES * C::A_BYTES;
-    const uint32_t s_epi = s_b + C::STAGES * C::B_BYTES;
-    const uint32_t s_bias = s_epi + C::EPI_BYTES;
-    const uint32_t s_bar = s_bias + C::BIAS_BYTES;
+    const uint32_t s_b = s_a + stages * C::A_BYTES;
+    const uint32_t s_epi = s_b + stages * C::B_BYTES;
+    const uint32_t s_bar = s_epi + C::EPI_WARPS * (bufs + PRE) * C::EPI_BUF;
     auto full = [&](uint32_t s) { return s_bar + 8u * s; };
-    auto empty = [&](uint32_t s) { return s_bar + 8u * (C::STAGES + s); };
-    auto tfull = [&](uint32_t a) { return s_bar + 8u * (2 * C::STAGES + a); };
-    auto tempty = [&](uint32_t a) { return s_bar + 8u * (2 * C::STAGES + 2 + a); };
-    const uint32_t mma_done = s_bar + 8u * (2 * C::STAGES + 4);
-    auto aux_full = [&](uint32_t j, uint32_t b) { return s_bar + 8u * (2 * C::STAGES + 5 + j * C::BUFS + b); };
-    const uint32_t tail = s_bar + 8u * (2 * C::STAGES + 5 + C::EPI_WARPS * C::BUFS);
+    auto empty = [&](uint32_t s) { return s_bar + 8u * (stages + s); };
+    auto tfull = [&](uint32_t a) { return s_bar + 8u * (2 * stages + a); };
+    auto tempty = [&](uint32_t a) { return s_bar + 8u * (2 * stages + 2 + a); };
+    const uint32_t mma_done = s_bar + 8u * (2 * stages + 4);
+    auto aux_full = [&](uint32_t j, uint32_t b) { return s_bar + 8u * (2 * stages + 5 + j * C::MAX_BUFS + b); };
+    const uint32_t tail = s_bar + 8u * (2 * stages + 5 + C::EPI_WARPS * C::MAX_BUFS);
     volatile uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(gbase + (tail - base));
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(gbase + (tail - base) + 4);
 
@@ -194,7 +213,7 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
         prefetch_tmap(&tmB);
     }
     if (warp == 3 && lane == 0) {
-        for (int s = 0; s < C::STAGES; ++s) {
+        for (uint32_t s = 0; s < stages; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
         }
@@ -203,7 +222,7 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
             mbar_init(tempty(a), C::EPI_WARPS * CG);
         }
         mbar_init(mma_done, 1);
-        for (int i = 0; i < C::EPI_WARPS * C::BUFS; ++i) mbar_init(aux_full(0, i), 1);
+        for (int i = 0; i < C::EPI_WARPS * C::MAX_BUFS; ++i) mbar_init(aux_full(0, i), 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -231,13 +250,13 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
         for (int32_t u = first; u < p.num_units && alive; u += step) {
             const LinUnit w = lin_unit<C>(u, p);
             const int32_t a_row = w.mb * C::TILE_M + static_cast<int32_t>(rank) * C::BM;
-            const int32_t b_row = w.nb * BN + static_cast<int32_t>(rank) * C::B_ROWS;
+            const int32_t b_row = w.nb * p.bn + static_cast<int32_t>(rank) * (p.bn / CG);
             for (int32_t kb = 0; kb < p.num_kb; ++kb) {
                 if (!wait_phase(empty(stage), phase ^ 1u, abort_flag, p, WAIT_PRODUCER_EMPTY)) {
                     alive = false;
                     break;
                 }
-                if (rank == 0 && leader) mbar_arrive_expect_tx(full(stage), C::TX_BYTES);
+                if (rank == 0 && leader) mbar_arrive_expect_tx(full(stage), p.tx_bytes);
                 const uint32_t fb = CG == 2 ? mapa(full(stage), 0) : full(stage);
                 auto load = [&](uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y) {
                     if constexpr (CG == 1)
@@ -256,14 +275,15 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
                     }
                     if (p.b_mn) {
 #pragma unroll
-                        for (int c = 0; c < C::B_ROWS / 64; ++c) load(db + c * C::BOX_BYTES, &tmB, b_row + 64 * c, k);
+                        for (int c = 0; c < C::B_ROWS / 64; ++c)
+                            if (64 * c * CG < p.bn) load(db + c * C::BOX_BYTES, &tmB, b_row + 64 * c, k);
                     } else {
                         load(db, &tmB, k, b_row);
                     }
                 }
                 __syncwarp();
                 ++issued;
-                if (++stage == C::STAGES) {
+                if (++stage == stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
@@ -271,15 +291,15 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
         }
         // every load has landed (seen on the even CTA's barriers) and every stage is released
         if (rank == 0) {
-            const uint32_t n = issued < C::STAGES ? issued : C::STAGES;
+            const uint32_t n = issued < stages ? issued : stages;
             for (uint32_t i = 1; i <= n; ++i) {
                 const uint32_t b = issued - i;
-                wait_drain(full(b % C::STAGES), (b / C::STAGES) & 1u, abort_flag, p);
+                wait_drain(full(b % stages), (b / stages) & 1u, abort_flag, p);
             }
         }
-        for (int i = 0; i < C::STAGES; ++i) {
+        for (uint32_t i = 0; i < stages; ++i) {
             if (!wait_drain(empty(stage), phase ^ 1u, abort_flag, p)) break;
-            if (++stage == C::STAGES) {
+            if (++stage == stages) {
                 stage = 0;
                 phase ^= 1u;
             }
@@ -290,7 +310,7 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
         // The whole warp runs the loop, one elected lane issues.
         if (rank == 0) {
             const bool leader = elect_one();
-            const uint32_t idesc = p.idesc | (uint32_t(BN >> 3) << 17) | (uint32_t((C::BM * CG) >> 4) << 24);
+            const uint32_t idesc = p.idesc | (uint32_t(p.bn >> 3) << 17) | (uint32_t((C::BM * CG) >> 4) << 24);
             // steps of a start address for K = 16, in 16-byte units: 32 bytes along a K-major row, or
             // 16 rows of 128 bytes
             const uint32_t a_step = p.a_mn ? (16 * 128) >> 4 : 32 >> 4, b_step = p.b_mn ? (16 * 128) >> 4 : 32 >> 4;
@@ -319,7 +339,7 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
                             mma_commit_pair(empty(stage), 0x3);
                     }
                     __syncwarp();
-                    if (++stage == C::STAGES) {
+                    if (++stage == stages) {
                         stage = 0;
                         phase ^= 1u;
                     }
@@ -352,48 +372,42 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
         // --------------------------------------------------------- epilogue
         const int j = warp - kRoleWarps;
         const int q = j & 3, h = j >> 2;
-        const uint32_t stg = s_epi + static_cast<uint32_t>(j) * C::WARP_BYTES;
-        const uint32_t stg_pre = stg + C::BUFS * C::EPI_BUF;
-        const uint32_t bias_at = s_bias + static_cast<uint32_t>(j) * (C::COLS * 4);
+        const uint32_t stg = s_epi + static_cast<uint32_t>(j) * (bufs + PRE) * C::EPI_BUF;
+        const uint32_t stg_pre = stg + bufs * C::EPI_BUF;
         const bool f32 = p.out == OUT_F32;
-        const int sub = f32 ? 32 : 64, subs = C::COLS / sub, esize = f32 ? 4 : 2;
+        const int sub = f32 ? 32 : 64, esize = f32 ? 4 : 2;
+        const int cols = h ? p.bn - C::COLS : C::COLS;  // of this warp (of the kernel's tile the host may use fewer)
         const bool aux_tma = p.aux != nullptr && tma_d;
+        // until the store that last used the next buffer has read it
+        auto wait_store = [&] {
+            if (bufs == 1)
+                bulk_wait_read<0>();
+            else
+                bulk_wait_read<1>();
+        };
         uint32_t acc = 0, acc_phase = 0, aux_phase = 0;  // aux_phase: bit b, parity of buffer b's next load
         uint32_t aux_pending = 0;                        // bit b: a load into buffer b has not been waited for
         bool alive = true;
         for (int32_t u = first; u < p.num_units && alive; u += step) {
             const LinUnit w = lin_unit<C>(u, p);
             const int32_t row0 = w.mb * C::TILE_M + static_cast<int32_t>(rank) * C::BM + 32 * q;
-            const int32_t col0 = w.nb * BN + C::COLS * h;
-            const bool work = row0 < p.M && col0 < p.N;
+            const int32_t col0 = w.nb * p.bn + C::COLS * h;
+            const int32_t col_end = min(col0 + cols, p.N);
+            const bool work = row0 < p.M && col0 < col_end;
             auto load_aux = [&](int s) {  // lane 0, by TMA; the buffer is free
-                mbar_arrive_expect_tx(aux_full(j, s % C::BUFS), C::EPI_BUF);
-                tma_load_3d(stg + (s % C::BUFS) * C::EPI_BUF, &tmAux, aux_full(j, s % C::BUFS), col0 + s * sub, row0, w.z);
+                const uint32_t b = static_cast<uint32_t>(s) & (bufs - 1);
+                mbar_arrive_expect_tx(aux_full(j, b), C::EPI_BUF);
+                tma_load_3d(stg + b * C::EPI_BUF, &tmAux, aux_full(j, b), col0 + s * sub, row0, w.z);
             };
             if (work) {
-                if (p.bias) {
-                    // the columns' bias, for reads that all lanes make at once; zeros without one
-                    __syncwarp();  // the last tile's have been read
-#pragma unroll
-                    for (int i = 0; i < C::COLS / 32; ++i) {
-                        const int32_t c = col0 + 32 * i + lane;
-                        float b = 0.f;
-                        if (c < p.N)
-                            b = p.bias_f32 ? __ldg(static_cast<const float *>(p.bias) + c)
-                                           : __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t *>(p.bias) + c)) << 16);
-                        st_shared_f32(bias_at + (32 * i + lane) * 4, b);
-                    }
-                }
                 if (aux_tma) {
                     __syncwarp();
                     if (lane == 0) {
                         bulk_wait_read<0>();  // the stores that used the buffers have read them
                         fence_proxy_async_smem();
-                        for (int s = 0; s < C::BUFS && s < subs; ++s)
-                            if (col0 + s * sub < p.N) load_aux(s);
+                        for (int s = 0; s < static_cast<int>(bufs) && col0 + s * sub < col_end; ++s) load_aux(s);
                     }
-                    for (int s = 0; s < C::BUFS && s < subs; ++s)
-                        if (col0 + s * sub < p.N) aux_pending |= 1u << s;
+                    for (int s = 0; s < static_cast<int>(bufs) && col0 + s * sub < col_end; ++s) aux_pending |= 1u << s;
                 }
                 __syncwarp();
             }
@@ -402,7 +416,7 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
             if (!__shfl_sync(0xffffffffu, ok, 0)) break;
             tc_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * BN + C::COLS * h;
-            const int chunks = !work ? 0 : min(C::COLS, p.N - col0 + 31) / 32;
+            const int chunks = !work ? 0 : (col_end - col0 + 31) / 32;
             // the accumulator is read: back to the MMA issuer
             auto release = [&] {
                 tc_fence_before();
@@ -420,16 +434,16 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(taddr + 32 * c, v);
                 const int s = 32 * c / sub;
-                const uint32_t buf = s % C::BUFS, at = stg + buf * C::EPI_BUF;
+                const uint32_t buf = static_cast<uint32_t>(s) & (bufs - 1), at = stg + buf * C::EPI_BUF;
                 const int32_t col = col0 + s * sub;  // of the subtile
                 const int piece = f32 ? 0 : (c & 1) * 4;  // 16-byte units of the chunk within the staged row
                 const bool head = f32 || (c & 1) == 0, done = f32 || (c & 1) == 1 || c + 1 == chunks;
-                const bool tma = tma_d && col + sub <= p.N;
-                const int rows = min(32, p.M - row0), left = min(p.N - col, sub) * esize;
+                const bool tma = tma_d && col + sub <= col_end;
+                const int rows = min(32, p.M - row0), left = min(col_end - col, sub) * esize;
                 if (head) {
                     // the subtile's buffer: free, or holding aux
                     if (aux_tma) {
-                        if (s >= C::BUFS) {
+                        if (s >= static_cast<int>(bufs)) {
                             __syncwarp();
                             if (lane == 0) {
                                 bulk_wait_read<0>();
@@ -446,7 +460,7 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
                         aux_phase ^= 1u << buf;
                         aux_pending &= ~(1u << buf);
                     } else {
-                        if (lane == 0) bulk_wait_read<C::BUFS - 1>();
+                        if (lane == 0) wait_store();
                         __syncwarp();
                         if (p.aux) {
                             stage_rows_in(static_cast<const char *>(p.aux) +
@@ -456,7 +470,7 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
                         }
                     }
                     if (PRE && aux_tma) {
-                        if (lane == 0) bulk_wait_read<C::BUFS - 1>();  // the other buffer's store, and pre's before it
+                        if (lane == 0) wait_store();  // the other buffer's store, and pre's before it
                         __syncwarp();
                     }
                 }
@@ -466,13 +480,36 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = p.num_kb > 0 ? p.alpha * __uint_as_float(v[i]) : 0.f;
                 if (p.bias) {
+                    // the same address in all lanes
+                    const int32_t c0 = col0 + 32 * c;
+                    if (p.bias_vec && c0 + 32 <= p.N) {
+                        if (p.bias_f32) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint4 b = ld_shared_v4(bias_at + (32 * c + 4 * i) * 4);
-                        x[4 * i] += __uint_as_float(b.x);
-                        x[4 * i + 1] += __uint_as_float(b.y);
-                        x[4 * i + 2] += __uint_as_float(b.z);
-                        x[4 * i + 3] += __uint_as_float(b.w);
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 b = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.bias) + c0) + i);
+                                x[4 * i] += b.x;
+                                x[4 * i + 1] += b.y;
+                                x[4 * i + 2] += b.z;
+                                x[4 * i + 3] += b.w;
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint4 b = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias) + c0) + i);
+                                const uint32_t b4[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    x[8 * i + 2 * e] += __uint_as_float(b4[e] << 16);
+                                    x[8 * i + 2 * e + 1] += __uint_as_float(b4[e] & 0xffff0000u);
+                                }
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c0 + i < p.N)
+                                x[i] += p.bias_f32 ? __ldg(static_cast<const float *>(p.bias) + c0 + i)
+                                                   : __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t *>(p.bias) + c0 + i)) << 16);
                     }
                 }
                 // x into this lane's row of a staging buffer
@@ -495,13 +532,24 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
                             st_shared_v4(row_at + (((piece + i) ^ (lane & 7)) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2],
                                          o[4 * i + 3]);
                         if (p.sym && w.nb > w.mb) {
-                            // the entry's mirror image: a column of this warp's is 32 consecutive values there
-                            uint16_t *const m = static_cast<uint16_t *>(p.D) + w.z * p.d_matrix + row0 + lane;
-                            const int32_t c0 = col0 + 32 * c;
+                            // The entry's mirror image: a column of this warp's is 32 consecutive values
+                            // there.  Lanes 2i and 2i + 1 exchange halves, so that an even lane holds two rows
+                            // of an even column, an odd one of the column behind it, and stores them at once.
+                            const int32_t r = row0 + (lane & ~1), c0 = col0 + 32 * c + (lane & 1);
+                            uint16_t *m = static_cast<uint16_t *>(p.D) + w.z * p.d_matrix + c0 * p.ldd + r;
+                            const int32_t many = p.M - r;  // rows there: rows of D, which is square, are even apart
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (row0 + lane < p.M && c0 + i < p.N)
-                                    m[static_cast<int64_t>(c0 + i) * p.ldd] = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
+                            for (int i = 0; i < 16; ++i) {
+                                const uint32_t got = __shfl_xor_sync(0xffffffffu, o[i], 1);
+                                const uint32_t two = lane & 1 ? __byte_perm(got, o[i], 0x7632) : __byte_perm(o[i], got, 0x5410);
+                                if (c0 + 2 * i < p.N) {
+                                    if (many >= 2)
+                                        *reinterpret_cast<uint32_t *>(m) = two;
+                                    else if (many == 1)
+                                        *m = static_cast<uint16_t>(two);
+                                }
+                                m += 2 * p.ldd;
+                            }
                         }
                     }
                 };
@@ -573,7 +621,7 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
             }
         }
         // loads of aux that a given-up wait left in flight
-        for (uint32_t b = 0; b < C::BUFS; ++b)
+        for (uint32_t b = 0; b < bufs; ++b)
             if ((aux_pending >> b) & 1u) wait_drain(aux_full(j, b), (aux_phase >> b) & 1u, abort_flag, p);
         if (lane == 0) bulk_wait<0>();
         __syncwarp();

@@ -16,14 +16,14 @@ cudaError_t linear_launch(const LinLaunch &L) {
     const int dev = current_device();
     const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
     if (!bit || !(prepared.load(std::memory_order_acquire) & bit)) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
         if (e != cudaSuccess) return e;
         if (bit) prepared.fetch_or(bit, std::memory_order_acq_rel);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(L.grid), 1, 1);
     cfg.blockDim = dim3(C::THREADS, 1, 1);
-    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.dynamicSmemBytes = C::smem_bytes(L.p.stages, L.p.bufs);
     cfg.stream = L.stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -40,11 +40,16 @@ cudaError_t linear_launch(const LinLaunch &L) {
     return cudaLaunchKernelEx(&cfg, kernel, L.a, L.b, L.d, L.aux, L.pre, L.p);
 }
 
+template <int BN, int CG, int PRE>
+int linear_stages(int bufs) {
+    return LinCfg<BN, CG, PRE>::stages(bufs);
+}
+
 }  // namespace
 }  // namespace ts
 
-#define TS_LINEAR_VARIANT(NAME, BN, CG, PRE)                                \
-    namespace ts {                                                          \
-    extern const LinVariant NAME;                                           \
-    const LinVariant NAME = {BN, CG, PRE, &linear_launch<BN, CG, PRE>};     \
+#define TS_LINEAR_VARIANT(NAME, BN, CG, PRE)                                                               \
+    namespace ts {                                                                                         \
+    extern const LinVariant NAME;                                                                          \
+    const LinVariant NAME = {BN, CG, PRE, &linear_launch<BN, CG, PRE>, &linear_stages<BN, CG, PRE>};       \
     }

@@ -20,6 +20,8 @@ struct LinParams {
     int32_t M, N;                     // of D
     int32_t tiles_m, tiles_n, num_kb;
     int32_t num_units, tiles_per_matrix;  // all matrices of a batch; one matrix (its upper triangle with `sym`)
+    int32_t bn, tx_bytes;             // columns of a tile; bytes of a stage's loads (both CTAs of a pair)
+    int32_t bufs;                     // staging buffers of an epilogue warp
     int32_t raster_group;
     FastDiv div_group_tiles, div_group_rows, div_last_rows;  // sym: the first divides by tiles_n + 1
     FastDiv div_matrix;
@@ -29,7 +31,8 @@ struct LinParams {
     int32_t aux_type;                 // of aux, of the same size as out
     int32_t act;                      // of the forward epilogue, or whose slope the backward one multiplies by
     int32_t slope;                    // 0: D = act(alpha * acc + bias) + beta * aux; 1: D = alpha * acc * act'(aux)
-    int32_t split, stages;            // the split kernel: CTAs of a cluster that share K, operand stages
+    int32_t stages;                   // of the operand ring
+    int32_t split;                    // the split kernel: CTAs of a cluster that share K
     int32_t sym;                      // 1: D is symmetric: tiles above the diagonal are stored twice
     int32_t store_bytes;              // 16, 4 or 2: what the bases and rows of D, aux and pre are aligned to
     float alpha, beta;
@@ -55,6 +58,7 @@ struct LinLaunch {
 struct LinVariant {
     int bn, cg, pre;
     cudaError_t (*launch)(const LinLaunch &);
+    int (*stages)(int bufs);
 };
 
 constexpr int kMaxSplit = 8;  // most CTAs that share a tile's K: the portable cluster size
