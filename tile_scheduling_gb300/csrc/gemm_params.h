@@ -21,6 +21,7 @@ enum : int32_t {
     WAIT_SCALES = 10,
     WAIT_PROMOTION = 11,
     WAIT_AUX = 12,
+    WAIT_GRID = 13,
 };
 
 // Device status word (library-owned, one per device):

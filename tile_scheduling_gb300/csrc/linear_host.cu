@@ -54,35 +54,42 @@ ts_status output_map(CUtensorMap *m, const void *ptr, int esize, int64_t M, int6
 
 }  // namespace
 
-ts_status linear_product(const LinCall &c) {
-    const int sms_ = device_sms(current_device());
-    if (sms_ <= 0) return fail(TS_ERR_CUDA, "cannot query the SM count");
-    const int64_t sms = sms_, nkb = cdiv(c.K, 64);
-    int tile = c.tile;
-    auto tri = [](int64_t n) { return n * (n + 1) / 2; };
+namespace {
+
+int64_t triangle(int64_t n) { return n * (n + 1) / 2; }
+
+// How a product runs: a tile of a persistent CTA or pair with `bn` columns, or (sv) a tile whose K is
+// shared by a cluster of `split` CTAs, `ctas` of them on an SM.
+struct LinPlan {
+    int bn, cg;
+    const SplitVariant *sv;
+    int split, ctas;
+    int64_t cycles;  // an estimate, from one launch to the next
+};
+
+LinPlan plan_product(const LinCall &c, int64_t sms) {
+    const int64_t nkb = cdiv(c.K, 64);
     const int64_t m1 = cdiv(c.M, 128), m2 = cdiv(c.M, 256), n1 = cdiv(c.N, 128), n2 = cdiv(c.N, 256);
-    const int64_t u1 = c.batch * (c.sym ? tri(n1) : m1 * n1), u2 = c.batch * m1 * n2,
-                  u3 = c.batch * (c.sym ? tri(n2) : m2 * n2);
+    const int64_t u1 = c.batch * (c.sym ? triangle(n1) : m1 * n1), u3 = c.batch * (c.sym ? triangle(n2) : m2 * n2);
+    LinPlan pl{128, 1, nullptr, 1, 1, INT64_MAX};
     // Few tiles: K shared by a cluster, the fewest cycles of a cluster size whose clusters all run at once.
-    const SplitVariant *sv = nullptr;
-    int split = 1, split_ctas = 1;
-    int64_t best = INT64_MAX;
-    if (tile == TS_TILE_AUTO && nkb > 0 && c.max_workers == 0) {
-        // Measured, cycles of a K block with all of a CTA's loads in flight and what is left without one:
-        // 512 x 512 x 768 with a bf16 output by 1 / 2 / 4 CTAs a tile 8.1 / 6.8 / 6.1 us, by a persistent
-        // CTA 6.5; 257 x 1023 x 777 9.6 / 7.5 / 6.8 and 8.2.
-        auto consider = [&](const SplitVariant &v, int64_t units, int64_t fixed) {
-            for (int k = v.swap ? 1 : 2; k <= kMaxSplit && k <= nkb; k *= 2) {
+    if (c.tile == TS_TILE_AUTO && nkb > 0 && c.max_workers == 0) {
+        // Cycles fitted to measurements: a K block, CTAs to launch, and the rest.  512 x 512 x 768 with a
+        // bf16 output by 2 / 4 CTAs a tile 6.7 / 5.4 us, by a persistent CTA 6.6; 768 x 768 x 768 6.7 / 6.8
+        // and 6.8; 1001 x 1001 x 1001 by 2 8.3 and 9.4; 128 x 4096 x 4096 10.7 / 9.1 and 17.1.  A gelu adds
+        // 2 us to the persistent CTA's epilogue and 0.5 to 0.9 here, a residual 0.5 and 0.4 to 0.8.
+        auto consider = [&](const SplitVariant &v, int64_t units, const int64_t (&fixed)[4]) {
+            for (int k = v.swap ? 1 : 2, i = v.swap ? 0 : 1; k <= kMaxSplit && k <= nkb; k *= 2, ++i) {
                 const int ctas = v.swap && units * k > sms ? 2 : 1;
                 if (units * k > ctas * sms || (k > 1 && v.clusters(k, ctas) < units)) break;
-                const int64_t t = cdiv(nkb, k) * 340 * ctas + fixed;
-                if (t < best) best = t, sv = &v, split = k, split_ctas = ctas;
+                const int64_t t = cdiv(nkb, k) * 400 * ctas + 25 * units * k + fixed[i] + (c.act ? 1000 : 0) + (c.aux ? 900 : 0);
+                if (t < pl.cycles) pl.cycles = t, pl.sv = &v, pl.split = k, pl.ctas = ctas;
             }
         };
-        consider(split_128, u1, 10700);
+        consider(split_128, u1, {0, 9350, 7500, 8200});
         // an operand with its rows contiguous comes in boxes of 64
         if (!c.sym && c.batch == 1 && c.M <= 64)
-            consider(c.M <= 32 && !c.a_mn ? split_swap_32 : split_swap_64, n1, 8000);
+            consider(c.M <= 32 && !c.a_mn ? split_swap_32 : split_swap_64, n1, {6000, 6000, 6000, 6000});
     }
     // Columns of a 256-column tile: the width whose waves of workers take the fewest cycles in all.
     // With B's rows contiguous only whole boxes of 64 of them for each CTA: 4096 x 2048 x 2048 on pairs
@@ -99,17 +106,36 @@ ts_status linear_product(const LinCall &c) {
     };
     int64_t w2, w3;
     const int64_t bn2 = width(m1, sms, 1, w2), bn3 = width(m2, sms / 2, 2, w3);
+    // The tile with the fewest cycles: waves of workers times what a K block of a tile takes, and the rest,
+    // in which the last epilogue shows.
+    const int64_t slow = (c.act ? 3000 : 0) + (c.aux ? 900 : 0) + (c.sym ? 5000 : 0);
+    const int64_t c1 = cdiv(u1, sms) * nkb * 340 + 8300 + slow;
+    const int64_t c2 = w2 * nkb * 590 * (bn2 + kWidthOverhead) / (256 + kWidthOverhead) + 9100 + slow;
+    const int64_t c3 = (c.sym ? cdiv(u3, sms / 2) * nkb * 520 : w3 * nkb * 520 * (bn3 + kWidthOverhead) / (256 + kWidthOverhead)) +
+                       9800 + slow;
+    int tile = c.tile;
     if (tile == TS_TILE_AUTO) {
-        // The tile with the fewest cycles: waves of workers times what a tile takes.
-        const int64_t c1 = cdiv(u1, sms) * (nkb * 340) + 8300;
-        const int64_t c2 = w2 * nkb * 540 * (bn2 + kWidthOverhead) / (256 + kWidthOverhead) + 9100;
-        const int64_t c3 = (c.sym ? cdiv(u3, sms / 2) * nkb * 520 : w3 * nkb * 520 * (bn3 + kWidthOverhead) / (256 + kWidthOverhead)) + 9800;
         const int64_t least = std::min(c1, std::min(c.sym ? c1 : c2, c3));
-        if (best >= least) sv = nullptr;
+        if (pl.cycles < least) return pl;
         tile = least == c1 ? TS_TILE_128x128 : least == c3 ? TS_TILE_256x256_2CTA : TS_TILE_128x256;
     }
-    const int cg = tile == TS_TILE_256x256_2CTA ? 2 : 1;
-    int bn = tile == TS_TILE_128x128 ? 128 : static_cast<int>(cg == 2 ? bn3 : bn2);
+    pl.sv = nullptr;
+    pl.bn = static_cast<int>(tile == TS_TILE_128x128 ? 128 : tile == TS_TILE_256x256_2CTA ? bn3 : bn2);
+    pl.cg = tile == TS_TILE_256x256_2CTA ? 2 : 1;
+    pl.cycles = tile == TS_TILE_128x128 ? c1 : tile == TS_TILE_256x256_2CTA ? c3 : c2;
+    return pl;
+}
+
+}  // namespace
+
+int64_t linear_cycles(const LinCall &c) { return plan_product(c, std::max(1, device_sms(current_device()))).cycles; }
+
+ts_status linear_product(const LinCall &c) {
+    const int64_t sms = device_sms(current_device()), nkb = cdiv(c.K, 64);
+    if (sms <= 0) return fail(TS_ERR_CUDA, "cannot query the SM count");
+    const LinPlan pl = plan_product(c, sms);
+    const SplitVariant *const sv = pl.sv;
+    const int bn = pl.bn, cg = pl.cg;
     const LinVariant *v = find_linear(bn > 128 ? 256 : 128, cg, c.pre ? 1 : 0);
     if (!v) return fail(TS_ERR_UNSUPPORTED, "no compiled variant");
 
@@ -118,7 +144,7 @@ ts_status linear_product(const LinCall &c) {
     LinParams &p = L.p;
     const bool swap = sv && sv->swap;
     const int64_t tiles_m = swap ? 1 : cdiv(c.M, sv ? 128 : 128 * cg), tiles_n = cdiv(c.N, sv ? 128 : bn);
-    const int64_t per = c.sym ? tri(tiles_n) : tiles_m * tiles_n, units = per * c.batch;
+    const int64_t per = c.sym ? triangle(tiles_n) : tiles_m * tiles_n, units = per * c.batch;
     if (units * cg > 0x7fffffffLL) return fail(TS_ERR_UNSUPPORTED, "too many output tiles");
     const int esize = c.out == OUT_F32 ? 4 : 2;
     p.store_bytes = 2;
@@ -190,9 +216,9 @@ ts_status linear_product(const LinCall &c) {
     p.status = status;
     L.stream = c.stream;
     if (sv) {
-        p.split = split;
-        p.stages = sv->stages(split, split_ctas);
-        L.grid = units * split;
+        p.split = pl.split;
+        p.stages = sv->stages(pl.split, pl.ctas);
+        L.grid = units * pl.split;
         const cudaError_t e = sv->launch(L);
         return e == cudaSuccess ? TS_OK : cuda_fail(e, "split product launch");
     }

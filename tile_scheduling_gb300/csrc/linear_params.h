@@ -93,6 +93,8 @@ struct LinCall {
 };
 // Plans and launches a product whose arguments have been checked.
 ts_status linear_product(const LinCall &c);
+// An estimate of its cycles, from one launch to the next.
+int64_t linear_cycles(const LinCall &c);
 
 // The forward product of at most so many rows of x runs in a kernel of its own.
 constexpr int kFewTokens = 8;

@@ -21,199 +21,28 @@
 
 #include "common.h"
 #include "linear_params.h"
+#include "orth.cuh"
 #include "ptx.cuh"
 
 namespace ts {
 namespace {
 
-constexpr float kOrthScale = 4096.f;
 constexpr int kOrthThreads = 256;
-constexpr int64_t kOrthChunks = 608;  // CTAs that share a matrix, at most: four for each SM
+constexpr int64_t kOrthChunks = 1216;  // CTAs that share the matrices, about: eight for each SM
 
-struct OrthParams {
-    const void *G;
-    int64_t ldg, g_matrix;
-    void *X;              // fp16 times kOrthScale, or bf16 itself (no steps)
-    int64_t ldx, x_matrix;
-    float *partial;       // [batch][chunks][3]
-    int64_t R, C, vecs;   // vecs: vectors of a row
-    FastDiv div_vecs;
-    int32_t chunks, to_bf16;
-    float eps;
-};
 
-template <class T, int V>
-__device__ __forceinline__ void load_row(const T *p, int count, float (&f)[V]) {
-    if (V > 1 && count == V) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (sizeof(T) == 4) {
-                f[i % V] = __uint_as_float(w[i]);
-            } else {
-                f[2 * i % V] = __uint_as_float(w[i] << 16);
-                f[(2 * i + 1) % V] = __uint_as_float(w[i] & 0xffff0000u);
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        f[i] = 0.f;
-        if (i < count) {
-            if constexpr (sizeof(T) == 4)
-                f[i] = __ldg(p + i);
-            else
-                f[i] = __uint_as_float(uint32_t(__ldg(p + i)) << 16);
-        }
-    }
-}
-
-// f(values, row, first column, how many) for the vectors of rows [r0, r1), four of a thread in flight.
-template <class T, int V, class F>
-__device__ __forceinline__ void each_vector(const OrthParams &p, const T *g, int64_t r0, int64_t r1, F &&f) {
-    constexpr int UN = 4;
-    const int64_t total = (r1 - r0) * p.vecs;
-    for (int64_t i0 = threadIdx.x; i0 < total; i0 += UN * kOrthThreads) {
-        float v[UN][V];
-        int64_t r[UN], c[UN];
-        int count[UN];
-#pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            const int64_t i = i0 + u * kOrthThreads;
-            count[u] = 0;
-            if (i < total) {
-                // a CTA's share has fewer than 2^31 vectors (checked on the host)
-                const int32_t row = fast_div(static_cast<int32_t>(i), p.div_vecs);
-                r[u] = r0 + row;
-                c[u] = (i - row * p.vecs) * V;
-                count[u] = static_cast<int>(min(static_cast<int64_t>(V), p.C - c[u]));
-                load_row<T, V>(g + r[u] * p.ldg + c[u], count[u], v[u]);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < UN; ++u)
-            if (count[u]) f(v[u], r[u], c[u], count[u]);
-    }
-}
-
-// The block's sums of three values, in thread 0, in a fixed order.
-template <class T>
-__device__ __forceinline__ void block_sum3(T &a, T &b, T &c) {
-    __shared__ T s[3][kOrthThreads / 32];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, d);
-        b += __shfl_xor_sync(0xffffffffu, b, d);
-        c += __shfl_xor_sync(0xffffffffu, c, d);
-    }
-    if (threadIdx.x % 32 == 0) {
-        s[0][threadIdx.x / 32] = a;
-        s[1][threadIdx.x / 32] = b;
-        s[2][threadIdx.x / 32] = c;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0)
-        for (int w = 1; w < kOrthThreads / 32; ++w) {
-            a += s[0][w];
-            b += s[1][w];
-            c += s[2][w];
-        }
-}
-
-// Sums of squares in three ranges, after Blue ("A Portable Fortran Program to Find the Euclidean
-// Norm of a Vector", 1978): as they are, and scaled by 2^-70 and 2^70 for values whose squares
-// leave fp32's range.
 template <class T, bool VEC>
 __global__ void __launch_bounds__(kOrthThreads) orth_norm_kernel(const __grid_constant__ OrthParams p) {
-    constexpr int V = VEC ? 16 / sizeof(T) : 1;
     grid_dep_wait();
     grid_dep_launch();
-    const T *g = static_cast<const T *>(p.G) + blockIdx.y * p.g_matrix;
-    float mid = 0.f, big = 0.f, tiny = 0.f;
-    const int64_t r0 = p.R * blockIdx.x / p.chunks, r1 = p.R * (blockIdx.x + 1) / p.chunks;
-    each_vector<T, V>(p, g, r0, r1, [&](const float (&f)[V], int64_t, int64_t, int) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const float b = f[k] * 0x1p-70f, t = f[k] * 0x1p70f;
-            mid = fmaf(f[k], f[k], mid);
-            big = fmaf(b, b, big);
-            tiny = fmaf(t, t, tiny);
-        }
-    });
-    block_sum3(mid, big, tiny);
-    if (threadIdx.x == 0) {
-        float *const q = p.partial + (static_cast<int64_t>(blockIdx.y) * p.chunks + blockIdx.x) * 3;
-        q[0] = mid;
-        q[1] = big;
-        q[2] = tiny;
-    }
+    orth_norm<T, VEC, kOrthThreads>(p, blockIdx.y, blockIdx.x);
 }
 
-// X = G / (|G|_F + eps)
 template <class T, bool VEC>
 __global__ void __launch_bounds__(kOrthThreads) orth_scale_kernel(const __grid_constant__ OrthParams p) {
-    constexpr int V = VEC ? 16 / sizeof(T) : 1;
     grid_dep_wait();
     grid_dep_launch();
-    __shared__ double sums[3];
-    {
-        double mid = 0.0, big = 0.0, tiny = 0.0;
-        const float *q = p.partial + static_cast<int64_t>(blockIdx.y) * p.chunks * 3;
-        for (int c = threadIdx.x; c < p.chunks; c += kOrthThreads) {
-            mid += static_cast<double>(q[3 * c]);
-            big += static_cast<double>(q[3 * c + 1]);
-            tiny += static_cast<double>(q[3 * c + 2]);
-        }
-        block_sum3(mid, big, tiny);
-        if (threadIdx.x == 0) {
-            sums[0] = mid;
-            sums[1] = big;
-            sums[2] = tiny;
-        }
-        __syncthreads();
-    }
-    // the middle sum where it neither overflowed (then it is infinite) nor lost what is below
-    // 2^-75 (then it is small); a NaN stays one
-    double sq = sums[0];
-    if (sums[1] >= 0x1p-20)
-        sq = sums[1] * 0x1p140;
-    else if (sums[0] < 0x1p-60)
-        sq = sums[2] * 0x1p-140;
-    // a power of two apart, so that neither the norm's reciprocal nor the product leaves fp32's range
-    const double inv = 1.0 / (sqrt(sq) + static_cast<double>(p.eps));
-    int e;
-    const float f0 = static_cast<float>(frexp(inv, &e));
-    const int e1 = isfinite(inv) ? e / 2 : 0, e2 = isfinite(inv) ? e - e1 : 0;
-    const float s1 = f0 * (p.to_bf16 ? 1.f : kOrthScale) * exp2f(static_cast<float>(e1)), s2 = exp2f(static_cast<float>(e2));
-    const T *g = static_cast<const T *>(p.G) + blockIdx.y * p.g_matrix;
-    uint16_t *x = static_cast<uint16_t *>(p.X) + blockIdx.y * p.x_matrix;
-    const bool whole = (p.ldx % V) == 0 && (p.x_matrix % V) == 0 && reinterpret_cast<uintptr_t>(p.X) % (2 * V) == 0;
-    const int64_t r0 = p.R * blockIdx.x / gridDim.x, r1 = p.R * (blockIdx.x + 1) / gridDim.x;
-    each_vector<T, V>(p, g, r0, r1, [&](const float (&f)[V], int64_t r, int64_t c, int count) {
-        uint16_t o[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const float v = f[k] * s2 * s1;
-            o[k] = p.to_bf16 ? static_cast<uint16_t>(pack_bf16x2(__float_as_uint(v), 0u))
-                             : static_cast<uint16_t>(pack_f16x2(__float_as_uint(v), 0u));
-        }
-        uint16_t *const at = x + r * p.ldx + c;
-        if (V > 1 && whole && count == V) {
-            uint32_t w[(V + 1) / 2];
-#pragma unroll
-            for (int k = 0; k < V / 2; ++k) w[k] = o[2 * k] | (uint32_t(o[2 * k + 1]) << 16);
-            if constexpr (V == 8)
-                *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
-            else if constexpr (V == 4)
-                *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < V; ++k)
-                if (k < count) at[k] = o[k];
-        }
-    });
+    orth_scale<T, VEC, kOrthThreads>(p, blockIdx.y, blockIdx.x);
 }
 
 // Where the iteration's matrices lie in the workspace, in bytes.
@@ -223,7 +52,8 @@ struct OrthPlan {
     int64_t a() const { return 2 * x_bytes; }
     int64_t b() const { return 2 * x_bytes + n_bytes; }
     int64_t partial() const { return 2 * x_bytes + 2 * n_bytes; }
-    int64_t total() const { return partial() + partial_bytes; }
+    int64_t barrier() const { return partial() + partial_bytes; }
+    int64_t total() const { return barrier() + 256; }
 };
 
 OrthPlan plan_orth(int64_t batch, int64_t R, int64_t C, int steps) {
@@ -234,9 +64,107 @@ OrthPlan plan_orth(int64_t batch, int64_t R, int64_t C, int steps) {
     o.ldn = cdiv(o.n, 8) * 8;
     o.x_bytes = steps > 0 ? round(batch * R * o.ldx * 2) : 0;
     o.n_bytes = steps > 0 ? round(batch * o.n * o.ldn * 2) : 0;
-    o.chunks = std::max<int64_t>(1, std::min<int64_t>({kOrthChunks, R, cdiv(R * C, 8192)}));
+    o.chunks = std::max<int64_t>(1, std::min<int64_t>({cdiv(kOrthChunks, batch), R, cdiv(R * C, 8192)}));
     o.partial_bytes = round(batch * o.chunks * 3 * 4);
     return o;
+}
+
+// Product `which` of step i, of matrices that are 4096 times their value.
+LinCall orth_product(const OrthRun &r, int32_t i, int which) {
+    const bool tall = r.R > r.C, last = i + 1 == r.steps;
+    const int64_t x_matrix = r.R * r.ldx, n_matrix = r.n * r.ldn;
+    const void *X = r.X[i & 1];
+    LinCall c;
+    std::memset(&c, 0, sizeof c);
+    c.f16 = 1;
+    c.out = c.aux_type = OUT_F16;
+    c.batch = r.batch;
+    c.timeout_s = r.timeout_s;
+    c.stream = r.stream;
+    if (which < 2) {
+        c.sym = 1;
+        c.M = c.N = r.n;
+        c.ldd = r.ldn;
+        c.d_matrix = n_matrix;
+    }
+    if (which == 0) {  // A = X X^T
+        c.A = c.B = X;
+        c.lda = c.ldb = r.ldx;
+        c.a_matrix = c.b_matrix = x_matrix;
+        c.a_mn = c.b_mn = tall;
+        c.D = r.A;
+        c.K = tall ? r.R : r.C;
+        c.alpha = 1.f / kOrthScale;
+    } else if (which == 1) {  // B = b A + c A^2
+        c.A = c.B = c.aux = r.A;
+        c.lda = c.ldb = c.ld_aux = r.ldn;
+        c.a_matrix = c.b_matrix = c.aux_matrix = n_matrix;
+        c.D = r.B;
+        c.K = r.n;
+        c.alpha = r.c / kOrthScale;
+        c.beta = r.b;
+    } else {  // X = a X + B X, or a X + X B
+        c.A = tall ? X : r.B;
+        c.lda = tall ? r.ldx : r.ldn;
+        c.a_matrix = tall ? x_matrix : n_matrix;
+        c.B = tall ? r.B : X;
+        c.ldb = tall ? r.ldn : r.ldx;
+        c.b_matrix = tall ? n_matrix : x_matrix;
+        c.b_mn = !tall;
+        c.aux = X;
+        c.ld_aux = r.ldx;
+        c.aux_matrix = x_matrix;
+        c.D = last ? r.O : r.X[(i + 1) & 1];
+        c.ldd = last ? r.ldo : r.ldx;
+        c.d_matrix = last ? r.o_matrix : x_matrix;
+        c.M = r.R;
+        c.N = r.C;
+        c.K = r.n;
+        c.out = last ? OUT_BF16 : OUT_F16;
+        c.alpha = last ? 1.f / (kOrthScale * kOrthScale) : 1.f / kOrthScale;
+        c.beta = last ? r.a / kOrthScale : r.a;
+    }
+    return c;
+}
+
+// One launch where it takes fewer cycles than the chain, by the chain's estimates and this one of a step:
+// a phase some 3 us (the barrier, the first loads, the stores), a K block of a tile 360 cycles with 64
+// columns and 600 with 128.  Measured, a bf16 matrix in a graph, one launch / chain: 64 x 64 50 / 67 us,
+// 512 x 768 85 / 94, 1024 x 1024 101 / 122, five of 512 x 512 107 / 123, 2048 x 1024 142 / 134, 2300 x 1001
+// 184 / 151.  (Outside a graph the chain's launches take the host some 80 us.)
+bool one_is_quicker(const OrthRun &r) {
+    const int64_t sms = device_sms(current_device());
+    if (sms <= 0 || r.steps == 0) return false;
+    int64_t chain = 0;
+    for (int which = 0; which < 3; ++which) chain += linear_cycles(orth_product(r, 0, which));
+    const OrthTiles t = orth_one_tiles(r, sms);
+    const int64_t kn = cdiv(r.n, 64), km = cdiv(std::max(r.R, r.C), 64);
+    const int64_t ws = cdiv(t.sym * r.batch, sms), wx = cdiv(t.x * r.batch, sms);
+    return 18000 + (t.bn == 64 ? 360 : 600) * (ws * (km + kn) + wx * kn) < chain;
+}
+
+// The iteration as a chain of launches.
+ts_status orth_chain(const OrthRun &r) {
+    const dim3 grid(static_cast<unsigned>(r.prep.chunks), static_cast<unsigned>(r.batch)), block(kOrthThreads);
+    cudaError_t e;
+    auto prepare = [&](auto norm, auto scale) {
+        e = launch_pdl(norm, grid, block, 0, r.stream, r.prep);
+        if (e == cudaSuccess) e = launch_pdl(scale, grid, block, 0, r.stream, r.prep);
+    };
+    if (r.f32)
+        r.vec ? prepare(orth_norm_kernel<float, true>, orth_scale_kernel<float, true>)
+              : prepare(orth_norm_kernel<float, false>, orth_scale_kernel<float, false>);
+    else
+        r.vec ? prepare(orth_norm_kernel<uint16_t, true>, orth_scale_kernel<uint16_t, true>)
+              : prepare(orth_norm_kernel<uint16_t, false>, orth_scale_kernel<uint16_t, false>);
+    if (e != cudaSuccess) return cuda_fail(e, "normalisation launch");
+
+    for (int32_t i = 0; i < r.steps; ++i)
+        for (int which = 0; which < 3; ++which) {
+            const ts_status s = linear_product(orth_product(r, i, which));
+            if (s != TS_OK) return s;
+        }
+    return TS_OK;
 }
 
 constexpr int64_t kMaxSide = 1 << 20, kMaxBatch = 65535;
@@ -301,12 +229,31 @@ ts_status ts_orthogonalise(const void *G, void *O, int64_t batch, int64_t R, int
         return fail(TS_ERR_INVALID_ARG, "the workspace overlaps G or O");
 
     char *const ws = static_cast<char *>(workspace);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool vec = reinterpret_cast<uintptr_t>(G) % 16 == 0 && (R <= 1 || (ldg * gsize) % 16 == 0) &&
-                     (batch <= 1 || (g_matrix * gsize) % 16 == 0);
-    const int V = vec ? 16 / gsize : 1;
-    OrthParams p;
-    std::memset(&p, 0, sizeof p);
+    OrthRun r;
+    std::memset(&r, 0, sizeof r);
+    r.f32 = gsize == 4;
+    r.vec = reinterpret_cast<uintptr_t>(G) % 16 == 0 && (R <= 1 || (ldg * gsize) % 16 == 0) &&
+            (batch <= 1 || (g_matrix * gsize) % 16 == 0);
+    r.batch = batch;
+    r.R = R;
+    r.C = C;
+    r.n = plan.n;
+    r.steps = steps;
+    r.a = a;
+    r.b = b;
+    r.c = cc;
+    for (int i = 0; i < 2; ++i) r.X[i] = reinterpret_cast<uint16_t *>(ws + plan.x(i));
+    r.A = reinterpret_cast<uint16_t *>(ws + plan.a());
+    r.B = reinterpret_cast<uint16_t *>(ws + plan.b());
+    r.ldx = plan.ldx;
+    r.ldn = plan.ldn;
+    r.O = O;
+    r.ldo = ldo;
+    r.o_matrix = o_matrix;
+    r.barrier = reinterpret_cast<int32_t *>(ws + plan.barrier());
+    r.timeout_s = o->timeout_s;
+    r.stream = static_cast<cudaStream_t>(stream);
+    OrthParams &p = r.prep;
     p.G = G;
     p.ldg = ldg;
     p.g_matrix = g_matrix;
@@ -316,93 +263,12 @@ ts_status ts_orthogonalise(const void *G, void *O, int64_t batch, int64_t R, int
     p.partial = reinterpret_cast<float *>(ws + plan.partial());
     p.R = R;
     p.C = C;
-    p.vecs = cdiv(C, V);
+    p.vecs = cdiv(C, r.vec ? 16 / gsize : 1);
     p.div_vecs = fast_div_for(p.vecs);
     p.chunks = static_cast<int32_t>(plan.chunks);
     p.to_bf16 = steps == 0;
     p.eps = o->eps > 0.f ? o->eps : 1e-7f;
-    const dim3 norm_grid(static_cast<unsigned>(plan.chunks), static_cast<unsigned>(batch));
-    const dim3 block(kOrthThreads);
-    cudaError_t e;
-    auto prepare = [&](auto norm, auto scale) {
-        e = launch_pdl(norm, norm_grid, block, 0, st, p);
-        if (e == cudaSuccess) e = launch_pdl(scale, norm_grid, block, 0, st, p);
-    };
-    if (gsize == 4)
-        vec ? prepare(orth_norm_kernel<float, true>, orth_scale_kernel<float, true>)
-            : prepare(orth_norm_kernel<float, false>, orth_scale_kernel<float, false>);
-    else
-        vec ? prepare(orth_norm_kernel<uint16_t, true>, orth_scale_kernel<uint16_t, true>)
-            : prepare(orth_norm_kernel<uint16_t, false>, orth_scale_kernel<uint16_t, false>);
-    if (e != cudaSuccess) return cuda_fail(e, "normalisation launch");
-
-    const bool tall = R > C;
-    const int64_t n = plan.n, x_matrix = R * plan.ldx, n_matrix = n * plan.ldn;
-    void *const A = ws + plan.a(), *const B = ws + plan.b();
-    LinCall base;
-    std::memset(&base, 0, sizeof base);
-    base.f16 = 1;
-    base.out = base.aux_type = OUT_F16;
-    base.batch = batch;
-    base.timeout_s = o->timeout_s;
-    base.stream = st;
-    for (int32_t i = 0; i < steps; ++i) {
-        const void *X = ws + plan.x(i & 1);
-        const bool last = i + 1 == steps;
-        // A = X X^T: 4096 A from the product of 4096 X with itself
-        LinCall c = base;
-        c.A = c.B = X;
-        c.lda = c.ldb = plan.ldx;
-        c.a_matrix = c.b_matrix = x_matrix;
-        c.a_mn = c.b_mn = tall;
-        c.D = A;
-        c.ldd = plan.ldn;
-        c.d_matrix = n_matrix;
-        c.M = c.N = n;
-        c.K = tall ? R : C;
-        c.sym = 1;
-        c.alpha = 1.f / kOrthScale;
-        ts_status s = linear_product(c);
-        if (s != TS_OK) return s;
-        // B = b A + c A^2
-        c = base;
-        c.A = c.B = c.aux = A;
-        c.lda = c.ldb = c.ld_aux = plan.ldn;
-        c.a_matrix = c.b_matrix = c.aux_matrix = n_matrix;
-        c.D = B;
-        c.ldd = plan.ldn;
-        c.d_matrix = n_matrix;
-        c.M = c.N = c.K = n;
-        c.sym = 1;
-        c.alpha = cc / kOrthScale;
-        c.beta = b;
-        s = linear_product(c);
-        if (s != TS_OK) return s;
-        // X = a X + B X, or a X + X B
-        c = base;
-        c.A = tall ? X : B;
-        c.lda = tall ? plan.ldx : plan.ldn;
-        c.a_matrix = tall ? x_matrix : n_matrix;
-        c.B = tall ? B : X;
-        c.ldb = tall ? plan.ldn : plan.ldx;
-        c.b_matrix = tall ? n_matrix : x_matrix;
-        c.b_mn = !tall;
-        c.aux = X;
-        c.ld_aux = plan.ldx;
-        c.aux_matrix = x_matrix;
-        c.D = last ? O : ws + plan.x((i + 1) & 1);
-        c.ldd = last ? ldo : plan.ldx;
-        c.d_matrix = last ? o_matrix : x_matrix;
-        c.M = R;
-        c.N = C;
-        c.K = n;
-        c.out = last ? OUT_BF16 : OUT_F16;
-        c.alpha = last ? 1.f / (kOrthScale * kOrthScale) : 1.f / kOrthScale;
-        c.beta = last ? a / kOrthScale : a;
-        s = linear_product(c);
-        if (s != TS_OK) return s;
-    }
-    return TS_OK;
+    return one_is_quicker(r) ? orth_one(r) : orth_chain(r);
 }
 
 }  // extern "C"

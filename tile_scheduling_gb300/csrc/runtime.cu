@@ -30,6 +30,7 @@ const char *wait_name(int where) {
         case WAIT_ROWS_CLC: return "row copy waiting for a CLC response";
         case WAIT_SCHED_PRODUCER: return "CLC scheduler waiting for the producer to begin its unit";
         case WAIT_SCALES: return "waiting for the buffer of a chunk of scales";
+        case WAIT_GRID: return "waiting for the other CTAs between the products of an orthogonalisation";
         case WAIT_AUX: return "epilogue waiting for the residual or pre-activation";
         case WAIT_PROMOTION: return "promotion warp waiting for scales or for a finished K block";
         default: return "unknown wait";

@@ -16,6 +16,17 @@ __device__ __forceinline__ void report_timeout(const P &p, int where) {
     atomicAdd(&p.status[2], 1ull);
 }
 
+// Scope of a kernel's waits, by its parameter block: the cluster, or (kCtaScope) the CTA.
+template <class P>
+constexpr bool kCtaScope = false;
+template <class P>
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+    if constexpr (kCtaScope<P>)
+        return mbar_try_wait_cta(bar, parity);
+    else
+        return mbar_try_wait(bar, parity);
+}
+
 // Bounded phase wait.  honor_abort: give up as soon as another role aborted
 // (role loops); drains pass false and rely on their own limit alone.
 template <class P>
@@ -23,7 +34,7 @@ static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uin
                                        bool honor_abort, const P &p, int where) {
     const uint64_t t0 = globaltimer();
     for (uint32_t n = 1;; ++n) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (try_wait<P>(bar, parity)) return true;
         if ((n & 15u) == 0) {
             if (honor_abort && *abort_flag) return false;
             if (globaltimer() - t0 > limit_ns) {
@@ -38,7 +49,7 @@ static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uin
 template <class P>
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *abort_flag,
                                            const P &p, int where) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (try_wait<P>(bar, parity)) return true;
     return wait_slow(bar, parity, p.timeout_ns, abort_flag, true, p, where);
 }
 
@@ -68,7 +79,7 @@ static __device__ __noinline__ bool wait_long_slow(uint32_t bar, uint32_t parity
                                                    const P &p, int where) {
     const uint64_t t0 = globaltimer();
     for (;;) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (try_wait<P>(bar, parity)) return true;
         if (*abort_flag) return false;
         if (globaltimer() - t0 > p.timeout_ns) {
             report_timeout(p, where);
@@ -82,14 +93,14 @@ static __device__ __noinline__ bool wait_long_slow(uint32_t bar, uint32_t parity
 template <class P>
 __device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag,
                                           const P &p, int where) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (try_wait<P>(bar, parity)) return true;
     return wait_long_slow(bar, parity, abort_flag, p, where);
 }
 
 template <class P>
 __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity, volatile int *abort_flag,
                                            const P &p) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (try_wait<P>(bar, parity)) return true;
     return wait_slow(bar, parity, p.drain_ns, abort_flag, false, p, WAIT_DRAIN);
 }
 
