@@ -163,8 +163,8 @@ ts_status linear_product(const LinCall &c) {
         // swapped, the rows of D are the instruction's columns
         CUtensorMap &a = swap ? L.b : L.a, &b = swap ? L.a : L.b;
         const int a_box = swap ? sv->bn : 128, b_box = sv ? 128 : bn / cg;
-        if ((s = operand_map(&a, c.A, c.a_mn, c.M, c.K, c.batch, c.lda, c.a_matrix, a_box)) != TS_OK) return s;
-        if ((s = operand_map(&b, c.B, c.b_mn, c.N, c.K, c.batch, c.ldb, c.b_matrix, b_box)) != TS_OK) return s;
+        if ((s = operand_map(&a, c.A, c.a_mn, c.a_rows ? c.a_rows : c.M, c.K, c.batch, c.lda, c.a_matrix, a_box)) != TS_OK) return s;
+        if ((s = operand_map(&b, c.B, c.b_mn, c.b_rows ? c.b_rows : c.N, c.K, c.batch, c.ldb, c.b_matrix, b_box)) != TS_OK) return s;
     }
     if (p.store_bytes == 16 && !sv) {
         if ((s = output_map(&L.d, c.D, esize, c.M, c.N, c.batch, c.ldd, c.d_matrix)) != TS_OK) return s;

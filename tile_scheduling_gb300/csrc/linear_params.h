@@ -74,6 +74,7 @@ struct SplitVariant {
 struct LinCall {
     const void *A, *B;
     int64_t lda, ldb, a_matrix, b_matrix;  // elements
+    int64_t a_rows, b_rows;                // rows that the operands have, 0: M and N (the rest of D comes of zeros)
     int a_mn, b_mn, f16;                   // f16: operands fp16, else bf16
     void *D;
     int64_t ldd, d_matrix;

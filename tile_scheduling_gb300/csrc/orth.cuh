@@ -197,7 +197,7 @@ struct OrthRun {
     int64_t batch, R, C, n;   // n: the shorter side
     int32_t steps;
     float a, b, c;
-    uint16_t *X[2], *A, *B;   // fp16 times kOrthScale: [batch][R][ldx], [batch][n][ldn]
+    uint16_t *X[2], *A, *B;   // fp16 times kOrthScale: [batch][R][ldx], [batch][ldn][ldn]
     int64_t ldx, ldn;
     void *O;                  // bf16
     int64_t ldo, o_matrix;

@@ -440,7 +440,7 @@ ts_status orth_one(const OrthRun &r) {
     p.ldx = r.ldx;
     p.ldn = r.ldn;
     p.x_matrix = r.R * r.ldx;
-    p.n_matrix = r.n * r.ldn;
+    p.n_matrix = r.ldn * r.ldn;
     p.O = static_cast<uint16_t *>(r.O);
     p.ldo = r.ldo;
     p.o_matrix = r.o_matrix;
@@ -464,7 +464,7 @@ ts_status orth_one(const OrthRun &r) {
     const uint16_t *const at[4] = {r.X[0], r.X[1], r.A, r.B};
     for (int i = 0; i < 4; ++i) {
         const int64_t rows = i < 2 ? r.R : r.n, cols = i < 2 ? r.C : r.n, ld = i < 2 ? r.ldx : r.ldn;
-        const int64_t dims[3] = {cols, rows, r.batch}, strides[2] = {ld * 2, rows * ld * 2};
+        const int64_t dims[3] = {cols, rows, r.batch}, strides[2] = {ld * 2, (i < 2 ? r.R : r.ldn) * ld * 2};
         for (int j = 0; j < 2; ++j) {
             const int box[3] = {64, 64 << j, 1};
             s = encode_map(&maps.m[i][j], at[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dims, strides, box);
