@@ -19,7 +19,8 @@
 namespace ts {
 namespace {
 
-constexpr int kActThreads = 512, kStripLanes = 8, kStripRows = kActThreads / kStripLanes;
+constexpr int kActThreads = 256;
+constexpr int kActCtas = 4;        // on an SM
 constexpr int kActUnroll = 4;      // rows of a thread in flight
 constexpr int kMaxActCluster = 8;
 
@@ -76,17 +77,17 @@ __device__ __forceinline__ void store_v(T *p, const float (&f)[V]) {
     }
 }
 
-// T: uint16_t (bf16) or float; VEC: rows start on 16-byte boundaries.
-template <class T, bool VEC>
-__global__ void __launch_bounds__(kActThreads, 2) act_grad_kernel(const __grid_constant__ ActParams p) {
+// T: uint16_t (bf16) or float; VEC: rows start on 16-byte boundaries; LANES: threads along a row.
+template <class T, bool VEC, int LANES>
+__global__ void __launch_bounds__(kActThreads, kActCtas) act_grad_kernel(const __grid_constant__ ActParams p) {
     constexpr int V = VEC ? 16 / sizeof(T) : 1;
-    constexpr int STRIP = kStripLanes * V;
-    __shared__ __align__(16) float part[kStripRows][STRIP];
+    constexpr int STRIP = LANES * V, ROWS = kActThreads / LANES;
+    __shared__ __align__(16) float part[ROWS][STRIP];
     grid_dep_wait();
     grid_dep_launch();
     const int rank = static_cast<int>(blockIdx.x) % p.cluster;
     const int64_t strip = blockIdx.x / p.cluster;
-    const int tx = threadIdx.x % kStripLanes, ty = threadIdx.x / kStripLanes;
+    const int tx = threadIdx.x % LANES, ty = threadIdx.x / LANES;
     const int64_t col = strip * STRIP + tx * V;
     const int64_t m0 = p.M * rank / p.cluster, m1 = p.M * (rank + 1) / p.cluster;
     const int count = static_cast<int>(max(int64_t(0), min(static_cast<int64_t>(V), p.N - col)));  // columns of this thread
@@ -98,11 +99,11 @@ __global__ void __launch_bounds__(kActThreads, 2) act_grad_kernel(const __grid_c
     auto rows = [&](auto tag) {
         constexpr int A = decltype(tag)::value;
         if (count == V) {
-            for (int64_t m = m0 + ty; m < m1; m += kActUnroll * kStripRows) {
+            for (int64_t m = m0 + ty; m < m1; m += kActUnroll * ROWS) {
                 Vec<T, V> g[kActUnroll], zz[kActUnroll];
 #pragma unroll
                 for (int k = 0; k < kActUnroll; ++k) {
-                    const int64_t r = m + k * kStripRows;
+                    const int64_t r = m + k * ROWS;
                     if (r < m1) {
                         g[k].load(gy + r * p.ldy);
                         if constexpr (A != ACT_NONE) zz[k].load(z + r * p.ldz);
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(kActThreads, 2) act_grad_kernel(const __grid_c
                 }
 #pragma unroll
                 for (int k = 0; k < kActUnroll; ++k) {
-                    const int64_t r = m + k * kStripRows;
+                    const int64_t r = m + k * ROWS;
                     if (r < m1) {
                         float o[V];
 #pragma unroll
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(kActThreads, 2) act_grad_kernel(const __grid_c
                 }
             }
         } else if (count > 0) {  // the last, shorter vector of the rows
-            for (int64_t m = m0 + ty; m < m1; m += kStripRows) {
+            for (int64_t m = m0 + ty; m < m1; m += ROWS) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     if (i < count) {
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kActThreads, 2) act_grad_kernel(const __grid_c
     static_assert(STRIP <= kActThreads, "a thread sums a column");
     float total = 0.f;
     if (threadIdx.x < STRIP) {
-        for (int r = 0; r < kStripRows; ++r) total += part[r][threadIdx.x];
+        for (int r = 0; r < ROWS; ++r) total += part[r][threadIdx.x];
         part[0][threadIdx.x] = total;  // only this thread reads the column
     }
     if (p.cluster > 1) {
@@ -165,11 +166,14 @@ __global__ void __launch_bounds__(kActThreads, 2) act_grad_kernel(const __grid_c
     if (rank == 0 && threadIdx.x < STRIP && strip * STRIP + threadIdx.x < p.N) p.gb[strip * STRIP + threadIdx.x] = total;
 }
 
-template <class T, bool VEC>
-cudaError_t launch_act_grad(const ActParams &p, cudaStream_t st) {
-    constexpr int64_t STRIP = kStripLanes * (VEC ? 16 / sizeof(T) : 1);
+template <class T, bool VEC, int LANES>
+cudaError_t launch_strips(ActParams &p, int64_t sms, cudaStream_t st) {
+    constexpr int64_t STRIP = LANES * (VEC ? 16 / sizeof(T) : 1);
+    // CTAs that share a strip's rows: while they all run at once, and have 64 rows each or more
+    const int64_t strips = cdiv(p.N, STRIP);
+    p.cluster = static_cast<int32_t>(std::max<int64_t>(1, std::min({int64_t{kMaxActCluster}, p.M / 64, kActCtas * sms / strips})));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(cdiv(p.N, STRIP) * p.cluster), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(strips * p.cluster), 1, 1);
     cfg.blockDim = dim3(kActThreads, 1, 1);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -181,7 +185,15 @@ cudaError_t launch_act_grad(const ActParams &p, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, act_grad_kernel<T, VEC>, p);
+    return cudaLaunchKernelEx(&cfg, act_grad_kernel<T, VEC, LANES>, p);
+}
+
+template <class T, bool VEC>
+cudaError_t launch_act_grad(ActParams &p, int64_t sms, cudaStream_t st) {
+    // Strips of 128 bytes, or of 64 where those would be too few for two CTAs on each SM.  (Rows of 8192
+    // columns: 70 us by 4 CTAs a strip, 77 by 8, which take two waves.)
+    const int64_t strips = cdiv(p.N, 8 * (VEC ? 16 / sizeof(T) : 1));
+    return strips * kMaxActCluster < 2 * sms ? launch_strips<T, VEC, 4>(p, sms, st) : launch_strips<T, VEC, 8>(p, sms, st);
 }
 
 }  // namespace
@@ -240,10 +252,11 @@ extern "C" ts_status ts_act_grad(const void *grad_y, const void *preact, void *g
     p.M = M;
     p.N = N;
     p.act = act;
-    p.cluster = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(kMaxActCluster, M / 64)));
-    if (cdiv(N, 8) * p.cluster > 0x7fffffffLL) return fail(TS_ERR_UNSUPPORTED, "too many columns");
+    const int64_t sms = device_sms(current_device());
+    if (sms <= 0) return fail(TS_ERR_CUDA, "cannot query the SM count");
+    if (cdiv(N, 4) * kMaxActCluster > 0x7fffffffLL) return fail(TS_ERR_UNSUPPORTED, "too many columns");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    auto pick = [&](auto t, auto v) { return launch_act_grad<decltype(t), decltype(v)::value>(p, st); };
+    auto pick = [&](auto t, auto v) { return launch_act_grad<decltype(t), decltype(v)::value>(p, sms, st); };
     const cudaError_t e = dtype == TS_OUT_F32 ? (vec ? pick(float(), std::true_type()) : pick(float(), std::false_type()))
                                               : (vec ? pick(uint16_t(), std::true_type()) : pick(uint16_t(), std::false_type()));
     return e == cudaSuccess ? TS_OK : cuda_fail(e, "activation gradient launch");

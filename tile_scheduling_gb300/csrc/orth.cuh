@@ -58,8 +58,7 @@ __device__ __forceinline__ void each_vector(const OrthParams &p, const T *g, int
     const int64_t total = (r1 - r0) * p.vecs;
     for (int64_t i0 = threadIdx.x; i0 < total; i0 += UN * THREADS) {
         float v[UN][V];
-        int64_t r[UN], c[UN];
-        int count[UN];
+        int32_t r[UN], c[UN], count[UN];  // R and C are at most 2^20
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
             const int64_t i = i0 + u * THREADS;
@@ -67,9 +66,9 @@ __device__ __forceinline__ void each_vector(const OrthParams &p, const T *g, int
             if (i < total) {
                 // a CTA's share has fewer than 2^31 vectors (checked on the host)
                 const int32_t row = fast_div(static_cast<int32_t>(i), p.div_vecs);
-                r[u] = r0 + row;
-                c[u] = (i - row * p.vecs) * V;
-                count[u] = static_cast<int>(min(static_cast<int64_t>(V), p.C - c[u]));
+                r[u] = static_cast<int32_t>(r0) + row;
+                c[u] = static_cast<int32_t>(i - row * p.vecs) * V;
+                count[u] = min(V, static_cast<int32_t>(p.C) - c[u]);
                 load_row<T, V>(g + r[u] * p.ldg + c[u], count[u], v[u]);
             }
         }
@@ -114,16 +113,31 @@ __device__ __forceinline__ void orth_norm(const OrthParams &p, int64_t z, int64_
     const T *g = static_cast<const T *>(p.G) + z * p.g_matrix;
     float mid = 0.f, big = 0.f, tiny = 0.f;
     const int64_t r0 = p.R * chunk / p.chunks, r1 = p.R * (chunk + 1) / p.chunks;
-    each_vector<THREADS, T, V>(p, g, r0, r1, [&](const float (&f)[V], int64_t, int64_t, int) {
+    float top = 0.f;
+    each_vector<THREADS, T, V>(p, g, r0, r1, [&](const float (&f)[V], int32_t, int32_t, int) {
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const float b = f[k] * 0x1p-70f, t = f[k] * 0x1p70f;
             mid = fmaf(f[k], f[k], mid);
-            big = fmaf(b, b, big);
-            tiny = fmaf(t, t, tiny);
+            top = fmaxf(top, fabsf(f[k]));
         }
     });
+    // The other two only where this share may matter to them: values above 2^55, whose squares reach
+    // 2^-30 of the least scaled sum that is used, or a small sum.
+    __shared__ int again;
     block_sum3<THREADS>(mid, big, tiny);
+    if (threadIdx.x == 0) again = mid < 0x1p-50f;
+    if (__syncthreads_or(top > 0x1p55f) || again) {
+        float none = 0.f;
+        each_vector<THREADS, T, V>(p, g, r0, r1, [&](const float (&f)[V], int32_t, int32_t, int) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const float b = f[k] * 0x1p-70f, t = f[k] * 0x1p70f;
+                big = fmaf(b, b, big);
+                tiny = fmaf(t, t, tiny);
+            }
+        });
+        block_sum3<THREADS>(none, big, tiny);
+    }
     if (threadIdx.x == 0) {
         float *const q = p.partial + (z * p.chunks + chunk) * 3;
         __stcg(q, mid);
@@ -165,7 +179,7 @@ __device__ __forceinline__ void orth_scale(const OrthParams &p, int64_t z, int64
     uint16_t *x = static_cast<uint16_t *>(p.X) + z * p.x_matrix;
     const bool whole = (p.ldx % V) == 0 && (p.x_matrix % V) == 0 && reinterpret_cast<uintptr_t>(p.X) % (2 * V) == 0;
     const int64_t r0 = p.R * chunk / p.chunks, r1 = p.R * (chunk + 1) / p.chunks;
-    each_vector<THREADS, T, V>(p, g, r0, r1, [&](const float (&f)[V], int64_t r, int64_t c, int count) {
+    each_vector<THREADS, T, V>(p, g, r0, r1, [&](const float (&f)[V], int32_t r, int32_t c, int count) {
         uint16_t o[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) {
