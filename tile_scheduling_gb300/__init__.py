@@ -946,6 +946,14 @@ _ACT = {"none": TS_ACT_NONE, "relu": TS_ACT_RELU, "gelu": TS_ACT_GELU, "gelu_tan
 _BF16 = {torch.bfloat16: TS_OUT_BF16}
 
 
+def _here(*tensors) -> None:
+    """Raise unless the tensors lie on the current device, where the kernels run."""
+    device = _raw_device() if _raw_device is not None else torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"a tensor lies on cuda:{t.get_device()} while the current device is cuda:{device}")
+
+
 def _like(t, name: str, other: str, code: int, shape):
     """(address, row stride) of an optional matrix of the output's type and shape."""
     if t is None:
@@ -977,6 +985,7 @@ def ts_linear(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, bias=None, act=
         b_type = _OUT[bias.dtype]
     r, ldr = _like(residual, "residual", "y", out, shape)
     z, ldz = _like(preact, "preact", "y", out, shape)
+    _here(x, w, y, bias, residual, preact)
     o = _PACK_LINEAR.pack(b, r, z, ldx, ldw, ldy, ldr, ldz, _ACT[act] if isinstance(act, str) else int(act), b_type,
                           _TILE[tile] if isinstance(tile, str) else int(tile), max_workers, timeout_s)
     st = _lib.ts_linear_packed(x.data_ptr(), w.data_ptr(), y.data_ptr(), M, N, K, out, o, _stream_of(stream))
@@ -996,6 +1005,7 @@ def ts_linear_grad_input(grad_z: torch.Tensor, w: torch.Tensor, grad_x: torch.Te
     if N2 != N or shape[0] != M or shape[1] != K:
         raise ValueError(f"shape mismatch: grad_z {tuple(grad_z.shape)}, w {tuple(w.shape)}, grad_x {tuple(grad_x.shape)}")
     z, ldz = _like(preact, "preact", "grad_x", out, shape)
+    _here(grad_z, w, grad_x, preact)
     o = _PACK_LINEAR_GRAD.pack(z, ldg, ldw, ldd, ldz, _ACT[act] if isinstance(act, str) else int(act),
                                _TILE[tile] if isinstance(tile, str) else int(tile), max_workers, 0, timeout_s)
     st = _lib.ts_linear_grad_input_packed(grad_z.data_ptr(), w.data_ptr(), grad_x.data_ptr(), M, N, K, out, o,
@@ -1015,6 +1025,7 @@ def ts_linear_grad_weight(grad_z: torch.Tensor, x: torch.Tensor, grad_w: torch.T
     if M2 != M or shape[0] != N or shape[1] != K:
         raise ValueError(f"shape mismatch: grad_z {tuple(grad_z.shape)}, x {tuple(x.shape)}, grad_w {tuple(grad_w.shape)}")
     r, ldr = _like(base, "base", "grad_w", out, shape)
+    _here(grad_z, x, grad_w, base)
     o = _PACK_LINEAR_GRAD.pack(r, ldg, ldx, ldd, ldr, TS_ACT_NONE, _TILE[tile] if isinstance(tile, str) else int(tile),
                                max_workers, 0, timeout_s)
     st = _lib.ts_linear_grad_weight_packed(grad_z.data_ptr(), x.data_ptr(), grad_w.data_ptr(), M, N, K, out, o,
@@ -1031,6 +1042,7 @@ def ts_act_grad(grad_y: torch.Tensor, preact, grad_z, grad_bias=None, act="none"
     dtype, shape, ldy = _matrix_of(grad_y, "grad_y", _OUT)
     z, ldz = _like(preact, "preact", "grad_y", dtype, shape)
     g, ldg = _like(grad_z, "grad_z", "grad_y", dtype, shape)
+    _here(grad_y, preact, grad_z, grad_bias)
     st = _lib.ts_act_grad(grad_y.data_ptr(), z, g, _dense(grad_bias, "grad_bias", _F32, (shape[1],)) if grad_bias is not None else 0,
                           shape[0], shape[1], dtype, _ACT[act] if isinstance(act, str) else int(act), ldy, ldz, ldg,
                           _stream_of(stream))
@@ -1069,6 +1081,7 @@ def ts_orthogonalise(g: torch.Tensor, out: torch.Tensor, steps=5, coefficients=(
         gm, om = g.stride(0), out.stride(0)
         if gm <= 0 or om <= 0:
             raise ValueError("matrices of g or out share memory (an expanded tensor)")
+    _here(g, out)
     need = _lib.ts_orthogonalise_workspace(n, R, C, steps)
     if need and workspace is None:
         workspace = _scratch_for(need, g.device, stream)
@@ -1076,6 +1089,7 @@ def ts_orthogonalise(g: torch.Tensor, out: torch.Tensor, steps=5, coefficients=(
     if workspace is not None:
         if not workspace.is_cuda or not workspace.is_contiguous():
             raise TypeError("workspace must be a contiguous CUDA tensor")
+        _here(workspace)
         ptr, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     o = _PACK_ORTH.pack(steps or -1, a, b, c, eps, 0, ldg, ldo, gm, om, timeout_s)
     st = _lib.ts_orthogonalise_packed(g.data_ptr(), out.data_ptr(), n, R, C, g_type, o, ptr, size, _stream_of(stream))

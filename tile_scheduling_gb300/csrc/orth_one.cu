@@ -79,11 +79,11 @@ __device__ __forceinline__ bool grid_barrier(const OneParams &p, int32_t count, 
     atomicAdd(p.barrier, 1);
     const int32_t want = count * static_cast<int32_t>(gridDim.x);
     const uint64_t t0 = globaltimer();
-    for (uint32_t n = 1;; ++n) {
+    for (;;) {
         int32_t v;
         asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p.barrier) : "memory");
         if (v >= want) return true;
-        if ((n & 63u) == 0 && globaltimer() - t0 > p.timeout_ns) {
+        if (globaltimer() - t0 > p.timeout_ns) {
             report_timeout(p, WAIT_GRID);
             *abort_flag = 1;
             return false;
