@@ -946,24 +946,58 @@ _ACT = {"none": TS_ACT_NONE, "relu": TS_ACT_RELU, "gelu": TS_ACT_GELU, "gelu_tan
 _BF16 = {torch.bfloat16: TS_OUT_BF16}
 
 
-def _here(*tensors) -> None:
-    """Raise unless the tensors lie on the current device, where the kernels run."""
-    device = _raw_device() if _raw_device is not None else torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"a tensor lies on cuda:{t.get_device()} while the current device is cuda:{device}")
+def _device() -> int:
+    """Index of the current device; on a machine without one a number that no tensor's device has."""
+    try:
+        return _raw_device() if _raw_device is not None else torch.cuda.current_device()
+    except RuntimeError:
+        return -2
 
 
-def _like(t, name: str, other: str, code: int, shape):
-    """(address, row stride) of an optional matrix of the output's type and shape."""
-    if t is None:
-        return 0, 0
-    c, s, ld = _matrix_of(t, name, _OUT)
+def _elsewhere(t, name: str, device: int) -> None:
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be on a CUDA device")
+    raise ValueError(f"{name} lies on cuda:{t.get_device()} while the current device is cuda:{device}")
+
+
+def _rows_of(t, name: str, dtypes, device: int, dims: int = 2):
+    """As _matrix_of, for a tensor of the current device."""
+    try:
+        code, shape, stride, at = dtypes[t.dtype], t.shape, t.stride(), t.get_device()
+    except (AttributeError, KeyError, TypeError):
+        _require(t, name, dtypes, dims)
+        raise
+    if at != device:
+        _elsewhere(t, name, device)
+    if len(shape) != dims:
+        _require(t, name, dtypes, dims)
+    cols = shape[-1]
+    if stride[-1] != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if shape[-2] <= 1:
+        return code, shape, 0
+    pitch = stride[-2]
+    if pitch == 0 and cols:
+        raise ValueError(f"{name} has rows that share memory (an expanded tensor)")
+    return code, shape, pitch
+
+
+def _like(t, name: str, other: str, code: int, shape, device: int):
+    """(address, row stride) of a matrix of the output's type and shape."""
+    c, s, ld = _rows_of(t, name, _OUT, device)
     if c != code:
         raise TypeError(f"{name} must have the type of {other}")
     if s != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(s)}")
     return t.data_ptr(), ld
+
+
+def _vector(t, name: str, dtypes, n: int, device: int) -> int:
+    """Address of a dense vector of n values on the current device."""
+    p = _dense(t, name, dtypes, (n,))
+    if t.get_device() != device:
+        _elsewhere(t, name, device)
+    return p
 
 
 def ts_linear(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, bias=None, act="none", residual=None, preact=None,
@@ -974,18 +1008,20 @@ def ts_linear(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, bias=None, act=
     and ``preact`` are [M, N] of y's type, and preact receives x @ w.T + bias.  residual may be y
     itself.  Rows may be strided; rows of x and w start on 16-byte boundaries.  Asynchronous on
     ``stream`` (default: torch's current stream)."""
-    _, (M, K), ldx = _matrix_of(x, "x", _BF16)
-    _, (N, K2), ldw = _matrix_of(w, "w", _BF16)
-    out, shape, ldy = _matrix_of(y, "y", _OUT)
+    device = _device()
+    _, (M, K), ldx = _rows_of(x, "x", _BF16, device)
+    _, (N, K2), ldw = _rows_of(w, "w", _BF16, device)
+    out, shape, ldy = _rows_of(y, "y", _OUT, device)
     if K2 != K or shape[0] != M or shape[1] != N:
         raise ValueError(f"shape mismatch: x {tuple(x.shape)}, w {tuple(w.shape)}, y {tuple(y.shape)}")
-    b = b_type = 0
+    b = b_type = r = ldr = z = ldz = 0
     if bias is not None:
-        b = _dense(bias, "bias", _OUT, (N,))
+        b = _vector(bias, "bias", _OUT, N, device)
         b_type = _OUT[bias.dtype]
-    r, ldr = _like(residual, "residual", "y", out, shape)
-    z, ldz = _like(preact, "preact", "y", out, shape)
-    _here(x, w, y, bias, residual, preact)
+    if residual is not None:
+        r, ldr = _like(residual, "residual", "y", out, shape, device)
+    if preact is not None:
+        z, ldz = _like(preact, "preact", "y", out, shape, device)
     o = _PACK_LINEAR.pack(b, r, z, ldx, ldw, ldy, ldr, ldz, _ACT[act] if isinstance(act, str) else int(act), b_type,
                           _TILE[tile] if isinstance(tile, str) else int(tile), max_workers, timeout_s)
     st = _lib.ts_linear_packed(x.data_ptr(), w.data_ptr(), y.data_ptr(), M, N, K, out, o, _stream_of(stream))
@@ -999,13 +1035,13 @@ def ts_linear_grad_input(grad_z: torch.Tensor, w: torch.Tensor, grad_x: torch.Te
 
     ``act`` and ``preact`` ([M, K] of grad_x's type) are those of the layer that made this one's input;
     without them grad_x is the gradient by that input.  w is read in place."""
-    _, (M, N), ldg = _matrix_of(grad_z, "grad_z", _BF16)
-    _, (N2, K), ldw = _matrix_of(w, "w", _BF16)
-    out, shape, ldd = _matrix_of(grad_x, "grad_x", _OUT)
+    device = _device()
+    _, (M, N), ldg = _rows_of(grad_z, "grad_z", _BF16, device)
+    _, (N2, K), ldw = _rows_of(w, "w", _BF16, device)
+    out, shape, ldd = _rows_of(grad_x, "grad_x", _OUT, device)
     if N2 != N or shape[0] != M or shape[1] != K:
         raise ValueError(f"shape mismatch: grad_z {tuple(grad_z.shape)}, w {tuple(w.shape)}, grad_x {tuple(grad_x.shape)}")
-    z, ldz = _like(preact, "preact", "grad_x", out, shape)
-    _here(grad_z, w, grad_x, preact)
+    z, ldz = _like(preact, "preact", "grad_x", out, shape, device) if preact is not None else (0, 0)
     o = _PACK_LINEAR_GRAD.pack(z, ldg, ldw, ldd, ldz, _ACT[act] if isinstance(act, str) else int(act),
                                _TILE[tile] if isinstance(tile, str) else int(tile), max_workers, 0, timeout_s)
     st = _lib.ts_linear_grad_input_packed(grad_z.data_ptr(), w.data_ptr(), grad_x.data_ptr(), M, N, K, out, o,
@@ -1019,13 +1055,13 @@ def ts_linear_grad_weight(grad_z: torch.Tensor, x: torch.Tensor, grad_w: torch.T
     """grad_w = base + grad_z.T @ x for bf16 grad_z [M, N] and x [M, K]; grad_w [N, K] is bf16 or fp32.
 
     ``base`` ([N, K] of grad_w's type, which may be grad_w itself) is what has been accumulated so far."""
-    _, (M, N), ldg = _matrix_of(grad_z, "grad_z", _BF16)
-    _, (M2, K), ldx = _matrix_of(x, "x", _BF16)
-    out, shape, ldd = _matrix_of(grad_w, "grad_w", _OUT)
+    device = _device()
+    _, (M, N), ldg = _rows_of(grad_z, "grad_z", _BF16, device)
+    _, (M2, K), ldx = _rows_of(x, "x", _BF16, device)
+    out, shape, ldd = _rows_of(grad_w, "grad_w", _OUT, device)
     if M2 != M or shape[0] != N or shape[1] != K:
         raise ValueError(f"shape mismatch: grad_z {tuple(grad_z.shape)}, x {tuple(x.shape)}, grad_w {tuple(grad_w.shape)}")
-    r, ldr = _like(base, "base", "grad_w", out, shape)
-    _here(grad_z, x, grad_w, base)
+    r, ldr = _like(base, "base", "grad_w", out, shape, device) if base is not None else (0, 0)
     o = _PACK_LINEAR_GRAD.pack(r, ldg, ldx, ldd, ldr, TS_ACT_NONE, _TILE[tile] if isinstance(tile, str) else int(tile),
                                max_workers, 0, timeout_s)
     st = _lib.ts_linear_grad_weight_packed(grad_z.data_ptr(), x.data_ptr(), grad_w.data_ptr(), M, N, K, out, o,
@@ -1039,12 +1075,12 @@ def ts_act_grad(grad_y: torch.Tensor, preact, grad_z, grad_bias=None, act="none"
 
     grad_y, preact and grad_z are [M, N], all bf16 or all fp32.  preact is None with act "none"; grad_z
     may be None (the bias gradient alone), or grad_y or preact itself."""
-    dtype, shape, ldy = _matrix_of(grad_y, "grad_y", _OUT)
-    z, ldz = _like(preact, "preact", "grad_y", dtype, shape)
-    g, ldg = _like(grad_z, "grad_z", "grad_y", dtype, shape)
-    _here(grad_y, preact, grad_z, grad_bias)
-    st = _lib.ts_act_grad(grad_y.data_ptr(), z, g, _dense(grad_bias, "grad_bias", _F32, (shape[1],)) if grad_bias is not None else 0,
-                          shape[0], shape[1], dtype, _ACT[act] if isinstance(act, str) else int(act), ldy, ldz, ldg,
+    device = _device()
+    dtype, shape, ldy = _rows_of(grad_y, "grad_y", _OUT, device)
+    z, ldz = _like(preact, "preact", "grad_y", dtype, shape, device) if preact is not None else (0, 0)
+    g, ldg = _like(grad_z, "grad_z", "grad_y", dtype, shape, device) if grad_z is not None else (0, 0)
+    st = _lib.ts_act_grad(grad_y.data_ptr(), z, g,
+                          _vector(grad_bias, "grad_bias", _F32, shape[1], device) if grad_bias is not None else 0, shape[0], shape[1], dtype, _ACT[act] if isinstance(act, str) else int(act), ldy, ldz, ldg,
                           _stream_of(stream))
     if st:
         _check(st)
@@ -1063,8 +1099,9 @@ def ts_orthogonalise(g: torch.Tensor, out: torch.Tensor, steps=5, coefficients=(
     and (a, b, c) = ``coefficients``, from X = g / (norm(g) + eps).  The workspace is one kept for each
     stream unless one is passed (ts_orthogonalise_workspace bytes, 256-byte aligned)."""
     dims = 3 if g.dim() == 3 else 2
-    g_type, shape, ldg = _matrix_of(g, "g", _OUT, dims)
-    _, o_shape, ldo = _matrix_of(out, "out", _BF16, dims)
+    device = _device()
+    g_type, shape, ldg = _rows_of(g, "g", _OUT, device, dims)
+    _, o_shape, ldo = _rows_of(out, "out", _BF16, device, dims)
     if o_shape != shape:
         raise ValueError(f"out must be {tuple(shape)}, not {tuple(o_shape)}")
     steps = int(steps)
@@ -1081,7 +1118,6 @@ def ts_orthogonalise(g: torch.Tensor, out: torch.Tensor, steps=5, coefficients=(
         gm, om = g.stride(0), out.stride(0)
         if gm <= 0 or om <= 0:
             raise ValueError("matrices of g or out share memory (an expanded tensor)")
-    _here(g, out)
     need = _lib.ts_orthogonalise_workspace(n, R, C, steps)
     if need and workspace is None:
         workspace = _scratch_for(need, g.device, stream)
@@ -1089,7 +1125,8 @@ def ts_orthogonalise(g: torch.Tensor, out: torch.Tensor, steps=5, coefficients=(
     if workspace is not None:
         if not workspace.is_cuda or not workspace.is_contiguous():
             raise TypeError("workspace must be a contiguous CUDA tensor")
-        _here(workspace)
+        if workspace.get_device() != device:
+            _elsewhere(workspace, "workspace", device)
         ptr, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     o = _PACK_ORTH.pack(steps or -1, a, b, c, eps, 0, ldg, ldo, gm, om, timeout_s)
     st = _lib.ts_orthogonalise_packed(g.data_ptr(), out.data_ptr(), n, R, C, g_type, o, ptr, size, _stream_of(stream))
