@@ -697,7 +697,9 @@ ts_status ts_moe_combine_grad(const void *grad_out, const void *y, const int32_t
 /* ------------------------------------------------------------------------
  * Operators of a linear layer: the product with its bias, activation and residual, the
  * gradients, and the orthogonalised update of its weights.  Every call is asynchronous on
- * `stream`, allocates nothing and launches programmatic dependents, as the calls above.
+ * `stream`, allocates nothing, may be captured into a graph, and launches programmatic
+ * dependents as the calls above (ts_orthogonalise of small matrices: one cooperative launch
+ * behind a memset of its workspace's barrier).
  * ---------------------------------------------------------------------- */
 typedef enum {
     TS_ACT_NONE = 0,
@@ -733,8 +735,8 @@ typedef struct {
  *
  * Sums, bias, activation and residual are fp32; y and preact are rounded once, to nearest even
  * (the activation takes z before that rounding).  Results are the same on every run.  Which sums
- * are formed in which order depends on the sizes, tile and max_workers; a NaN or infinity shows in
- * the rows and columns that use it.
+ * are formed in which order depends on the sizes, the options that are given and the GPU's number
+ * of SMs; a NaN or infinity shows in the rows and columns that use it.
  * M == 0 or N == 0: no-op.  K == 0: y = act(bias) + residual.  Rows of x and w must start on
  * 16-byte boundaries (strides multiples of 8), or the call returns TS_ERR_UNSUPPORTED.  y must not
  * overlap x, w or bias, nor the residual unless it is the residual; preact overlaps nothing.
@@ -789,7 +791,8 @@ ts_status ts_linear_grad_weight(const void *grad_z, const void *x, void *grad_w,
  *             and ldg (0 = N); preact is NULL with TS_ACT_NONE and only then; grad_z may be NULL
  *             (the bias gradient alone), or grad_y or preact itself
  *   grad_bias device fp32 [N] or NULL: the sum of the values before they are rounded to grad_z's
- *             type, in fp32 and in an order that depends on M and the rows' alignment alone
+ *             type, in fp32 and in an order that depends on M, N, the rows' alignment and the
+ *             GPU's number of SMs, and is the same on every run
  *
  * Any alignment and pitch is taken; rows on 16-byte boundaries move in vectors.
  */

@@ -541,17 +541,12 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
                             // of an even column, an odd one of the column behind it, and stores them at once.
                             const int32_t r = row0 + (lane & ~1), c0 = col0 + 32 * c + (lane & 1);
                             uint16_t *m = static_cast<uint16_t *>(p.D) + w.z * p.d_matrix + c0 * p.ldd + r;
-                            const int32_t many = p.M - r;  // rows there: rows of D, which is square, are even apart
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 const uint32_t got = __shfl_xor_sync(0xffffffffu, o[i], 1);
                                 const uint32_t two = lane & 1 ? __byte_perm(got, o[i], 0x7632) : __byte_perm(o[i], got, 0x5410);
-                                if (c0 + 2 * i < p.N) {
-                                    if (many >= 2)
-                                        *reinterpret_cast<uint32_t *>(m) = two;
-                                    else if (many == 1)
-                                        *m = static_cast<uint16_t>(two);
-                                }
+                                // rows of the mirror image: D, of a multiple of eight rows and columns, is square
+                                if (c0 + 2 * i < p.N && r < p.M) *reinterpret_cast<uint32_t *>(m) = two;
                                 m += 2 * p.ldd;
                             }
                         }

@@ -8,7 +8,7 @@
 // barrier, and needs a second barrier before a CTA may leave.
 //
 // What bounds it is latency: one TMA round trip (some 0.8 us), the exchange, and the launch; a
-// persistent CTA that walks the K loop alone fetches 160 KB per round trip and needs several.
+// persistent CTA that walks the K loop alone has 192 KB in flight and needs several.
 //
 // SWAP: the rows of D (few tokens) are the instruction's columns and the columns of D (the rows of
 // w) its 128 rows, so that a tile reads 128 rows of w for BN = 32 or 64 tokens.
@@ -220,7 +220,8 @@ __global__ void __launch_bounds__(SplitCfg<BN, SWAP>::THREADS, 2)
         if (leader) mma_commit(mma_done);
     }
     __syncwarp();
-    wait_phase(mma_done, 0, abort_flag, p, WAIT_EPI_TMEM_FULL);
+    // given up or not, the instructions in flight have completed before TMEM is read and freed
+    if (!wait_phase(mma_done, 0, abort_flag, p, WAIT_EPI_TMEM_FULL)) wait_drain(mma_done, 0, abort_flag, p);
     __syncwarp();
     tc_fence_after();
     if (p.split > 1) cluster_wait();
