@@ -51,10 +51,11 @@ __device__ __forceinline__ void load_row(const T *p, int count, float (&f)[V]) {
     }
 }
 
-// f(values, row, first column, how many) for the vectors of rows [r0, r1), four of a thread in flight.
+// f(values, row, first column, how many) for the vectors of rows [r0, r1), four of a thread in flight (single
+// values: sixteen).
 template <int THREADS, class T, int V, class F>
 __device__ __forceinline__ void each_vector(const OrthParams &p, const T *g, int64_t r0, int64_t r1, F &&f) {
-    constexpr int UN = 4;
+    constexpr int UN = V > 1 ? 4 : 16;
     const int64_t total = (r1 - r0) * p.vecs;
     for (int64_t i0 = threadIdx.x; i0 < total; i0 += UN * THREADS) {
         float v[UN][V];

@@ -55,9 +55,10 @@ template <>
 constexpr bool kCtaScope<OneParams> = true;
 namespace {
 
-// Tensor maps of X (two buffers), A and b A + c A^2, in boxes of 64 x 64 and of 64 of K by 128 rows.
+// Tensor maps of X (two buffers), A and b A + c A^2, in boxes of 64 of K by 64 and by 128 rows; of X with
+// its columns as the operand's rows, in boxes of 64 x 64.
 struct OneMaps {
-    CUtensorMap m[4][2];
+    CUtensorMap m[4][2], mn[2];
 };
 
 struct OnePhase {
@@ -125,6 +126,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
         *abort_flag = 0;
         fence_mbar_init();
         for (int i = 0; i < 8; ++i) prefetch_tmap(&maps.m[i >> 1][i & 1]);
+        for (int i = 0; i < 2; ++i) prefetch_tmap(&maps.mn[i]);
     }
     if (warp == 1) {
         tmem_alloc<1>(tail, 256);
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
                             auto load = [&](uint32_t dst, int32_t m, bool mn, int32_t row, uint32_t boxes) {
                                 if (mn) {  // boxes of 64 rows side by side
                                     for (uint32_t c = 0; c < boxes; ++c)
-                                        tma_load_3d(dst + c * kOneBoxBytes, &maps.m[m][0], full(stage), row + 64 * static_cast<int32_t>(c), k, z);
+                                        tma_load_3d(dst + c * kOneBoxBytes, &maps.mn[m], full(stage), row + 64 * static_cast<int32_t>(c), k, z);
                                 } else {
                                     tma_load_3d(dst, &maps.m[m][boxes - 1], full(stage), k, row, z);
                                 }
@@ -464,12 +466,16 @@ ts_status orth_one(const OrthRun &r) {
     const uint16_t *const at[4] = {r.X[0], r.X[1], r.A, r.B};
     for (int i = 0; i < 4; ++i) {
         const int64_t rows = i < 2 ? r.R : r.n, cols = i < 2 ? r.C : r.n, ld = i < 2 ? r.ldx : r.ldn;
-        const int64_t dims[3] = {cols, rows, r.batch}, strides[2] = {ld * 2, (i < 2 ? r.R : r.ldn) * ld * 2};
-        for (int j = 0; j < 2; ++j) {
-            const int box[3] = {64, 64 << j, 1};
-            s = encode_map(&maps.m[i][j], at[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dims, strides, box);
-            if (s != TS_OK) return s;
-        }
+        const int64_t strides[2] = {ld * 2, (i < 2 ? r.R : r.ldn) * ld * 2};
+        auto encode = [&](CUtensorMap &m, int64_t width, int box_rows) {
+            const int64_t dims[3] = {width, rows, r.batch};
+            const int box[3] = {64, box_rows, 1};
+            return encode_map(&m, at[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dims, strides, box);
+        };
+        for (int j = 0; j < 2; ++j)
+            if ((s = encode(maps.m[i][j], cols, 64 << j)) != TS_OK) return s;
+        // to the end of a sector, as in the products' maps
+        if (i < 2 && (s = encode(maps.mn[i], cdiv(cols, 16) * 16, 64)) != TS_OK) return s;
     }
     static std::atomic<uint64_t> prepared{0};  // devices
     const int dev = current_device();

@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kOrthThreads = 256;
 constexpr int64_t kOrthChunks = 1216;  // CTAs that share the matrices, about: eight for each SM
-
+constexpr int64_t kOrthShare = 1024;   // vectors (or single values) of a CTA, while there are more of them
 
 template <class T, bool VEC>
 __global__ void __launch_bounds__(kOrthThreads) orth_norm_kernel(const __grid_constant__ OrthParams p) {
@@ -66,7 +66,7 @@ OrthPlan plan_orth(int64_t batch, int64_t R, int64_t C, int steps) {
     o.ldn = cdiv(o.n, 64) * 64;
     o.x_bytes = steps > 0 ? round(batch * R * o.ldx * 2) : 0;
     o.n_bytes = steps > 0 ? round(batch * o.ldn * o.ldn * 2) : 0;
-    o.chunks = std::max<int64_t>(1, std::min<int64_t>({cdiv(kOrthChunks, batch), R, cdiv(R * C, 8192)}));
+    o.chunks = std::max<int64_t>(1, std::min<int64_t>({cdiv(kOrthChunks, batch), R, cdiv(R * C, kOrthShare)}));
     o.partial_bytes = round(batch * o.chunks * 3 * 4);
     return o;
 }
@@ -137,7 +137,7 @@ LinCall orth_product(const OrthRun &r, int32_t i, int which) {
 // a phase some 3 us (the barrier, the first loads, the stores), a K block of a tile 360 cycles with 64
 // columns and 600 with 128.  Measured, a bf16 matrix in a graph, one launch / chain: 64 x 64 50 / 67 us,
 // 512 x 768 85 / 94, 1024 x 1024 101 / 122, five of 512 x 512 107 / 123, 2048 x 1024 142 / 134, 2300 x 1001
-// 184 / 151.  (Outside a graph the chain's launches take the host some 80 us.)
+// 151 / 137.  (Outside a graph the chain's launches take the host some 80 us.)
 bool one_is_quicker(const OrthRun &r) {
     const int64_t sms = device_sms(current_device());
     if (sms <= 0 || r.steps == 0) return false;
@@ -271,7 +271,7 @@ ts_status ts_orthogonalise(const void *G, void *O, int64_t batch, int64_t R, int
     p.C = C;
     p.vecs = cdiv(C, r.vec ? 16 / gsize : 1);
     p.div_vecs = fast_div_for(p.vecs);
-    p.chunks = static_cast<int32_t>(plan.chunks);
+    p.chunks = static_cast<int32_t>(std::min(plan.chunks, cdiv(R * p.vecs, kOrthShare)));
     p.to_bf16 = steps == 0;
     p.eps = o->eps > 0.f ? o->eps : 1e-7f;
     return one_is_quicker(r) ? orth_one(r) : orth_chain(r);
