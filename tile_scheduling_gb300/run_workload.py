@@ -27,7 +27,7 @@ GEMMS = {"gemm256": synth.GEMM_256, "gemm4096": synth.GEMM_4096, "gemm8192": syn
 
 def main(argv=None):
     ap = argparse.ArgumentParser()
-    ap.add_argument("workload", choices=sorted(GEMMS) + ["grouped", "copy", "rows", "moe", "fp8"])
+    ap.add_argument("workload", choices=sorted(GEMMS) + ["grouped", "copy", "rows", "moe", "fp8", "linear", "orth"])
     ap.add_argument("--launches", type=int, default=3)
     ap.add_argument("--sched", default=None, choices=["static", "clc", "nonpersistent"])
     ap.add_argument("--tile", default=None)
@@ -76,6 +76,35 @@ def main(argv=None):
         rows = saved["offsets"].diff()
         print(f"moe {T} tokens x {k} of {E} experts, {N} x {K}: {int(rows.min())} to {int(rows.max())} rows each, "
               f"x{a.launches} ok")
+        return 0
+    if a.workload == "linear":
+        # a linear layer, forward and backward: every operator of one, in its order, and the orthogonalised update
+        M, N, K = 2048, 4096, 4096
+        g = torch.Generator("cuda").manual_seed(1)
+        bf16 = torch.bfloat16
+        x, w = torch.randn((M, K), device="cuda", generator=g).to(bf16), (torch.randn((N, K), device="cuda", generator=g) / K ** 0.5).to(bf16)
+        bias, grad_y = torch.randn(N, device="cuda", generator=g), torch.randn((M, N), device="cuda", generator=g).to(bf16)
+        y, z, grad_z = (torch.empty((M, N), dtype=bf16, device="cuda") for _ in range(3))
+        grad_x, grad_w, update = torch.empty_like(x), torch.empty_like(w), torch.empty_like(w)
+        grad_bias = torch.empty(N, device="cuda")
+        for _ in range(a.launches):
+            ts.ts_linear(x, w, y, bias=bias, act="silu", preact=z, tile=a.tile or "auto")
+            ts.ts_act_grad(grad_y, z, grad_z, grad_bias, act="silu")
+            ts.ts_linear_grad_input(grad_z, w, grad_x, tile=a.tile or "auto")
+            ts.ts_linear_grad_weight(grad_z, x, grad_w, tile=a.tile or "auto")
+            ts.ts_orthogonalise(grad_w, update)
+        ts.ts_sync_and_check()
+        print(f"linear {M} x {N} x {K} {a.tile or 'auto'}, forward, backward, update x{a.launches} ok")
+        return 0
+    if a.workload == "orth":
+        # the orthogonalised update of a small matrix (one launch)
+        g = torch.Generator("cuda").manual_seed(1)
+        grad = torch.randn((512, 768), device="cuda", generator=g).bfloat16()
+        update = torch.empty_like(grad)
+        for _ in range(a.launches):
+            ts.ts_orthogonalise(grad, update)
+        ts.ts_sync_and_check()
+        print(f"orth 512 x 768 x{a.launches} ok")
         return 0
     if a.workload == "fp8":
         # one block-scaled 8-bit product (4096^3)
