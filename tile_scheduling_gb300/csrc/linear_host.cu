@@ -71,8 +71,23 @@ struct LinPlan {
     int64_t cycles;  // an estimate, from one launch to the next
 };
 
+// Cycles that the loads of 16 rows of an operand take for a K block (or of 16 of its rows of K, 64 wide):
+// a row is 128 bytes, one line of memory where rows start on lines, else two, and five sectors where rows
+// start off sectors.  Measured on K blocks of 256 and 384 rows: on lines no more than the rest of a K
+// block, on sectors 1.9 cycles a row (480 to 510 and 720), off them 2.8 (700 to 720 and 1040).
+int64_t row_cycles(const void *ptr, int64_t rows, int64_t ld, int64_t batch, int64_t matrix) {
+    const uint64_t at = reinterpret_cast<uintptr_t>(ptr) | (rows > 1 ? ld * 2 : 0) | (batch > 1 ? matrix * 2 : 0);
+    return at % 128 == 0 ? 16 : at % 32 == 0 ? 30 : 44;
+}
+
 LinPlan plan_product(const LinCall &c, int64_t sms) {
     const int64_t nkb = cdiv(c.K, 64);
+    const int64_t load_a = row_cycles(c.A, c.a_mn ? c.K : c.M, c.lda, c.batch, c.a_matrix);
+    const int64_t load_b = row_cycles(c.B, c.b_mn ? c.K : c.N, c.ldb, c.batch, c.b_matrix);
+    // cycles of a K block: what they are with rows on lines, or the loads of so many rows of A and B
+    auto block = [&](int64_t cycles, int64_t rows_a, int64_t rows_b) {
+        return std::max(cycles, (rows_a * load_a + rows_b * load_b) / 16);
+    };
     const int64_t m1 = cdiv(c.M, 128), m2 = cdiv(c.M, 256), n1 = cdiv(c.N, 128), n2 = cdiv(c.N, 256);
     const int64_t u1 = c.batch * (c.sym ? triangle(n1) : m1 * n1), u3 = c.batch * (c.sym ? triangle(n2) : m2 * n2);
     LinPlan pl{128, 1, nullptr, 1, 1, INT64_MAX};
@@ -86,7 +101,7 @@ LinPlan plan_product(const LinCall &c, int64_t sms) {
             for (int k = v.swap ? 1 : 2, i = v.swap ? 0 : 1; k <= kMaxSplit && k <= nkb; k *= 2, ++i) {
                 const int ctas = v.swap && units * k > sms ? 2 : 1;
                 if (units * k > ctas * sms || (k > 1 && v.clusters(k, ctas) < units)) break;
-                const int64_t t = cdiv(nkb, k) * 400 * ctas + 25 * units * k + fixed[i] + (c.act ? 1000 : 0) + (c.aux ? 900 : 0);
+                const int64_t t = cdiv(nkb, k) * block(400, v.swap ? v.bn : 128, 128) * ctas + 25 * units * k + fixed[i] + (c.act ? 1000 : 0) + (c.aux ? 900 : 0);
                 if (t < pl.cycles) pl.cycles = t, pl.sv = &v, pl.split = k, pl.ctas = ctas;
             }
         };
@@ -96,6 +111,9 @@ LinPlan plan_product(const LinCall &c, int64_t sms) {
             consider(c.M <= 32 && !c.a_mn ? split_swap_32 : split_swap_64, n1, {6000, 6000, 6000, 6000});
     }
     // Columns of a 256-column tile: the width whose waves of workers take the fewest cycles in all.
+    auto cost = [&](int64_t pair, int64_t bn) {  // of a K block
+        return block((pair == 2 ? 520 : 590) * (bn + kWidthOverhead) / (256 + kWidthOverhead), 128, bn / pair);
+    };
     // With B's rows contiguous only whole boxes of 64 of them for each CTA: 4096 x 2048 x 2048 on pairs
     // 24.6 us with 256 columns, 30.1 with 240 (which take as many waves, and K-major 24.6 as well).
     auto width = [&](int64_t rows, int64_t workers, int64_t pair, int64_t &waves) {
@@ -104,7 +122,7 @@ LinPlan plan_product(const LinCall &c, int64_t sms) {
         for (int64_t b = 240; !c.sym && b > 128; b -= 16) {
             if (c.b_mn && b % (64 * pair) != 0) continue;
             const int64_t w = cdiv(rows * cdiv(c.N, b) * c.batch, workers);
-            if (w * (b + kWidthOverhead) < waves * (bn + kWidthOverhead)) bn = b, waves = w;
+            if (w * cost(pair, b) < waves * cost(pair, bn)) bn = b, waves = w;
         }
         return bn;
     };
@@ -113,10 +131,9 @@ LinPlan plan_product(const LinCall &c, int64_t sms) {
     // The tile with the fewest cycles: waves of workers times what a K block of a tile takes, and the rest,
     // in which the last epilogue shows.
     const int64_t slow = (c.act ? 3000 : 0) + (c.aux ? 900 : 0) + (c.sym ? 5000 : 0);
-    const int64_t c1 = cdiv(u1, sms) * nkb * 340 + 8300 + slow;
-    const int64_t c2 = w2 * nkb * 590 * (bn2 + kWidthOverhead) / (256 + kWidthOverhead) + 9100 + slow;
-    const int64_t c3 = (c.sym ? cdiv(u3, sms / 2) * nkb * 520 : w3 * nkb * 520 * (bn3 + kWidthOverhead) / (256 + kWidthOverhead)) +
-                       9800 + slow;
+    const int64_t c1 = cdiv(u1, sms) * nkb * block(340, 128, 128) + 8300 + slow;
+    const int64_t c2 = w2 * nkb * cost(1, bn2) + 9100 + slow;
+    const int64_t c3 = (c.sym ? cdiv(u3, sms / 2) : w3) * nkb * cost(2, bn3) + 9800 + slow;
     int tile = c.tile;
     if (tile == TS_TILE_AUTO) {
         const int64_t least = std::min(c1, std::min(c.sym ? c1 : c2, c3));
