@@ -85,8 +85,8 @@ LinPlan plan_product(const LinCall &c, int64_t sms) {
     const int64_t load_a = row_cycles(c.A, c.a_mn ? c.K : c.M, c.lda, c.batch, c.a_matrix);
     const int64_t load_b = row_cycles(c.B, c.b_mn ? c.K : c.N, c.ldb, c.batch, c.b_matrix);
     // cycles of a K block: what they are with rows on lines, or the loads of so many rows of A and B
-    auto block = [&](int64_t cycles, int64_t rows_a, int64_t rows_b) {
-        return std::max(cycles, (rows_a * load_a + rows_b * load_b) / 16);
+    auto block = [&](int64_t cycles, int64_t rows_a, int64_t rows_b, int64_t b_least = 0) {
+        return std::max(cycles, (rows_a * load_a + rows_b * std::max(load_b, b_least)) / 16);
     };
     const int64_t m1 = cdiv(c.M, 128), m2 = cdiv(c.M, 256), n1 = cdiv(c.N, 128), n2 = cdiv(c.N, 256);
     const int64_t u1 = c.batch * (c.sym ? triangle(n1) : m1 * n1), u3 = c.batch * (c.sym ? triangle(n2) : m2 * n2);
@@ -110,17 +110,19 @@ LinPlan plan_product(const LinCall &c, int64_t sms) {
         if (!c.sym && c.batch == 1 && c.M <= 64)
             consider(c.M <= 32 && !c.a_mn ? split_swap_32 : split_swap_64, n1, {6000, 6000, 6000, 6000});
     }
-    // Columns of a 256-column tile: the width whose waves of workers take the fewest cycles in all.
+    // Columns of a 256-column tile: the width whose waves of workers take the fewest cycles in all.  With
+    // B's rows contiguous a CTA's columns start on sectors, and on lines where they are whole boxes of 64:
+    // 4096 x 4096 x 4096 on pairs 81 us with 224 columns (four waves either way), 87 with 256;
+    // 4096 x 2048 x 2048 24.6 with 256, 30.1 with 240, whose halves start off sectors.
     auto cost = [&](int64_t pair, int64_t bn) {  // of a K block
-        return block((pair == 2 ? 520 : 590) * (bn + kWidthOverhead) / (256 + kWidthOverhead), 128, bn / pair);
+        return block((pair == 2 ? 520 : 590) * (bn + kWidthOverhead) / (256 + kWidthOverhead), 128, bn / pair,
+                     c.b_mn && bn % (64 * pair) != 0 ? 30 : 0);
     };
-    // With B's rows contiguous only whole boxes of 64 of them for each CTA: 4096 x 2048 x 2048 on pairs
-    // 24.6 us with 256 columns, 30.1 with 240 (which take as many waves, and K-major 24.6 as well).
     auto width = [&](int64_t rows, int64_t workers, int64_t pair, int64_t &waves) {
         int64_t bn = 256;
         waves = cdiv(rows * n2 * c.batch, workers);
         for (int64_t b = 240; !c.sym && b > 128; b -= 16) {
-            if (c.b_mn && b % (64 * pair) != 0) continue;
+            if (c.b_mn && b % (16 * pair) != 0) continue;
             const int64_t w = cdiv(rows * cdiv(c.N, b) * c.batch, workers);
             if (w * cost(pair, b) < waves * cost(pair, bn)) bn = b, waves = w;
         }
