@@ -115,11 +115,18 @@ __global__ void __launch_bounds__(kActThreads, kActCtas) act_grad_kernel(const _
                     if (r < m1) {
                         float o[V];
 #pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            o[i] = g[k].get(i);
-                            if constexpr (A != ACT_NONE) o[i] *= act_slope<A>(zz[k].get(i));
-                            sum[i] += o[i];
+                        for (int i = 0; i < V; ++i) o[i] = g[k].get(i);
+                        if constexpr (A != ACT_NONE) {
+                            constexpr int W = V > 1 ? 1 : 0;  // a single value goes as a pair of itself
+#pragma unroll
+                            for (int i = 0; i < V; i += 1 + W) {
+                                float other;
+                                split(two(o[i], o[i + W]) * act_slope<A>(two(zz[k].get(i), zz[k].get(i + W))), o[i],
+                                      W ? o[i + W] : other);
+                            }
                         }
+#pragma unroll
+                        for (int i = 0; i < V; ++i) sum[i] += o[i];
                         if (p.gz) store_v<T, V>(gz + r * p.ldg, o);
                     }
                 }
@@ -130,7 +137,10 @@ __global__ void __launch_bounds__(kActThreads, kActCtas) act_grad_kernel(const _
                 for (int i = 0; i < V; ++i) {
                     if (i < count) {
                         float g = to_f32(gy[m * p.ldy + i]);
-                        if constexpr (A != ACT_NONE) g *= act_slope<A>(to_f32(z[m * p.ldz + i]));
+                        if constexpr (A != ACT_NONE) {
+                            float other;
+                            split(two(g) * act_slope<A>(two(to_f32(z[m * p.ldz + i]))), g, other);
+                        }
                         sum[i] += g;
                         if (p.gz) {
                             const float one[1] = {g};

@@ -1,3 +1,3 @@
 #include "linear_launch.cuh"
 
-TS_LINEAR_VARIANT(linear_128_1_pre, 128, 1, 1)
+TS_LINEAR_VARIANT(linear_128_1_pre, 128, 1, LIN_PRE)

@@ -1,0 +1,3 @@
+#include "linear_launch.cuh"
+
+TS_LINEAR_VARIANT(linear_256_1_bare, 256, 1, LIN_BARE)

@@ -1,0 +1,3 @@
+#include "linear_launch.cuh"
+
+TS_LINEAR_VARIANT(linear_256_2_full, 256, 2, LIN_FULL)

@@ -7,8 +7,9 @@
 
 namespace ts {
 
-extern const SplitVariant split_128, split_swap_64, split_swap_32;
-extern const LinVariant linear_128_1, linear_128_1_pre, linear_256_1, linear_256_1_pre, linear_256_2, linear_256_2_pre;
+extern const SplitVariant split_128[3], split_swap_64[3], split_swap_32[3];  // by the type of D
+#define TS_LINEAR_MODES(TILE) linear_##TILE##_bare, linear_##TILE##_full, linear_##TILE##_pre, linear_##TILE##_slope
+extern const LinVariant TS_LINEAR_MODES(128_1), TS_LINEAR_MODES(256_1), TS_LINEAR_MODES(256_2);
 
 namespace {
 
@@ -20,12 +21,10 @@ constexpr int kRasterGroup = 8;
 // What a tile takes beside its columns, as columns: the loads and barriers of a K block.
 constexpr int64_t kWidthOverhead = 16;
 
-const LinVariant *find_linear(int bn, int cg, int pre) {
-    static const LinVariant *const all[] = {&linear_128_1,     &linear_128_1_pre, &linear_256_1,
-                                            &linear_256_1_pre, &linear_256_2,     &linear_256_2_pre};
-    for (const LinVariant *v : all)
-        if (v->bn == bn && v->cg == cg && v->pre == pre) return v;
-    return nullptr;
+const LinVariant &find_linear(int bn, int cg, int mode) {
+#define TS_LINEAR_TILE(TILE) {&linear_##TILE##_bare, &linear_##TILE##_full, &linear_##TILE##_pre, &linear_##TILE##_slope}
+    static const LinVariant *const all[3][4] = {TS_LINEAR_TILE(128_1), TS_LINEAR_TILE(256_1), TS_LINEAR_TILE(256_2)};
+    return *all[cg == 2 ? 2 : bn > 128 ? 1 : 0][mode];
 }
 
 int64_t aligned_pitch(int64_t ld, int64_t rows, int64_t cols, int unit) {
@@ -82,6 +81,7 @@ int64_t row_cycles(const void *ptr, int64_t rows, int64_t ld, int64_t batch, int
 
 LinPlan plan_product(const LinCall &c, int64_t sms) {
     const int64_t nkb = cdiv(c.K, 64);
+    const int kind = c.f16 ? OUT_F16 : c.out;
     const int64_t load_a = row_cycles(c.A, c.a_mn ? c.K : c.M, c.lda, c.batch, c.a_matrix);
     const int64_t load_b = row_cycles(c.B, c.b_mn ? c.K : c.N, c.ldb, c.batch, c.b_matrix);
     // cycles of a K block: what they are with rows on lines, or the loads of so many rows of A and B
@@ -105,10 +105,10 @@ LinPlan plan_product(const LinCall &c, int64_t sms) {
                 if (t < pl.cycles) pl.cycles = t, pl.sv = &v, pl.split = k, pl.ctas = ctas;
             }
         };
-        consider(split_128, u1, {0, 9350, 7500, 8200});
+        consider(split_128[kind], u1, {0, 9350, 7500, 8200});
         // an operand with its rows contiguous comes in boxes of 64
         if (!c.sym && c.batch == 1 && c.M <= 64)
-            consider(c.M <= 32 && !c.a_mn ? split_swap_32 : split_swap_64, n1, {6000, 6000, 6000, 6000});
+            consider(c.M <= 32 && !c.a_mn ? split_swap_32[kind] : split_swap_64[kind], n1, {6000, 6000, 6000, 6000});
     }
     // Columns of a 256-column tile: the width whose waves of workers take the fewest cycles in all.  With
     // B's rows contiguous a CTA's columns start on sectors, and on lines where they are whole boxes of 64:
@@ -159,8 +159,7 @@ ts_status linear_product(const LinCall &c) {
     const LinPlan pl = plan_product(c, sms);
     const SplitVariant *const sv = pl.sv;
     const int bn = pl.bn, cg = pl.cg;
-    const LinVariant *v = find_linear(bn > 128 ? 256 : 128, cg, c.pre ? 1 : 0);
-    if (!v) return fail(TS_ERR_UNSUPPORTED, "no compiled variant");
+    const LinVariant &v = find_linear(bn, cg, c.pre ? LIN_PRE : c.slope && c.act ? LIN_SLOPE : c.bias || c.act ? LIN_FULL : LIN_BARE);
 
     LinLaunch L;
     std::memset(&L, 0, sizeof L);
@@ -216,7 +215,6 @@ ts_status linear_product(const LinCall &c) {
     const uint32_t type = c.f16 ? 0u : 1u;
     p.idesc = (1u << 4) | (type << 7) | (type << 10) | (uint32_t(p.a_mn) << 15) | (uint32_t(p.b_mn) << 16);
     p.out = c.out;
-    p.aux_type = c.aux_type;
     p.act = c.act;
     p.slope = c.slope;
     p.sym = c.sym;
@@ -251,11 +249,11 @@ ts_status linear_product(const LinCall &c) {
     // Short K loops leave the epilogue as the bound: 4096 x 4096 x 256 14.7 us with two buffers, 15.7 with
     // one; x 1024 23.9 both.  Long ones need the ring: 2047 x 4096 x 6144 59.0 and 57.3.
     p.bufs = nkb <= 8 ? 2 : 1;
-    p.stages = v->stages(p.bufs);
+    p.stages = v.stages(p.bufs);
     int64_t workers = std::min<int64_t>(units, sms / cg);
     if (c.max_workers > 0) workers = std::min<int64_t>(workers, c.max_workers);
     L.grid = workers * cg;
-    const cudaError_t e = v->launch(L);
+    const cudaError_t e = v.launch[c.f16 ? OUT_F16 : c.out](L);
     return e == cudaSuccess ? TS_OK : cuda_fail(e, "linear product launch");
 }
 
@@ -356,7 +354,7 @@ ts_status grad_product(const char *b_name, const char *d_name, const Matrix &A, 
     c.N = D.cols;
     c.K = K;
     c.batch = 1;
-    c.out = c.aux_type = out;
+    c.out = out;
     c.act = slope ? o->act : ACT_NONE;
     c.slope = slope;
     c.alpha = c.beta = 1.f;
@@ -423,7 +421,7 @@ ts_status ts_linear(const void *x, const void *w, void *y, int64_t M, int64_t N,
     c.N = N;
     c.K = K;
     c.batch = 1;
-    c.out = c.aux_type = out_dtype;
+    c.out = out_dtype;
     c.act = o->act;
     c.alpha = c.beta = 1.f;
     c.tile = o->tile;

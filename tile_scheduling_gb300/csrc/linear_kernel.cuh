@@ -181,11 +181,16 @@ __device__ __forceinline__ LinUnit lin_unit(int32_t u, const LinParams &p) {
     return w;
 }
 
-template <int BN, int CG, int PRE>
-__global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
+// OUT: type of D.  OUT_BF16 and OUT_F32 are a layer's products (alpha = beta = 1, aux and pre of D's type, not
+// symmetric); OUT_F16 the iteration's: D fp16 or bf16 (p.out), aux fp16, without bias, activation and pre.
+// One kernel for all of them is slower: what the epilogue's loop executes then comes from places far apart,
+// and it waits for its instructions (8192 x 4096 x 64 in bf16 21.6 us, on its own 16.2).
+template <int BN, int CG, int MODE, int OUT>
+__global__ void __launch_bounds__(LinCfg<BN, CG, MODE == LIN_PRE>::THREADS, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmAux,
                   const __grid_constant__ CUtensorMap tmPre, const __grid_constant__ LinParams p) {
+    constexpr bool PRE = MODE == LIN_PRE;
     using C = LinCfg<BN, CG, PRE>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -378,8 +383,8 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
         const int q = j & 3, h = j >> 2;
         const uint32_t stg = s_epi + static_cast<uint32_t>(j) * (bufs + PRE) * C::EPI_BUF;
         const uint32_t stg_pre = stg + bufs * C::EPI_BUF;
-        const bool f32 = p.out == OUT_F32;
-        const int sub = f32 ? 32 : 64, esize = f32 ? 4 : 2;
+        constexpr bool f32 = OUT == OUT_F32, iteration = OUT == OUT_F16, full = MODE == LIN_FULL || PRE;
+        constexpr int sub = f32 ? 32 : 64, esize = f32 ? 4 : 2;
         const int cols = h ? p.bn - C::COLS : C::COLS;  // of this warp (of the kernel's tile the host may use fewer)
         const bool aux_tma = p.aux != nullptr && tma_d;
         // until the store that last used the next buffer has read it
@@ -420,7 +425,6 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
             if (!__shfl_sync(0xffffffffu, ok, 0)) break;
             tc_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * BN + C::COLS * h;
-            const int chunks = !work ? 0 : (col_end - col0 + 31) / 32;
             // the accumulator is read: back to the MMA issuer
             auto release = [&] {
                 tc_fence_before();
@@ -432,75 +436,97 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
                         mbar_arrive_cluster(mapa(tempty(acc), 0));
                 }
             };
-            if (chunks == 0) release();
+            if (!work) release();
+            const int rows = min(32, p.M - row0);
+            // a subtile at a time
 #pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(taddr + 32 * c, v);
-                const int s = 32 * c / sub;
+            for (int32_t s = 0, col = col0; work && col < col_end; ++s, col += sub) {
                 const uint32_t buf = static_cast<uint32_t>(s) & (bufs - 1), at = stg + buf * C::EPI_BUF;
-                const int32_t col = col0 + s * sub;  // of the subtile
-                const int piece = f32 ? 0 : (c & 1) * 4;  // 16-byte units of the chunk within the staged row
-                const bool head = f32 || (c & 1) == 0, done = f32 || (c & 1) == 1 || c + 1 == chunks;
-                const bool tma = tma_d && col + sub <= col_end;
-                const int rows = min(32, p.M - row0), left = min(col_end - col, sub) * esize;
-                if (head) {
-                    // the subtile's buffer: free, or holding aux
-                    if (aux_tma) {
-                        if (s >= static_cast<int>(bufs)) {
-                            __syncwarp();
-                            if (lane == 0) {
-                                bulk_wait_read<0>();
-                                fence_proxy_async_smem();
-                                load_aux(s);
-                            }
-                            aux_pending |= 1u << buf;
-                        }
-                        const bool got = wait_phase(aux_full(j, buf), (aux_phase >> buf) & 1u, abort_flag, p, WAIT_AUX);
-                        if (!__all_sync(0xffffffffu, got)) {
-                            alive = false;
-                            break;
-                        }
-                        aux_phase ^= 1u << buf;
-                        aux_pending &= ~(1u << buf);
-                    } else {
-                        if (lane == 0) wait_store();
+                const int left = min(col_end - col, sub) * esize;
+                const bool tma = tma_d && left == 128;
+                // its buffer: free, or holding aux
+                if (aux_tma) {
+                    if (s >= static_cast<int>(bufs)) {
                         __syncwarp();
-                        if (p.aux) {
-                            stage_rows_in(static_cast<const char *>(p.aux) +
-                                              (w.z * p.aux_matrix + static_cast<int64_t>(row0) * p.ld_aux + col) * esize,
-                                          p.ld_aux * esize, rows, left, p.store_bytes, at, lane);
-                            __syncwarp();
+                        if (lane == 0) {
+                            bulk_wait_read<0>();
+                            fence_proxy_async_smem();
+                            load_aux(s);
                         }
+                        aux_pending |= 1u << buf;
                     }
-                    if (PRE && aux_tma) {
-                        if (lane == 0) wait_store();  // the other buffer's store, and pre's before it
+                    const bool got = wait_phase(aux_full(j, buf), (aux_phase >> buf) & 1u, abort_flag, p, WAIT_AUX);
+                    if (!__all_sync(0xffffffffu, got)) {
+                        alive = false;
+                        break;
+                    }
+                    aux_phase ^= 1u << buf;
+                    aux_pending &= ~(1u << buf);
+                } else {
+                    if (lane == 0) wait_store();
+                    __syncwarp();
+                    if (p.aux) {
+                        stage_rows_in(static_cast<const char *>(p.aux) +
+                                          (w.z * p.aux_matrix + static_cast<int64_t>(row0) * p.ld_aux + col) * esize,
+                                      p.ld_aux * esize, rows, left, p.store_bytes, at, lane);
                         __syncwarp();
                     }
                 }
-                tmem_ld_wait();
-                if (c + 1 == chunks) release();
-                float x[32];
+                if (PRE && aux_tma) {
+                    if (lane == 0) wait_store();  // the other buffer's store, and pre's before it
+                    __syncwarp();
+                }
+                // 32 columns at a time: a subtile of fp32, half of a 16-bit one
+#pragma unroll 1
+                for (int32_t c0 = col, piece = 0; c0 < min(col + sub, col_end); c0 += 32, piece += 4) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(taddr + (c0 - col0), v);
+                    // The bias of the columns, fetched beside the accumulator: the same addresses in all lanes,
+                    // or, where they are not whole vectors, a column a lane.
+                    const bool bias_vec = p.bias_vec && c0 + 32 <= p.N;
+                    uint4 bias[full ? 8 : 1];
+                    if (full && p.bias) {
+                        if (!bias_vec) {
+                            if (c0 + lane < p.N)
+                                bias[0].x = p.bias_f32 ? __ldg(static_cast<const uint32_t *>(p.bias) + c0 + lane)
+                                                       : uint32_t(__ldg(static_cast<const uint16_t *>(p.bias) + c0 + lane)) << 16;
+                        } else if (p.bias_f32) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = p.num_kb > 0 ? p.alpha * __uint_as_float(v[i]) : 0.f;
-                if (p.bias) {
-                    // the same address in all lanes
-                    const int32_t c0 = col0 + 32 * c;
-                    if (p.bias_vec && c0 + 32 <= p.N) {
-                        if (p.bias_f32) {
+                            for (int i = 0; i < 8; ++i) bias[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const float *>(p.bias) + c0) + i);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) bias[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias) + c0) + i);
+                        }
+                    }
+                    tmem_ld_wait();
+                    if (c0 + 32 >= col_end) release();
+                    float x[32];
+                    if (p.num_kb > 0) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            x[i] = __uint_as_float(v[i]), x[i + 1] = __uint_as_float(v[i + 1]);
+                            if constexpr (iteration) split(two(p.alpha) * two(x[i], x[i + 1]), x[i], x[i + 1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = 0.f;
+                    }
+                    if (full && p.bias) {
+                        if (!bias_vec) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) x[i] += __uint_as_float(__shfl_sync(0xffffffffu, bias[0].x, i));
+                        } else if (p.bias_f32) {
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                const float4 b = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.bias) + c0) + i);
-                                x[4 * i] += b.x;
-                                x[4 * i + 1] += b.y;
-                                x[4 * i + 2] += b.z;
-                                x[4 * i + 3] += b.w;
+                                x[4 * i] += __uint_as_float(bias[i].x);
+                                x[4 * i + 1] += __uint_as_float(bias[i].y);
+                                x[4 * i + 2] += __uint_as_float(bias[i].z);
+                                x[4 * i + 3] += __uint_as_float(bias[i].w);
                             }
                         } else {
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const uint4 b = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias) + c0) + i);
-                                const uint32_t b4[4] = {b.x, b.y, b.z, b.w};
+                                const uint32_t b4[4] = {bias[i].x, bias[i].y, bias[i].z, bias[i].w};
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     x[8 * i + 2 * e] += __uint_as_float(b4[e] << 16);
@@ -508,111 +534,109 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, PRE>::THREADS, 1)
                                 }
                             }
                         }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c0 + i < p.N)
-                                x[i] += p.bias_f32 ? __ldg(static_cast<const float *>(p.bias) + c0 + i)
-                                                   : __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t *>(p.bias) + c0 + i)) << 16);
                     }
-                }
-                // x into this lane's row of a staging buffer
-                auto put = [&](uint32_t buffer) {
-                    const uint32_t row_at = buffer + lane * 128;
-                    if (f32) {
+                    // x into this lane's row of a staging buffer
+                    auto put = [&](uint32_t buffer) {
+                        const uint32_t row_at = buffer + lane * 128;
+                        if constexpr (f32) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            st_shared_v4(row_at + ((i ^ (lane & 7)) << 4), __float_as_uint(x[4 * i]),
-                                         __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]),
-                                         __float_as_uint(x[4 * i + 3]));
-                    } else {
-                        uint32_t o[16];
+                            for (int i = 0; i < 8; ++i)
+                                st_shared_v4(row_at + ((i ^ (lane & 7)) << 4), __float_as_uint(x[4 * i]),
+                                             __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]),
+                                             __float_as_uint(x[4 * i + 3]));
+                        } else {
+                            uint32_t o[16];
+                            if (iteration && p.out == OUT_F16) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            o[i] = p.out == OUT_BF16 ? pack_bf16x2(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]))
-                                                     : pack_f16x2(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]));
+                                for (int i = 0; i < 16; ++i)
+                                    o[i] = pack_f16x2(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]));
+                            } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            st_shared_v4(row_at + (((piece + i) ^ (lane & 7)) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2],
-                                         o[4 * i + 3]);
-                        if (p.sym && w.nb > w.mb) {
-                            // The entry's mirror image: a column of this warp's is 32 consecutive values
-                            // there.  Lanes 2i and 2i + 1 exchange halves, so that an even lane holds two rows
-                            // of an even column, an odd one of the column behind it, and stores them at once.
-                            const int32_t r = row0 + (lane & ~1), c0 = col0 + 32 * c + (lane & 1);
-                            uint16_t *m = static_cast<uint16_t *>(p.D) + w.z * p.d_matrix + c0 * p.ldd + r;
+                                for (int i = 0; i < 16; ++i)
+                                    o[i] = pack_bf16x2(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]));
+                            }
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const uint32_t got = __shfl_xor_sync(0xffffffffu, o[i], 1);
-                                const uint32_t two = lane & 1 ? __byte_perm(got, o[i], 0x7632) : __byte_perm(o[i], got, 0x5410);
-                                // rows of the mirror image: D, of a multiple of eight rows and columns, is square
-                                if (c0 + 2 * i < p.N && r < p.M) *reinterpret_cast<uint32_t *>(m) = two;
-                                m += 2 * p.ldd;
+                            for (int i = 0; i < 4; ++i)
+                                st_shared_v4(row_at + (((piece + i) ^ (lane & 7)) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2],
+                                             o[4 * i + 3]);
+                            if (iteration && p.sym && w.nb > w.mb) {
+                                // The entry's mirror image: a column of this warp's is 32 consecutive values
+                                // there.  Lanes 2i and 2i + 1 exchange halves, so that an even lane holds two rows
+                                // of an even column, an odd one of the column behind it, and stores them at once.
+                                const int32_t r = row0 + (lane & ~1), cm = c0 + (lane & 1);
+                                uint16_t *m = static_cast<uint16_t *>(p.D) + w.z * p.d_matrix + cm * p.ldd + r;
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    const uint32_t got = __shfl_xor_sync(0xffffffffu, o[i], 1);
+                                    const uint32_t both = lane & 1 ? __byte_perm(got, o[i], 0x7632) : __byte_perm(o[i], got, 0x5410);
+                                    // rows of the mirror image: D, of a multiple of eight rows and columns, is square
+                                    if (cm + 2 * i < p.N && r < p.M) *reinterpret_cast<uint32_t *>(m) = both;
+                                    m += 2 * p.ldd;
+                                }
+                            }
+                        }
+                    };
+                    if constexpr (PRE) put(stg_pre);
+                    float a[32];
+                    if (p.aux) {
+                        const uint32_t row_at = at + lane * 128;
+                        if constexpr (f32) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const uint4 t = ld_shared_v4(row_at + ((i ^ (lane & 7)) << 4));
+                                a[4 * i] = __uint_as_float(t.x);
+                                a[4 * i + 1] = __uint_as_float(t.y);
+                                a[4 * i + 2] = __uint_as_float(t.z);
+                                a[4 * i + 3] = __uint_as_float(t.w);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint4 t = ld_shared_v4(row_at + (((piece + i) ^ (lane & 7)) << 4));
+                                const uint32_t w4[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    a[8 * i + 2 * e] = iteration ? f16_to_f32(static_cast<uint16_t>(w4[e])) : __uint_as_float(w4[e] << 16);
+                                    a[8 * i + 2 * e + 1] = iteration ? f16_to_f32(static_cast<uint16_t>(w4[e] >> 16))
+                                                                     : __uint_as_float(w4[e] & 0xffff0000u);
+                                }
                             }
                         }
                     }
-                };
-                // the staged subtile leaves for `dst`
-                auto leave = [&](uint32_t buffer, const CUtensorMap *map, void *dst, int64_t matrix, int64_t ld) {
-                    if (tma) fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (tma) tma_store_3d(map, buffer, col, row0, w.z, policy_evict_first());
-                        bulk_commit();
+                    if constexpr (MODE == LIN_SLOPE) {
+                        apply_slope(p.act, x, a);
+                    } else {
+                        if constexpr (full) apply_act(p.act, x);
+                        if (p.aux) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                if constexpr (iteration)
+                                    split(fma(two(p.beta), two(a[i], a[i + 1]), two(x[i], x[i + 1])), x[i], x[i + 1]);
+                                else
+                                    split(two(a[i], a[i + 1]) + two(x[i], x[i + 1]), x[i], x[i + 1]);
+                            }
+                        }
                     }
-                    if (!tma)
+                    put(at);
+                }
+                // the staged subtiles leave
+                auto leave = [&](uint32_t buffer, const CUtensorMap *map, void *dst, int64_t matrix, int64_t ld) {
+                    if (tma) {
+                        tma_store_3d(map, buffer, col, row0, w.z, policy_evict_first());
+                    } else {
                         stage_rows_out(static_cast<char *>(dst) +
                                            (w.z * matrix + static_cast<int64_t>(row0) * ld + col) * esize,
                                        ld * esize, rows, left, p.store_bytes, buffer, lane);
+                    }
                 };
-                if (PRE) {
-                    put(stg_pre);
-                    if (done) leave(stg_pre, &tmPre, p.pre, 0, p.ld_pre);
+                if (tma) fence_proxy_async_smem();
+                __syncwarp();
+                if constexpr (PRE) {
+                    if (!tma || lane == 0) leave(stg_pre, &tmPre, p.pre, 0, p.ld_pre);
+                    if (lane == 0) bulk_commit();
                 }
-                float a[32];
-                if (p.aux) {
-                    const uint32_t row_at = at + lane * 128;
-                    if (f32) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint4 t = ld_shared_v4(row_at + ((i ^ (lane & 7)) << 4));
-                            a[4 * i] = __uint_as_float(t.x);
-                            a[4 * i + 1] = __uint_as_float(t.y);
-                            a[4 * i + 2] = __uint_as_float(t.z);
-                            a[4 * i + 3] = __uint_as_float(t.w);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint4 t = ld_shared_v4(row_at + (((piece + i) ^ (lane & 7)) << 4));
-                            const uint32_t w4[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                a[8 * i + 2 * e] = p.aux_type == OUT_BF16 ? __uint_as_float(w4[e] << 16)
-                                                                          : f16_to_f32(static_cast<uint16_t>(w4[e]));
-                                a[8 * i + 2 * e + 1] = p.aux_type == OUT_BF16 ? __uint_as_float(w4[e] & 0xffff0000u)
-                                                                              : f16_to_f32(static_cast<uint16_t>(w4[e] >> 16));
-                            }
-                        }
-                    }
-                }
-                if (p.slope) {
-                    with_act(p.act, [&](auto tag) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] *= act_slope<decltype(tag)::value>(a[i]);
-                    });
-                } else {
-                    with_act(p.act, [&](auto tag) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = act_of<decltype(tag)::value>(x[i]);
-                    });
-                    if (p.aux) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = fmaf(p.beta, a[i], x[i]);
-                    }
-                }
-                put(at);
-                if (done) leave(at, &tmD, p.D, p.d_matrix, p.ldd);
+                if (!tma || lane == 0) leave(at, &tmD, p.D, p.d_matrix, p.ldd);
+                if (lane == 0) bulk_commit();
             }
             if (++acc == 2) {
                 acc = 0;

@@ -8,10 +8,10 @@
 namespace ts {
 namespace {
 
-template <int BN, int CG, int PRE>
+template <int BN, int CG, int MODE, int OUT>
 cudaError_t linear_launch(const LinLaunch &L) {
-    using C = LinCfg<BN, CG, PRE>;
-    auto *kernel = linear_kernel<BN, CG, PRE>;
+    using C = LinCfg<BN, CG, MODE == LIN_PRE>;
+    auto *kernel = linear_kernel<BN, CG, MODE, OUT>;
     static std::atomic<uint64_t> prepared{0};  // devices
     const int dev = current_device();
     const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
@@ -40,16 +40,28 @@ cudaError_t linear_launch(const LinLaunch &L) {
     return cudaLaunchKernelEx(&cfg, kernel, L.a, L.b, L.d, L.aux, L.pre, L.p);
 }
 
-template <int BN, int CG, int PRE>
+template <int BN, int CG, int MODE>
 int linear_stages(int bufs) {
-    return LinCfg<BN, CG, PRE>::stages(bufs);
+    return LinCfg<BN, CG, MODE == LIN_PRE>::stages(bufs);
+}
+
+template <int BN, int CG, int MODE>
+constexpr auto iteration_launch() -> cudaError_t (*)(const LinLaunch &) {
+    if constexpr (MODE == LIN_BARE)
+        return &linear_launch<BN, CG, MODE, OUT_F16>;
+    else
+        return nullptr;
 }
 
 }  // namespace
 }  // namespace ts
 
-#define TS_LINEAR_VARIANT(NAME, BN, CG, PRE)                                                               \
-    namespace ts {                                                                                         \
-    extern const LinVariant NAME;                                                                          \
-    const LinVariant NAME = {BN, CG, PRE, &linear_launch<BN, CG, PRE>, &linear_stages<BN, CG, PRE>};       \
+// One for each type of D.
+#define TS_LINEAR_VARIANT(NAME, BN, CG, MODE)                                                                     \
+    namespace ts {                                                                                                \
+    extern const LinVariant NAME;                                                                                 \
+    const LinVariant NAME = {BN, CG, MODE,                                                                        \
+                             {&linear_launch<BN, CG, MODE, OUT_BF16>, &linear_launch<BN, CG, MODE, OUT_F32>,      \
+                              iteration_launch<BN, CG, MODE>()},                                                  \
+                             &linear_stages<BN, CG, MODE>};                                                       \
     }

@@ -27,15 +27,14 @@ struct LinParams {
     FastDiv div_matrix;
     int32_t a_mn, b_mn;               // 1: the operand lies with its rows of D (its columns) contiguous, not K
     uint32_t idesc;                   // MMA instruction descriptor without the tile shape
-    int32_t out;                      // OUT_BF16 / OUT_F32 / OUT_F16, also of pre
-    int32_t aux_type;                 // of aux, of the same size as out
+    int32_t out;                      // OUT_BF16 / OUT_F32 / OUT_F16, also of pre (and of aux but in the iteration)
     int32_t act;                      // of the forward epilogue, or whose slope the backward one multiplies by
     int32_t slope;                    // 0: D = act(alpha * acc + bias) + beta * aux; 1: D = alpha * acc * act'(aux)
     int32_t stages;                   // of the operand ring
     int32_t split;                    // the split kernel: CTAs of a cluster that share K
     int32_t sym;                      // 1: D is symmetric: tiles above the diagonal are stored twice
     int32_t store_bytes;              // 16, 4 or 2: what the bases and rows of D, aux and pre are aligned to
-    float alpha, beta;
+    float alpha, beta;                // the iteration's products; 1 otherwise
     const void *bias;                 // N values added to every row, or NULL
     int32_t bias_f32, bias_vec;       // bias_vec: it starts on a 16-byte boundary
     const void *aux;                  // residual or pre-activation [M][N], or NULL
@@ -55,9 +54,12 @@ struct LinLaunch {
     cudaStream_t stream;
 };
 
+// What a product's epilogue has beside the sum: aux at most; bias, activation and aux; pre as well; the slope.
+enum : int { LIN_BARE, LIN_FULL, LIN_PRE, LIN_SLOPE };
+
 struct LinVariant {
-    int bn, cg, pre;
-    cudaError_t (*launch)(const LinLaunch &);
+    int bn, cg, mode;
+    cudaError_t (*launch[3])(const LinLaunch &);  // by the type of D, OUT_F16: the iteration's products
     int (*stages)(int bufs);
 };
 
@@ -75,7 +77,7 @@ struct LinCall {
     const void *A, *B;
     int64_t lda, ldb, a_matrix, b_matrix;  // elements
     int64_t a_rows, b_rows;                // rows that the operands have, 0: M and N (the rest of D comes of zeros)
-    int a_mn, b_mn, f16;                   // f16: operands fp16, else bf16
+    int a_mn, b_mn, f16;                   // f16: a product of the iteration, with fp16 operands and aux; else bf16, aux as D
     void *D;
     int64_t ldd, d_matrix;
     const void *aux;
@@ -85,7 +87,7 @@ struct LinCall {
     const void *bias;
     int bias_f32;
     int64_t M, N, K, batch;
-    int out, aux_type, act, slope, sym;
+    int out, act, slope, sym;
     float alpha, beta;
     int tile;                              // ts_tile
     int64_t max_workers;

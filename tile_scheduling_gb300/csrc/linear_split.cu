@@ -6,22 +6,22 @@
 namespace ts {
 namespace {
 
-template <int BN, bool SWAP>
+template <int BN, bool SWAP, int OUT>
 cudaError_t split_prepare() {
     static std::atomic<uint64_t> prepared{0};  // devices
     const int dev = current_device();
     const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
     if (bit && (prepared.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(linear_split_kernel<BN, SWAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(linear_split_kernel<BN, SWAP, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kSmemLimit);
     if (e == cudaSuccess && bit) prepared.fetch_or(bit, std::memory_order_acq_rel);
     return e;
 }
 
-template <int BN, bool SWAP>
+template <int BN, bool SWAP, int OUT>
 cudaError_t split_launch(const LinLaunch &L) {
     using C = SplitCfg<BN, SWAP>;
-    const cudaError_t e = split_prepare<BN, SWAP>();
+    const cudaError_t e = split_prepare<BN, SWAP, OUT>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(L.grid), 1, 1);
@@ -40,17 +40,17 @@ cudaError_t split_launch(const LinLaunch &L) {
         attr[1].val.clusterDim.z = 1;
         cfg.numAttrs = 2;
     }
-    return cudaLaunchKernelEx(&cfg, linear_split_kernel<BN, SWAP>, L.a, L.b, L.p);
+    return cudaLaunchKernelEx(&cfg, linear_split_kernel<BN, SWAP, OUT>, L.a, L.b, L.p);
 }
 
 // Clusters of `size` CTAs that run at once with one or two of them on an SM (0: none, or an error),
 // asked once per size.
-template <int BN, bool SWAP>
+template <int BN, bool SWAP, int OUT>
 int split_clusters(int size, int ctas) {
     using C = SplitCfg<BN, SWAP>;
     static std::atomic<int> known[2][kMaxSplit + 1];  // their number + 1; devices of a process are alike
     if (const int n = known[ctas - 1][size].load(std::memory_order_relaxed)) return n - 1;
-    if (split_prepare<BN, SWAP>() != cudaSuccess) return 0;
+    if (split_prepare<BN, SWAP, OUT>() != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(size), 1, 1);
     cfg.blockDim = dim3(C::THREADS, 1, 1);
@@ -63,7 +63,7 @@ int split_clusters(int size, int ctas) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, linear_split_kernel<BN, SWAP>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, linear_split_kernel<BN, SWAP, OUT>, &cfg) != cudaSuccess) {
         (void)cudaGetLastError();
         return 0;
     }
@@ -71,19 +71,21 @@ int split_clusters(int size, int ctas) {
     return n;
 }
 
-template <int BN, bool SWAP>
+template <int BN, bool SWAP, int OUT>
 int split_stages(int split, int ctas) {
     return SplitCfg<BN, SWAP>::stages(split, ctas);
 }
 
+template <int BN, bool SWAP, int OUT>
+constexpr SplitVariant variant() {
+    return {BN, SWAP, &split_launch<BN, SWAP, OUT>, &split_clusters<BN, SWAP, OUT>, &split_stages<BN, SWAP, OUT>};
+}
+
 }  // namespace
 
-extern const SplitVariant split_128, split_swap_64, split_swap_32;
-const SplitVariant split_128 = {128, 0, &split_launch<128, false>, &split_clusters<128, false>,
-                                &split_stages<128, false>};
-const SplitVariant split_swap_64 = {64, 1, &split_launch<64, true>, &split_clusters<64, true>,
-                                &split_stages<64, true>};
-const SplitVariant split_swap_32 = {32, 1, &split_launch<32, true>, &split_clusters<32, true>,
-                                &split_stages<32, true>};
+extern const SplitVariant split_128[3], split_swap_64[3], split_swap_32[3];
+const SplitVariant split_128[3] = {variant<128, false, 0>(), variant<128, false, 1>(), variant<128, false, 2>()};
+const SplitVariant split_swap_64[3] = {variant<64, true, 0>(), variant<64, true, 1>(), variant<64, true, 2>()};
+const SplitVariant split_swap_32[3] = {variant<32, true, 0>(), variant<32, true, 1>(), variant<32, true, 2>()};
 
 }  // namespace ts

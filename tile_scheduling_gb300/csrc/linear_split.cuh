@@ -102,7 +102,8 @@ __device__ __forceinline__ void store8(void *q, int64_t i, int type, bool whole,
     }
 }
 
-template <int BN, bool SWAP>
+// OUT as in the persistent kernel.
+template <int BN, bool SWAP, int OUT>
 __global__ void __launch_bounds__(SplitCfg<BN, SWAP>::THREADS, 2)
     linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ LinParams p) {
@@ -271,18 +272,20 @@ __global__ void __launch_bounds__(SplitCfg<BN, SWAP>::THREADS, 2)
     const int32_t row_at = row0 + (SWAP ? 0 : part * share), col_at = col0 + (SWAP ? part * share : 0);
     // A lane a group, or (symmetric) a lane a row: an entry's mirror image then lies next to that of
     // the lane beside it.
-    const bool mirror = p.sym && w.nb > w.mb;
+    constexpr bool iteration = OUT == OUT_F16;
+    const int out = iteration && p.out == OUT_BF16 ? OUT_BF16 : OUT;
+    const bool sym = iteration && p.sym, mirror = sym && w.nb > w.mb;
     const int32_t log_r = 31 - __clz(share);
-    const int32_t turns = p.sym ? share << log_g : R << log_g;
+    const int32_t turns = sym ? share << log_g : R << log_g;
 #pragma unroll 1
     for (int32_t i = static_cast<int32_t>(threadIdx.x); i < turns; i += C::THREADS) {
-        const int32_t r = p.sym ? i & (share - 1) : i >> log_g, g = p.sym ? i >> log_r : i & ((1 << log_g) - 1);
+        const int32_t r = sym ? i & (share - 1) : i >> log_g, g = sym ? i >> log_r : i & ((1 << log_g) - 1);
         const int32_t row = row_at + r, col = col_at + 8 * g;
         const int32_t count = min(8, p.N - col);
         if (count <= 0 || r >= R) continue;
         const bool whole = count == 8 && p.store_bytes == 16;
         float a[8];
-        if (p.aux) load8(p.aux, w.z * p.aux_matrix + row * p.ld_aux + col, p.aux_type, whole, count, a);
+        if (p.aux) load8(p.aux, w.z * p.aux_matrix + row * p.ld_aux + col, OUT, whole, count, a);
         float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         const uint32_t at = s_slot + (SWAP ? (r * share + 8 * g) * 4 : (2 * g * (share + 1) + r) * 16);
         const uint32_t next = SWAP ? 16 : (share + 1) * 16;            // the group's other four columns
@@ -297,34 +300,30 @@ __global__ void __launch_bounds__(SplitCfg<BN, SWAP>::THREADS, 2)
                 x[6] += __uint_as_float(v.z), x[7] += __uint_as_float(v.w);
             }
         }
+        if constexpr (iteration) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] *= p.alpha;
-        if (p.bias) {
+            for (int k = 0; k < 8; ++k) x[k] *= p.alpha;
+        }
+        if (!iteration && p.bias) {
             float b[8];
             load8(p.bias, col, p.bias_f32 ? OUT_F32 : OUT_BF16, p.bias_vec && count == 8, count, b);
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[k] += b[k];
         }
-        if (p.pre) store8(p.pre, row * p.ld_pre + col, p.out, whole, count, x);
-        if (p.slope) {
-            with_act(p.act, [&](auto tag) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) x[k] *= act_slope<decltype(tag)::value>(a[k]);
-            });
+        if (!iteration && p.pre) store8(p.pre, row * p.ld_pre + col, OUT, whole, count, x);
+        if (!iteration && p.slope) {
+            apply_slope(p.act, x, a);
         } else {
-            with_act(p.act, [&](auto tag) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) x[k] = act_of<decltype(tag)::value>(x[k]);
-            });
+            if constexpr (!iteration) apply_act(p.act, x);
             if (p.aux) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) x[k] = fmaf(p.beta, a[k], x[k]);
+                for (int k = 0; k < 8; ++k) x[k] = iteration ? fmaf(p.beta, a[k], x[k]) : x[k] + a[k];
             }
         }
-        store8(p.D, w.z * p.d_matrix + row * p.ldd + col, p.out, whole, count, x);
+        store8(p.D, w.z * p.d_matrix + row * p.ldd + col, out, whole, count, x);
         if (mirror) {
             uint32_t o[4];
-            pack8(p.out, x, o);
+            pack8(out, x, o);
             uint16_t *const m = static_cast<uint16_t *>(p.D) + w.z * p.d_matrix + row;
 #pragma unroll
             for (int k = 0; k < 8; ++k)

@@ -81,7 +81,7 @@ LinCall orth_product(const OrthRun &r, int32_t i, int which) {
     LinCall c;
     std::memset(&c, 0, sizeof c);
     c.f16 = 1;
-    c.out = c.aux_type = OUT_F16;
+    c.out = OUT_F16;
     c.batch = r.batch;
     c.timeout_s = r.timeout_s;
     c.stream = r.stream;
