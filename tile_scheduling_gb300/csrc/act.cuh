@@ -150,24 +150,24 @@ __device__ __forceinline__ void with_act(int act, F &&f) {
         case ACT_GELU: f(ActTag<ACT_GELU>{}); break;
         case ACT_GELU_TANH: f(ActTag<ACT_GELU_TANH>{}); break;
         case ACT_SILU: f(ActTag<ACT_SILU>{}); break;
-        default: break;
+        default: f(ActTag<ACT_NONE>{}); break;
     }
 }
 // x[i] = act(x[i]), and x[i] *= act'(a[i]), for an even number of values
-template <int N>
-__device__ __forceinline__ void apply_act(int act, float (&x)[N]) {
-    with_act(act, [&](auto tag) {
+template <int ACT, int N>
+__device__ __forceinline__ void apply_act(float (&x)[N]) {
+    if constexpr (ACT != ACT_NONE) {
 #pragma unroll
-        for (int i = 0; i < N; i += 2) split(act_of<decltype(tag)::value>(two(x[i], x[i + 1])), x[i], x[i + 1]);
-    });
+        for (int i = 0; i < N; i += 2) split(act_of<ACT>(two(x[i], x[i + 1])), x[i], x[i + 1]);
+    }
 }
-template <int N>
-__device__ __forceinline__ void apply_slope(int act, float (&x)[N], const float (&a)[N]) {
-    with_act(act, [&](auto tag) {
+template <int ACT, int N>
+__device__ __forceinline__ void apply_slope(float (&x)[N], const float (&a)[N]) {
+    if constexpr (ACT != ACT_NONE) {
 #pragma unroll
         for (int i = 0; i < N; i += 2)
-            split(two(x[i], x[i + 1]) * act_slope<decltype(tag)::value>(two(a[i], a[i + 1])), x[i], x[i + 1]);
-    });
+            split(two(x[i], x[i + 1]) * act_slope<ACT>(two(a[i], a[i + 1])), x[i], x[i + 1]);
+    }
 }
 
 }  // namespace ts

@@ -151,10 +151,7 @@ __global__ void __launch_bounds__(kActThreads, kActCtas) act_grad_kernel(const _
             }
         }
     };
-    if (p.act == ACT_NONE)
-        rows(ActTag<ACT_NONE>{});
-    else
-        with_act(p.act, rows);
+    with_act(p.act, rows);
     if (!p.gb) return;
 #pragma unroll
     for (int i = 0; i < V; ++i) part[ty][tx * V + i] = sum[i];

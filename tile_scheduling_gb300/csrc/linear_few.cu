@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kFewThreads, CTAS) linear_few_kernel(const __g
     if (p.bias) z += value(p.bias, n, p.bias_f32);
     if (p.pre) store(p.pre, m * p.ld_pre + n, z);
     float one[2] = {z, z};
-    apply_act(p.act, one);
+    with_act(p.act, [&](auto act) { apply_act<decltype(act)::value>(one); });
     float f = one[0];
     if (p.aux) f += value(p.aux, m * p.ld_aux + n, p.out == OUT_F32);
     store(p.y, m * p.ldy + n, f);

@@ -397,6 +397,8 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, MODE == LIN_PRE>::THREADS, 1)
         uint32_t acc = 0, acc_phase = 0, aux_phase = 0;  // aux_phase: bit b, parity of buffer b's next load
         uint32_t aux_pending = 0;                        // bit b: a load into buffer b has not been waited for
         bool alive = true;
+        auto tiles = [&](auto act) {
+        constexpr int ACT = decltype(act)::value;
         for (int32_t u = first; u < p.num_units && alive; u += step) {
             const LinUnit w = lin_unit<C>(u, p);
             const int32_t row0 = w.mb * C::TILE_M + static_cast<int32_t>(rank) * C::BM + 32 * q;
@@ -604,9 +606,9 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, MODE == LIN_PRE>::THREADS, 1)
                         }
                     }
                     if constexpr (MODE == LIN_SLOPE) {
-                        apply_slope(p.act, x, a);
+                        apply_slope<ACT>(x, a);
                     } else {
-                        if constexpr (full) apply_act(p.act, x);
+                        apply_act<ACT>(x);
                         if (p.aux) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 2) {
@@ -643,6 +645,12 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, MODE == LIN_PRE>::THREADS, 1)
                 acc_phase ^= 1u;
             }
         }
+        };
+        // a loop for each activation, so that a tile's instructions lie together
+        if constexpr (MODE == LIN_BARE)
+            tiles(ActTag<ACT_NONE>{});
+        else
+            with_act(p.act, tiles);
         // loads of aux that a given-up wait left in flight
         for (uint32_t b = 0; b < bufs; ++b)
             if ((aux_pending >> b) & 1u) wait_drain(aux_full(j, b), (aux_phase >> b) & 1u, abort_flag, p);

@@ -312,9 +312,9 @@ __global__ void __launch_bounds__(SplitCfg<BN, SWAP>::THREADS, 2)
         }
         if (!iteration && p.pre) store8(p.pre, row * p.ld_pre + col, OUT, whole, count, x);
         if (!iteration && p.slope) {
-            apply_slope(p.act, x, a);
+            with_act(p.act, [&](auto act) { apply_slope<decltype(act)::value>(x, a); });
         } else {
-            if constexpr (!iteration) apply_act(p.act, x);
+            if constexpr (!iteration) with_act(p.act, [&](auto act) { apply_act<decltype(act)::value>(x); });
             if (p.aux) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) x[k] = iteration ? fmaf(p.beta, a[k], x[k]) : x[k] + a[k];
