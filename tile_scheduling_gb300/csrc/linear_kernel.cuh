@@ -56,10 +56,10 @@ struct LinCfg {
     // with short K loops alone, where the epilogue's latency shows (see the host).
     static constexpr int EPI_BUF = 32 * 128, MAX_BUFS = 2;
     static constexpr int TMEM_COLS = 2 * BN;
-    static constexpr int BAR_BYTES = 512;
+    static constexpr int BAR_BYTES = 512, BIAS_BYTES = EPI_WARPS * 128;
     static constexpr int MAX_STAGES = 8;
     static constexpr int smem_bytes(int stages, int bufs) {
-        return 1024 + stages * STAGE_BYTES + EPI_WARPS * (bufs + PRE) * EPI_BUF + BAR_BYTES;
+        return 1024 + stages * STAGE_BYTES + EPI_WARPS * (bufs + PRE) * EPI_BUF + BIAS_BYTES + BAR_BYTES;
     }
     static constexpr int stages(int bufs) {
         const int n = (kSmemLimit - smem_bytes(0, bufs)) / STAGE_BYTES;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, MODE == LIN_PRE>::THREADS, 1)
     const uint32_t s_a = base;
     const uint32_t s_b = s_a + stages * C::A_BYTES;
     const uint32_t s_epi = s_b + stages * C::B_BYTES;
-    const uint32_t s_bar = s_epi + C::EPI_WARPS * (bufs + PRE) * C::EPI_BUF;
+    const uint32_t s_bias = s_epi + C::EPI_WARPS * (bufs + PRE) * C::EPI_BUF, s_bar = s_bias + C::BIAS_BYTES;
     auto full = [&](uint32_t s) { return s_bar + 8u * s; };
     auto empty = [&](uint32_t s) { return s_bar + 8u * (stages + s); };
     auto tfull = [&](uint32_t a) { return s_bar + 8u * (2 * stages + a); };
@@ -397,6 +397,20 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, MODE == LIN_PRE>::THREADS, 1)
         uint32_t acc = 0, acc_phase = 0, aux_phase = 0;  // aux_phase: bit b, parity of buffer b's next load
         uint32_t aux_pending = 0;                        // bit b: a load into buffer b has not been waited for
         bool alive = true;
+        // The bias of a tile's columns, one of every 32 for a lane, fetched a tile ahead: a tile's columns are
+        // seldom those of the tile before, and the fetch comes from L2.
+        constexpr int CHUNKS = C::COLS / 32;
+        float bias[CHUNKS];
+        const uint32_t bias_at = s_bias + 128 * j;
+        auto fetch_bias = [&](int32_t u) {
+            const int32_t c0 = u < p.num_units ? lin_unit<C>(u, p).nb * p.bn + C::COLS * h + lane : p.N;
+#pragma unroll
+            for (int i = 0; i < CHUNKS; ++i)
+                bias[i] = c0 + 32 * i >= p.N ? 0.f
+                          : p.bias_f32       ? __ldg(static_cast<const float *>(p.bias) + c0 + 32 * i)
+                                             : __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t *>(p.bias) + c0 + 32 * i)) << 16);
+        };
+        if (full && p.bias) fetch_bias(first);
         auto tiles = [&](auto act) {
         constexpr int ACT = decltype(act)::value;
         for (int32_t u = first; u < p.num_units && alive; u += step) {
@@ -440,6 +454,12 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, MODE == LIN_PRE>::THREADS, 1)
             };
             if (!work) release();
             const int rows = min(32, p.M - row0);
+            float bias_now[CHUNKS];
+            if (full && p.bias) {
+#pragma unroll
+                for (int i = 0; i < CHUNKS; ++i) bias_now[i] = bias[i];
+                fetch_bias(u + step);
+            }
             // a subtile at a time
 #pragma unroll 1
             for (int32_t s = 0, col = col0; work && col < col_end; ++s, col += sub) {
@@ -483,22 +503,13 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, MODE == LIN_PRE>::THREADS, 1)
                 for (int32_t c0 = col, piece = 0; c0 < min(col + sub, col_end); c0 += 32, piece += 4) {
                     uint32_t v[32];
                     tmem_ld_32x32b_x32(taddr + (c0 - col0), v);
-                    // The bias of the columns, fetched beside the accumulator: the same addresses in all lanes,
-                    // or, where they are not whole vectors, a column a lane.
-                    const bool bias_vec = p.bias_vec && c0 + 32 <= p.N;
-                    uint4 bias[full ? 8 : 1];
                     if (full && p.bias) {
-                        if (!bias_vec) {
-                            if (c0 + lane < p.N)
-                                bias[0].x = p.bias_f32 ? __ldg(static_cast<const uint32_t *>(p.bias) + c0 + lane)
-                                                       : uint32_t(__ldg(static_cast<const uint16_t *>(p.bias) + c0 + lane)) << 16;
-                        } else if (p.bias_f32) {
+                        float b = bias_now[0];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) bias[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const float *>(p.bias) + c0) + i);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) bias[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias) + c0) + i);
-                        }
+                        for (int i = 1; i < CHUNKS; ++i) b = c0 - col0 == 32 * i ? bias_now[i] : b;
+                        __syncwarp();  // the last chunk's have been read
+                        st_shared_f32(bias_at + 4 * lane, b);
+                        __syncwarp();
                     }
                     tmem_ld_wait();
                     if (c0 + 32 >= col_end) release();
@@ -514,27 +525,11 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, MODE == LIN_PRE>::THREADS, 1)
                         for (int i = 0; i < 32; ++i) x[i] = 0.f;
                     }
                     if (full && p.bias) {
-                        if (!bias_vec) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) x[i] += __uint_as_float(__shfl_sync(0xffffffffu, bias[0].x, i));
-                        } else if (p.bias_f32) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                x[4 * i] += __uint_as_float(bias[i].x);
-                                x[4 * i + 1] += __uint_as_float(bias[i].y);
-                                x[4 * i + 2] += __uint_as_float(bias[i].z);
-                                x[4 * i + 3] += __uint_as_float(bias[i].w);
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t b4[4] = {bias[i].x, bias[i].y, bias[i].z, bias[i].w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    x[8 * i + 2 * e] += __uint_as_float(b4[e] << 16);
-                                    x[8 * i + 2 * e + 1] += __uint_as_float(b4[e] & 0xffff0000u);
-                                }
-                            }
+                        for (int i = 0; i < 8; ++i) {  // the same address in all lanes
+                            const uint4 b = ld_shared_v4(bias_at + 16 * i);
+                            split(two(x[4 * i], x[4 * i + 1]) + two(__uint_as_float(b.x), __uint_as_float(b.y)), x[4 * i], x[4 * i + 1]);
+                            split(two(x[4 * i + 2], x[4 * i + 3]) + two(__uint_as_float(b.z), __uint_as_float(b.w)), x[4 * i + 2], x[4 * i + 3]);
                         }
                     }
                     // x into this lane's row of a staging buffer
