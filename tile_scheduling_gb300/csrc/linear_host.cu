@@ -114,17 +114,21 @@ LinPlan plan_product(const LinCall &c, int64_t sms) {
     // B's rows contiguous a CTA's columns start on sectors, and on lines where they are whole boxes of 64:
     // 4096 x 4096 x 4096 on pairs 81 us with 224 columns (four waves either way), 87 with 256;
     // 4096 x 2048 x 2048 24.6 with 256, 30.1 with 240, whose halves start off sectors.
-    auto cost = [&](int64_t pair, int64_t bn) {  // of a K block
+    auto cost = [&](int64_t pair, int64_t bn) {  // of a K block on a 256-column tile
         return block((pair == 2 ? 520 : 590) * (bn + kWidthOverhead) / (256 + kWidthOverhead), 128, bn / pair,
                      c.b_mn && bn % (64 * pair) != 0 ? 30 : 0);
     };
+    // Short K loops hide behind the epilogues: cycles of one, from 8192 x 4096 x 64 on 128- and 256-column tiles
+    // (bf16 18.5 and 15.4 us, with silu 28.2 and 27.1, with a residual 29.5 and 27.9; fp32 22.4 and 23.6).
+    const int64_t column = 1250 + (c.act ? 1450 : 0) + (c.aux ? 1650 : 0) + (c.out == OUT_F32 ? 600 : 0);
+    auto tile_cycles = [&](int64_t k_block, int64_t bn) { return std::max(nkb * k_block, 900 + bn * column / 128); };
     auto width = [&](int64_t rows, int64_t workers, int64_t pair, int64_t &waves) {
         int64_t bn = 256;
         waves = cdiv(rows * n2 * c.batch, workers);
         for (int64_t b = 240; !c.sym && b > 128; b -= 16) {
             if (c.b_mn && b % (16 * pair) != 0) continue;
             const int64_t w = cdiv(rows * cdiv(c.N, b) * c.batch, workers);
-            if (w * cost(pair, b) < waves * cost(pair, bn)) bn = b, waves = w;
+            if (w * tile_cycles(cost(pair, b), b) < waves * tile_cycles(cost(pair, bn), bn)) bn = b, waves = w;
         }
         return bn;
     };
@@ -133,9 +137,9 @@ LinPlan plan_product(const LinCall &c, int64_t sms) {
     // The tile with the fewest cycles: waves of workers times what a K block of a tile takes, and the rest,
     // in which the last epilogue shows.
     const int64_t slow = (c.act ? 3000 : 0) + (c.aux ? 900 : 0) + (c.sym ? 5000 : 0);
-    const int64_t c1 = cdiv(u1, sms) * nkb * block(340, 128, 128) + 8300 + slow;
-    const int64_t c2 = w2 * nkb * cost(1, bn2) + 9100 + slow;
-    const int64_t c3 = (c.sym ? cdiv(u3, sms / 2) : w3) * nkb * cost(2, bn3) + 9800 + slow;
+    const int64_t c1 = cdiv(u1, sms) * tile_cycles(block(340, 128, 128), 128) + 8300 + slow;
+    const int64_t c2 = w2 * tile_cycles(cost(1, bn2), bn2) + 9100 + slow;
+    const int64_t c3 = (c.sym ? cdiv(u3, sms / 2) : w3) * tile_cycles(cost(2, bn3), bn3) + 9800 + slow;
     int tile = c.tile;
     if (tile == TS_TILE_AUTO) {
         const int64_t least = std::min(c1, std::min(c.sym ? c1 : c2, c3));

@@ -411,235 +411,279 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, MODE == LIN_PRE>::THREADS, 1)
                                              : __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t *>(p.bias) + c0 + 32 * i)) << 16);
         };
         if (full && p.bias) fetch_bias(first);
-        auto tiles = [&](auto act) {
-        constexpr int ACT = decltype(act)::value;
-        for (int32_t u = first; u < p.num_units && alive; u += step) {
+        // Where this warp's subtiles lie.
+        struct Place {
+            int32_t row0, col0, col_end, z;
+            bool work;
+        };
+        auto place = [&](int32_t u) {
             const LinUnit w = lin_unit<C>(u, p);
-            const int32_t row0 = w.mb * C::TILE_M + static_cast<int32_t>(rank) * C::BM + 32 * q;
-            const int32_t col0 = w.nb * p.bn + C::COLS * h;
-            const int32_t col_end = min(col0 + cols, p.N);
-            const bool work = row0 < p.M && col0 < col_end;
-            auto load_aux = [&](int s) {  // lane 0, by TMA; the buffer is free
-                const uint32_t b = static_cast<uint32_t>(s) & (bufs - 1);
+            Place t;
+            t.row0 = w.mb * C::TILE_M + static_cast<int32_t>(rank) * C::BM + 32 * q;
+            t.col0 = w.nb * p.bn + C::COLS * h;
+            t.col_end = min(t.col0 + cols, p.N);
+            t.z = w.z;
+            t.work = t.row0 < p.M && t.col0 < t.col_end;
+            return t;
+        };
+        // aux by TMA: one subtile's load into a free buffer
+        auto load_aux = [&](uint32_t b, int32_t col, int32_t row, int32_t z) {
+            if (lane == 0) {
                 mbar_arrive_expect_tx(aux_full(j, b), C::EPI_BUF);
-                tma_load_3d(stg + b * C::EPI_BUF, &tmAux, aux_full(j, b), col0 + s * sub, row0, w.z);
-            };
-            if (work) {
-                if (aux_tma) {
+                tma_load_3d(stg + b * C::EPI_BUF, &tmAux, aux_full(j, b), col, row, z);
+            }
+            aux_pending |= 1u << b;
+        };
+        // With two buffers aux is loaded a subtile ahead, over the end of a tile too.
+        const bool ahead = aux_tma && bufs == 2;
+        int32_t next_u = first, next_col = 0;
+        Place next;
+        auto next_tile = [&] {
+            for (; next_u < p.num_units; next_u += step) {
+                next = place(next_u);
+                next_col = next.col0;
+                if (next.work) break;
+            }
+        };
+        auto load_next = [&](uint32_t b) {
+            if (next_u >= p.num_units) return;
+            load_aux(b, next_col, next.row0, next.z);
+            if ((next_col += sub) >= next.col_end) {
+                next_u += step;
+                next_tile();
+            }
+        };
+        if (ahead) {
+            next_tile();
+            load_next(0);
+        }
+        uint32_t buf = 0;  // of the subtile
+        auto tiles = [&](auto act) {
+            constexpr int ACT = decltype(act)::value;
+            for (int32_t u = first; u < p.num_units && alive; u += step) {
+                const LinUnit w = lin_unit<C>(u, p);
+                const Place t = place(u);
+                const int32_t row0 = t.row0, col0 = t.col0, col_end = t.col_end;
+                const bool work = t.work;
+                if (work && aux_tma && !ahead) {
+                    if (lane == 0) {
+                        bulk_wait_read<0>();  // the store that used the buffer has read it
+                        fence_proxy_async_smem();
+                    }
+                    load_aux(0, col0, row0, w.z);
+                    __syncwarp();
+                }
+                int ok = 1;
+                if (lane == 0) ok = wait_long(tfull(acc), acc_phase, abort_flag, p, WAIT_EPI_TMEM_FULL);
+                if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+                tc_fence_after();
+                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * BN + C::COLS * h;
+                // the accumulator is read: back to the MMA issuer
+                auto release = [&] {
+                    tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        bulk_wait_read<0>();  // the stores that used the buffers have read them
-                        fence_proxy_async_smem();
-                        for (int s = 0; s < static_cast<int>(bufs) && col0 + s * sub < col_end; ++s) load_aux(s);
-                    }
-                    for (int s = 0; s < static_cast<int>(bufs) && col0 + s * sub < col_end; ++s) aux_pending |= 1u << s;
-                }
-                __syncwarp();
-            }
-            int ok = 1;
-            if (lane == 0) ok = wait_long(tfull(acc), acc_phase, abort_flag, p, WAIT_EPI_TMEM_FULL);
-            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-            tc_fence_after();
-            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * BN + C::COLS * h;
-            // the accumulator is read: back to the MMA issuer
-            auto release = [&] {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (CG == 1)
-                        mbar_arrive(tempty(acc));
-                    else
-                        mbar_arrive_cluster(mapa(tempty(acc), 0));
-                }
-            };
-            if (!work) release();
-            const int rows = min(32, p.M - row0);
-            float bias_now[CHUNKS];
-            if (full && p.bias) {
-#pragma unroll
-                for (int i = 0; i < CHUNKS; ++i) bias_now[i] = bias[i];
-                fetch_bias(u + step);
-            }
-            // a subtile at a time
-#pragma unroll 1
-            for (int32_t s = 0, col = col0; work && col < col_end; ++s, col += sub) {
-                const uint32_t buf = static_cast<uint32_t>(s) & (bufs - 1), at = stg + buf * C::EPI_BUF;
-                const int left = min(col_end - col, sub) * esize;
-                const bool tma = tma_d && left == 128;
-                // its buffer: free, or holding aux
-                if (aux_tma) {
-                    if (s >= static_cast<int>(bufs)) {
-                        __syncwarp();
-                        if (lane == 0) {
-                            bulk_wait_read<0>();
-                            fence_proxy_async_smem();
-                            load_aux(s);
-                        }
-                        aux_pending |= 1u << buf;
-                    }
-                    const bool got = wait_phase(aux_full(j, buf), (aux_phase >> buf) & 1u, abort_flag, p, WAIT_AUX);
-                    if (!__all_sync(0xffffffffu, got)) {
-                        alive = false;
-                        break;
-                    }
-                    aux_phase ^= 1u << buf;
-                    aux_pending &= ~(1u << buf);
-                } else {
-                    if (lane == 0) wait_store();
-                    __syncwarp();
-                    if (p.aux) {
-                        stage_rows_in(static_cast<const char *>(p.aux) +
-                                          (w.z * p.aux_matrix + static_cast<int64_t>(row0) * p.ld_aux + col) * esize,
-                                      p.ld_aux * esize, rows, left, p.store_bytes, at, lane);
-                        __syncwarp();
-                    }
-                }
-                if (PRE && aux_tma) {
-                    if (lane == 0) wait_store();  // the other buffer's store, and pre's before it
-                    __syncwarp();
-                }
-                // 32 columns at a time: a subtile of fp32, half of a 16-bit one
-#pragma unroll 1
-                for (int32_t c0 = col, piece = 0; c0 < min(col + sub, col_end); c0 += 32, piece += 4) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(taddr + (c0 - col0), v);
-                    if (full && p.bias) {
-                        float b = bias_now[0];
-#pragma unroll
-                        for (int i = 1; i < CHUNKS; ++i) b = c0 - col0 == 32 * i ? bias_now[i] : b;
-                        __syncwarp();  // the last chunk's have been read
-                        st_shared_f32(bias_at + 4 * lane, b);
-                        __syncwarp();
-                    }
-                    tmem_ld_wait();
-                    if (c0 + 32 >= col_end) release();
-                    float x[32];
-                    if (p.num_kb > 0) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            x[i] = __uint_as_float(v[i]), x[i + 1] = __uint_as_float(v[i + 1]);
-                            if constexpr (iteration) split(two(p.alpha) * two(x[i], x[i + 1]), x[i], x[i + 1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = 0.f;
-                    }
-                    if (full && p.bias) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {  // the same address in all lanes
-                            const uint4 b = ld_shared_v4(bias_at + 16 * i);
-                            split(two(x[4 * i], x[4 * i + 1]) + two(__uint_as_float(b.x), __uint_as_float(b.y)), x[4 * i], x[4 * i + 1]);
-                            split(two(x[4 * i + 2], x[4 * i + 3]) + two(__uint_as_float(b.z), __uint_as_float(b.w)), x[4 * i + 2], x[4 * i + 3]);
-                        }
-                    }
-                    // x into this lane's row of a staging buffer
-                    auto put = [&](uint32_t buffer) {
-                        const uint32_t row_at = buffer + lane * 128;
-                        if constexpr (f32) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                st_shared_v4(row_at + ((i ^ (lane & 7)) << 4), __float_as_uint(x[4 * i]),
-                                             __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]),
-                                             __float_as_uint(x[4 * i + 3]));
-                        } else {
-                            uint32_t o[16];
-                            if (iteration && p.out == OUT_F16) {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    o[i] = pack_f16x2(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]));
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    o[i] = pack_bf16x2(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]));
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                st_shared_v4(row_at + (((piece + i) ^ (lane & 7)) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2],
-                                             o[4 * i + 3]);
-                            if (iteration && p.sym && w.nb > w.mb) {
-                                // The entry's mirror image: a column of this warp's is 32 consecutive values
-                                // there.  Lanes 2i and 2i + 1 exchange halves, so that an even lane holds two rows
-                                // of an even column, an odd one of the column behind it, and stores them at once.
-                                const int32_t r = row0 + (lane & ~1), cm = c0 + (lane & 1);
-                                uint16_t *m = static_cast<uint16_t *>(p.D) + w.z * p.d_matrix + cm * p.ldd + r;
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const uint32_t got = __shfl_xor_sync(0xffffffffu, o[i], 1);
-                                    const uint32_t both = lane & 1 ? __byte_perm(got, o[i], 0x7632) : __byte_perm(o[i], got, 0x5410);
-                                    // rows of the mirror image: D, of a multiple of eight rows and columns, is square
-                                    if (cm + 2 * i < p.N && r < p.M) *reinterpret_cast<uint32_t *>(m) = both;
-                                    m += 2 * p.ldd;
-                                }
-                            }
-                        }
-                    };
-                    if constexpr (PRE) put(stg_pre);
-                    float a[32];
-                    if (p.aux) {
-                        const uint32_t row_at = at + lane * 128;
-                        if constexpr (f32) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const uint4 t = ld_shared_v4(row_at + ((i ^ (lane & 7)) << 4));
-                                a[4 * i] = __uint_as_float(t.x);
-                                a[4 * i + 1] = __uint_as_float(t.y);
-                                a[4 * i + 2] = __uint_as_float(t.z);
-                                a[4 * i + 3] = __uint_as_float(t.w);
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint4 t = ld_shared_v4(row_at + (((piece + i) ^ (lane & 7)) << 4));
-                                const uint32_t w4[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    a[8 * i + 2 * e] = iteration ? f16_to_f32(static_cast<uint16_t>(w4[e])) : __uint_as_float(w4[e] << 16);
-                                    a[8 * i + 2 * e + 1] = iteration ? f16_to_f32(static_cast<uint16_t>(w4[e] >> 16))
-                                                                     : __uint_as_float(w4[e] & 0xffff0000u);
-                                }
-                            }
-                        }
-                    }
-                    if constexpr (MODE == LIN_SLOPE) {
-                        apply_slope<ACT>(x, a);
-                    } else {
-                        apply_act<ACT>(x);
-                        if (p.aux) {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                if constexpr (iteration)
-                                    split(fma(two(p.beta), two(a[i], a[i + 1]), two(x[i], x[i + 1])), x[i], x[i + 1]);
-                                else
-                                    split(two(a[i], a[i + 1]) + two(x[i], x[i + 1]), x[i], x[i + 1]);
-                            }
-                        }
-                    }
-                    put(at);
-                }
-                // the staged subtiles leave
-                auto leave = [&](uint32_t buffer, const CUtensorMap *map, void *dst, int64_t matrix, int64_t ld) {
-                    if (tma) {
-                        tma_store_3d(map, buffer, col, row0, w.z, policy_evict_first());
-                    } else {
-                        stage_rows_out(static_cast<char *>(dst) +
-                                           (w.z * matrix + static_cast<int64_t>(row0) * ld + col) * esize,
-                                       ld * esize, rows, left, p.store_bytes, buffer, lane);
+                        if constexpr (CG == 1)
+                            mbar_arrive(tempty(acc));
+                        else
+                            mbar_arrive_cluster(mapa(tempty(acc), 0));
                     }
                 };
-                if (tma) fence_proxy_async_smem();
-                __syncwarp();
-                if constexpr (PRE) {
-                    if (!tma || lane == 0) leave(stg_pre, &tmPre, p.pre, 0, p.ld_pre);
+                if (!work) release();
+                const int rows = min(32, p.M - row0);
+                float bias_now[CHUNKS];
+                if (full && p.bias) {
+#pragma unroll
+                    for (int i = 0; i < CHUNKS; ++i) bias_now[i] = bias[i];
+                    fetch_bias(u + step);
+                }
+                // a subtile at a time
+#pragma unroll 1
+                for (int32_t col = col0; work && col < col_end; col += sub, buf ^= bufs - 1) {
+                    const uint32_t at = stg + buf * C::EPI_BUF;
+                    const int left = min(col_end - col, sub) * esize;
+                    const bool tma = tma_d && left == 128;
+                    // its buffer: free, or holding aux
+                    if (aux_tma) {
+                        if (!ahead && col > col0) {
+                            __syncwarp();
+                            if (lane == 0) {
+                                bulk_wait_read<0>();
+                                fence_proxy_async_smem();
+                            }
+                            load_aux(buf, col, row0, w.z);
+                        }
+                        const bool got = wait_phase(aux_full(j, buf), (aux_phase >> buf) & 1u, abort_flag, p, WAIT_AUX);
+                        if (!__all_sync(0xffffffffu, got)) {
+                            alive = false;
+                            break;
+                        }
+                        aux_phase ^= 1u << buf;
+                        aux_pending &= ~(1u << buf);
+                    } else {
+                        if (lane == 0) wait_store();
+                        __syncwarp();
+                        if (p.aux) {
+                            stage_rows_in(static_cast<const char *>(p.aux) +
+                                              (w.z * p.aux_matrix + static_cast<int64_t>(row0) * p.ld_aux + col) * esize,
+                                          p.ld_aux * esize, rows, left, p.store_bytes, at, lane);
+                            __syncwarp();
+                        }
+                    }
+                    if (PRE && aux_tma) {
+                        if (lane == 0) wait_store();  // the last store of pre has read its buffer
+                        __syncwarp();
+                    }
+                    // 32 columns at a time: a subtile of fp32, half of a 16-bit one
+#pragma unroll 1
+                    for (int32_t c0 = col, piece = 0; c0 < min(col + sub, col_end); c0 += 32, piece += 4) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(taddr + (c0 - col0), v);
+                        if (full && p.bias) {
+                            float b = bias_now[0];
+#pragma unroll
+                            for (int i = 1; i < CHUNKS; ++i) b = c0 - col0 == 32 * i ? bias_now[i] : b;
+                            __syncwarp();  // the last chunk's have been read
+                            st_shared_f32(bias_at + 4 * lane, b);
+                            __syncwarp();
+                        }
+                        tmem_ld_wait();
+                        if (c0 + 32 >= col_end) release();
+                        float x[32];
+                        if (p.num_kb > 0) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                x[i] = __uint_as_float(v[i]), x[i + 1] = __uint_as_float(v[i + 1]);
+                                if constexpr (iteration) split(two(p.alpha) * two(x[i], x[i + 1]), x[i], x[i + 1]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) x[i] = 0.f;
+                        }
+                        if (full && p.bias) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {  // the same address in all lanes
+                                const uint4 b = ld_shared_v4(bias_at + 16 * i);
+                                split(two(x[4 * i], x[4 * i + 1]) + two(__uint_as_float(b.x), __uint_as_float(b.y)), x[4 * i], x[4 * i + 1]);
+                                split(two(x[4 * i + 2], x[4 * i + 3]) + two(__uint_as_float(b.z), __uint_as_float(b.w)), x[4 * i + 2], x[4 * i + 3]);
+                            }
+                        }
+                        // x into this lane's row of a staging buffer
+                        auto put = [&](uint32_t buffer) {
+                            const uint32_t row_at = buffer + lane * 128;
+                            if constexpr (f32) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    st_shared_v4(row_at + ((i ^ (lane & 7)) << 4), __float_as_uint(x[4 * i]),
+                                                 __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]),
+                                                 __float_as_uint(x[4 * i + 3]));
+                            } else {
+                                uint32_t o[16];
+                                if (iteration && p.out == OUT_F16) {
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i)
+                                        o[i] = pack_f16x2(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]));
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i)
+                                        o[i] = pack_bf16x2(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]));
+                                }
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    st_shared_v4(row_at + (((piece + i) ^ (lane & 7)) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2],
+                                                 o[4 * i + 3]);
+                                if (iteration && p.sym && w.nb > w.mb) {
+                                    // The entry's mirror image: a column of this warp's is 32 consecutive values
+                                    // there.  Lanes 2i and 2i + 1 exchange halves, so that an even lane holds two rows
+                                    // of an even column, an odd one of the column behind it, and stores them at once.
+                                    const int32_t r = row0 + (lane & ~1), cm = c0 + (lane & 1);
+                                    uint16_t *m = static_cast<uint16_t *>(p.D) + w.z * p.d_matrix + cm * p.ldd + r;
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) {
+                                        const uint32_t got = __shfl_xor_sync(0xffffffffu, o[i], 1);
+                                        const uint32_t both = lane & 1 ? __byte_perm(got, o[i], 0x7632) : __byte_perm(o[i], got, 0x5410);
+                                        // rows of the mirror image: D, of a multiple of eight rows and columns, is square
+                                        if (cm + 2 * i < p.N && r < p.M) *reinterpret_cast<uint32_t *>(m) = both;
+                                        m += 2 * p.ldd;
+                                    }
+                                }
+                            }
+                        };
+                        if constexpr (PRE) put(stg_pre);
+                        float a[32];
+                        if (p.aux) {
+                            const uint32_t row_at = at + lane * 128;
+                            if constexpr (f32) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const uint4 t = ld_shared_v4(row_at + ((i ^ (lane & 7)) << 4));
+                                    a[4 * i] = __uint_as_float(t.x);
+                                    a[4 * i + 1] = __uint_as_float(t.y);
+                                    a[4 * i + 2] = __uint_as_float(t.z);
+                                    a[4 * i + 3] = __uint_as_float(t.w);
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const uint4 t = ld_shared_v4(row_at + (((piece + i) ^ (lane & 7)) << 4));
+                                    const uint32_t w4[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        a[8 * i + 2 * e] = iteration ? f16_to_f32(static_cast<uint16_t>(w4[e])) : __uint_as_float(w4[e] << 16);
+                                        a[8 * i + 2 * e + 1] = iteration ? f16_to_f32(static_cast<uint16_t>(w4[e] >> 16))
+                                                                         : __uint_as_float(w4[e] & 0xffff0000u);
+                                    }
+                                }
+                            }
+                            if (ahead && c0 == col) {
+                                // the other buffer: the store before this one has read it
+                                if (lane == 0) {
+                                    bulk_wait_read<0>();
+                                    fence_proxy_async_smem();
+                                }
+                                load_next(buf ^ 1u);
+                            }
+                        }
+                        if constexpr (MODE == LIN_SLOPE) {
+                            apply_slope<ACT>(x, a);
+                        } else {
+                            apply_act<ACT>(x);
+                            if (p.aux) {
+#pragma unroll
+                                for (int i = 0; i < 32; i += 2) {
+                                    if constexpr (iteration)
+                                        split(fma(two(p.beta), two(a[i], a[i + 1]), two(x[i], x[i + 1])), x[i], x[i + 1]);
+                                    else
+                                        split(two(a[i], a[i + 1]) + two(x[i], x[i + 1]), x[i], x[i + 1]);
+                                }
+                            }
+                        }
+                        put(at);
+                    }
+                    // the staged subtiles leave
+                    auto leave = [&](uint32_t buffer, const CUtensorMap *map, void *dst, int64_t matrix, int64_t ld) {
+                        if (tma) {
+                            tma_store_3d(map, buffer, col, row0, w.z, policy_evict_first());
+                        } else {
+                            stage_rows_out(static_cast<char *>(dst) +
+                                               (w.z * matrix + static_cast<int64_t>(row0) * ld + col) * esize,
+                                           ld * esize, rows, left, p.store_bytes, buffer, lane);
+                        }
+                    };
+                    if (tma) fence_proxy_async_smem();
+                    __syncwarp();
+                    if constexpr (PRE) {
+                        if (!tma || lane == 0) leave(stg_pre, &tmPre, p.pre, 0, p.ld_pre);
+                        if (lane == 0) bulk_commit();
+                    }
+                    if (!tma || lane == 0) leave(at, &tmD, p.D, p.d_matrix, p.ldd);
                     if (lane == 0) bulk_commit();
                 }
-                if (!tma || lane == 0) leave(at, &tmD, p.D, p.d_matrix, p.ldd);
-                if (lane == 0) bulk_commit();
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
             }
-            if (++acc == 2) {
-                acc = 0;
-                acc_phase ^= 1u;
-            }
-        }
         };
         // a loop for each activation, so that a tile's instructions lie together
         if constexpr (MODE == LIN_BARE)
