@@ -93,22 +93,31 @@ LinPlan plan_product(const LinCall &c, int64_t sms) {
     LinPlan pl{128, 1, nullptr, 1, 1, INT64_MAX};
     // Few tiles: K shared by a cluster, the fewest cycles of a cluster size whose clusters all run at once.
     if (c.tile == TS_TILE_AUTO && nkb > 0 && c.max_workers == 0) {
-        // Cycles fitted to measurements: a K block, CTAs to launch, and the rest.  512 x 512 x 768 with a
-        // bf16 output by 2 / 4 CTAs a tile 6.7 / 5.4 us, by a persistent CTA 6.6; 768 x 768 x 768 6.7 / 6.8
-        // and 6.8; 1001 x 1001 x 1001 by 2 8.3 and 9.4; 128 x 4096 x 4096 10.7 / 9.1 and 17.1.  A gelu adds
-        // 2 us to the persistent CTA's epilogue and 0.5 to 0.9 here, a residual 0.5 and 0.4 to 0.8.
-        auto consider = [&](const SplitVariant &v, int64_t units, const int64_t (&fixed)[4]) {
+        // Cycles fitted to measurements: K blocks of a CTA, its launch, and the rest.  Of 128-column tiles with a
+        // bf16 output, K 512, by 2 / 4 / 8 CTAs a tile and by a persistent CTA: 9 tiles 5.7 / 5.2 / 5.9 and
+        // 5.4 us, 36 tiles 5.9 / 6.4 and 5.5; a silu adds 0.4 to the first and 0.9 to the last, a residual
+        // 0.7 and 0.4.  Of tiles for 32 tokens, K 1024, by 1 / 2 / 4 / 8 CTAs: 16 tiles 5.2 / 4.4 / 3.8 / 8.0
+        // (which do not all run at once), 64 tiles 5.4 / 5.1; for 64 tokens 6.2 / 5.1 / 4.4 and 6.2 / 5.7.
+        struct Fit {
+            int64_t block[4], cta, rest[4];  // by 1, 2, 4 and 8 CTAs a tile
+        };
+        auto consider = [&](const SplitVariant &v, int64_t units, const Fit &f) {
             for (int k = v.swap ? 1 : 2, i = v.swap ? 0 : 1; k <= kMaxSplit && k <= nkb; k *= 2, ++i) {
                 const int ctas = v.swap && units * k > sms ? 2 : 1;
                 if (units * k > ctas * sms || (k > 1 && v.clusters(k, ctas) < units)) break;
-                const int64_t t = cdiv(nkb, k) * block(400, v.swap ? v.bn : 128, 128) * ctas + 25 * units * k + fixed[i] + (c.act ? 1000 : 0) + (c.aux ? 900 : 0);
+                const int64_t t = cdiv(nkb, k) * block(f.block[i], v.swap ? v.bn : 128, 128) * ctas + f.cta * units * k +
+                                  f.rest[i] + (c.act ? 900 : 0) + (c.aux ? 1300 : 0);
                 if (t < pl.cycles) pl.cycles = t, pl.sv = &v, pl.split = k, pl.ctas = ctas;
             }
         };
-        consider(split_128[kind], u1, {0, 9350, 7500, 8200});
+        consider(split_128[kind], u1, {{0, 390, 500, 500}, 18, {0, 9200, 8900, 10100}});
         // an operand with its rows contiguous comes in boxes of 64
-        if (!c.sym && c.batch == 1 && c.M <= 64)
-            consider(c.M <= 32 && !c.a_mn ? split_swap_32[kind] : split_swap_64[kind], n1, {6000, 6000, 6000, 6000});
+        if (!c.sym && c.batch == 1 && c.M <= 64) {
+            if (c.M <= 32 && !c.a_mn)
+                consider(split_swap_32[kind], n1, {{290, 290, 380, 470}, 10, {5600, 6500, 6100, 6300}});
+            else
+                consider(split_swap_64[kind], n1, {{290, 290, 380, 470}, 10, {7200, 7500, 7000, 7700}});
+        }
     }
     // Columns of a 256-column tile: the width whose waves of workers take the fewest cycles in all.  With
     // B's rows contiguous a CTA's columns start on sectors, and on lines where they are whole boxes of 64:
@@ -118,17 +127,19 @@ LinPlan plan_product(const LinCall &c, int64_t sms) {
         return block((pair == 2 ? 520 : 590) * (bn + kWidthOverhead) / (256 + kWidthOverhead), 128, bn / pair,
                      c.b_mn && bn % (64 * pair) != 0 ? 30 : 0);
     };
-    // Short K loops hide behind the epilogues: cycles of one, from 8192 x 4096 x 64 on 128- and 256-column tiles
+    // A wave behind another takes its K loop or, if that is shorter, an epilogue: cycles of one, from 8192 x 4096 x 64 on 128- and 256-column tiles
     // (bf16 18.5 and 15.4 us, with silu 28.2 and 27.1, with a residual 29.5 and 27.9; fp32 22.4 and 23.6).
     const int64_t column = 1250 + (c.act ? 1450 : 0) + (c.aux ? 1650 : 0) + (c.out == OUT_F32 ? 600 : 0);
-    auto tile_cycles = [&](int64_t k_block, int64_t bn) { return std::max(nkb * k_block, 900 + bn * column / 128); };
+    auto wave_cycles = [&](int64_t waves, int64_t k_block, int64_t bn) {
+        return (waves - 1) * std::max(nkb * k_block, 900 + bn * column / 128) + nkb * k_block;
+    };
     auto width = [&](int64_t rows, int64_t workers, int64_t pair, int64_t &waves) {
         int64_t bn = 256;
         waves = cdiv(rows * n2 * c.batch, workers);
         for (int64_t b = 240; !c.sym && b > 128; b -= 16) {
             if (c.b_mn && b % (16 * pair) != 0) continue;
             const int64_t w = cdiv(rows * cdiv(c.N, b) * c.batch, workers);
-            if (w * tile_cycles(cost(pair, b), b) < waves * tile_cycles(cost(pair, bn), bn)) bn = b, waves = w;
+            if (wave_cycles(w, cost(pair, b), b) < wave_cycles(waves, cost(pair, bn), bn)) bn = b, waves = w;
         }
         return bn;
     };
@@ -136,10 +147,12 @@ LinPlan plan_product(const LinCall &c, int64_t sms) {
     const int64_t bn2 = width(m1, sms, 1, w2), bn3 = width(m2, sms / 2, 2, w3);
     // The tile with the fewest cycles: waves of workers times what a K block of a tile takes, and the rest,
     // in which the last epilogue shows.
-    const int64_t slow = (c.act ? 3000 : 0) + (c.aux ? 900 : 0) + (c.sym ? 5000 : 0);
-    const int64_t c1 = cdiv(u1, sms) * tile_cycles(block(340, 128, 128), 128) + 8300 + slow;
-    const int64_t c2 = w2 * tile_cycles(cost(1, bn2), bn2) + 9100 + slow;
-    const int64_t c3 = (c.sym ? cdiv(u3, sms / 2) : w3) * tile_cycles(cost(2, bn3), bn3) + 9800 + slow;
+    // (Plain, 9 and 144 tiles: 128 columns 7700 cycles, 256 9200 and 11100, pairs 9400 and 12400.)
+    const int64_t slow = (c.act ? 2100 : 0) + (c.aux ? 700 : 0) + (c.sym ? 5000 : 0);
+    const int64_t slow2 = (c.act ? 3000 : 0) + (c.aux ? 1300 : 0) + (c.sym ? 5000 : 0);
+    const int64_t c1 = wave_cycles(cdiv(u1, sms), block(385, 128, 128), 128) + 7700 + slow;
+    const int64_t c2 = wave_cycles(w2, cost(1, bn2), bn2) + 9200 + 13 * std::min(m1 * n2 * c.batch, sms) + slow2;
+    const int64_t c3 = wave_cycles(c.sym ? cdiv(u3, sms / 2) : w3, cost(2, bn3), bn3) + 9400 + 40 * std::min(u3, sms / 2) + slow2;
     int tile = c.tile;
     if (tile == TS_TILE_AUTO) {
         const int64_t least = std::min(c1, std::min(c.sym ? c1 : c2, c3));
