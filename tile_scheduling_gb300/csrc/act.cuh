@@ -11,9 +11,8 @@
 // Mathematical Functions, 7.1.26), which is off by at most 1.5e-7, about as much as fp32 itself
 // near 1; its exponential is the one that the slope needs as well.
 //
-// What bounds them is the exponential and the reciprocal, 16 of which an SM takes in a cycle: two of
-// them a value.  The rest goes two values to an instruction.  (8192 x 8192 bf16 gradients through gelu:
-// FIGURE us; one value at a time 94, with erff 123.)
+// An exponential and a reciprocal are taken for each value, the rest two values to an instruction: 8192 x
+// 8192 bf16 gradients through gelu 72 us, bound by memory (one value at a time 94, with erff 123).
 #pragma once
 #include "linear_params.h"
 

@@ -263,9 +263,10 @@ ts_status linear_product(const LinCall &c) {
     p.bn = bn;
     // boxes of 64 rows where an operand's rows are contiguous, which may pass the tile's columns
     p.tx_bytes = cg * (128 * 128 + (c.b_mn ? cdiv(bn / cg, 64) * 64 : bn / cg) * 128);
-    // Short K loops leave the epilogue as the bound: 4096 x 4096 x 256 14.7 us with two buffers, 15.7 with
-    // one; x 1024 23.9 both.  Long ones need the ring: 2047 x 4096 x 6144 59.0 and 57.3.
-    p.bufs = nkb <= 8 ? 2 : 1;
+    // Short K loops leave the epilogue as the bound, which two buffers keep moving: 4096 x 4096 x 256 with a
+    // residual 15.5 us, 16.9 with one; x 1024 with gelu_tanh and preact 27.8 and 28.6 (alone 22.8 and 22.7).
+    // Long ones need the ring: x 2048 48.4 and 45.9.
+    p.bufs = nkb <= (c.act || c.aux || c.pre ? 16 : 8) ? 2 : 1;
     p.stages = v.stages(p.bufs);
     int64_t workers = std::min<int64_t>(units, sms / cg);
     if (c.max_workers > 0) workers = std::min<int64_t>(workers, c.max_workers);

@@ -36,7 +36,7 @@ struct LinParams {
     int32_t store_bytes;              // 16, 4 or 2: what the bases and rows of D, aux and pre are aligned to
     float alpha, beta;                // the iteration's products; 1 otherwise
     const void *bias;                 // N values added to every row, or NULL
-    int32_t bias_f32, bias_vec;       // bias_vec: it starts on a 16-byte boundary
+    int32_t bias_f32, bias_vec;       // bias_vec (for the split kernel): it starts on a 16-byte boundary
     const void *aux;                  // residual or pre-activation [M][N], or NULL
     int64_t ld_aux, aux_matrix;
     void *pre;                        // alpha * acc + bias, or NULL
