@@ -1079,9 +1079,9 @@ def ts_act_grad(grad_y: torch.Tensor, preact, grad_z, grad_bias=None, act="none"
     dtype, shape, ldy = _rows_of(grad_y, "grad_y", _OUT, device)
     z, ldz = _like(preact, "preact", "grad_y", dtype, shape, device) if preact is not None else (0, 0)
     g, ldg = _like(grad_z, "grad_z", "grad_y", dtype, shape, device) if grad_z is not None else (0, 0)
-    st = _lib.ts_act_grad(grad_y.data_ptr(), z, g,
-                          _vector(grad_bias, "grad_bias", _F32, shape[1], device) if grad_bias is not None else 0, shape[0], shape[1], dtype, _ACT[act] if isinstance(act, str) else int(act), ldy, ldz, ldg,
-                          _stream_of(stream))
+    b = _vector(grad_bias, "grad_bias", _F32, shape[1], device) if grad_bias is not None else 0
+    st = _lib.ts_act_grad(grad_y.data_ptr(), z, g, b, shape[0], shape[1], dtype,
+                          _ACT[act] if isinstance(act, str) else int(act), ldy, ldz, ldg, _stream_of(stream))
     if st:
         _check(st)
 

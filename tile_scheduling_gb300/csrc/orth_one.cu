@@ -77,8 +77,8 @@ __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence
 // Arrive and wait until all CTAs have arrived `count` times; one thread.
 __device__ __forceinline__ bool grid_barrier(const OneParams &p, int32_t count, volatile int *abort_flag) {
     __threadfence();
-    atomicAdd(p.barrier, 1);
     const int32_t want = count * static_cast<int32_t>(gridDim.x);
+    atomicAdd(p.barrier, 1);
     const uint64_t t0 = globaltimer();
     for (;;) {
         int32_t v;
@@ -141,7 +141,6 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     int32_t arrivals = 0;
     auto next_phase = [&] {  // all threads; false: give up
         fence_proxy_async_global();
-        __threadfence();
         __syncthreads();
         if (threadIdx.x == 0) grid_barrier(p, ++arrivals, abort_flag);
         __syncthreads();
