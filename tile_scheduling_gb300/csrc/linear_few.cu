@@ -10,9 +10,9 @@
 // Where N gives too few CTAs, a cluster's CTAs share K as well.  The partial sums are added in a
 // fixed order, so results do not depend on timing.
 //
-// While the CTAs all run at once they ask for their part of w to be brought into L2 before they wait
-// for the previous kernel in the stream: a prefetch changes nothing that a later write could not, and
-// the data it fetches is read after the wait.
+// While the CTAs all run at once they ask for the start of their part of w to be brought into L2 before
+// they wait for the previous kernel in the stream: a prefetch changes nothing that a later write could
+// not, and the data it fetches is read after the wait.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -30,6 +30,9 @@ constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
 constexpr int kFewRows = 16;     // of w a CTA takes
 constexpr int kFewBlock = 32;    // of K a warp takes at a time
 constexpr int kFewCluster = 8;
+// Bytes of a row that are asked for ahead: what the previous kernel's end covers.  More of them compete with the
+// loads: one token, 4096 x 28672 39.6 us, 53.7 with whole rows, 40.0 with none; 4096 x 4096 7.4, 7.3 and 8.0.
+constexpr int32_t kFewPrefetch = 4096;
 constexpr int kFewDeep = 8, kFewShallow = 3;  // blocks in flight with two and with four CTAs on an SM
 
 struct FewParams {
@@ -76,7 +79,7 @@ __global__ void __launch_bounds__(kFewThreads, CTAS) linear_few_kernel(const __g
     const int32_t b1 = b0 + p.blocks / p.split + (rank < p.blocks % p.split ? 1 : 0);
     const int32_t end = min(b1 * kFewBlock, p.K);
     if (p.prefetch && threadIdx.x < kFewRows && n0 + static_cast<int>(threadIdx.x) < p.N) {
-        const int32_t bytes = ((end - b0 * kFewBlock) * 2) & ~15;
+        const int32_t bytes = min(kFewPrefetch, (end - b0 * kFewBlock) * 2) & ~15;
         if (bytes > 0) prefetch_l2(p.w + (n0 + static_cast<int>(threadIdx.x)) * p.ldw + b0 * kFewBlock, bytes);
     }
     grid_dep_wait();
