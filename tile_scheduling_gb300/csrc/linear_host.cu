@@ -98,15 +98,19 @@ LinPlan plan_product(const LinCall &c, int64_t sms) {
         // 5.4 us, 36 tiles 5.9 / 6.4 and 5.5; a silu adds 0.4 to the first and 0.9 to the last, a residual
         // 0.7 and 0.4.  Of tiles for 32 tokens, K 1024, by 1 / 2 / 4 / 8 CTAs: 16 tiles 5.2 / 4.4 / 3.8 / 8.0
         // (which do not all run at once), 64 tiles 5.4 / 5.1; for 64 tokens 6.2 / 5.1 / 4.4 and 6.2 / 5.7.
+        // For up to 32 tokens also more tiles than run at once, two on an SM: 9 and 16 tokens, 65536 x 2048, 45 us,
+        // by persistent CTAs 64 and 63; 128000 x 4096 159, 192 and 161.  (For 64 tokens 50 and 47.)
         struct Fit {
             int64_t block[4], cta, rest[4];  // by 1, 2, 4 and 8 CTAs a tile
         };
         auto consider = [&](const SplitVariant &v, int64_t units, const Fit &f) {
             for (int k = v.swap ? 1 : 2, i = v.swap ? 0 : 1; k <= kMaxSplit && k <= nkb; k *= 2, ++i) {
                 const int ctas = v.swap && units * k > sms ? 2 : 1;
-                if (units * k > ctas * sms || (k > 1 && v.clusters(k, ctas) < units)) break;
-                const int64_t t = cdiv(nkb, k) * block(f.block[i], v.swap ? v.bn : 128, 128) * ctas + f.cta * units * k +
-                                  f.rest[i] + (c.act ? 900 : 0) + (c.aux ? 1300 : 0);
+                const bool queue = v.bn == 32 && k == 1 && ctas == 2;
+                if ((units * k > ctas * sms && !queue) || (k > 1 && v.clusters(k, ctas) < units)) break;
+                const int64_t loop = cdiv(nkb, k) * block(f.block[i], v.swap ? v.bn : 128, 128);
+                const int64_t t = (queue ? loop * units / sms : loop * ctas) + f.cta * units * k + f.rest[i] +
+                                  (c.act ? 900 : 0) + (c.aux ? 1300 : 0);
                 if (t < pl.cycles) pl.cycles = t, pl.sv = &v, pl.split = k, pl.ctas = ctas;
             }
         };
