@@ -105,8 +105,12 @@ __device__ __forceinline__ void block_sum3(T &a, T &b, T &c) {
 }
 
 // Sums of squares in three ranges, after Blue ("A Portable Fortran Program to Find the Euclidean
-// Norm of a Vector", 1978): as they are, and scaled by 2^-70 and 2^70 for values whose squares
-// leave fp32's range.
+// Norm of a Vector", 1978): as they are, and scaled for values whose squares leave fp32's range.
+// A matrix has at most 2^40 values (checked on the host).  Scaled by kBigScale = 2^-100 the squares of
+// values up to 2^128 sum to at most 2^96.  The third sum is used where the first is below 2^-60, so that
+// values are below 2^-30: scaled by kTinyScale = 2^90 their squares sum to less than 2^120, and the
+// least fp32 value's square is 2^-118.
+constexpr float kBigScale = 0x1p-100f, kTinyScale = 0x1p90f;
 // One of p.chunks shares of matrix z, by THREADS threads.
 template <class T, bool VEC, int THREADS>
 __device__ __forceinline__ void orth_norm(const OrthParams &p, int64_t z, int64_t chunk) {
@@ -122,17 +126,19 @@ __device__ __forceinline__ void orth_norm(const OrthParams &p, int64_t z, int64_
             top = fmaxf(top, fabsf(f[k]));
         }
     });
-    // The other two only where this share may matter to them: values above 2^55, whose squares reach
-    // 2^-30 of the least scaled sum that is used, or a small sum.
+    // The other two only where this share may matter to them.  The sum of large values is used where the
+    // plain sum is infinite, 2^128 or more: shares of values up to 2^30 add less than 2^60 * 2^40 = 2^100 to
+    // that, a share of 2^-28, and cannot overflow it.  The sum of tiny ones is used where the plain sum is
+    // below 2^-60, and so every share's.
     __shared__ int again;
     block_sum3<THREADS>(mid, big, tiny);
     if (threadIdx.x == 0) again = mid < 0x1p-50f;
-    if (__syncthreads_or(top > 0x1p55f) || again) {
+    if (__syncthreads_or(top > 0x1p30f) || again) {
         float none = 0.f;
         each_vector<THREADS, T, V>(p, g, r0, r1, [&](const float (&f)[V], int32_t, int32_t, int) {
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                const float b = f[k] * 0x1p-70f, t = f[k] * 0x1p70f;
+                const float b = f[k] * kBigScale, t = f[k] * kTinyScale;
                 big = fmaf(b, b, big);
                 tiny = fmaf(t, t, tiny);
             }
@@ -162,20 +168,27 @@ __device__ __forceinline__ void orth_scale(const OrthParams &p, int64_t z, int64
         }
         block_sum3<THREADS>(mid, big, tiny);
         if (threadIdx.x == 0) {
-            // The middle sum where it neither overflowed (then it is infinite) nor lost what is below 2^-75
-            // (then it is small); a NaN stays one.  x = g * s2 * s1, with s2 the power of two that brings
-            // g, the norm and eps into the sum's range.
-            float sum = mid, s2 = 1.f;
-            if (big >= 0x1p-20f)
-                sum = big, s2 = 0x1p-70f;
-            else if (mid < 0x1p-60f)
-                sum = tiny, s2 = 0x1p70f;
-            factors[0] = (p.to_bf16 ? 1.f : kOrthScale) / (sqrtf(sum) + p.eps * s2);
-            factors[1] = s2;
+            // The plain sum where it neither overflowed (then it is infinite) nor lost what is below 2^-75
+            // (then it is small); a NaN stays one.  x = g * first * second; one of them is a power of two that
+            // brings g, the norm and eps into fp32's range.
+            const float scale = p.to_bf16 ? 1.f : kOrthScale;
+            float first = 1.f, second;
+            if (isinf(mid)) {
+                first = scale / (sqrtf(big) + p.eps * kBigScale);
+                second = kBigScale;
+            } else if (mid < 0x1p-60f) {
+                const float norm = sqrtf(tiny), sum = norm / kTinyScale + p.eps;
+                if (sum < 0x1p-100f) first = kTinyScale;  // whose reciprocal might overflow
+                second = scale / (sum < 0x1p-100f ? norm + p.eps * kTinyScale : sum);
+            } else {
+                second = scale / (sqrtf(mid) + p.eps);
+            }
+            factors[0] = first;
+            factors[1] = second;
         }
         __syncthreads();
     }
-    const float s1 = factors[0], s2 = factors[1];
+    const float first = factors[0], second = factors[1];
     const T *g = static_cast<const T *>(p.G) + z * p.g_matrix;
     uint16_t *x = static_cast<uint16_t *>(p.X) + z * p.x_matrix;
     const bool whole = (p.ldx % V) == 0 && (p.x_matrix % V) == 0 && reinterpret_cast<uintptr_t>(p.X) % (2 * V) == 0;
@@ -184,7 +197,7 @@ __device__ __forceinline__ void orth_scale(const OrthParams &p, int64_t z, int64
         uint16_t o[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const float v = f[k] * s2 * s1;
+            const float v = f[k] * first * second;
             o[k] = p.to_bf16 ? static_cast<uint16_t>(pack_bf16x2(__float_as_uint(v), 0u))
                              : static_cast<uint16_t>(pack_f16x2(__float_as_uint(v), 0u));
         }
