@@ -139,12 +139,14 @@ __global__ void __launch_bounds__(kOneThreads, 1)
 
     // ------------------------------------------------ normalisation
     int32_t arrivals = 0;
-    auto next_phase = [&] {  // all threads; false: give up
+    // All threads; false: give up.  One thread decides for the CTA: a warp that read the flag for itself might
+    // see what a quicker one sets in the phase behind the barrier, and leave the others alone at the next.
+    auto next_phase = [&] {
         fence_proxy_async_global();
         __syncthreads();
-        if (threadIdx.x == 0) grid_barrier(p, ++arrivals, abort_flag);
-        __syncthreads();
-        return *abort_flag == 0;
+        int stop = 0;
+        if (threadIdx.x == 0) stop = !grid_barrier(p, ++arrivals, abort_flag) || *abort_flag;
+        return __syncthreads_or(stop) == 0;
     };
     const int64_t shares = static_cast<int64_t>(p.batch) * p.prep.chunks;
     auto prepare = [&](auto type, auto vec) {
@@ -152,18 +154,17 @@ __global__ void __launch_bounds__(kOneThreads, 1)
         constexpr bool VEC = decltype(vec)::value;
         for (int64_t i = cta; i < shares; i += ctas)
             orth_norm<T, VEC, kOneThreads>(p.prep, i / p.prep.chunks, i % p.prep.chunks);
-        if (!next_phase()) return;
+        if (!next_phase()) return false;
         for (int64_t i = cta; i < shares; i += ctas)
             orth_scale<T, VEC, kOneThreads>(p.prep, i / p.prep.chunks, i % p.prep.chunks);
+        return true;
     };
-    if (p.g_f32)
-        p.g_vec ? prepare(float(), std::true_type()) : prepare(float(), std::false_type());
-    else
-        p.g_vec ? prepare(uint16_t(), std::true_type()) : prepare(uint16_t(), std::false_type());
+    const bool prepared = p.g_f32 ? (p.g_vec ? prepare(float(), std::true_type()) : prepare(float(), std::false_type()))
+                                  : (p.g_vec ? prepare(uint16_t(), std::true_type()) : prepare(uint16_t(), std::false_type()));
 
     // ------------------------------------------------ products
     uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, issued = 0;
-    for (int32_t step = 0; step < 3 * p.steps; ++step) {
+    for (int32_t step = 0; prepared && step < 3 * p.steps; ++step) {
         if (!next_phase()) break;
         const int32_t which = step % 3, iter = step / 3;
         OnePhase f;
