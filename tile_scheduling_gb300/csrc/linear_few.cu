@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kFewThreads, CTAS) linear_few_kernel(const __g
     const int32_t b1 = b0 + p.blocks / p.split + (rank < p.blocks % p.split ? 1 : 0);
     const int32_t end = min(b1 * kFewBlock, p.K);
     if (p.prefetch && threadIdx.x < kFewRows && n0 + static_cast<int>(threadIdx.x) < p.N) {
-        const int32_t bytes = min(kFewPrefetch, (end - b0 * kFewBlock) * 2) & ~15;
+        const int32_t bytes = min(kFewPrefetch / 2, end - b0 * kFewBlock) * 2 & ~15;
         if (bytes > 0) prefetch_l2(p.w + (n0 + static_cast<int>(threadIdx.x)) * p.ldw + b0 * kFewBlock, bytes);
     }
     grid_dep_wait();
@@ -93,9 +93,10 @@ __global__ void __launch_bounds__(kFewThreads, CTAS) linear_few_kernel(const __g
         uint4 a0[UN], a1[UN], xx[UN];
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
-            const int32_t k = (b + u * kFewWarps) * kFewBlock + 8 * t;
+            const int32_t bu = b + u * kFewWarps;
             a0[u] = a1[u] = xx[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (k < end) {
+            if (bu < b1) {
+                const int32_t k = bu * kFewBlock + 8 * t;
                 a0[u] = load_k(w0, k, end);
                 a1[u] = load_k(w1, k, end);
                 xx[u] = load_k(x, k, end);
