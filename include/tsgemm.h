@@ -719,7 +719,8 @@ typedef struct {
     int32_t bias_type;      /* ts_out_dtype of bias */
     int32_t tile;           /* ts_tile */
     int32_t max_workers;    /* cap on persistent workers (CTAs or 2-CTA clusters) */
-    double timeout_s;       /* limit of an mbarrier wait in the kernel, at most 60; 0 = 2 s */
+    double timeout_s;       /* limit of an mbarrier wait in the kernel, at most 60; 0 = 2 s, and 1 us for
+                               each 64 terms of a sum */
 } ts_linear_opts;
 
 /*
@@ -754,7 +755,8 @@ typedef struct {
     int32_t tile;           /* ts_tile */
     int32_t max_workers;
     int32_t reserved;
-    double timeout_s;       /* limit of an mbarrier wait in the kernel, at most 60; 0 = 2 s */
+    double timeout_s;       /* limit of an mbarrier wait in the kernel, at most 60; 0 = 2 s, and 1 us for
+                               each 64 terms of a sum */
 } ts_linear_grad_opts;
 
 /*

@@ -127,3 +127,26 @@ def test_outputs_with_strides_past_2_32(lib, rows, odd):
     lib.ts_act_grad(gy, gy, gy, gb, act="relu")
     lib.ts_sync_and_check()
     assert torch.equal(gy.double(), want.relu()) and torch.equal(gb.double(), want.relu().sum(0))
+
+
+@pytest.mark.parametrize("tile", ["auto", "128x128"])
+def test_longest_sum(lib, tile):
+    """K loops of some seconds by one CTA, with the default limit of a wait."""
+    M, N = MOST, 8
+    at = _places(M)
+    x, gw = torch.zeros((M, N), dtype=BF16, device="cuda"), torch.empty((N, N), device="cuda")
+    x[at] = _values(len(at), N)
+    lib.ts_linear_grad_weight(x, x, gw, tile=tile)
+    lib.ts_sync_and_check()
+    assert torch.equal(gw.double(), x[at].double().t() @ x[at].double())
+
+
+def test_longest_rows_of_nine_tokens(lib):
+    M, N, K = 9, 1, MOST
+    at = _places(K)
+    x, w = (torch.zeros((r, K), dtype=BF16, device="cuda") for r in (M, N))
+    x[:, at], w[:, at] = _values(M, len(at)), _values(N, len(at), 2)
+    y = torch.empty((M, N), device="cuda")
+    lib.ts_linear(x, w, y)
+    lib.ts_sync_and_check()
+    assert torch.equal(y.double(), x[:, at].double() @ w[:, at].double().t())

@@ -15,7 +15,9 @@ namespace {
 
 constexpr int64_t kMaxSize = 0x7fffffffLL - 511;  // the last tile's coordinates stay in 32 bits
 constexpr int64_t kMaxPitch = int64_t(1) << 37;
-constexpr double kDefaultTimeoutS = 2.0;
+// The epilogue of a tile waits for the whole of its K loop, some 0.2 us for 64 of K: what a wait may take by itself,
+// and for each K block.
+constexpr double kDefaultTimeoutS = 2.0, kDefaultBlockS = 1e-6;
 constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
 constexpr int kRasterGroup = 8;
 // What a tile takes beside its columns, as columns: the loads and barriers of a K block.
@@ -252,7 +254,7 @@ ts_status linear_product(const LinCall &c) {
     p.D = c.D;
     p.ldd = c.ldd;
     p.d_matrix = c.d_matrix;
-    const double tmo = c.timeout_s > 0 ? c.timeout_s : kDefaultTimeoutS;
+    const double tmo = c.timeout_s > 0 ? c.timeout_s : kDefaultTimeoutS + kDefaultBlockS * static_cast<double>(nkb);
     p.timeout_ns = std::max<uint64_t>(1, static_cast<uint64_t>(std::min(tmo, 60.0) * 1e9));
     p.drain_ns = kDrainNs;
     p.status = status;
