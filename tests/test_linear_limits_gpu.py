@@ -150,3 +150,36 @@ def test_longest_rows_of_nine_tokens(lib):
     lib.ts_linear(x, w, y)
     lib.ts_sync_and_check()
     assert torch.equal(y.double(), x[:, at].double() @ w[:, at].double().t())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("act", ["none", "relu"])
+def test_activation_gradient_of_most_columns(lib, dtype, act):
+    N = MOST
+    at = _places(N)
+    gy = torch.zeros((1, N), dtype=dtype, device="cuda")
+    gy[:, at] = _values(1, len(at)).to(dtype)
+    gb = torch.full((N,), 7.0, device="cuda")
+    want = gy[0, at].double()
+    if act == "relu":
+        want = want.relu()
+        lib.ts_act_grad(gy, gy, gy, gb, act=act)
+    else:
+        lib.ts_act_grad(gy, None, None, gb)
+    lib.ts_sync_and_check()
+    assert torch.equal(gb[at].double(), want) and torch.equal(gy[0, at].double(), want)
+    assert _elsewhere_zero(gb, at, 0) and _elsewhere_zero(gy, at, 1)
+
+
+@pytest.mark.parametrize("N", [1, 8])
+def test_activation_gradient_of_most_rows(lib, N):
+    M = MOST
+    at = _places(M)
+    gy = torch.zeros((M, N), dtype=BF16, device="cuda")
+    gy[at] = _values(len(at), N)
+    gb = torch.empty(N, device="cuda")
+    want = gy[at].double().relu()
+    lib.ts_act_grad(gy, gy, gy, gb, act="relu")
+    lib.ts_sync_and_check()
+    assert torch.equal(gb.double(), want.sum(0)) and torch.equal(gy[at].double(), want)
+    assert _elsewhere_zero(gy, at, 0)

@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(kActThreads, kActCtas) act_grad_kernel(const _
 template <class T, bool VEC, int LANES>
 cudaError_t launch_strips(ActParams &p, int64_t sms, cudaStream_t st) {
     constexpr int64_t STRIP = LANES * (VEC ? 16 / sizeof(T) : 1);
-    // CTAs that share a strip's rows: while they all run at once, and have 64 rows each or more
+    // CTAs that share a strip's rows: while they all run at once, and have 64 rows each or more.  (One where there are
+    // many strips: of eight values or more then, so that no grid has more than 2^28 CTAs.)
     const int64_t strips = cdiv(p.N, STRIP);
     p.cluster = static_cast<int32_t>(std::max<int64_t>(1, std::min({int64_t{kMaxActCluster}, p.M / 64, kActCtas * sms / strips})));
     cudaLaunchConfig_t cfg = {};
@@ -261,7 +262,6 @@ extern "C" ts_status ts_act_grad(const void *grad_y, const void *preact, void *g
     p.act = act;
     const int64_t sms = device_sms(current_device());
     if (sms <= 0) return fail(TS_ERR_CUDA, "cannot query the SM count");
-    if (cdiv(N, 4) * kMaxActCluster > 0x7fffffffLL) return fail(TS_ERR_UNSUPPORTED, "too many columns");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     auto pick = [&](auto t, auto v) { return launch_act_grad<decltype(t), decltype(v)::value>(p, sms, st); };
     const cudaError_t e = dtype == TS_OUT_F32 ? (vec ? pick(float(), std::true_type()) : pick(float(), std::false_type()))
