@@ -472,6 +472,7 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, MODE == LIN_PRE>::THREADS, 1)
                 const int32_t row0 = t.row0, col0 = t.col0, col_end = t.col_end;
                 const bool work = t.work;
                 if (work && aux_tma && !ahead) {
+                    __syncwarp();  // all lanes have stored what the last tile left in the buffer
                     if (lane == 0) {
                         bulk_wait_read<0>();  // the store that used the buffer has read it
                         fence_proxy_async_smem();
@@ -642,7 +643,8 @@ __global__ void __launch_bounds__(LinCfg<BN, CG, MODE == LIN_PRE>::THREADS, 1)
                                 }
                             }
                             if (ahead && c0 == col) {
-                                // the other buffer: the store before this one has read it
+                                // the other buffer: all lanes, or the store before this one, have read it
+                                __syncwarp();
                                 if (lane == 0) {
                                     bulk_wait_read<0>();
                                     fence_proxy_async_smem();
