@@ -59,6 +59,20 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn(ts_status *err) {
     return fn;
 }
 
+// Needs the device's context to be current.  A thread that has made no runtime call that binds one (torch may serve
+// its allocations from what it keeps) gets it here: cudaSetDevice binds the context of the thread's device.
+CUresult encode_tiled(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap *m, CUtensorMapDataType dt, int rank, const void *ptr,
+                      const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle) {
+    const cuuint32_t estr[3] = {1, 1, 1};
+    auto call = [&] {
+        return fn(m, dt, static_cast<cuuint32_t>(rank), const_cast<void *>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    const CUresult r = call();
+    return r == CUDA_ERROR_INVALID_CONTEXT && cudaSetDevice(current_device()) == cudaSuccess ? call() : r;
+}
+
 }  // namespace
 
 ts_status encode_map(CUtensorMap *m, const void *ptr, CUtensorMapDataType dt, int rank, const int64_t *dims,
@@ -67,15 +81,13 @@ ts_status encode_map(CUtensorMap *m, const void *ptr, CUtensorMapDataType dt, in
     auto fn = encode_fn(&err);
     if (!fn) return err;
     cuuint64_t d[3], st[2];
-    cuuint32_t b[3], e[3] = {1, 1, 1};
+    cuuint32_t b[3];
     for (int i = 0; i < rank; ++i) {
         d[i] = static_cast<cuuint64_t>(dims[i]);
         b[i] = static_cast<cuuint32_t>(box[i]);
         if (i > 0) st[i - 1] = static_cast<cuuint64_t>(strides[i - 1]);
     }
-    CUresult r = fn(m, dt, static_cast<cuuint32_t>(rank), const_cast<void *>(ptr), d, st, b, e,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = encode_tiled(fn, m, dt, rank, ptr, d, st, b, swizzle);
     if (r != CUDA_SUCCESS)
         return fail(TS_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled failed (%d) for rows of %lld elements, pitch %lld B",
                     static_cast<int>(r), static_cast<long long>(dims[0]), static_cast<long long>(strides[0]));
@@ -95,9 +107,7 @@ ts_status make_map(CUtensorMap *m, const void *ptr, CUtensorMapDataType dt, int 
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * esize)};
     cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = fn(m, dt, 2, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = encode_tiled(fn, m, dt, 2, ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (r != CUDA_SUCCESS)
         return fail(TS_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled failed (%d) for a %lld x %lld tensor, pitch %lld B",
                     static_cast<int>(r), static_cast<long long>(rows), static_cast<long long>(cols),
@@ -117,9 +127,7 @@ ts_status make_map_d(CUtensorMap *m, const void *ptr, CUtensorMapDataType dt, in
                           static_cast<cuuint64_t>(depth)};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * esize), static_cast<cuuint64_t>(rows * ld * esize)};
     cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = fn(m, dt, 3, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = encode_tiled(fn, m, dt, 3, ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (r != CUDA_SUCCESS)
         return fail(TS_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled failed (%d) for D of %lld x %lld x %lld, pitch %lld B",
                     static_cast<int>(r), static_cast<long long>(depth), static_cast<long long>(rows),
