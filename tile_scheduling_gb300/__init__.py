@@ -855,20 +855,21 @@ class _Scratch(threading.local):
 _SCRATCH = _Scratch()
 
 
-def _scratch_for(nbytes: int, device, stream) -> torch.Tensor:
+def _scratch_for(nbytes: int, device, stream, keep=True) -> torch.Tensor:
     """Uninitialised scratch of at least ``nbytes``, kept per device and stream and allocated on the stream
     it serves, so that calls on different streams never share one (nor do graphs, which may replay at once).
     Each thread keeps its own: a call launches several kernels that hand counts on through the scratch, and
-    on a stream that threads share another's may come between them."""
+    on a stream that threads share another's may come between them.  Without ``keep`` it is the call's own: once
+    the caller drops it, torch's allocator hands it out again on the same stream, behind what was launched."""
     handle = _stream_of(stream)
     if stream is not None and handle != _stream_of(None):
         # as on that stream: whether it captures, and where memory that the call returns is used next
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(handle, device=device)
         with torch.cuda.stream(stream):
-            return _scratch_for(nbytes, device, None)
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)  # the graph's own
+            return _scratch_for(nbytes, device, None, keep)
+    if not keep or torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)  # capturing: the graph's own
     key = (device, handle)
     ws = _SCRATCH.kept.get(key)
     if ws is None or ws.numel() < nbytes:
@@ -1096,8 +1097,8 @@ def ts_orthogonalise(g: torch.Tensor, out: torch.Tensor, steps=5, coefficients=(
     """out = the Newton-Schulz orthogonalisation of g [R, C], or of each matrix of g [batch, R, C].
 
     g is bf16 or fp32, out bf16 of the same shape; ``steps`` times X = a X + (b A + c A A) X with A = X X^T
-    and (a, b, c) = ``coefficients``, from X = g / (norm(g) + eps).  The workspace is one kept for each
-    stream unless one is passed (ts_orthogonalise_workspace bytes, 256-byte aligned)."""
+    and (a, b, c) = ``coefficients``, from X = g / (norm(g) + eps).  The workspace is allocated for the call
+    unless one is passed (ts_orthogonalise_workspace bytes, 256-byte aligned)."""
     dims = 3 if g.dim() == 3 else 2
     device = _device()
     g_type, shape, ldg = _rows_of(g, "g", _OUT, device, dims)
@@ -1120,7 +1121,7 @@ def ts_orthogonalise(g: torch.Tensor, out: torch.Tensor, steps=5, coefficients=(
             raise ValueError("matrices of g or out share memory (an expanded tensor)")
     need = _lib.ts_orthogonalise_workspace(n, R, C, steps)
     if need and workspace is None:
-        workspace = _scratch_for(need, g.device, stream)
+        workspace = _scratch_for(need, g.device, stream, keep=False)  # as large as some matrices, not some counts
     ptr = size = 0
     if workspace is not None:
         if not workspace.is_cuda or not workspace.is_contiguous():
