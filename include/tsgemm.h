@@ -740,7 +740,8 @@ typedef struct {
  * of SMs; a NaN or infinity shows in the rows and columns that use it.
  * M == 0 or N == 0: no-op.  K == 0: y = act(bias) + residual.  Rows of x and w must start on
  * 16-byte boundaries (strides multiples of 8), or the call returns TS_ERR_UNSUPPORTED.  y must not
- * overlap x, w or bias, nor the residual unless it is the residual; preact overlaps nothing.
+ * overlap x, w or bias, nor the residual unless it is the residual; preact overlaps nothing.  Column
+ * ranges of rows of one pitch (in bytes) do not overlap; of other matrices the address ranges decide.
  */
 ts_status ts_linear(const void *x, const void *w, void *y, int64_t M, int64_t N, int64_t K, int32_t out_dtype,
                     const ts_linear_opts *opts, void *stream);
@@ -796,7 +797,8 @@ ts_status ts_linear_grad_weight(const void *grad_z, const void *x, void *grad_w,
  *             type, in fp32 and in an order that depends on M, N, the rows' alignment and the
  *             GPU's number of SMs, and is the same on every run
  *
- * Any alignment and pitch is taken; rows on 16-byte boundaries move in vectors.
+ * Any alignment and pitch is taken; rows on 16-byte boundaries move in vectors.  grad_z and grad_bias
+ * overlap nothing else, in the sense of ts_linear.
  */
 ts_status ts_act_grad(const void *grad_y, const void *preact, void *grad_z, float *grad_bias, int64_t M, int64_t N,
                       int32_t dtype, int32_t act, int64_t ldy, int64_t ldp, int64_t ldg, void *stream);
@@ -821,7 +823,8 @@ typedef struct {
  * (R > C: A = X^T X, X = a X + X (b A + c A^2), which is the same).
  *
  *   G  device, [batch][R][C], bf16 (g_type = TS_OUT_BF16) or fp32 (TS_OUT_F32), any alignment and pitch
- *   O  device, bf16 [batch][R][C], any alignment and pitch; must not overlap G
+ *   O  device, bf16 [batch][R][C], any alignment and pitch; must not overlap G (in the sense of ts_linear)
+ *      Matrices of G and of O lie behind one another or side by side (a row of each before the next row).
  *   workspace  device scratch of ts_orthogonalise_workspace(batch, R, C, steps) bytes (steps as they
  *              run), 256-byte aligned, no initialisation; launches that may overlap on the GPU
  *              need separate workspaces

@@ -236,17 +236,12 @@ extern "C" ts_status ts_act_grad(const void *grad_y, const void *preact, void *g
     }
     if (reinterpret_cast<uintptr_t>(grad_bias) % 4) return fail(TS_ERR_INVALID_ARG, "grad_bias is not aligned to 4 bytes");
     if (M > 1) vec &= (ldy * esize) % 16 == 0 && (!preact || (ldp * esize) % 16 == 0) && (!grad_z || (ldg * esize) % 16 == 0);
-    const int64_t ybytes = M > 0 ? ((M - 1) * ldy + N) * esize : 0, zbytes = M > 0 ? ((M - 1) * ldp + N) * esize : 0,
-                  gbytes = M > 0 ? ((M - 1) * ldg + N) * esize : 0;
+    const RowsInMemory y{grad_y, M, N * esize, ldy * esize}, z{preact, M, N * esize, ldp * esize}, g{grad_z, M, N * esize, ldg * esize},
+        bias{grad_bias, M > 0 ? 1 : 0, 4 * N, 4 * N};
     // each element of grad_z is written by the thread that has read the others at its place
-    auto clash = [&](const void *q, int64_t bytes, int64_t ld) {
-        return grad_z && q && bytes && ranges_overlap(grad_z, gbytes, q, bytes) && !(q == grad_z && (ld == ldg || M <= 1));
-    };
-    if (clash(grad_y, ybytes, ldy) || clash(preact, zbytes, ldp))
-        return fail(TS_ERR_INVALID_ARG, "grad_z overlaps an input, and is not that input");
-    if (grad_bias && M > 0 &&
-        (ranges_overlap(grad_bias, 4 * N, grad_y, ybytes) || (preact && ranges_overlap(grad_bias, 4 * N, preact, zbytes)) ||
-         (grad_z && ranges_overlap(grad_bias, 4 * N, grad_z, gbytes))))
+    auto clash = [&](const RowsInMemory &q) { return rows_overlap(g, q) && !(q.ptr == g.ptr && (q.pitch == g.pitch || M <= 1)); };
+    if (clash(y) || clash(z)) return fail(TS_ERR_INVALID_ARG, "grad_z overlaps an input, and is not that input");
+    if (rows_overlap(bias, y) || rows_overlap(bias, z) || rows_overlap(bias, g))
         return fail(TS_ERR_INVALID_ARG, "grad_bias overlaps a matrix");
     ActParams p;
     std::memset(&p, 0, sizeof p);

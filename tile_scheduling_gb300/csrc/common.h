@@ -74,6 +74,24 @@ inline bool ranges_overlap(const void *a, int64_t abytes, const void *b, int64_t
     return a0 < b0 + static_cast<uintptr_t>(bbytes) && b0 < a0 + static_cast<uintptr_t>(abytes);
 }
 
+// A matrix in memory: rows of `width` bytes, `pitch` bytes (at least as many) from one to the next.
+struct RowsInMemory {
+    const void *ptr;
+    int64_t rows, width, pitch;
+};
+// Whether two of them share a byte.  Rows of one pitch lie side by side where their places in it are apart; of
+// matrices of different pitches the address ranges decide.
+inline bool rows_overlap(const RowsInMemory &a, const RowsInMemory &b) {
+    auto bytes = [](const RowsInMemory &m) { return m.rows > 0 && m.width > 0 ? (m.rows - 1) * m.pitch + m.width : 0; };
+    if (!a.ptr || !b.ptr || !bytes(a) || !bytes(b) || !ranges_overlap(a.ptr, bytes(a), b.ptr, bytes(b))) return false;
+    if (a.rows == 1 && b.rows == 1) return true;
+    if (a.rows > 1 && b.rows > 1 && a.pitch != b.pitch) return true;
+    const int64_t pitch = a.rows > 1 ? a.pitch : b.pitch;
+    int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.ptr) - reinterpret_cast<uintptr_t>(a.ptr)) % pitch;
+    if (at < 0) at += pitch;
+    return at < a.width || at + b.width > pitch;
+}
+
 struct GemmVariant {
     int bn, cg, out, epi_warps, merge, log, stages, smem_bytes;
     ts_gemm_protocol protocol;  // barrier layout and arrival counts of this variant

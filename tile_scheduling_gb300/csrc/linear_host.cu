@@ -287,12 +287,10 @@ struct Matrix {
     const void *ptr;
     int64_t rows, cols, ld;
     int esize;
-    int64_t bytes() const { return rows > 0 && cols > 0 ? ((rows - 1) * ld + cols) * esize : 0; }
+    RowsInMemory in_memory() const { return {ptr, rows, cols * esize, ld * esize}; }
 };
 
-bool overlap(const Matrix &a, const Matrix &b) {
-    return a.ptr && b.ptr && a.bytes() && b.bytes() && ranges_overlap(a.ptr, a.bytes(), b.ptr, b.bytes());
-}
+bool overlap(const Matrix &a, const Matrix &b) { return rows_overlap(a.in_memory(), b.in_memory()); }
 
 ts_status check_sizes(int64_t M, int64_t N, int64_t K, int32_t out, int32_t act, int32_t tile, int32_t max_workers,
                       double timeout_s) {

@@ -175,6 +175,21 @@ ts_status orth_chain(const OrthRun &r) {
 
 constexpr int64_t kMaxSide = 1 << 20, kMaxBatch = 65535;
 
+// Matrices of a batch lie behind one another, or side by side: a row of each before the next row.
+bool behind(int64_t R, int64_t C, int64_t ld, int64_t matrix) { return matrix >= (R - 1) * ld + C; }
+bool matrices_overlap(int64_t batch, int64_t R, int64_t C, int64_t ld, int64_t matrix) {
+    return !behind(R, C, ld, matrix) && (matrix < C || ld < (batch - 1) * matrix + C);
+}
+// All rows of a batch as rows of one pitch, or what encloses them.
+RowsInMemory rows_of_batch(const void *ptr, int64_t batch, int64_t R, int64_t C, int64_t ld, int64_t matrix, int64_t esize) {
+    if (batch == 1) return {ptr, R, C * esize, ld * esize};
+    if (!behind(R, C, ld, matrix)) return {ptr, R, ((batch - 1) * matrix + C) * esize, ld * esize};
+    if (R == 1) return {ptr, batch, C * esize, matrix * esize};
+    if (matrix % ld == 0) return {ptr, (batch - 1) * (matrix / ld) + R, C * esize, ld * esize};
+    const int64_t all = ((batch - 1) * matrix + (R - 1) * ld + C) * esize;
+    return {ptr, 1, all, all};
+}
+
 }  // namespace
 }  // namespace ts
 
@@ -215,8 +230,8 @@ ts_status ts_orthogonalise(const void *G, void *O, int64_t batch, int64_t R, int
         return fail(TS_ERR_INVALID_ARG, "row strides must cover a row (ldg=%lld ldo=%lld)", static_cast<long long>(ldg),
                     static_cast<long long>(ldo));
     const int64_t g_matrix = o->g_matrix ? o->g_matrix : R * ldg, o_matrix = o->o_matrix ? o->o_matrix : R * ldo;
-    if (batch > 1 && (g_matrix < (R - 1) * ldg + C || o_matrix < (R - 1) * ldo + C || g_matrix > (int64_t(1) << 37) ||
-                      o_matrix > (int64_t(1) << 37)))
+    if (batch > 1 && R > 0 && C > 0 && (matrices_overlap(batch, R, C, ldg, g_matrix) || matrices_overlap(batch, R, C, ldo, o_matrix) ||
+                      g_matrix > (int64_t(1) << 37) || o_matrix > (int64_t(1) << 37)))
         return fail(TS_ERR_INVALID_ARG, "matrices overlap or are too far apart (g_matrix=%lld o_matrix=%lld)",
                     static_cast<long long>(g_matrix), static_cast<long long>(o_matrix));
     if (batch == 0 || R == 0 || C == 0) return TS_OK;
@@ -224,14 +239,15 @@ ts_status ts_orthogonalise(const void *G, void *O, int64_t batch, int64_t R, int
     const int gsize = g_type == TS_OUT_F32 ? 4 : 2;
     if (reinterpret_cast<uintptr_t>(G) % gsize || reinterpret_cast<uintptr_t>(O) % 2)
         return fail(TS_ERR_INVALID_ARG, "G or O is not aligned to its element size");
-    const int64_t gbytes = ((batch - 1) * g_matrix + (R - 1) * ldg + C) * gsize, obytes = ((batch - 1) * o_matrix + (R - 1) * ldo + C) * 2;
+    const RowsInMemory g_rows = rows_of_batch(G, batch, R, C, ldg, g_matrix, gsize), o_rows = rows_of_batch(O, batch, R, C, ldo, o_matrix, 2);
     const OrthPlan plan = plan_orth(batch, R, C, steps);
     if (!workspace || workspace_bytes < plan.total())
         return fail(TS_ERR_INVALID_ARG, "the workspace must hold %lld bytes", static_cast<long long>(plan.total()));
     if (reinterpret_cast<uintptr_t>(workspace) % 256)
         return fail(TS_ERR_INVALID_ARG, "the workspace must start on a 256-byte boundary");
-    if (ranges_overlap(G, gbytes, O, obytes)) return fail(TS_ERR_INVALID_ARG, "O overlaps G");
-    if (ranges_overlap(workspace, plan.total(), G, gbytes) || ranges_overlap(workspace, plan.total(), O, obytes))
+    if (rows_overlap(g_rows, o_rows)) return fail(TS_ERR_INVALID_ARG, "O overlaps G");
+    const RowsInMemory scratch{workspace, 1, plan.total(), plan.total()};
+    if (rows_overlap(scratch, g_rows) || rows_overlap(scratch, o_rows))
         return fail(TS_ERR_INVALID_ARG, "the workspace overlaps G or O");
 
     char *const ws = static_cast<char *>(workspace);
