@@ -735,9 +735,14 @@ typedef struct {
  *   M, N, K  sizes, each in [0, 2^31 - 512]
  *
  * Sums, bias, activation and residual are fp32; y and preact are rounded once, to nearest even
- * (the activation takes z before that rounding).  Results are the same on every run.  Which sums
- * are formed in which order depends on the sizes, the options that are given and the GPU's number
- * of SMs; a NaN or infinity shows in the rows and columns that use it.
+ * (the activation takes z before that rounding).  The sums of products are the tensor core's, which
+ * cuts each of its fp32 additions towards zero instead of rounding it: the result is off towards zero
+ * by some 1e-9 of its norm for each term that one CTA adds up (4096 terms 4.4e-6; rounded additions
+ * 6e-7), which bf16 results show from some 10^6 terms on; a caller who minds it sums shorter pieces
+ * (ts_linear_grad_weight adds them up in fp32 and rounds). Results are the same on every run of the same call.  Which sums
+ * are formed in which order depends on the sizes, the options that are given, how the operands'
+ * addresses and rows are aligned, and the GPU's number of SMs; a NaN or infinity shows in the rows
+ * and columns that use it.
  * M == 0 or N == 0: no-op.  K == 0: y = act(bias) + residual.  Rows of x and w must start on
  * 16-byte boundaries (strides multiples of 8), or the call returns TS_ERR_UNSUPPORTED.  y must not
  * overlap x, w or bias, nor the residual unless it is the residual; preact overlaps nothing.  Column
@@ -780,7 +785,8 @@ ts_status ts_linear_grad_input(const void *grad_z, const void *w, void *grad_x, 
  *
  *   grad_z  device, bf16 [M][N];  x  device, bf16 [M][K];  grad_w  device, bf16 or fp32 [N][K]
  *
- * Both operands are read in place.  M == 0: grad_w = aux, or zeros.
+ * Both operands are read in place.  M == 0: grad_w = aux, or zeros.  aux is added to a finished sum, once and
+ * rounded; the sum itself is cut towards zero as ts_linear's is, also where aux is what earlier calls left.
  */
 ts_status ts_linear_grad_weight(const void *grad_z, const void *x, void *grad_w, int64_t M, int64_t N, int64_t K,
                                 int32_t out_dtype, const ts_linear_grad_opts *opts, void *stream);

@@ -20,7 +20,9 @@ namespace ts {
 namespace {
 
 constexpr int kActThreads = 256;
-constexpr int kActCtas = 4;        // on an SM
+// On an SM: the 64 registers that leaves a thread are 6 too few for bf16 vectors, which spill 24 bytes (17 words
+// loaded again in a loop over rows that waits for memory: 5.6 TB/s of 6.8).
+constexpr int kActCtas = 4;
 constexpr int kActUnroll = 4;      // rows of a thread in flight
 constexpr int kMaxActCluster = 8;
 

@@ -10,6 +10,11 @@
 // around, in place.  With `sym` D is symmetric: the tiles on and above the diagonal are computed
 // and those above it stored twice.
 //
+// The tensor core's additions cut towards zero instead of rounding: a sum that one CTA forms is off by some
+// 1e-9 for each term (an fp32 gradient over 4096 rows by 4.4e-6 of its norm, over 1024 or by four CTAs
+// 1.0e-6; rounded additions 2.5e-7 to 6e-7).  Bf16 results do not show it.  Sums moved to registers every few K
+// blocks would round, for as many more reads of the accumulator.
+//
 // Warp roles (384 threads, one CTA per SM):
 //   warp 0       TMA producer of the operand ring
 //   warp 1       TMEM allocator and MMA issuer

@@ -65,7 +65,7 @@ __device__ __forceinline__ void each_vector(const OrthParams &p, const T *g, int
             const int64_t i = i0 + u * THREADS;
             count[u] = 0;
             if (i < total) {
-                // a CTA's share has fewer than 2^31 vectors (checked on the host)
+                // a CTA's share has fewer than 2^31 vectors: see where the host chooses the shares
                 const int32_t row = fast_div(static_cast<int32_t>(i), p.div_vecs);
                 r[u] = static_cast<int32_t>(r0) + row;
                 c[u] = static_cast<int32_t>(i - row * p.vecs) * V;
@@ -229,7 +229,7 @@ struct OrthRun {
     int64_t ldx, ldn;
     void *O;                  // bf16
     int64_t ldo, o_matrix;
-    int32_t *barrier;         // two counters of the one-launch form
+    int32_t *barrier;         // the one-launch form's counter of arrivals
     double timeout_s;
     cudaStream_t stream;
 };

@@ -66,6 +66,9 @@ OrthPlan plan_orth(int64_t batch, int64_t R, int64_t C, int steps) {
     o.ldn = cdiv(o.n, 64) * 64;
     o.x_bytes = steps > 0 ? round(batch * R * o.ldx * 2) : 0;
     o.n_bytes = steps > 0 ? round(batch * o.ldn * o.ldn * 2) : 0;
+    // A share has fewer than 2^31 values, which the kernels count on: a batch has at most 2^40, so that with 1216
+    // CTAs for one matrix a share has 2^40 / 1216, a whole matrix among more than 1216 fewer, and fewer CTAs
+    // than that have a row of up to 2^20 each or a share of some 1024.
     o.chunks = std::max<int64_t>(1, std::min<int64_t>({cdiv(kOrthChunks, batch), R, cdiv(R * C, kOrthShare)}));
     o.partial_bytes = round(batch * o.chunks * 3 * 4);
     return o;
