@@ -739,10 +739,10 @@ typedef struct {
  * cuts each of its fp32 additions towards zero instead of rounding it: the result is off towards zero
  * by some 1e-9 of its norm for each term that one CTA adds up (4096 terms 4.4e-6; rounded additions
  * 6e-7), which bf16 results show from some 10^6 terms on; a caller who minds it sums shorter pieces
- * (ts_linear_grad_weight adds them up in fp32 and rounds). Results are the same on every run of the same call.  Which sums
- * are formed in which order depends on the sizes, the options that are given, how the operands'
- * addresses and rows are aligned, and the GPU's number of SMs; a NaN or infinity shows in the rows
- * and columns that use it.
+ * (ts_linear_grad_weight adds them up in fp32 and rounds).
+ * Results are the same on every run of the same call.  Which sums are formed in which order depends on
+ * the sizes, the options that are given, how the operands' addresses and rows are aligned, and the
+ * GPU's number of SMs; a NaN or infinity shows in the rows and columns that use it.
  * M == 0 or N == 0: no-op.  K == 0: y = act(bias) + residual.  Rows of x and w must start on
  * 16-byte boundaries (strides multiples of 8), or the call returns TS_ERR_UNSUPPORTED.  y must not
  * overlap x, w or bias, nor the residual unless it is the residual; preact overlaps nothing.  Column

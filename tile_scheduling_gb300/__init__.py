@@ -1111,8 +1111,8 @@ def ts_orthogonalise(g: torch.Tensor, out: torch.Tensor, steps=5, coefficients=(
     if not eps > _SCALE_ZERO:
         raise ValueError("eps must be above 0 in fp32")
     a, b, c = coefficients
-    if a == b == c == 0:
-        raise ValueError("the coefficients must not all be 0")
+    if all(abs(v) <= _SCALE_ZERO for v in (a, b, c)):
+        raise ValueError("the coefficients must not all be 0 in fp32")
     n, R, C = (1, *shape) if dims == 2 else shape
     gm = om = 0
     if n > 1:

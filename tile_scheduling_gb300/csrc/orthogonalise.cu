@@ -138,8 +138,8 @@ LinCall orth_product(const OrthRun &r, int32_t i, int which) {
 
 // One launch where it takes fewer cycles than the chain, by the chain's estimates and this one of a step:
 // a phase some 3 us (the barrier, the first loads, the stores), a K block of a tile 360 cycles with 64
-// columns and 600 with 128.  Measured, a bf16 matrix in a graph, one launch / chain: 128 x 128 57 / 76 us,
-// 512 x 768 85 / 90, 1024 x 1024 100 / 112, two of 700 x 700 100 / 118, 1280 x 1280 141 / 134, 2048 x 1024
+// columns and 600 with 128.  Measured, a bf16 matrix in a graph, one launch / chain: 128 x 128 61 / 76 us,
+// 512 x 768 85 / 90, 1024 x 1024 101 / 112, two of 700 x 700 100 / 118, 1280 x 1280 141 / 134, 2048 x 1024
 // 143 / 121, 2304 x 1008 149 / 125.  (Outside a graph the chain's launches take the host some 80 us.)
 bool one_is_quicker(const OrthRun &r) {
     const int64_t sms = device_sms(current_device());
